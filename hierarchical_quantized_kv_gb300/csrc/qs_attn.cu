@@ -1594,13 +1594,14 @@ extern "C" {
 
 qs_status qs_attn_workspace_size_gqa(const qs_cache *c, int32_t n_q, int32_t group,
                                      size_t *bytes) {
-  qs_status s = check_cache(c);
+  qs_status s = check_cache_any(c);
   if (s != QS_OK) return s;
+  const int bits = c->upper_bits & ~QS_PAGED;
   if (!bytes || n_q < 1 || n_q > kMaxQ || group < 1 || group * n_q > kMaxR) return QS_ERR_ARG;
   int P0 = 0, P1 = 0, P2 = 0;
-  if ((s = grid_size(QS_DRAFT_UPPER4, false, c->upper_bits, 1, P0)) != QS_OK) return s;
-  if ((s = grid_size(QS_DRAFT_UPPER4, true, c->upper_bits, 1, P1)) != QS_OK) return s;
-  if ((s = grid_size(QS_VERIFY_INT8, false, c->upper_bits, (group * n_q + 7) / 8, P2)) != QS_OK) return s;
+  if ((s = grid_size(QS_DRAFT_UPPER4, false, bits, 1, P0)) != QS_OK) return s;
+  if ((s = grid_size(QS_DRAFT_UPPER4, true, bits, 1, P1)) != QS_OK) return s;
+  if ((s = grid_size(QS_VERIFY_INT8, false, bits, (group * n_q + 7) / 8, P2)) != QS_OK) return s;
   const int P = P0 > P1 ? (P0 > P2 ? P0 : P2) : (P1 > P2 ? P1 : P2);
   *bytes = ws_bytes(P, c->B, c->H, group * n_q);
   return QS_OK;

@@ -111,8 +111,19 @@ qs_status qs_cache_bytes(int32_t B, int32_t H, int32_t D, int32_t G, int32_t cap
   return QS_OK;
 }
 
+qs_status qs_paged_cache_bytes(int32_t B, int32_t H, int32_t D, int32_t G, int32_t n_pages,
+                               qs_cache_bytes_t *out) {
+  if (n_pages <= 0) return QS_ERR_ARG;
+  const qs_status s = qs_cache_bytes(B, H, D, G, 1, out);
+  if (s != QS_OK) return s;
+  const size_t slots = (size_t)n_pages * H;
+  out->k_upper = out->k_lower = out->v_upper = out->v_lower = slots * G * (D / 2);
+  out->meta = slots * 4 * 128 * 2;
+  return QS_OK;
+}
+
 qs_status qs_state_reset(const qs_cache *c, qs_stream_t stream) {
-  qs_status s = check_cache(c);
+  qs_status s = check_cache_any(c);
   if (s != QS_OK) return s;
   cudaError_t e = cudaMemsetAsync(c->state, 0, (size_t)c->B * QS_STATE_WORDS * 4,
                                   (cudaStream_t)stream);
@@ -123,7 +134,7 @@ qs_status qs_state_reset(const qs_cache *c, qs_stream_t stream) {
 
 qs_status qs_buffer_append(const qs_cache *c, const uint16_t *k_new, const uint16_t *v_new,
                            int32_t n_new, qs_stream_t stream) {
-  qs_status s = check_cache(c);
+  qs_status s = check_cache_any(c);
   if (s != QS_OK) return s;
   if (!k_new || !v_new || n_new < 1 || n_new > kRing) return QS_ERR_ARG;
   if (!aligned16(k_new) || !aligned16(v_new)) return QS_ERR_ALIGN;
@@ -133,7 +144,7 @@ qs_status qs_buffer_append(const qs_cache *c, const uint16_t *k_new, const uint1
 }
 
 qs_status qs_buffer_rollback(const qs_cache *c, const int32_t *d_n_drop, qs_stream_t stream) {
-  qs_status s = check_cache(c);
+  qs_status s = check_cache_any(c);
   if (s != QS_OK) return s;
   if (!d_n_drop) return QS_ERR_ARG;
   return launch_pdl(rollback_kernel, dim3((c->B + 127) / 128), dim3(128), 0, (cudaStream_t)stream,
@@ -141,7 +152,7 @@ qs_status qs_buffer_rollback(const qs_cache *c, const int32_t *d_n_drop, qs_stre
 }
 
 qs_status qs_need_flush(const qs_cache *c, int32_t n_next, uint8_t *d_mask, qs_stream_t stream) {
-  qs_status s = check_cache(c);
+  qs_status s = check_cache_any(c);
   if (s != QS_OK) return s;
   if (!d_mask || n_next < 0) return QS_ERR_ARG;
   return launch_pdl(need_flush_kernel, dim3((c->B + 127) / 128), dim3(128), 0,
@@ -149,7 +160,7 @@ qs_status qs_need_flush(const qs_cache *c, int32_t n_next, uint8_t *d_mask, qs_s
 }
 
 qs_status qs_get_errors(const qs_cache *c, int32_t *h_err, qs_stream_t stream) {
-  qs_status s = check_cache(c);
+  qs_status s = check_cache_any(c);
   if (s != QS_OK) return s;
   if (!h_err) return QS_ERR_ARG;
   cudaStream_t st = (cudaStream_t)stream;

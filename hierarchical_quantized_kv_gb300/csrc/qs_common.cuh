@@ -23,17 +23,54 @@ constexpr int kMaxQ = 8;        // queries per call (one n8 MMA tile)
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-inline qs_status check_cache(const qs_cache *c) {
+// A cache of either kind (contiguous groups or pages): for the calls that
+// touch only the buffer and the counters.
+inline qs_status check_cache_any(const qs_cache *c) {
   if (!c || !c->state || !c->arrive || !c->buf_k || !c->buf_v) return QS_ERR_ARG;
   if (c->B <= 0 || c->H <= 0 || c->cap_groups <= 0) return QS_ERR_SHAPE;
   if (c->D != kD || c->G != kG) return QS_ERR_UNSUPPORTED;
   if (c->B > kMaxB) return QS_ERR_UNSUPPORTED;
-  if (c->upper_bits != 4 && c->upper_bits != 2) return QS_ERR_ARG;
+  const int bits = c->upper_bits & ~QS_PAGED;
+  if (bits != 4 && bits != 2) return QS_ERR_ARG;
   if (!c->k_upper || !c->k_lower || !c->v_upper || !c->v_lower || !c->meta) return QS_ERR_ARG;
   const void *ps[] = {c->k_upper, c->k_lower, c->v_upper, c->v_lower,
                       c->meta,    c->buf_k,   c->buf_v,   c->state, c->arrive};
   for (const void *p : ps)
     if (!aligned16(p)) return QS_ERR_ALIGN;
+  return QS_OK;
+}
+
+// A cache with contiguous groups: the calls that index the group arrays by
+// sequence refuse a paged one.
+inline qs_status check_cache(const qs_cache *c) {
+  const qs_status s = check_cache_any(c);
+  if (s != QS_OK) return s;
+  return (c->upper_bits & QS_PAGED) ? QS_ERR_ARG : QS_OK;
+}
+
+// The page table a kernel gets: none (null) for contiguous groups.
+struct Pages {
+  const int32_t *table;  // [B][cap_groups]
+  int n_pages;
+};
+
+// A cache and its pages: pg must be given exactly for a cache with QS_PAGED.
+// out: the cache with the flag taken off, as the kernels take it.
+inline qs_status check_pages(const qs_cache *c, const qs_pages *pg, bool need_pages, qs_cache *out,
+                             Pages *pages) {
+  const qs_status s = check_cache_any(c);
+  if (s != QS_OK) return s;
+  const bool paged = (c->upper_bits & QS_PAGED) != 0;
+  if (paged != (pg != nullptr) || (need_pages && !paged)) return QS_ERR_ARG;
+  *pages = Pages{nullptr, 0};
+  if (paged) {
+    if (!pg->table) return QS_ERR_ARG;
+    if (pg->n_pages <= 0) return QS_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(pg->table) % 4) return QS_ERR_ALIGN;
+    *pages = Pages{pg->table, pg->n_pages};
+  }
+  *out = *c;
+  out->upper_bits &= ~QS_PAGED;
   return QS_OK;
 }
 
@@ -111,6 +148,19 @@ __device__ __forceinline__ constexpr bool smem_in(uint32_t, uint32_t) { return t
 // [i, i + n) inside an array of len elements
 __device__ __forceinline__ bool in_range(size_t i, size_t n, size_t len) {
   return i <= len && n <= len - i;
+}
+
+// Entries of the group arrays: [B][H][cap_groups], or [n_pages][H].
+__device__ __forceinline__ size_t group_slots(const qs_cache &c, const Pages &pg) {
+  return pg.table ? (size_t)pg.n_pages * c.H : (size_t)c.B * c.H * c.cap_groups;
+}
+// The entry of group g (0 <= g < cap_groups) of sequence b, head h in the
+// group arrays; -1 if its page lies outside the pool.
+__device__ __forceinline__ long long group_slot(const qs_cache &c, const Pages &pg, int b, int h,
+                                                int g) {
+  if (!pg.table) return ((long long)b * c.H + h) * c.cap_groups + g;
+  const int page = __ldg(pg.table + (size_t)b * c.cap_groups + g);
+  return page >= 0 && page < pg.n_pages ? (long long)page * c.H + h : -1;
 }
 
 // Upper bound on any single pipeline wait; a healthy call takes well under a

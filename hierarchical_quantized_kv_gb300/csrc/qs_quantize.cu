@@ -310,13 +310,14 @@ __device__ void quantize_loaded(FlushSmem<QW> &S, const __half (*kt)[kSlice],
 // One CTA's share of quantizing a group of G tokens whose fp16 key and value
 // rows (D channels each, row stride D) start at gk and gv: key channels
 // [32 part, 32 part + 32) and value tokens [32 part, 32 part + 32), written
-// as group `grp` (index into the [B][H][cap] group arrays).  32 QW threads.
+// as group `grp` (index into the n_grp entries of the group arrays).  32 QW
+// threads.
 template <int QW>
 __device__ void quantize_part(FlushSmem<QW> &S, const __half *gk, const __half *gv,
-                              const qs_cache &c, size_t grp, int part, int tid) {
+                              const qs_cache &c, size_t n_grp, size_t grp, int part, int tid) {
   // checked build: a group index out of the arrays writes nothing (the same
   // for every thread of the CTA)
-  if (!chk(in_range(grp, 1, (size_t)c.B * c.H * c.cap_groups), 20)) return;
+  if (!chk(in_range(grp, 1, n_grp), 20)) return;
   load_part<QW, false>(S.k, S.v, gk, gv, part, tid);
   __syncthreads();
   quantize_loaded(S, S.k, S.v, c, grp, part, tid);
@@ -337,7 +338,7 @@ struct PrefillSmem {
 // tokens (qs_need_flush's rule; mask unused); else the masked ones (all
 // without a mask).
 __global__ void __launch_bounds__(32 * kFlushWarps)
-    flush_kernel(qs_cache c, const uint8_t *__restrict__ mask, int n_next) {
+    flush_kernel(qs_cache c, Pages pg, const uint8_t *__restrict__ mask, int n_next) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   FlushSmem<kFlushWarps> &S = *reinterpret_cast<FlushSmem<kFlushWarps> *>(smem_raw);
   const int part = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
@@ -354,6 +355,9 @@ __global__ void __launch_bounds__(32 * kFlushWarps)
     } else if (act && (ng < 0 || ng >= c.cap_groups)) {
       if (lead) atomicOr(&st[QS_ST_ERR], QS_DEV_CAPACITY);
       act = 0;
+    } else if (act && group_slot(c, pg, b, h, ng) < 0) {
+      if (lead) atomicOr(&st[QS_ST_ERR], QS_DEV_PAGE);
+      act = 0;
     }
     S.act = act;
     S.base = st[QS_ST_HALF_BASE] & 1;
@@ -366,7 +370,7 @@ __global__ void __launch_bounds__(32 * kFlushWarps)
   const __half *gk = reinterpret_cast<const __half *>(c.buf_k) + (bh * kRing + base * kG) * kD;
   const __half *gv = reinterpret_cast<const __half *>(c.buf_v) + (bh * kRing + base * kG) * kD;
 
-  quantize_part(S, gk, gv, c, bh * c.cap_groups + g, part, tid);
+  quantize_part(S, gk, gv, c, group_slots(c, pg), (size_t)group_slot(c, pg, b, h, g), part, tid);
   __syncthreads();
   // every CTA of the sequence has read the old counters once the ticket
   // reaches kParts H - 1 (the planes are published by the kernel's end)
@@ -385,7 +389,8 @@ __global__ void __launch_bounds__(32 * kFlushWarps)
 // while the current one is quantized; the last two blocks copy buffer halves
 // 0 and 1.  The CTA that arrives last on the sequence's ticket writes the
 // counters, so every CTA reads the old (empty) ones first.
-__global__ void __launch_bounds__(32 * kPrefillWarps) prefill_kernel(qs_cache c, const uint16_t *__restrict__ k,
+__global__ void __launch_bounds__(32 * kPrefillWarps) prefill_kernel(qs_cache c, Pages pg,
+                                                     const uint16_t *__restrict__ k,
                                                      const uint16_t *__restrict__ v, int T,
                                                      const int32_t *__restrict__ len, int nq) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -417,6 +422,16 @@ __global__ void __launch_bounds__(32 * kPrefillWarps) prefill_kernel(qs_cache c,
   __syncthreads();
   if (!S.act) return;
   const int ng = S.g, fill = S.base;
+  if (pg.table) {
+    // every page the prompt needs, looked at by every CTA alike: a bad one
+    // leaves the whole sequence unchanged
+    int bad = 0;
+    for (int g = tid; g < ng; g += 32 * kPrefillWarps) bad |= group_slot(c, pg, b, h, g) < 0;
+    if (__syncthreads_or(bad)) {
+      if (h == 0 && x == 0 && tid == 0) atomicOr(&st[QS_ST_ERR], QS_DEV_PAGE);
+      return;
+    }
+  }
   const size_t bh = (size_t)b * c.H + h;
   const uint16_t *kp = k + bh * T * kD, *vp = v + bh * T * kD;
   if (x < nq) {
@@ -446,13 +461,14 @@ __global__ void __launch_bounds__(32 * kPrefillWarps) prefill_kernel(qs_cache c,
       }
       __syncthreads();  // quarter i's rows, copied by every thread, are visible
       const int g = i >> 2;
+      const size_t grp = (size_t)group_slot(c, pg, b, h, g);
       // checked build: the group's prompt rows inside the prompt array
       if (chk(in_range(((size_t)g + 1) * kG, 0, (size_t)T), 22) &&
-          chk(in_range(bh * c.cap_groups + g, 1, (size_t)c.B * c.H * c.cap_groups), 20)) {
+          chk(in_range(grp, 1, group_slots(c, pg)), 20)) {
         if (i & 1)
-          quantize_loaded(S, PS.k1, PS.v1, c, bh * c.cap_groups + g, i & 3, tid);
+          quantize_loaded(S, PS.k1, PS.v1, c, grp, i & 3, tid);
         else
-          quantize_loaded(S, S.k, S.v, c, bh * c.cap_groups + g, i & 3, tid);
+          quantize_loaded(S, S.k, S.v, c, grp, i & 3, tid);
       }
       __syncthreads();  // the buffer and the scratch are free for the next quarters
     }
@@ -499,39 +515,79 @@ qs_status set_smem_once(const void *kernel, int smem, int *mask) {
 int g_flush_ready = 0, g_prefill_ready = 0;  // one bit per device ordinal below 32
 }  // namespace
 
-extern "C" qs_status qs_prefill(const qs_cache *c, const uint16_t *k, const uint16_t *v, int32_t T,
-                                const int32_t *d_len, qs_stream_t stream) {
-  qs_status s = check_cache(c);
-  if (s != QS_OK) return s;
+namespace {
+
+qs_status prefill(const qs_cache &c, const Pages &pg, const uint16_t *k, const uint16_t *v, int32_t T,
+                  const int32_t *d_len, qs_stream_t stream) {
   if (!k || !v || !d_len || T < 0 || T > (1 << 26)) return QS_ERR_ARG;
   if (!aligned16(k) || !aligned16(v)) return QS_ERR_ALIGN;
   const int smem = (int)sizeof(PrefillSmem<kPrefillWarps>);
-  if ((s = set_smem_once((const void *)prefill_kernel, smem, &g_prefill_ready)) != QS_OK) return s;
+  const qs_status s = set_smem_once((const void *)prefill_kernel, smem, &g_prefill_ready);
+  if (s != QS_OK) return s;
   const int gmax = T > 2 * kG ? (T - 2 * kG + kG - 1) / kG : 0;
   const int nq = (4 * gmax + kPrefillQuarters - 1) / kPrefillQuarters;
-  return launch_pdl(prefill_kernel, dim3(nq + 2, c->H, c->B), dim3(32 * kPrefillWarps), smem,
-                    (cudaStream_t)stream, *c, k, v, (int)T, d_len, nq);
+  return launch_pdl(prefill_kernel, dim3(nq + 2, c.H, c.B), dim3(32 * kPrefillWarps), smem,
+                    (cudaStream_t)stream, c, pg, k, v, (int)T, d_len, nq);
 }
 
-extern "C" qs_status qs_quantize_flush(const qs_cache *c, const uint8_t *d_mask,
-                                       qs_stream_t stream) {
-  qs_status s = check_cache(c);
-  if (s != QS_OK) return s;
+qs_status flush(const qs_cache &c, const Pages &pg, const uint8_t *d_mask, int n_next,
+                qs_stream_t stream) {
   const int smem = (int)sizeof(FlushSmem<kFlushWarps>);
-  if ((s = set_smem_once((const void *)flush_kernel, smem, &g_flush_ready)) != QS_OK) return s;
-  return launch_pdl(flush_kernel, dim3(kParts, c->H, c->B), dim3(32 * kFlushWarps), smem,
-                    (cudaStream_t)stream, *c, d_mask, -1);
+  const qs_status s = set_smem_once((const void *)flush_kernel, smem, &g_flush_ready);
+  if (s != QS_OK) return s;
+  return launch_pdl(flush_kernel, dim3(kParts, c.H, c.B), dim3(32 * kFlushWarps), smem,
+                    (cudaStream_t)stream, c, pg, d_mask, n_next);
 }
 
-extern "C" qs_status qs_quantize_flush_due(const qs_cache *c, int32_t n_next, qs_stream_t stream) {
-  qs_status s = check_cache(c);
+}  // namespace
+
+extern "C" {
+
+qs_status qs_prefill(const qs_cache *c, const uint16_t *k, const uint16_t *v, int32_t T,
+                     const int32_t *d_len, qs_stream_t stream) {
+  const qs_status s = check_cache(c);
+  return s != QS_OK ? s : prefill(*c, Pages{nullptr, 0}, k, v, T, d_len, stream);
+}
+
+qs_status qs_prefill_paged(const qs_cache *c, const qs_pages *pg, const uint16_t *k,
+                           const uint16_t *v, int32_t T, const int32_t *d_len, qs_stream_t stream) {
+  qs_cache cc;
+  Pages pages;
+  const qs_status s = check_pages(c, pg, true, &cc, &pages);
+  return s != QS_OK ? s : prefill(cc, pages, k, v, T, d_len, stream);
+}
+
+qs_status qs_quantize_flush(const qs_cache *c, const uint8_t *d_mask, qs_stream_t stream) {
+  const qs_status s = check_cache(c);
+  return s != QS_OK ? s : flush(*c, Pages{nullptr, 0}, d_mask, -1, stream);
+}
+
+qs_status qs_quantize_flush_paged(const qs_cache *c, const qs_pages *pg, const uint8_t *d_mask,
+                                  qs_stream_t stream) {
+  qs_cache cc;
+  Pages pages;
+  const qs_status s = check_pages(c, pg, true, &cc, &pages);
+  return s != QS_OK ? s : flush(cc, pages, d_mask, -1, stream);
+}
+
+qs_status qs_quantize_flush_due(const qs_cache *c, int32_t n_next, qs_stream_t stream) {
+  const qs_status s = check_cache(c);
   if (s != QS_OK) return s;
   if (n_next < 0 || n_next > kRing) return QS_ERR_ARG;
-  const int smem = (int)sizeof(FlushSmem<kFlushWarps>);
-  if ((s = set_smem_once((const void *)flush_kernel, smem, &g_flush_ready)) != QS_OK) return s;
-  return launch_pdl(flush_kernel, dim3(kParts, c->H, c->B), dim3(32 * kFlushWarps), smem,
-                    (cudaStream_t)stream, *c, static_cast<const uint8_t *>(nullptr), (int)n_next);
+  return flush(*c, Pages{nullptr, 0}, nullptr, n_next, stream);
 }
+
+qs_status qs_quantize_flush_due_paged(const qs_cache *c, const qs_pages *pg, int32_t n_next,
+                                      qs_stream_t stream) {
+  qs_cache cc;
+  Pages pages;
+  const qs_status s = check_pages(c, pg, true, &cc, &pages);
+  if (s != QS_OK) return s;
+  if (n_next < 0 || n_next > kRing) return QS_ERR_ARG;
+  return flush(cc, pages, nullptr, n_next, stream);
+}
+
+}  // extern "C"
 
 #if QS_CHECKED
 // Checked build only: this file's failure count and first failing tag.

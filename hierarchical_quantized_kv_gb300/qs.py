@@ -19,7 +19,8 @@ QS_DRAFT_UPPER4, QS_VERIFY_INT8 = 0, 1
 QS_STATIC_WS_BYTES = 8 << 20
 DEV_OVERFLOW, DEV_OVER_ROLLBACK, DEV_FLUSH_UNCOMMITTED, DEV_CAPACITY, DEV_NQ_GT_FILL, DEV_TIMEOUT = (
     1, 2, 4, 8, 16, 32)
-DEV_PREFILL = 64
+DEV_PREFILL, DEV_PAGE = 64, 128
+QS_PAGED = 0x100
 ST_N_GROUPS, ST_FILL, ST_PENDING, ST_HALF_BASE, ST_ERR, ST_TICKET = range(6)
 STATE_WORDS = 8
 META_K_SCALE, META_K_ZERO, META_V_SCALE, META_V_ZERO = range(4)
@@ -32,6 +33,10 @@ class QsCacheStruct(ctypes.Structure):
     _fields_ = [("B", _I32), ("H", _I32), ("D", _I32), ("G", _I32), ("cap_groups", _I32),
                 ("upper_bits", _I32), ("k_upper", _P), ("k_lower", _P), ("v_upper", _P), ("v_lower", _P),
                 ("meta", _P), ("buf_k", _P), ("buf_v", _P), ("state", _P), ("arrive", _P)]
+
+
+class QsPagesStruct(ctypes.Structure):
+    _fields_ = [("table", _P), ("n_pages", _I32)]
 
 
 class QsCacheBytes(ctypes.Structure):
@@ -51,6 +56,12 @@ _lib = None
 # exported entry points and their argument types
 _SIGS = {
     "qs_cache_bytes": [_I32, _I32, _I32, _I32, _I32, ctypes.POINTER(QsCacheBytes)],
+    "qs_paged_cache_bytes": [_I32, _I32, _I32, _I32, _I32, ctypes.POINTER(QsCacheBytes)],
+    "qs_quantize_flush_paged": [ctypes.POINTER(QsCacheStruct), ctypes.POINTER(QsPagesStruct), _P, _P],
+    "qs_quantize_flush_due_paged": [ctypes.POINTER(QsCacheStruct), ctypes.POINTER(QsPagesStruct),
+                                    _I32, _P],
+    "qs_prefill_paged": [ctypes.POINTER(QsCacheStruct), ctypes.POINTER(QsPagesStruct), _P, _P, _I32,
+                         _P, _P],
     "qs_state_reset": [ctypes.POINTER(QsCacheStruct), _P],
     "qs_buffer_append": [ctypes.POINTER(QsCacheStruct), _P, _P, _I32, _P],
     "qs_buffer_rollback": [ctypes.POINTER(QsCacheStruct), _P, _P],
@@ -66,6 +77,8 @@ _SIGS = {
     "qs_attn_decode_gqa": [ctypes.POINTER(QsCacheStruct), ctypes.c_int, _P, _I32, _I32, ctypes.c_float,
                            _P, _P, _P, ctypes.c_size_t, _P],
     "qs_prefill": [ctypes.POINTER(QsCacheStruct), _P, _P, _I32, _P, _P],
+    "qs_cache_read": [ctypes.POINTER(QsCacheStruct), ctypes.POINTER(QsPagesStruct), ctypes.c_int,
+                      _I32, _I32, _P, _P, _P],
     "qs_spec_accept": [_P, _P, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _P],
     "qs_attn_decode_static_ws": [ctypes.POINTER(QsCacheStruct), ctypes.c_int, _P, _I32,
                                  ctypes.c_float, _P, _P, _P],
@@ -149,33 +162,70 @@ class Cache:
     def __init__(self, B, H, cap_groups, device="cuda", D=128, G=128, upper_bits=4):
         """upper_bits: the top bits of each 8-bit code the draft reads (4, or
         2 for the two-bit draft layout of include/qs.h)."""
+        qs_cache_bytes(B, H, cap_groups, D, G)  # validates the sizes
+        self._alloc(B, H, cap_groups, device, D, G, upper_bits, (B, H, cap_groups))
+        self.struct = self._struct(upper_bits)
+        self._ref = ctypes.byref(self.struct)
+
+    def _alloc(self, B, H, cap_groups, device, D, G, upper_bits, slots):
         import torch
         self.B, self.H, self.D, self.G, self.cap = B, H, D, G, cap_groups
         self.upper_bits = upper_bits
-        qs_cache_bytes(B, H, cap_groups, D, G)  # validates the sizes
         u8 = dict(dtype=torch.uint8, device=device)
         f16 = dict(dtype=torch.float16, device=device)
-        self.k_upper = torch.zeros((B, H, cap_groups, G, D // 2), **u8)
-        self.k_lower = torch.zeros((B, H, cap_groups, G, D // 2), **u8)
-        self.v_upper = torch.zeros((B, H, cap_groups, G // 32, D, 16), **u8)
-        self.v_lower = torch.zeros((B, H, cap_groups, G // 32, D, 16), **u8)
-        self.meta = torch.zeros((B, H, cap_groups, 4, 128), **f16)
+        self.k_upper = torch.zeros(slots + (G, D // 2), **u8)
+        self.k_lower = torch.zeros(slots + (G, D // 2), **u8)
+        self.v_upper = torch.zeros(slots + (G // 32, D, 16), **u8)
+        self.v_lower = torch.zeros(slots + (G // 32, D, 16), **u8)
+        self.meta = torch.zeros(slots + (4, 128), **f16)
         self.buf_k = torch.zeros((B, H, 2 * G, D), **f16)
         self.buf_v = torch.zeros((B, H, 2 * G, D), **f16)
         self.state = torch.zeros((B, STATE_WORDS), dtype=torch.int32, device=device)
         self.arrive = torch.zeros((B, H), dtype=torch.int32, device=device)
-        self.struct = QsCacheStruct(B, H, D, G, cap_groups, upper_bits,
-                                    self.k_upper.data_ptr(), self.k_lower.data_ptr(),
-                                    self.v_upper.data_ptr(), self.v_lower.data_ptr(),
-                                    self.meta.data_ptr(), self.buf_k.data_ptr(),
-                                    self.buf_v.data_ptr(), self.state.data_ptr(),
-                                    self.arrive.data_ptr())
-        self._ref = ctypes.byref(self.struct)
+
+    def _struct(self, upper_bits):
+        return QsCacheStruct(self.B, self.H, self.D, self.G, self.cap, upper_bits,
+                             self.k_upper.data_ptr(), self.k_lower.data_ptr(),
+                             self.v_upper.data_ptr(), self.v_lower.data_ptr(),
+                             self.meta.data_ptr(), self.buf_k.data_ptr(),
+                             self.buf_v.data_ptr(), self.state.data_ptr(),
+                             self.arrive.data_ptr())
+
+    # the qs_pages argument of the calls that take an optional one: none
+    _pages_ref = None
 
     def nbytes(self):
         return sum(t.numel() * t.element_size() for t in
                    (self.k_upper, self.k_lower, self.v_upper, self.v_lower, self.meta,
                     self.buf_k, self.buf_v, self.state, self.arrive))
+
+
+class PagedCache(Cache):
+    """A cache whose groups lie in a pool of n_pages pages (include/qs.h,
+    qs_pages): the group arrays are [n_pages, H, ...], ``table`` (int32 [B,
+    cap_groups], filled with -1) names the page of each sequence's groups and
+    is the caller's to fill.  The calls for contiguous caches refuse it."""
+
+    def __init__(self, B, H, cap_groups, n_pages, device="cuda", D=128, G=128, upper_bits=4):
+        import torch
+        qs_cache_bytes(B, H, cap_groups, D, G)  # validates the sizes
+        qs_paged_cache_bytes(B, H, n_pages, D, G)
+        self.n_pages = n_pages
+        self._alloc(B, H, cap_groups, device, D, G, upper_bits, (n_pages, H))
+        self.table = torch.full((B, cap_groups), -1, dtype=torch.int32, device=device)
+        self.struct = self._struct(upper_bits | QS_PAGED)
+        self._ref = ctypes.byref(self.struct)
+        self.pages_struct = QsPagesStruct(self.table.data_ptr(), n_pages)
+        self._pages_ref = ctypes.byref(self.pages_struct)
+
+    def nbytes(self):
+        return super().nbytes() + self.table.numel() * self.table.element_size()
+
+
+def qs_paged_cache_bytes(B, H, n_pages, D=128, G=128):
+    out = QsCacheBytes()
+    _check("qs_paged_cache_bytes", lib().qs_paged_cache_bytes(B, H, D, G, n_pages, ctypes.byref(out)))
+    return {n: getattr(out, n) for n, _ in QsCacheBytes._fields_}
 
 
 def qs_state_reset(cache, stream=None):
@@ -217,6 +267,36 @@ def qs_prefill(cache, k, v, lens, stream=None):
     assert k.is_contiguous() and v.is_contiguous() and k.shape == v.shape
     _check("qs_prefill", lib().qs_prefill(cache._ref, _ptr(k), _ptr(v), int(k.shape[2]), _ptr(lens),
                                           _stream(stream)))
+
+
+def qs_quantize_flush_paged(cache, mask=None, stream=None):
+    """qs_quantize_flush on a PagedCache."""
+    _check("qs_quantize_flush_paged", lib().qs_quantize_flush_paged(
+        cache._ref, cache._pages_ref, _ptr(mask), _stream(stream)))
+
+
+def qs_quantize_flush_due_paged(cache, n_next, stream=None):
+    """qs_quantize_flush_due on a PagedCache."""
+    _check("qs_quantize_flush_due_paged", lib().qs_quantize_flush_due_paged(
+        cache._ref, cache._pages_ref, int(n_next), _stream(stream)))
+
+
+def qs_prefill_paged(cache, k, v, lens, stream=None):
+    """qs_prefill on a PagedCache."""
+    assert k.is_contiguous() and v.is_contiguous() and k.shape == v.shape
+    _check("qs_prefill_paged", lib().qs_prefill_paged(cache._ref, cache._pages_ref, _ptr(k), _ptr(v),
+                                                      int(k.shape[2]), _ptr(lens), _stream(stream)))
+
+
+def qs_cache_read(cache, mode, k, v, tok0=0, stream=None):
+    """Tokens [tok0, tok0 + T) of each sequence as fp16 rows into k, v: fp16
+    [B, H, T, D] contiguous device tensors, one of them may be None.  Rows past
+    a sequence's last token stay as they were."""
+    T = (v if k is None else k).shape[2] if k is not None or v is not None else 0
+    for t in (k, v):
+        assert t is None or (t.is_contiguous() and t.shape == (cache.B, cache.H, T, cache.D))
+    _check("qs_cache_read", lib().qs_cache_read(cache._ref, cache._pages_ref, int(mode), int(tok0),
+                                                int(T), _ptr(k), _ptr(v), _stream(stream)))
 
 
 def qs_spec_accept(p, q, draft, u, e, n_accept, token, n_drop, stream=None):

@@ -89,8 +89,10 @@ enum {
   QS_DEV_NQ_GT_FILL = 16,        /* attention with n_q > buffered tokens */
   QS_DEV_TIMEOUT = 32,           /* a pipeline wait ran out of time (never
                                     expected; the call's results are invalid) */
-  QS_DEV_PREFILL = 64            /* prefill of a non-empty cache, or a prompt
+  QS_DEV_PREFILL = 64,           /* prefill of a non-empty cache, or a prompt
                                     length outside [0, T] */
+  QS_DEV_PAGE = 128              /* a page table entry in use outside
+                                    [0, n_pages) */
 };
 
 /* Per-sequence counters: int32 state[B][QS_STATE_WORDS]. */
@@ -112,7 +114,8 @@ enum { QS_META_K_SCALE = 0, QS_META_K_ZERO = 1, QS_META_V_SCALE = 2, QS_META_V_Z
  * aligned.  Logical buffer token i of sequence b lives in slot
  * (half_base * G + i) mod 2G.  Sizes for each array: qs_cache_bytes.
  *
- *  upper_bits  4 or 2: how many top bits of C_INT8 the draft reads (below).
+ *  upper_bits  4 or 2: how many top bits of C_INT8 the draft reads (below);
+ *      with QS_PAGED added, the groups lie in pages (qs_pages, below).
  *  k_upper, k_lower  uint8 [B][H][cap][G tokens][D/2]: C_U / C_L of the keys,
  *      token-major; byte i of a token row holds channel 2i in bits 0-3 and
  *      channel 2i+1 in bits 4-7 (64 bytes per token).
@@ -151,7 +154,7 @@ enum { QS_META_K_SCALE = 0, QS_META_K_ZERO = 1, QS_META_V_SCALE = 2, QS_META_V_Z
  */
 typedef struct {
   int32_t B, H, D, G, cap_groups;
-  int32_t upper_bits;     /* 4 or 2 */
+  int32_t upper_bits;     /* 4 or 2, plus QS_PAGED for a paged cache */
   uint8_t *k_upper, *k_lower, *v_upper, *v_lower;
   uint16_t *meta;         /* fp16 bits */
   uint16_t *buf_k, *buf_v; /* fp16 bits */
@@ -171,6 +174,41 @@ typedef struct {
  * double buffer of two halves of G tokens), not a memory layout. */
 qs_status qs_cache_bytes(int32_t B, int32_t H, int32_t D, int32_t G, int32_t cap_groups,
                          qs_cache_bytes_t *out);
+
+/* Added to qs_cache.upper_bits: the group arrays are a pool of pages. */
+#define QS_PAGED 0x100
+
+/* The pages of a paged cache (upper_bits 4 | QS_PAGED or 2 | QS_PAGED): a page
+ * is one group of all H heads, and the group arrays are pools of n_pages
+ * pages instead of B x cap_groups groups:
+ *   k_upper, k_lower  uint8 [n_pages][H][G tokens][D/2]
+ *   v_upper, v_lower  uint8 [n_pages][H][G/32][D][16]
+ *   meta              fp16 [n_pages][H][4][128]
+ * with the bytes inside a group as above.  Group g of sequence b lies in page
+ * table[b * cap_groups + g]; cap_groups is then only the width of the table
+ * (the most groups a sequence may have).  Buffers, state and arrive are as for
+ * a contiguous cache.  The table (int32 [B][cap_groups], device memory,
+ * 4-byte aligned) is the caller's: entries below n_groups must be valid, the
+ * entry of a group about to be written before the call that writes it, the
+ * rest is not read.  Sequences may share pages (a common prefix); a page that
+ * is written (flush, prefill) must belong to one sequence alone.  An entry in
+ * use outside [0, n_pages) gives QS_DEV_PAGE: a write leaves the sequence
+ * unchanged, a read leaves the group out.
+ * Calls on a paged cache: the *_paged ones, those that take an optional
+ * qs_pages, and those that touch no group (qs_state_reset, qs_buffer_append,
+ * qs_buffer_rollback, qs_need_flush, qs_get_errors, the workspace sizes).
+ * Every other call refuses it (QS_ERR_ARG), as the *_paged calls refuse a
+ * contiguous one.  No counterpart on the pages: it lets a serving process
+ * share one pool among sequences of unknown length. */
+typedef struct {
+  const int32_t *table;
+  int32_t n_pages;
+} qs_pages;
+
+/* Byte size of every array of a paged cache.  Pure host function; errors as
+ * qs_cache_bytes. */
+qs_status qs_paged_cache_bytes(int32_t B, int32_t H, int32_t D, int32_t G, int32_t n_pages,
+                               qs_cache_bytes_t *out);
 
 /* Zero every sequence's counters (empty cache) and the attention arrival
  * counters.  Asynchronous memsets.  No counterpart on the pages: it is this
@@ -242,6 +280,37 @@ qs_status qs_quantize_flush_due(const qs_cache *c, int32_t n_next, qs_stream_t s
  * "What carries the argument" (groups of G tokens, two buffer halves). */
 qs_status qs_prefill(const qs_cache *c, const uint16_t *k, const uint16_t *v, int32_t T,
                      const int32_t *d_len, qs_stream_t stream);
+
+/* qs_quantize_flush, qs_quantize_flush_due and qs_prefill on a paged cache:
+ * the same groups, written to the pages the table names for them.  A page out
+ * of range among those a sequence needs gives QS_DEV_PAGE and leaves that
+ * sequence unchanged (the other preconditions come first). */
+qs_status qs_quantize_flush_paged(const qs_cache *c, const qs_pages *pg, const uint8_t *d_mask,
+                                  qs_stream_t stream);
+qs_status qs_quantize_flush_due_paged(const qs_cache *c, const qs_pages *pg, int32_t n_next,
+                                      qs_stream_t stream);
+qs_status qs_prefill_paged(const qs_cache *c, const qs_pages *pg, const uint16_t *k,
+                           const uint16_t *v, int32_t T, const int32_t *d_len, qs_stream_t stream);
+
+/* Read the cache back: tokens [tok0, tok0 + T) of each sequence as fp16 rows.
+ *   pg    NULL for a contiguous cache, the pages of a paged one;
+ *   mode  QS_VERIFY_INT8: quantized tokens as the verify pass sees them, or
+ *         QS_DRAFT_UPPER4: as the draft does; buffered tokens (committed and
+ *         pending) as they were appended;
+ *   k, v  fp16 [B][H][T][D] device arrays; row t holds token tok0 + t.  One
+ *         of them may be NULL.
+ * A quantized token's row is s * code + z rounded once to fp16 (a value past
+ * the largest finite one, which only a group that spans the type's whole range
+ * can give, is held there).  Rows at or past a sequence's last token, and rows
+ * of a group whose page is out of range (QS_DEV_PAGE), are left as they were.
+ * Errors: QS_ERR_ARG (both k and v NULL, tok0 outside 0..2^30, T outside
+ * 1..2^26, bad mode, pg missing or not wanted), QS_ERR_ALIGN.  Ownership: the
+ * call writes k and v (and error words) only.  Source: "QuantSpec Guide",
+ * "1. Hierarchical Two-Level Quantization with Bit-Sharing" (the target
+ * reconstructs INT8 from both planes, the draft from the upper one); the pages
+ * only use these values inside attention. */
+qs_status qs_cache_read(const qs_cache *c, const qs_pages *pg, qs_mode mode, int32_t tok0, int32_t T,
+                        uint16_t *k, uint16_t *v, qs_stream_t stream);
 
 /* Speculative-sampling acceptance for B sequences with gamma draft tokens
  * each (1 <= gamma <= 64), vocabulary V; all arrays are device arrays, read

@@ -1,0 +1,89 @@
+"""Test-side model of a paged cache: an oracle cache's groups scattered over a
+pool of pages, and gathered back, in the layout include/qs.h gives."""
+import numpy as np
+
+import oracle
+from hierarchical_quantized_kv_gb300 import qs
+from tests import layout
+
+GROUP_ARRAYS = ("k_upper", "k_lower", "v_upper", "v_lower", "meta")
+
+
+def random_table(rng, n_groups, cap, n_pages):
+    """int32 [B, cap]: distinct pages for each sequence's first n_groups[b]
+    groups in random order, the unused entries out of range on both sides."""
+    B = len(n_groups)
+    table = np.where(rng.random((B, cap)) < 0.5, -7, n_pages + 1000).astype(np.int32)
+    pages = rng.permutation(n_pages)
+    at = 0
+    for b, n in enumerate(n_groups):
+        table[b, :n] = pages[at:at + n]
+        at += n
+    return table
+
+
+def paged_copy(torch, oc, rng, upper_bits=4, spare=3, n_pages=None):
+    """A qs.PagedCache with the oracle cache's content in randomly chosen
+    pages; the rest of the pool holds 0xA5 bytes."""
+    n = [oc.counters(b)["n_groups"] for b in range(oc.B)]
+    n_pages = n_pages or max(1, sum(n) + spare)
+    cache = qs.PagedCache(oc.B, oc.H, oc.cap, n_pages, upper_bits=upper_bits)
+    table = random_table(rng, n, oc.cap, n_pages)
+    cache.table.copy_(torch.from_numpy(table))
+    arrs = layout.device_arrays(oc, upper_bits)
+    for name in GROUP_ARRAYS:
+        a = arrs[name]
+        pool = np.full((n_pages,) + a.shape[1:2] + a.shape[3:], 0xA5, a.dtype)
+        if a.dtype == np.uint16:
+            pool[:] = 0x7E00  # NaN scales and zeros in pages nobody owns
+        for b in range(oc.B):
+            for g in range(n[b]):
+                pool[table[b, g]] = a[b, :, g]
+        put(torch, getattr(cache, name), pool)
+    for name in ("buf_k", "buf_v", "state"):
+        put(torch, getattr(cache, name), arrs[name])
+    return cache
+
+
+def put(torch, t, a):
+    src = torch.from_numpy(np.ascontiguousarray(a.view(np.int16) if a.dtype == np.uint16 else a))
+    if t.dtype == torch.float16:
+        src = src.view(torch.float16)
+    t.copy_(src.reshape(t.shape))
+
+
+def assert_groups_equal(cache, oc, what=""):
+    """The pages the table names hold the oracle's groups bit for bit, the
+    buffers and counters (but the error words) are the oracle's."""
+    got = layout.read_device(cache)
+    want = layout.device_arrays(oc, cache.upper_bits)
+    table = cache.table.cpu().numpy()
+    for b in range(oc.B):
+        n = oc.counters(b)["n_groups"]
+        for name in GROUP_ARRAYS:
+            assert np.array_equal(got[name][table[b, :n]].swapaxes(0, 1), want[name][b, :, :n]), \
+                "%s: %s of sequence %d differs" % (what, name, b)
+    for name in ("buf_k", "buf_v"):
+        assert np.array_equal(got[name].reshape(want[name].shape), want[name]), (what, name)
+    g, w = got["state"].copy(), want["state"].copy()
+    g[:, oracle.ERR] = w[:, oracle.ERR] = 0
+    assert np.array_equal(g, w), what
+
+
+def dequantized(oc, b, upper_only, upper_bits=4):
+    """fp64 keys and values [H, n_groups * G + fill, D] of sequence b as one
+    pass sees them, from the oracle's codes, scales and zeros."""
+    n = oc.counters(b)["n_groups"]
+    f = lambda x: x.view(np.float16).astype(np.float64)
+    step = 1 << (8 - upper_bits)
+
+    def value(code):
+        code = code.astype(np.float64)
+        return np.floor(code / step) * step + step / 2 if upper_only else code
+
+    k = value(oc.kq[b, :, :n]) * f(oc.ks[b, :, :n])[:, :, None, :] + f(oc.kz[b, :, :n])[:, :, None, :]
+    v = value(oc.vq[b, :, :n]) * f(oc.vs[b, :, :n])[:, :, :, None] + f(oc.vz[b, :, :n])[:, :, :, None]
+    flat = lambda x: x.reshape(oc.H, n * oc.G, oc.D)
+    buf = [oc.buffer_tokens(b, h) for h in range(oc.H)]
+    return (np.concatenate([flat(k), f(np.stack([x[0] for x in buf]))], 1),
+            np.concatenate([flat(v), f(np.stack([x[1] for x in buf]))], 1))
