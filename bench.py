@@ -49,7 +49,7 @@ def kernel_source_hash():
     traffic figure still describes the kernel that runs)."""
     import hashlib
     h = hashlib.sha256()
-    for f in ("qs_attn.cu", "qs_common.cuh"):
+    for f in ("qs_split.cuh", "qs_common.cuh"):
         with open(os.path.join(ROOT, "hierarchical_quantized_kv_gb300", "csrc", f), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()

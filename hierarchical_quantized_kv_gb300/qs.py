@@ -19,7 +19,7 @@ QS_DRAFT_UPPER4, QS_VERIFY_INT8 = 0, 1
 QS_STATIC_WS_BYTES = 8 << 20
 DEV_OVERFLOW, DEV_OVER_ROLLBACK, DEV_FLUSH_UNCOMMITTED, DEV_CAPACITY, DEV_NQ_GT_FILL, DEV_TIMEOUT = (
     1, 2, 4, 8, 16, 32)
-DEV_PREFILL, DEV_PAGE = 64, 128
+DEV_PREFILL, DEV_PAGE, DEV_SELECT = 64, 128, 256
 QS_PAGED = 0x100
 ST_N_GROUPS, ST_FILL, ST_PENDING, ST_HALF_BASE, ST_ERR, ST_TICKET = range(6)
 STATE_WORDS = 8
@@ -77,6 +77,12 @@ _SIGS = {
     "qs_attn_decode_gqa": [ctypes.POINTER(QsCacheStruct), ctypes.c_int, _P, _I32, _I32, ctypes.c_float,
                            _P, _P, _P, ctypes.c_size_t, _P],
     "qs_prefill": [ctypes.POINTER(QsCacheStruct), _P, _P, _I32, _P, _P],
+    "qs_attn_decode_paged": [ctypes.POINTER(QsCacheStruct), ctypes.POINTER(QsPagesStruct),
+                             ctypes.c_int, _P, _P, _I32, _P, _I32, _I32, ctypes.c_float, _P, _P, _P,
+                             ctypes.c_size_t, _P],
+    "qs_attn_decode_sparse": [ctypes.POINTER(QsCacheStruct), ctypes.POINTER(QsPagesStruct),
+                              ctypes.c_int, _P, _I32, _P, _P, _I32, _P, _I32, _I32, ctypes.c_float,
+                              _P, _P, _P, ctypes.c_size_t, _P],
     "qs_cache_read": [ctypes.POINTER(QsCacheStruct), ctypes.POINTER(QsPagesStruct), ctypes.c_int,
                       _I32, _I32, _P, _P, _P],
     "qs_spec_accept": [_P, _P, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _P],
@@ -367,6 +373,37 @@ def qs_attn_decode_append(cache, mode, k_new, v_new, q, softmax_scale, out, lse=
     _check("qs_attn_decode_append", lib().qs_attn_decode_append(
         cache._ref, int(mode), _ptr(k_new), _ptr(v_new), k_new.shape[2], _ptr(q), n_q, int(group),
         float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def _n_new(k_new, v_new):
+    if k_new is None and v_new is None:
+        return 0
+    assert k_new.is_contiguous() and v_new.is_contiguous() and k_new.shape == v_new.shape
+    return k_new.shape[2]
+
+
+def qs_attn_decode_paged(cache, mode, q, softmax_scale, out, lse=None, workspace=None, group=1,
+                         k_new=None, v_new=None, stream=None):
+    """qs_attn_decode_gqa on a PagedCache, or with k_new, v_new (fp16 [B, H,
+    n_new, D]) qs_attn_decode_append on it."""
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("qs_attn_decode_paged", lib().qs_attn_decode_paged(
+        cache._ref, cache._pages_ref, int(mode), _ptr(k_new), _ptr(v_new), _n_new(k_new, v_new),
+        _ptr(q), q.shape[2], int(group), float(softmax_scale), _ptr(out), _ptr(lse),
+        _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def qs_attn_decode_sparse(cache, mode, sel, q, softmax_scale, out, lse=None, workspace=None, group=1,
+                          k_new=None, v_new=None, stream=None):
+    """Decode attention (cache: a Cache or a PagedCache) over the groups named
+    in sel, int32 [B, H, k] (-1: none), and the buffer; k_new, v_new as for
+    qs_attn_decode_paged."""
+    assert sel.is_contiguous() and sel.shape[:2] == (cache.B, cache.H)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("qs_attn_decode_sparse", lib().qs_attn_decode_sparse(
+        cache._ref, cache._pages_ref, int(mode), _ptr(sel), sel.shape[2], _ptr(k_new), _ptr(v_new),
+        _n_new(k_new, v_new), _ptr(q), q.shape[2], int(group), float(softmax_scale), _ptr(out),
+        _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 def qs_get_errors(cache, stream=None):

@@ -91,8 +91,10 @@ enum {
                                     expected; the call's results are invalid) */
   QS_DEV_PREFILL = 64,           /* prefill of a non-empty cache, or a prompt
                                     length outside [0, T] */
-  QS_DEV_PAGE = 128              /* a page table entry in use outside
+  QS_DEV_PAGE = 128,             /* a page table entry in use outside
                                     [0, n_pages) */
+  QS_DEV_SELECT = 256            /* a selected group that the sequence does not
+                                    have */
 };
 
 /* Per-sequence counters: int32 state[B][QS_STATE_WORDS]. */
@@ -409,6 +411,40 @@ qs_status qs_attn_decode_append(const qs_cache *c, qs_mode mode, const uint16_t 
                                 int32_t n_q, int32_t group, float softmax_scale, uint16_t *out,
                                 float *lse, void *workspace, size_t workspace_bytes,
                                 qs_stream_t stream);
+
+/* Decode attention over a paged cache: qs_attn_decode_gqa, with the groups
+ * where the page table puts them (the same results as a contiguous cache of
+ * the same content).  With n_new > 0 the tokens k_new, v_new are appended
+ * first, as in qs_attn_decode_append; without an append pass NULL, NULL, 0.
+ * A group whose page is out of range is left out of the softmax and flags
+ * QS_DEV_PAGE.  Arguments, workspace (qs_attn_workspace_size_gqa) and errors
+ * as for those calls; QS_ERR_ARG also for k_new, v_new and n_new that do not
+ * go together.  Source: Pith review page, Appendix E (Flash Decoding: split
+ * the cache's length, join by log-sum-exp). */
+qs_status qs_attn_decode_paged(const qs_cache *c, const qs_pages *pg, qs_mode mode,
+                               const uint16_t *k_new, const uint16_t *v_new, int32_t n_new,
+                               const uint16_t *q, int32_t n_q, int32_t group, float softmax_scale,
+                               uint16_t *out, float *lse, void *workspace, size_t workspace_bytes,
+                               qs_stream_t stream);
+
+/* Decode attention over selected groups: as qs_attn_decode_paged (pg NULL: a
+ * contiguous cache), but each KV head of a sequence attends over the groups
+ * its row of sel names, and over the whole buffer.
+ *   sel  int32 [B][H][k_sel] device array, k_sel >= 1, 4-byte aligned: group
+ *        indices of (sequence, KV head), in any order, -1 for none.  The first
+ *        min(k_sel, n_groups) entries of a row are read (the row
+ *        qs_select_groups writes never needs more).  A group named twice counts
+ *        twice; an index that is neither -1 nor one of the sequence's groups is
+ *        left out and flags QS_DEV_SELECT.
+ * A row without any group leaves the buffer alone.  Errors as
+ * qs_attn_decode_paged, plus QS_ERR_ARG for a null sel or k_sel < 1.  Source:
+ * Pith review page (sparse-KV drafting named as work to combine with this
+ * cache); the rest is this library's. */
+qs_status qs_attn_decode_sparse(const qs_cache *c, const qs_pages *pg, qs_mode mode,
+                                const int32_t *sel, int32_t k_sel, const uint16_t *k_new,
+                                const uint16_t *v_new, int32_t n_new, const uint16_t *q, int32_t n_q,
+                                int32_t group, float softmax_scale, uint16_t *out, float *lse,
+                                void *workspace, size_t workspace_bytes, qs_stream_t stream);
 
 /* Size of the fixed scratch array behind qs_attn_decode_static_ws. */
 #define QS_STATIC_WS_BYTES (8u << 20)

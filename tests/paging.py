@@ -87,3 +87,46 @@ def dequantized(oc, b, upper_only, upper_bits=4):
     buf = [oc.buffer_tokens(b, h) for h in range(oc.H)]
     return (np.concatenate([flat(k), f(np.stack([x[0] for x in buf]))], 1),
             np.concatenate([flat(v), f(np.stack([x[1] for x in buf]))], 1))
+
+
+def counts(oc, b, sel=None):
+    """How often each group of sequence b takes part, [H, n_groups]: once, or
+    as often as the first min(k, n_groups) entries of the head's row name it."""
+    n = oc.counters(b)["n_groups"]
+    if sel is None:
+        return np.ones((oc.H, n))
+    c = np.zeros((oc.H, n))
+    for h in range(oc.H):
+        for g in sel[b, h, :min(sel.shape[2], n)]:
+            if 0 <= g < n:
+                c[h, g] += 1
+    return c
+
+
+def attention(oc, q, upper_only, group=1, upper_bits=4, sel=None, times=None, scale=None):
+    """Textbook softmax attention in fp64 over the dequantized tokens, each
+    weighted by how often its group takes part (counts, or times [B][H, n]),
+    and the causal part of the buffer: (out, lse), zeros and -inf where
+    n_q > fill."""
+    B, Hq, n_q, D = q.shape
+    scale = float(np.float32(1.0 / np.sqrt(D) if scale is None else scale))
+    out, lse = np.zeros(q.shape), np.full(q.shape[:3], -np.inf)
+    for b in range(B):
+        n, fill = oc.counters(b)["n_groups"], oc.counters(b)["fill"]
+        if n_q > fill:
+            continue
+        k, v = dequantized(oc, b, upper_only, upper_bits)
+        c = counts(oc, b, sel) if times is None else times[b]
+        for i in range(Hq):
+            h = i // group
+            w = np.concatenate([np.repeat(c[h], oc.G), np.ones(fill)])
+            with np.errstate(divide="ignore"):
+                logw = np.log(w)
+            for j in range(n_q):
+                s = scale * (k[h] @ q[b, i, j].astype(np.float64)) + logw
+                s[n * oc.G + fill - n_q + j + 1:] = -np.inf
+                m = s.max()
+                p = np.exp(s - m)
+                out[b, i, j] = (p @ v[h]) / p.sum()
+                lse[b, i, j] = m + np.log(p.sum())
+    return out, lse

@@ -32,8 +32,13 @@ PAGED_ONLY = {
     "qs_quantize_flush_paged": lambda f, c, pg: f(c, pg, None, None),
     "qs_quantize_flush_due_paged": lambda f, c, pg: f(c, pg, 1, None),
     "qs_prefill_paged": lambda f, c, pg: f(c, pg, P, P, 10, P, None),
+    "qs_attn_decode_paged": lambda f, c, pg: f(c, pg, 0, None, None, 0, P, 1, 1, ctypes.c_float(0.1), P,
+                                               None, P, 1 << 30, None),
 }
+F = ctypes.c_float
 EITHER = {
+    "qs_attn_decode_sparse": lambda f, c, pg: f(c, pg, 0, P, 3, None, None, 0, P, 1, 1, F(0.1), P, None,
+                                                P, 1 << 30, None),
     "qs_cache_read": lambda f, c, pg: f(c, pg, 1, 0, 5, P, P, None),
 }
 #: calls for contiguous groups
@@ -103,3 +108,29 @@ def test_read_arguments(L, paged):
         assert f(c, pg, 1, 0, T, P, P, None) == qs.QS_ERR_ARG
     assert f(c, pg, 1, 0, 5, odd, P, None) == qs.QS_ERR_ALIGN
     assert f(c, pg, 1, 0, 5, None, odd, None) == qs.QS_ERR_ALIGN
+
+
+def test_listed_attention_arguments(L):
+    c, pg, odd = cache(True), pages(), ctypes.c_void_p(0x20002)
+
+    def paged(mode=0, k=None, v=None, n=0, q=P, n_q=1, group=1, scale=0.1, out=P, lse=None):
+        return L.qs_attn_decode_paged(c, pg, mode, k, v, n, q, n_q, group, F(scale), out, lse, P,
+                                      1 << 30, None)
+
+    def sparse(sel=P, k_sel=3, **kw):
+        a = dict(dict(mode=0, k=None, v=None, n=0, q=P, n_q=1, group=1, scale=0.1, out=P, lse=None), **kw)
+        return L.qs_attn_decode_sparse(c, pg, a["mode"], sel, k_sel, a["k"], a["v"], a["n"], a["q"],
+                                       a["n_q"], a["group"], F(a["scale"]), a["out"], a["lse"], P,
+                                       1 << 30, None)
+
+    for f in (paged, sparse):
+        for kw in (dict(mode=2), dict(q=None), dict(out=None), dict(n_q=0), dict(n_q=9), dict(group=0),
+                   dict(n_q=5, group=5), dict(n_q=8, group=1 << 29), dict(scale=0.0),
+                   dict(scale=float("nan")), dict(k=P), dict(v=P, n=1), dict(n=1), dict(k=P, v=P),
+                   dict(k=P, v=P, n=257), dict(k=P, v=P, n=-1)):
+            assert f(**kw) == qs.QS_ERR_ARG, kw
+        for kw in (dict(q=odd), dict(out=odd), dict(lse=odd), dict(k=odd, v=P, n=1), dict(k=P, v=odd, n=1)):
+            assert f(**kw) == qs.QS_ERR_ALIGN, kw
+    assert sparse(sel=None) == qs.QS_ERR_ARG
+    assert sparse(k_sel=0) == qs.QS_ERR_ARG
+    assert sparse(sel=odd) == qs.QS_ERR_ALIGN
