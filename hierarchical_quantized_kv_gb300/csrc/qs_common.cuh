@@ -79,6 +79,20 @@ inline qs_status launch_status() {
   return e == cudaSuccess ? QS_OK : QS_ERR_CUDA;
 }
 
+// Opt a kernel into its dynamic shared memory once per device (mask: one bit per
+// device ordinal below 32).
+inline qs_status set_smem_once(const void *kernel, int smem, int *mask) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return QS_ERR_CUDA;
+  if (dev >= 32 || !(__atomic_load_n(mask, __ATOMIC_ACQUIRE) & (1 << dev))) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+        cudaSuccess)
+      return QS_ERR_CUDA;
+    if (dev < 32) __atomic_fetch_or(mask, 1 << dev, __ATOMIC_RELEASE);
+  }
+  return QS_OK;
+}
+
 // Launch with programmatic stream serialization: the kernel may be scheduled
 // while its predecessor in the stream is still running; it calls pdl_wait()
 // before touching memory the predecessor writes, which restores stream order.

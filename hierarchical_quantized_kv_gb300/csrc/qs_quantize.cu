@@ -500,18 +500,6 @@ __global__ void __launch_bounds__(32 * kPrefillWarps) prefill_kernel(qs_cache c,
 using namespace qs;
 
 namespace {
-// Opt the kernels into their dynamic shared memory once per device.
-qs_status set_smem_once(const void *kernel, int smem, int *mask) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return QS_ERR_CUDA;
-  if (dev >= 32 || !(__atomic_load_n(mask, __ATOMIC_ACQUIRE) & (1 << dev))) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-        cudaSuccess)
-      return QS_ERR_CUDA;
-    if (dev < 32) __atomic_fetch_or(mask, 1 << dev, __ATOMIC_RELEASE);
-  }
-  return QS_OK;
-}
 int g_flush_ready = 0, g_prefill_ready = 0;  // one bit per device ordinal below 32
 }  // namespace
 

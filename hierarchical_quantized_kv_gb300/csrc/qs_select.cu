@@ -1,0 +1,420 @@
+// qs_select.cu -- which groups of the cache a KV head should attend over: the
+// k groups whose keys could score highest against the head's queries.
+//
+// The cache already holds a box around the keys of every group: channel d of
+// its tokens lies in [z_d, z_d + 255 s_d] (zero and scale of the per-channel
+// quantization).  The largest score a key in that box can have with a query q,
+//   sum_d max(q_d z_d, q_d (z_d + 255 s_d)) = q . z + 255 relu(q) . s,
+// bounds the score of every token of the group, and is two dot products with
+// the 512 bytes of scales and zeros the attention reads anyway.  A head's
+// score for a group is the maximum over its query rows.
+//
+// Which of two close groups is taken must not depend on rounding, so the order
+// is that of the exact sums: scores come from the tensor cores in fp32 with a
+// bound E on their error; a group more than 2 E above the k-th largest score
+// is in, one more than 2 E below is out, and only what lies between (usually
+// the k-th group alone) is summed again in fp64.
+//
+// Bound by latency at one sequence (512 B per group and head: 4 MB for a 32k
+// context of 32 heads) and by HBM for large batches.  A cluster of CTAs per
+// (sequence, KV head) shares the scoring; its first CTA, in whose shared
+// memory the scores meet, selects.
+#include <cooperative_groups.h>
+#include <float.h>
+#include <math.h>
+
+#include "qs_common.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace qs {
+namespace {
+
+constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
+constexpr int kTile = 16;  // groups a warp scores at once (rows of the MMA)
+constexpr int kMaxRows = 24;
+// Groups per sequence: score (4 bytes), fp64 sum (8), list entry (4) and flag
+// (1) of each lie in shared memory.
+constexpr int kMaxSelectGroups = 12800;
+
+struct SelectSmem {
+  double *exact;   // [n] fp64 score of list entry i
+  float *score;    // [n]
+  int *list;       // [n] groups near the border, ascending
+  uint8_t *flag;   // [n] 1: selected
+  __device__ static SelectSmem at(uint8_t *p, int cap) {
+    SelectSmem s;
+    s.exact = reinterpret_cast<double *>(p);
+    s.score = reinterpret_cast<float *>(p + (size_t)8 * cap);
+    s.list = reinterpret_cast<int *>(p + (size_t)12 * cap);
+    s.flag = p + (size_t)16 * cap;
+    return s;
+  }
+};
+constexpr size_t select_smem(int cap) { return (size_t)17 * cap; }
+
+// Keys whose unsigned order is the numbers' order (-0 and +0 alike, NaN as the
+// lowest number).
+__device__ __forceinline__ uint32_t key_of(float x) {
+  x = x == x ? x + 0.0f : -INFINITY;
+  const uint32_t u = __float_as_uint(x);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ unsigned long long key_of(double x) {
+  x = x == x ? x + 0.0 : -INFINITY;
+  const unsigned long long u = __double_as_longlong(x);
+  return u >> 63 ? ~u : u | (1ull << 63);
+}
+
+struct BlockScratch {
+  int hist[256];
+  int warp[kSelWarps];
+  int digit, above;
+};
+
+// Key of the k-th largest of n values (1 <= k <= n), and how many are larger:
+// radix selection from the top byte down, by the whole CTA.
+template <typename T, typename K>
+__device__ K kth_largest(const T *v, int n, int k, int *n_above, BlockScratch &S) {
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  K prefix = 0;
+  int need = k;
+#pragma unroll 1
+  for (int shift = 8 * (int)sizeof(K) - 8; shift >= 0; shift -= 8) {
+    S.hist[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kSelThreads) {
+      const K key = key_of(v[i]);
+      // (shifted twice: a shift by the key's whole width is undefined)
+      if (((key >> shift) >> 8) == prefix) atomicAdd(&S.hist[(int)(key >> shift) & 255], 1);
+    }
+    __syncthreads();
+    // thread t: values in bins above 255 - t (bins in descending order)
+    const int bin = 255 - tid, cnt = S.hist[bin];
+    int incl = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) S.warp[w] = incl;
+    __syncthreads();
+    for (int i = 0; i < w; ++i) incl += S.warp[i];
+    if (incl >= need && incl - cnt < need) {
+      S.digit = bin;
+      S.above = incl - cnt;
+    }
+    __syncthreads();
+    prefix = (prefix << 8) | (K)S.digit;
+    need -= S.above;
+  }
+  *n_above = k - need;
+  return prefix;
+}
+
+// Positions in order: the number of set predicates before this thread's in
+// the CTA, and the total.  Called by the whole CTA.
+__device__ __forceinline__ int block_rank(bool pred, int *total, BlockScratch &S) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const unsigned m = __ballot_sync(0xffffffffu, pred);
+  __syncthreads();  // the previous call's counts have been read
+  if (lane == 0) S.warp[w] = __popc(m);
+  __syncthreads();
+  int before = __popc(m & ((1u << lane) - 1)), sum = 0;
+  for (int i = 0; i < kSelWarps; ++i) {
+    if (i == w) before += sum;
+    sum += S.warp[i];
+  }
+  *total = sum;
+  return before;
+}
+
+// Channel in position p of a key scale / zero row.
+__device__ __forceinline__ int kmeta_channel(int p) {
+  return 32 * ((p >> 3) & 3) + 8 * (p >> 5) + 2 * ((p >> 2) & 1) + ((p >> 1) & 1) + 4 * (p & 1);
+}
+
+__device__ __forceinline__ uint4 ldg16(const uint16_t *p) {
+  return __ldg(reinterpret_cast<const uint4 *>(p));
+}
+
+// Grid (cluster size, H, B).  NCG: column groups of eight query rows.
+template <int NCG>
+__global__ void __launch_bounds__(kSelThreads)
+    select_kernel(qs_cache c, Pages pg, const uint16_t *__restrict__ q, int R, int k_sel,
+                  int32_t *__restrict__ sel) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  __shared__ BlockScratch S;
+  __shared__ float s_err[8];  // largest sum of magnitudes each CTA met
+  __shared__ int s_mag;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), n_ranks = (int)cluster.num_blocks();
+  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  const int w = tid >> 5, lane = tid & 31, r = lane >> 2, cq = lane & 3;
+  SelectSmem M = SelectSmem::at(smem_raw, c.cap_groups);
+  if (tid == 0) s_mag = 0;
+  pdl_trigger();
+  pdl_wait();
+  int32_t *st = c.state + (size_t)b * QS_STATE_WORDS;
+  const int n = min(max(st[QS_ST_N_GROUPS], 0), c.cap_groups);
+  const size_t bh = (size_t)b * c.H + h;
+  int32_t *out = sel + bh * k_sel;
+  if (n <= k_sel) {  // all of them (the whole cluster alike)
+    if (rank == 0)
+      for (int i = tid; i < k_sel; i += kSelThreads) out[i] = i < n ? i : -1;
+    return;
+  }
+  // the first CTA's shared memory is written below: it must have started
+  cluster.barrier_arrive();
+
+  // ---- scores: a warp takes 16 groups.  A = their zero (or scale) rows, as
+  // stored: lane (r, cq) loads 16 bytes of rows r and r + 8, which are two
+  // k-blocks' fragments; B = q in the order of those rows.
+  const uint16_t *qh = q + bh * R * kD;
+  uint32_t q0[NCG][8], q1[NCG][8];
+#pragma unroll
+  for (int g = 0; g < NCG; ++g) {
+    const int row = 8 * g + r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (row < R) x = ldg16(qh + (size_t)row * kD + 32 * cq + 8 * i);
+      q0[g][2 * i] = prmt(x.x, x.z, 0x5410);
+      q1[g][2 * i] = prmt(x.x, x.z, 0x7632);
+      q0[g][2 * i + 1] = prmt(x.y, x.w, 0x5410);
+      q1[g][2 * i + 1] = prmt(x.y, x.w, 0x7632);
+    }
+  }
+  const int n_tiles = (n + kTile - 1) / kTile;
+  float *score0 = cluster.map_shared_rank(M.score, 0);
+  bool started = false;
+  float mag = 0.f;
+#pragma unroll 1
+  for (int t = rank * kSelWarps + w; t < n_tiles; t += n_ranks * kSelWarps) {
+    uint4 zr[2][4], sr[2][4];  // zero and scale rows of groups r and r + 8
+    bool good[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int g = kTile * t + r + 8 * j;
+      const long long place = g < n ? group_slot(c, pg, b, h, g) : -1;
+      good[j] = place >= 0;
+      if (g < n && place < 0 && h == 0 && cq == 0) atomicOr(&st[QS_ST_ERR], QS_DEV_PAGE);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        zr[j][i] = sr[j][i] = make_uint4(0, 0, 0, 0);
+        if (good[j]) {
+          const uint16_t *m = c.meta + (size_t)place * 4 * 128 + 8 * (4 * i + cq);
+          sr[j][i] = ldg16(m + QS_META_K_SCALE * 128);
+          zr[j][i] = ldg16(m + QS_META_K_ZERO * 128);
+        }
+      }
+    }
+    float best[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int g = 0; g < NCG; ++g) {
+      // each MMA starts from zero and its result is added in fp32, so the
+      // tensor core's own rounding never runs along a chain
+      float az[4] = {0, 0, 0, 0}, as[4] = {0, 0, 0, 0}, aa[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int kb = 0; kb < 8; ++kb) {
+        const int i = kb >> 1;
+        const uint32_t z0 = kb & 1 ? zr[0][i].z : zr[0][i].x, z2 = kb & 1 ? zr[0][i].w : zr[0][i].y;
+        const uint32_t z1 = kb & 1 ? zr[1][i].z : zr[1][i].x, z3 = kb & 1 ? zr[1][i].w : zr[1][i].y;
+        const uint32_t s0 = kb & 1 ? sr[0][i].z : sr[0][i].x, s2 = kb & 1 ? sr[0][i].w : sr[0][i].y;
+        const uint32_t s1 = kb & 1 ? sr[1][i].z : sr[1][i].x, s3 = kb & 1 ? sr[1][i].w : sr[1][i].y;
+        const uint32_t b0 = q0[g][kb], b1 = q1[g][kb];
+        const uint32_t p0 = h2_as_u32(__hmax2(u32_as_h2(b0), u32_as_h2(0u)));
+        const uint32_t p1 = h2_as_u32(__hmax2(u32_as_h2(b1), u32_as_h2(0u)));
+        constexpr uint32_t kAbs = 0x7FFF7FFFu;
+        float dz[4] = {0, 0, 0, 0}, ds[4] = {0, 0, 0, 0}, da[4] = {0, 0, 0, 0};
+        mma16816(dz, z0, z1, z2, z3, b0, b1);
+        mma16816(ds, s0, s1, s2, s3, p0, p1);
+        mma16816(da, z0 & kAbs, z1 & kAbs, z2 & kAbs, z3 & kAbs, b0 & kAbs, b1 & kAbs);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          az[x] += dz[x];
+          as[x] += ds[x];
+          aa[x] += da[x];
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {  // rows r (x < 2) and r + 8, columns 2 cq + x % 2
+        if (8 * g + 2 * cq + (x & 1) < R) {
+          best[x >> 1] = fmaxf(best[x >> 1], fmaf(255.f, as[x], az[x]));
+          const float a = fmaf(255.f, as[x], aa[x]);
+          mag = a < FLT_MAX ? fmaxf(mag, a) : INFINITY;  // (NaN too)
+        }
+      }
+    }
+    if (!started) {
+      cluster.barrier_wait();
+      started = true;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float x = best[j];
+      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+      const int g = kTile * t + r + 8 * j;
+      if (cq == 0 && g < n) score0[g] = good[j] ? x : -INFINITY;
+    }
+  }
+  if (!started) cluster.barrier_wait();
+  mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
+  mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
+  mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, 4));
+  mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, 8));
+  mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, 16));
+  __syncthreads();
+  if (lane == 0) atomicMax(&s_mag, __float_as_int(mag));  // mag >= 0: ordered as integers
+  __syncthreads();
+  if (tid == 0) *cluster.map_shared_rank(&s_err[rank], 0) = __int_as_float(s_mag);
+  cluster.sync();  // all scores and magnitudes are in the first CTA
+  if (rank != 0) return;
+
+  // ---- selection.  One MMA adds 17 numbers, aligned to the largest and cut
+  // no coarser than 2^-23 of it: off by less than 2^-18.9 of the sum of their
+  // magnitudes; the eight fp32 additions and the last multiply-add add
+  // 9 x 2^-24.  Together under 2^-18.
+  float E = 0.f;
+  for (int i = 0; i < n_ranks; ++i) E = fmaxf(E, s_err[i]);
+  E *= 0x1p-18f;
+  int above;
+  const uint32_t key = kth_largest<float, uint32_t>(M.score, n, k_sel, &above, S);
+  const float T = __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+  // (infinite or NaN limits, from queries that are not finite, leave every
+  // group to the fp64 sums)
+  const float hi = __fadd_ru(T, 2.f * E), lo = __fadd_rd(T, -2.f * E);
+  int m = 0, n_in = 0;
+  for (int base = 0; base < n; base += kSelThreads) {
+    const int g = base + tid;
+    const float x = g < n ? M.score[g] : 0.f;
+    const bool in = g < n && x > hi, near = g < n && !in && !(x < lo);
+    int tot;
+    const int at = m + block_rank(near, &tot, S);
+    if (g < n) M.flag[g] = in;
+    if (near) M.list[at] = g;
+    m += tot;
+    n_in += __syncthreads_count(in);
+  }
+  const int need = k_sel - n_in;  // of the m groups near the border
+  if (need >= m) {
+    for (int i = tid; i < m; i += kSelThreads) M.flag[M.list[i]] = 1;
+  } else if (need > 0) {
+    // fp64 sums: a warp per group, lane l holds positions 4 l .. 4 l + 3
+    for (int i = w; i < m; i += kSelWarps) {
+      const long long place = group_slot(c, pg, b, h, M.list[i]);
+      double best = -INFINITY;
+      if (place >= 0) {
+        const uint16_t *mt = c.meta + (size_t)place * 4 * 128 + 4 * lane;
+        const uint2 sw = __ldg(reinterpret_cast<const uint2 *>(mt + QS_META_K_SCALE * 128));
+        const uint2 zw = __ldg(reinterpret_cast<const uint2 *>(mt + QS_META_K_ZERO * 128));
+        const float2 s01 = __half22float2(u32_as_h2(sw.x)), s23 = __half22float2(u32_as_h2(sw.y));
+        const float2 z01 = __half22float2(u32_as_h2(zw.x)), z23 = __half22float2(u32_as_h2(zw.y));
+        const float s[4] = {s01.x, s01.y, s23.x, s23.y}, z[4] = {z01.x, z01.y, z23.x, z23.y};
+        for (int row = 0; row < R; ++row) {
+          double d = 0;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const double qv = (double)__half2float(
+                __ushort_as_half(__ldg(qh + (size_t)row * kD + kmeta_channel(4 * lane + x))));
+            // (products of two fp16 numbers, and 255 of them, are exact)
+            d += qv * z[x];
+            d += 255.0 * (qv > 0 ? qv : 0.0) * s[x];
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+          best = fmax(best, d);
+        }
+      }
+      if (lane == 0) M.exact[i] = best;
+    }
+    __syncthreads();
+    const unsigned long long k64 =
+        kth_largest<double, unsigned long long>(M.exact, m, need, &above, S);
+    // those above the need-th, then those equal to it from the lowest index on
+    int equal = 0;
+    for (int base = 0; base < m; base += kSelThreads) {
+      const int i = base + tid;
+      const unsigned long long x = i < m ? key_of(M.exact[i]) : 0;
+      int tot;
+      const int at = equal + block_rank(i < m && x == k64, &tot, S);
+      if (i < m && (x > k64 || (x == k64 && at < need - above))) M.flag[M.list[i]] = 1;
+      equal += tot;
+    }
+  }
+  __syncthreads();
+  int done = 0;
+  for (int base = 0; base < n; base += kSelThreads) {
+    const int g = base + tid;
+    const bool in = g < n && M.flag[g];
+    int tot;
+    const int at = done + block_rank(in, &tot, S);
+    if (in && at < k_sel) out[at] = g;
+    done += tot;
+  }
+  for (int i = done + tid; i < k_sel; i += kSelThreads) out[i] = -1;  // (never with finite queries)
+}
+
+// CTAs per (sequence, KV head): one per 128 groups (a tile for each warp), at
+// most 8, as long as the whole grid stays within four CTAs an SM.
+int cluster_size(const qs_cache &c, int sms) {
+  int n = 1;
+  while (n < 8 && n * kSelWarps * kTile < c.cap_groups && (long long)c.B * c.H * n * 2 <= 4ll * sms) n *= 2;
+  return n;
+}
+
+int g_sel_ready[3] = {0, 0, 0};  // one bit per device ordinal below 32
+
+template <int NCG>
+qs_status launch_select(const qs_cache &c, const Pages &pg, const uint16_t *q, int R, int k_sel,
+                        int32_t *sel, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return QS_ERR_CUDA;
+  const qs_status s = set_smem_once((const void *)select_kernel<NCG>,
+                                    (int)select_smem(kMaxSelectGroups), &g_sel_ready[NCG - 1]);
+  if (s != QS_OK) return s;
+  const int cl = cluster_size(c, sms);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cl, c.H, c.B);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = select_smem(c.cap_groups);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cl;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, select_kernel<NCG>, c, pg, q, R, k_sel, sel) == cudaSuccess
+             ? QS_OK
+             : QS_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace qs
+
+using namespace qs;
+
+extern "C" qs_status qs_select_groups(const qs_cache *c, const qs_pages *pg, const uint16_t *q,
+                                      int32_t n_q, int32_t group, int32_t k_sel, int32_t *sel,
+                                      qs_stream_t stream) {
+  qs_cache cc;
+  Pages pages;
+  const qs_status s = check_pages(c, pg, false, &cc, &pages);
+  if (s != QS_OK) return s;
+  if (!q || !sel || n_q < 1 || n_q > kMaxQ || group < 1 || group > kMaxRows ||
+      group * n_q > kMaxRows || k_sel < 1)
+    return QS_ERR_ARG;
+  if (cc.cap_groups > kMaxSelectGroups) return QS_ERR_UNSUPPORTED;
+  if (!aligned16(q) || reinterpret_cast<uintptr_t>(sel) % 4) return QS_ERR_ALIGN;
+  const int R = group * n_q;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (R <= 8) return launch_select<1>(cc, pages, q, R, k_sel, sel, st);
+  return R <= 16 ? launch_select<2>(cc, pages, q, R, k_sel, sel, st)
+                 : launch_select<3>(cc, pages, q, R, k_sel, sel, st);
+}

@@ -83,6 +83,8 @@ _SIGS = {
     "qs_attn_decode_sparse": [ctypes.POINTER(QsCacheStruct), ctypes.POINTER(QsPagesStruct),
                               ctypes.c_int, _P, _I32, _P, _P, _I32, _P, _I32, _I32, ctypes.c_float,
                               _P, _P, _P, ctypes.c_size_t, _P],
+    "qs_select_groups": [ctypes.POINTER(QsCacheStruct), ctypes.POINTER(QsPagesStruct), _P, _I32, _I32,
+                         _I32, _P, _P],
     "qs_cache_read": [ctypes.POINTER(QsCacheStruct), ctypes.POINTER(QsPagesStruct), ctypes.c_int,
                       _I32, _I32, _P, _P, _P],
     "qs_spec_accept": [_P, _P, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _P],
@@ -391,6 +393,15 @@ def qs_attn_decode_paged(cache, mode, q, softmax_scale, out, lse=None, workspace
         cache._ref, cache._pages_ref, int(mode), _ptr(k_new), _ptr(v_new), _n_new(k_new, v_new),
         _ptr(q), q.shape[2], int(group), float(softmax_scale), _ptr(out), _ptr(lse),
         _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def qs_select_groups(cache, q, sel, group=1, stream=None):
+    """For each KV head the sel.shape[2] groups whose keys could score highest
+    against q (fp16 [B, H*group, n_q, D]) into sel, int32 [B, H, k]."""
+    assert sel.is_contiguous() and sel.shape[:2] == (cache.B, cache.H)
+    _check("qs_select_groups", lib().qs_select_groups(
+        cache._ref, cache._pages_ref, _ptr(q), q.shape[2], int(group), sel.shape[2], _ptr(sel),
+        _stream(stream)))
 
 
 def qs_attn_decode_sparse(cache, mode, sel, q, softmax_scale, out, lse=None, workspace=None, group=1,

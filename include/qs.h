@@ -427,6 +427,31 @@ qs_status qs_attn_decode_paged(const qs_cache *c, const qs_pages *pg, qs_mode mo
                                uint16_t *out, float *lse, void *workspace, size_t workspace_bytes,
                                qs_stream_t stream);
 
+/* Select, for each KV head, the k_sel groups whose keys could score highest
+ * against the head's query rows: input of qs_attn_decode_sparse.
+ *   pg   NULL for a contiguous cache, the pages of a paged one;
+ *   q    fp16 [B][H*group][n_q][D] device, as for the attention (1 <= n_q <= 8,
+ *        group * n_q <= 24), finite;
+ *   sel  int32 [B][H][k_sel] (out), 4-byte aligned: group indices in ascending
+ *        order, -1 behind the last when the sequence has fewer than k_sel.
+ * The score of a group is the largest, over the head's query rows, of
+ *   sum_d max(q_d z_d, q_d (z_d + 255 s_d)),
+ * z_d and s_d being the group's key zero and scale of channel d: no key of the
+ * group scores above it (before the softmax scale).  The order is that of the
+ * exact sums (close ones are summed in fp64), ties go to the lower index.  The
+ * selection depends on the quantized groups only, not on the buffer; one
+ * selection may serve several draft steps.  With n_groups <= k_sel the scores
+ * are not formed.  A group whose page is out of range scores below every other
+ * and flags QS_DEV_PAGE.  Queries that are not finite give some valid
+ * selection.  One launch.  Errors: QS_ERR_ARG (null q or sel, n_q, group or
+ * k_sel out of range, pg missing or not wanted), QS_ERR_UNSUPPORTED
+ * (cap_groups > 12800, a context of 1.6 million tokens), QS_ERR_ALIGN.
+ * Source: Pith review page (sparse-KV drafting named as work to combine with
+ * this cache) and Appendix D (keys quantized per channel, whose zero and scale
+ * are the box); the score is this library's. */
+qs_status qs_select_groups(const qs_cache *c, const qs_pages *pg, const uint16_t *q, int32_t n_q,
+                           int32_t group, int32_t k_sel, int32_t *sel, qs_stream_t stream);
+
 /* Decode attention over selected groups: as qs_attn_decode_paged (pg NULL: a
  * contiguous cache), but each KV head of a sequence attends over the groups
  * its row of sel names, and over the whole buffer.

@@ -130,3 +130,28 @@ def attention(oc, q, upper_only, group=1, upper_bits=4, sel=None, times=None, sc
                 out[b, i, j] = (p @ v[h]) / p.sum()
                 lse[b, i, j] = m + np.log(p.sum())
     return out, lse
+
+
+def select(oc, q, k, group=1, left_out=()):
+    """The k groups of each KV head with the largest box scores, by definition:
+    every channel's larger product, summed in fp64 (the sums of these fp16
+    products are exact or nearly so), the largest over the head's query rows;
+    ties to the lower index, ascending, -1 behind.  left_out: (b, g) pairs
+    that score below all others."""
+    f = lambda x: x.view(np.float16).astype(np.float64)
+    n_q = q.shape[2]
+    sel = np.full((oc.B, oc.H, k), -1, np.int32)
+    for b in range(oc.B):
+        n = oc.counters(b)["n_groups"]
+        for h in range(oc.H):
+            lo = f(oc.kz[b, h, :n])
+            hi = lo + 255 * f(oc.ks[b, h, :n])
+            rows = q[b, h * group:(h + 1) * group].reshape(group * n_q, -1).astype(np.float64)
+            score = np.full(n, -np.inf)
+            for row in rows:
+                score = np.maximum(score, np.maximum(row * lo, row * hi).sum(-1))
+            if n > k:
+                score[[g for bb, g in left_out if bb == b]] = -np.inf
+            best = np.sort(np.lexsort((np.arange(n), -score))[:k])
+            sel[b, h, :len(best)] = best
+    return sel

@@ -37,6 +37,7 @@ PAGED_ONLY = {
 }
 F = ctypes.c_float
 EITHER = {
+    "qs_select_groups": lambda f, c, pg: f(c, pg, P, 1, 1, 3, P, None),
     "qs_attn_decode_sparse": lambda f, c, pg: f(c, pg, 0, P, 3, None, None, 0, P, 1, 1, F(0.1), P, None,
                                                 P, 1 << 30, None),
     "qs_cache_read": lambda f, c, pg: f(c, pg, 1, 0, 5, P, P, None),
@@ -134,3 +135,18 @@ def test_listed_attention_arguments(L):
     assert sparse(sel=None) == qs.QS_ERR_ARG
     assert sparse(k_sel=0) == qs.QS_ERR_ARG
     assert sparse(sel=odd) == qs.QS_ERR_ALIGN
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_select_arguments(L, paged):
+    c, pg = cache(paged), pages() if paged else None
+
+    def f(c=c, q=P, n_q=1, group=1, k=3, sel=P):
+        return L.qs_select_groups(c, pg, q, n_q, group, k, sel, None)
+
+    for kw in (dict(q=None), dict(sel=None), dict(n_q=0), dict(n_q=9), dict(group=0), dict(group=25),
+               dict(n_q=5, group=5), dict(n_q=8, group=1 << 29), dict(k=0), dict(k=-1)):
+        assert f(**kw) == qs.QS_ERR_ARG, kw
+    assert f(q=ctypes.c_void_p(0x20008)) == qs.QS_ERR_ALIGN
+    assert f(sel=ctypes.c_void_p(0x20002)) == qs.QS_ERR_ALIGN
+    assert f(c=cache(paged, cap_groups=12801)) == qs.QS_ERR_UNSUPPORTED
