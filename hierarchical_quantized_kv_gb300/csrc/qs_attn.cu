@@ -13,9 +13,9 @@ qs_status qs_attn_workspace_size_gqa(const qs_cache *c, int32_t n_q, int32_t gro
   const int bits = c->upper_bits & ~QS_PAGED;
   if (!bytes || n_q < 1 || n_q > kMaxQ || group < 1 || group * n_q > kMaxR) return QS_ERR_ARG;
   int P0 = 0, P1 = 0, P2 = 0;
-  if ((s = grid_size<false>(QS_DRAFT_UPPER4, false, bits, 1, P0)) != QS_OK) return s;
-  if ((s = grid_size<false>(QS_DRAFT_UPPER4, true, bits, 1, P1)) != QS_OK) return s;
-  if ((s = grid_size<false>(QS_VERIFY_INT8, false, bits, (group * n_q + 7) / 8, P2)) != QS_OK) return s;
+  if ((s = grid_size<kContiguous>(QS_DRAFT_UPPER4, false, bits, 1, P0)) != QS_OK) return s;
+  if ((s = grid_size<kContiguous>(QS_DRAFT_UPPER4, true, bits, 1, P1)) != QS_OK) return s;
+  if ((s = grid_size<kContiguous>(QS_VERIFY_INT8, false, bits, (group * n_q + 7) / 8, P2)) != QS_OK) return s;
   const int P = P0 > P1 ? (P0 > P2 ? P0 : P2) : (P1 > P2 ? P1 : P2);
   *bytes = ws_bytes(P, c->B, c->H, group * n_q);
   return QS_OK;
@@ -43,8 +43,10 @@ qs_status decode_contiguous(const qs_cache *c, qs_mode mode, const uint16_t *q, 
   prm.k_new = k_new;
   prm.v_new = v_new;
   prm.n_new = n_new;
-  return decode<false>(prm, mode, q, n_q, group, softmax_scale, out, lse, workspace,
-                       workspace_bytes, stream);
+  const qs_status f = fill_params<kContiguous>(prm, mode, q, n_q, group, softmax_scale, out, lse,
+                                               workspace, workspace_bytes);
+  if (f != QS_OK) return f;
+  return launch_kind<kContiguous>(mode, packed_rows(mode, prm.R), prm, (cudaStream_t)stream);
 }
 
 }  // namespace

@@ -377,22 +377,8 @@ qs_status launch_select(const qs_cache &c, const Pages &pg, const uint16_t *q, i
                                     (int)select_smem(kMaxSelectGroups), &g_sel_ready[NCG - 1]);
   if (s != QS_OK) return s;
   const int cl = cluster_size(c, sms);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cl, c.H, c.B);
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = select_smem(c.cap_groups);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cl;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, select_kernel<NCG>, c, pg, q, R, k_sel, sel) == cudaSuccess
-             ? QS_OK
-             : QS_ERR_CUDA;
+  return launch_pdl_cluster(select_kernel<NCG>, dim3(cl, c.H, c.B), dim3(kSelThreads), cl,
+                            select_smem(c.cap_groups), stream, c, pg, q, R, k_sel, sel);
 }
 
 }  // namespace

@@ -64,6 +64,9 @@ template <bool PAD>
 constexpr int tail_row() { return PAD ? 272 : 256; }
 constexpr int kOffKU = 0, kOffVU = 8192, kOffMeta = 16384, kOffKL = 17408, kOffVL = 25600;
 
+// The kernel's variants (see split_kernel).
+enum { kContiguous = 0, kListed = 1, kClustered = 2 };
+
 template <int MODE>
 struct Cfg;
 template <>
@@ -84,6 +87,10 @@ constexpr int align16(int x) { return (x + 15) & ~15; }
 // Units of a CTA's range whose places in the group arrays are looked up at
 // kernel start (listed variants); those past them are looked up when issued.
 constexpr int kListMax = 2048;
+constexpr int kMaxCluster = 8;  // CTAs per segment of the clustered kernel (portable limit)
+// A CTA's own arrays in finish_cluster: partials and l, maxima of rows and warps.
+template <int NW>
+constexpr int kFinishBytes = NW * 8 * (kD + 1) * 4 + kMaxR * 4 + NW * 8 * 4;
 
 template <int MODE>
 struct Layout {
@@ -103,6 +110,8 @@ struct Layout {
   static constexpr int kLiveOff = align16(kSmemBytes);
   static constexpr int kListOff = align16(kLiveOff + 4 * Cfg<MODE>::kStages);
   static constexpr int kSmemBytesListed = kListOff + 4 * kListMax;
+  static_assert(kFinishBytes<kWarps> + kMaxCluster * kMaxR * (kD * 4 + 8) <= kBarOff,
+                "the clustered kernel's partials and sums overlay the stages");
   static_assert(kStageBytes % 16 == 0 && kBarOff % 16 == 0 && kZeroOff % 16 == 0,
                 "bulk copies and ldmatrix rows need 16-byte aligned shared memory");
 };
@@ -118,6 +127,7 @@ struct Params {
               // position r % n_q)
   int ncg;    // column groups of eight rows, ceil(R / 8): warp w serves group w % ncg
   int P;      // split-kernel grid size (number of contiguous unit ranges)
+  int C;      // clustered variant: CTAs per cluster (P = B * H * C)
   float sl2;  // softmax_scale * log2(e)
   uint64_t wait_ns;  // limit on each pipeline wait (kWaitLimitNs outside tests)
   int no_issue;      // test entry only: issue no copy, so that every wait runs out
@@ -145,6 +155,25 @@ __device__ __forceinline__ Tables tables_at(uint8_t *smem, int off) {
                 t + 6 * kMaxB};
 }
 
+// Sequence b's counters into its table entries; returns its segments' length
+// in units (0: n_q > fill, nothing to see).
+template <int TT, bool IDX>
+__device__ __forceinline__ int sequence_entry(const qs_cache &c, int n_q, int n_new, int n_sel,
+                                              const Tables &T, int b) {
+  const int32_t *st = c.state + (size_t)b * QS_STATE_WORDS;
+  // clamped so that no counter value can address outside the arrays
+  const int ng_all = min(max(st[QS_ST_N_GROUPS], 0), c.cap_groups);
+  const int ng = IDX ? min(ng_all, n_sel) : ng_all;
+  const int fill_raw = st[QS_ST_FILL];
+  const int fold = min(max(fill_raw, 0), kRing);
+  const int fill = (n_new > 0 && fill_raw >= 0 && fill_raw + n_new <= kRing) ? fold + n_new : fold;
+  T.ng[b] = ng;
+  T.fill[b] = fill;
+  T.fold[b] = fold;
+  T.hb[b] = st[QS_ST_HALF_BASE] & 1;
+  return (n_q <= fill) ? ng + (fill + TT - 1) / TT : 0;
+}
+
 // Warp-cooperative: read counters, segment lengths (units per head), the
 // exclusive prefix of units (x H) and the ordinal of each sequence's first
 // segment (segments of sequences without units are skipped) into the tables.
@@ -161,18 +190,7 @@ __device__ long long build_tables(const qs_cache &c, int n_q, int n_new, int n_s
   for (int i = 0; i < per; ++i) {
     const int b = b0 + i;
     if (b < c.B) {
-      const int32_t *st = c.state + (size_t)b * QS_STATE_WORDS;
-      // clamped so that no counter value can address outside the arrays
-      const int ng_all = min(max(st[QS_ST_N_GROUPS], 0), c.cap_groups);
-      const int ng = IDX ? min(ng_all, n_sel) : ng_all;
-      const int fill_raw = st[QS_ST_FILL];
-      const int fold = min(max(fill_raw, 0), kRing);
-      const int fill = (n_new > 0 && fill_raw >= 0 && fill_raw + n_new <= kRing) ? fold + n_new : fold;
-      T.ng[b] = ng;
-      T.fill[b] = fill;
-      T.fold[b] = fold;
-      T.hb[b] = st[QS_ST_HALF_BASE] & 1;
-      const int len = (n_q <= fill) ? ng + (fill + TT - 1) / TT : 0;
+      const int len = sequence_entry<TT, IDX>(c, n_q, n_new, n_sel, T, b);
       T.len[b] = len;
       local += len;
       local_ne += len > 0;
@@ -221,8 +239,10 @@ __device__ __forceinline__ int cta_of(long long x, long long U, int P) {
 // seek() costs a compare while x stays in the current segment.
 struct Seg {
   int b = -1, h = 0, u = 0, s0 = 0, len = 0, ord = 0;
+  // ONE: x lies in this segment in any case (the clustered kernel)
+  template <bool ONE = false>
   __device__ void seek(int x, const Tables &T, int B) {
-    if (b >= 0 && x >= s0 && x < s0 + len) {
+    if (ONE || (b >= 0 && x >= s0 && x < s0 + len)) {
       u = x - s0;
       return;
     }
@@ -453,6 +473,45 @@ __device__ __noinline__ int unit_place(const Params &prm, int b, int h, int u) {
   return (int)grp;  // a group takes 33 KB: places stay far below 2^31
 }
 
+// The copies of a group (its entry grp in the group arrays) into a stage, by
+// one thread.
+template <int MODE, int UB>
+__device__ __forceinline__ void issue_group(const qs_cache &c, size_t grp, size_t n_grp, uint32_t dst,
+                                            uint32_t bar) {
+  using C = Cfg<MODE>;
+  // checked build: a copy out of bounds reads group 0 (and lands in the
+  // stage's start) instead, so its barrier still completes
+  if (!chk(in_range(grp, 1, n_grp), 3)) grp = 0;
+  if (!chk(smem_in(dst, C::kGroupBytes), 2)) dst = smem_addr(prm_smem_base());
+  const uint64_t pol = l2_evict_first_policy();  // planes are read once per call
+  constexpr int kUp = (MODE == QS_DRAFT_UPPER4 && UB == 2) ? 4096 : 8192;
+  mbar_arrive_expect_tx(bar, C::kGroupBytes - 2 * (8192 - kUp));
+  bulk_g2s_hint(dst + kOffKU, c.k_upper + grp * 8192, kUp, bar, pol);
+  bulk_g2s_hint(dst + kOffVU, c.v_upper + grp * 8192, kUp, bar, pol);
+  bulk_g2s_hint(dst + kOffMeta, c.meta + grp * 512, 1024, bar, pol);
+  if (MODE == QS_VERIFY_INT8) {
+    bulk_g2s_hint(dst + kOffKL, c.k_lower + grp * 8192, 8192, bar, pol);
+    bulk_g2s_hint(dst + kOffVL, c.v_lower + grp * 8192, 8192, bar, pol);
+  }
+}
+
+// The n_bulk unpadded ring rows of a buffer chunk from slot row r0 on (and the
+// byte count of all its rows), by one thread.
+template <int MODE>
+__device__ __forceinline__ void issue_ring_rows(const qs_cache &c, size_t r0, int n_bulk, int rows,
+                                                uint32_t dst, uint32_t bar) {
+  constexpr int kRow = tail_row<false>(), TT = Cfg<MODE>::kTailTok;
+  mbar_arrive_expect_tx(bar, rows * 2 * kD * 2);
+  if (n_bulk > 0) {
+    // checked build: rows out of the ring read row 0 instead
+    if (!chk(in_range(r0, n_bulk, (size_t)c.B * c.H * kRing), 4)) r0 = 0;
+    uint32_t dk = dst, dv = dst + TT * kRow;
+    if (!chk(smem_in(dv, n_bulk * kRow), 2)) dk = dv = smem_addr(prm_smem_base());
+    bulk_g2s(dk, c.buf_k + r0 * kD, n_bulk * kRow, bar);
+    bulk_g2s(dv, c.buf_v + r0 * kD, n_bulk * kRow, bar);
+  }
+}
+
 // With a fused append, buffer rows at or past the old fill come straight
 // from the appended tokens (the ring gets them in the same launch, not read
 // back here).  place (listed variants): the group's place in the group arrays;
@@ -467,25 +526,12 @@ __device__ __forceinline__ void issue_unit(const Params &prm, const Tables &T, c
   const size_t bh = (size_t)cu.b * c.H + cu.h;
   const int ng = T.ng[cu.b];
   if (cu.u < ng) {
-    if (IDX && place < 0) {
-      if (lane == 0) mbar_arrive(bar);
-    } else if (lane == 0) {
-      size_t grp = IDX ? (size_t)place : bh * c.cap_groups + cu.u;
-      // checked build: a copy out of bounds reads group 0 (and lands in the
-      // stage's start) instead, so its barrier still completes
-      if (!chk(in_range(grp, 1, IDX ? group_slots(c, prm.pg) : (size_t)c.B * c.H * c.cap_groups), 3))
-        grp = 0;
-      if (!chk(smem_in(dst, C::kGroupBytes), 2)) dst = smem_addr(prm_smem_base());
-      const uint64_t pol = l2_evict_first_policy();  // planes are read once per call
-      constexpr int kUp = (MODE == QS_DRAFT_UPPER4 && UB == 2) ? 4096 : 8192;
-      mbar_arrive_expect_tx(bar, C::kGroupBytes - 2 * (8192 - kUp));
-      bulk_g2s_hint(dst + kOffKU, c.k_upper + grp * 8192, kUp, bar, pol);
-      bulk_g2s_hint(dst + kOffVU, c.v_upper + grp * 8192, kUp, bar, pol);
-      bulk_g2s_hint(dst + kOffMeta, c.meta + grp * 512, 1024, bar, pol);
-      if (MODE == QS_VERIFY_INT8) {
-        bulk_g2s_hint(dst + kOffKL, c.k_lower + grp * 8192, 8192, bar, pol);
-        bulk_g2s_hint(dst + kOffVL, c.v_lower + grp * 8192, 8192, bar, pol);
-      }
+    if (lane == 0) {
+      if (IDX && place < 0)
+        mbar_arrive(bar);
+      else
+        issue_group<MODE, UB>(c, IDX ? (size_t)place : bh * c.cap_groups + cu.u,
+                              IDX ? group_slots(c, prm.pg) : (size_t)c.B * c.H * c.cap_groups, dst, bar);
     }
   } else {
     // A buffer chunk: rows fp16 rows of K, then of V.  The rows before the
@@ -501,18 +547,7 @@ __device__ __forceinline__ void issue_unit(const Params &prm, const Tables &T, c
     // engine spends about as long on a 256-byte copy as on an 8 KB one);
     // padded: one copy per row
     const int n_bulk = PAD ? 0 : max(0, min(rows, fold - i0));
-    if (lane == 0) {
-      mbar_arrive_expect_tx(bar, rows * 2 * kD * 2);
-      if (n_bulk > 0) {
-        size_t r0 = bh * kRing + slot0;
-        // checked build: rows out of the ring read row 0 instead
-        if (!chk(in_range(r0, n_bulk, (size_t)c.B * c.H * kRing), 4)) r0 = 0;
-        uint32_t dk = dst, dv = dst + TT * kRow;
-        if (!chk(smem_in(dv, n_bulk * kRow), 2)) dk = dv = smem_addr(prm_smem_base());
-        bulk_g2s(dk, c.buf_k + r0 * kD, n_bulk * kRow, bar);
-        bulk_g2s(dv, c.buf_v + r0 * kD, n_bulk * kRow, bar);
-      }
-    }
+    if (lane == 0) issue_ring_rows<MODE>(c, bh * kRing + slot0, n_bulk, rows, dst, bar);
     __syncwarp();
     const int n_rest = rows - n_bulk;
     for (int rr = lane; rr < 2 * n_rest; rr += 32) {
@@ -798,6 +833,134 @@ __device__ __noinline__ void merge_rows(const float *srcA, int cgA, int kstrideA
 }
 #endif
 
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t mapa(uint32_t a, int rank) {
+  uint32_t d;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(rank));
+  return d;
+}
+__device__ __forceinline__ void st_cluster2(uint32_t a, float x, float y) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(a), "f"(x), "f"(y) : "memory");
+}
+__device__ __forceinline__ void st_cluster4(uint32_t a, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(v.x), "f"(v.y),
+               "f"(v.z), "f"(v.w)
+               : "memory");
+}
+
+// The end of a clustered segment, by all CTAs of the cluster: a CTA's warps
+// scale their O and l to the CTA's maximum, so that they only add up, and the
+// CTAs' sums meet in the first one's shared memory, which writes the output.
+// (The log-sum-exp merges of the split kernel, done on a cluster's shared
+// memory instead, took 7.3 us of a 13.3 us call: every warp ran some thousand
+// instructions of them.)
+//   mx    float [NW][8]: maxima of each warp's eight rows
+//   part  float [NW][8][128], then l [NW][8]: scaled partials
+//   row_m float [24]: the CTA's maxima of the rows
+//   sum   float [C][R][128], then (l, maximum) [C][R]: the CTAs' sums, in the
+//         first CTA
+// all of them in the stages.  keep: the stages must not be written (copies may
+// still land there; the results are invalid then).  Every CTA takes part in
+// any case: the others count on the barriers, and write to the first one's
+// shared memory.
+template <int NW>
+__device__ __forceinline__ void finish_cluster(Softmax &sm, float oscale, bool pk, uint8_t *smem,
+                                               uint32_t sbase, int C, int rank, int ncg, int R,
+                                               bool keep, bool write, uint16_t *out, float *lse) {
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, cq = lane & 3;
+  const int cg = w % ncg, per = NW / ncg, j0 = pk ? cq : 2 * cq;
+  cluster_arrive();  // this CTA's stages are free
+  float *parts = reinterpret_cast<float *>(smem), *part = parts + w * 8 * kD;
+  float *part_l = parts + NW * 8 * kD + w * 8, *row_m = parts + NW * 8 * (kD + 1), *mx = row_m + kMaxR;
+  if (r == 0 && !keep) {
+    mx[w * 8 + j0] = sm.m[0];
+    if (!pk) mx[w * 8 + j0 + 1] = sm.m[1];
+  }
+  const float l0 = warp_sum8(sm.l[0]), l1 = pk ? 0.f : warp_sum8(sm.l[1]);
+  const float v0 = warp_sum8(sm.bv[0]), v1 = pk ? 0.f : warp_sum8(sm.bv[1]);
+  __syncthreads();
+  float M0 = -INFINITY, M1 = -INFINITY;
+  for (int e = r; e < per; e += 8) {
+    M0 = fmaxf(M0, mx[(cg + e * ncg) * 8 + j0]);
+    if (!pk) M1 = fmaxf(M1, mx[(cg + e * ncg) * 8 + j0 + 1]);
+  }
+  M0 = warp_max8(M0);
+  if (!pk) M1 = warp_max8(M1);
+  // (a warp that saw nothing adds zeros)
+  const float f0 = sm.m[0] == -INFINITY ? 0.f : fast_exp2(sm.m[0] - M0);
+  const float f1 = sm.m[1] == -INFINITY ? 0.f : fast_exp2(sm.m[1] - M1);
+  const float s0 = f0 * oscale, s1 = f1 * oscale, b0 = f0 * v0, b1 = f1 * v1;
+  if (!keep) {
+#pragma unroll
+    for (int md = 0; md < 8; ++md) {
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int d = 16 * md + r + 8 * hh;
+        part[j0 * kD + d] = fmaf(sm.o[md][2 * hh], s0, b0);
+        if (!pk) part[(j0 + 1) * kD + d] = fmaf(sm.o[md][2 * hh + 1], s1, b1);
+      }
+    }
+    if (r == 0) {
+      part_l[j0] = l0 * f0;
+      if (!pk) part_l[j0 + 1] = l1 * f1;
+      if (w < ncg) {
+        row_m[8 * cg + j0] = M0;
+        if (!pk) row_m[8 * cg + j0 + 1] = M1;
+      }
+    }
+  }
+  const uint32_t sum = sbase + kFinishBytes<NW>, sum_l = sum + C * R * kD * 4;
+  __syncthreads();
+  cluster_wait();  // the first CTA's stages are free
+  for (int i = threadIdx.x; i < R * 32; i += NW * 32) {
+    const int j = i >> 5, c4 = i & 31;
+    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < per; ++k) {
+      const float4 x = *reinterpret_cast<const float4 *>(
+          parts + (((j >> 3) + k * ncg) * 8 + (j & 7)) * kD + 4 * c4);
+      A.x += x.x; A.y += x.y; A.z += x.z; A.w += x.w;
+    }
+    st_cluster4(mapa(sum + ((rank * R + j) * kD + 4 * c4) * 4, 0), A);
+  }
+  if (threadIdx.x < R) {
+    const int j = threadIdx.x;
+    float l = 0.f;
+    for (int k = 0; k < per; ++k) l += parts[NW * 8 * kD + ((j >> 3) + k * ncg) * 8 + (j & 7)];
+    st_cluster2(mapa(sum_l + (rank * R + j) * 8, 0), l, row_m[j]);
+  }
+  cluster_arrive();
+  if (rank != 0) return;  // (the first CTA's shared memory holds all that is still read)
+  cluster_wait();
+  if (!write) return;
+  const float *sums = reinterpret_cast<const float *>(smem + (sum - sbase));
+  const float2 *lm = reinterpret_cast<const float2 *>(smem + (sum_l - sbase));
+  for (int i = threadIdx.x; i < R * 32; i += NW * 32) {
+    const int j = i >> 5, c4 = i & 31;
+    float M = -INFINITY, L = 0.f;
+    for (int k = 0; k < C; ++k) M = fmaxf(M, lm[k * R + j].y);
+    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < C; ++k) {
+      const float4 x = *reinterpret_cast<const float4 *>(sums + (k * R + j) * kD + 4 * c4);
+      const float2 y = lm[k * R + j];
+      const float f = y.y == -INFINITY ? 0.f : fast_exp2(y.y - M);  // (a CTA without units)
+      A.x = fmaf(f, x.x, A.x); A.y = fmaf(f, x.y, A.y);
+      A.z = fmaf(f, x.z, A.z); A.w = fmaf(f, x.w, A.w);
+      L = fmaf(f, y.x, L);
+    }
+    const float Ld = L > 0.f ? L : 1.f;
+    uint2 h;
+    h.x = pack_half2(A.x / Ld, A.y / Ld);
+    h.y = pack_half2(A.z / Ld, A.w / Ld);
+    *reinterpret_cast<uint2 *>(out + j * kD + 4 * c4) = h;
+    if (lse && c4 == 0) lse[j] = (M - kExpShift + log2f(L)) * 0.69314718055994531f;
+  }
+}
+
 // One warp's partial of a piece (unnormalized, log2 domain; m = -inf if the
 // warp saw no visible token; O as accumulated times oscale, plus the value
 // bias) in the layout merge_rows reads: rows
@@ -853,11 +1016,13 @@ __device__ __forceinline__ bool wait_issued(volatile int *issued, int i, uint64_
 // = row c): one MMA per k-block instead of two, and one softmax column per
 // thread.
 // NW: warps per CTA (12, or kVerifyWarps for a verify tile of <= 16 rows).
-// IDX: groups lie where a page table and / or a list of selected groups puts
-// them (unit_place); a variant of its own, so that the contiguous kernel
-// carries none of it.
-template <int MODE, bool PK, int UB, int NW, bool IDX>
+// KIND: kContiguous; kListed: groups lie where a page table and / or a list of
+// selected groups puts them (unit_place); kClustered: listed, each segment
+// shared by one cluster of CTAs.  Variants of their own, so that the
+// contiguous kernel carries nothing of the others.
+template <int MODE, bool PK, int UB, int NW, int KIND>
 __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
+  constexpr bool IDX = KIND != kContiguous, CL = KIND == kClustered;
   using C = Cfg<MODE>;
   using L = Layout<MODE>;
   constexpr int TT = C::kTailTok, S = C::kStages;
@@ -897,29 +1062,66 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
   }
   if (threadIdx.x < 8) reinterpret_cast<uint32_t *>(smem + L::kZeroOff)[threadIdx.x] = 0;
   pdl_trigger();
-  pdl_wait();  // counters, cache and queries are written by earlier kernels
-  if (w == 0) {
-    const long long tot =
-        build_tables<TT, IDX>(c, prm.n_q, prm.n_new, IDX && prm.sel ? prm.k_sel : INT_MAX, T, lane);
-    if (lane == 0) s_total = tot;
+  if (CL) {
+    // While the kernel before still runs: bring what the start reads one after
+    // the other towards L2, and its translations with it (L1 would be stale)
+    const int seg = blockIdx.x / prm.C, b = seg / c.H;
+    if (threadIdx.x == 0) prefetch_l2(c.state + (size_t)b * QS_STATE_WORDS);
+    if (threadIdx.x - 32 < 2 * prm.R) prefetch_l2(prm.q + (size_t)seg * prm.R * kD + (threadIdx.x - 32) * 64);
+    if (prm.sel)
+      for (int i = 32 * threadIdx.x; i < prm.k_sel; i += 32 * NW * 32)
+        prefetch_l2(prm.sel + (size_t)seg * prm.k_sel + i);
+    if (prm.pg.table)
+      for (int i = 32 * threadIdx.x; i < c.cap_groups; i += 32 * NW * 32)
+        prefetch_l2(prm.pg.table + (size_t)b * c.cap_groups + i);
   }
-  __syncthreads();
-  const long long U = s_total;
+  pdl_wait();  // counters, cache and queries are written by earlier kernels
+  const int n_sel = IDX && prm.sel ? prm.k_sel : INT_MAX;
+  // clustered: this CTA's segment and its share of it, and its sequence's counters
+  Seg seg_cl;
+  int cl_x0 = 0, cl_n = 0;
+  if (CL) {
+    const int seg = blockIdx.x / prm.C, rank = blockIdx.x % prm.C;
+    seg_cl.b = seg / c.H;
+    seg_cl.h = seg % c.H;
+    if (threadIdx.x == 0)
+      T.len[seg_cl.b] = sequence_entry<TT, IDX>(c, prm.n_q, prm.n_new, n_sel, T, seg_cl.b);
+    __syncthreads();
+    seg_cl.len = T.len[seg_cl.b];
+    cl_x0 = seg_cl.len * rank / prm.C;
+    cl_n = seg_cl.len * (rank + 1) / prm.C - cl_x0;
+  } else {
+    if (w == 0) {
+      const long long tot = build_tables<TT, IDX>(c, prm.n_q, prm.n_new, n_sel, T, lane);
+      if (lane == 0) s_total = tot;
+    }
+    __syncthreads();
+  }
+  const long long U = CL ? 0 : s_total;
   const int p = blockIdx.x;
   const int R = prm.R, ncg = prm.ncg, cg = w % ncg;  // this warp's column group
   const int stride = R * kD + 2 * kMaxR;             // floats per partial
 
-  if (prm.n_new > 0 && w == NW - 1) {
-    // The fused append, by a warp that issues no first copy.  Every CTA has
-    // read the counters above; the CTA whose ticket comes last commits the
+  auto append = [&]() {
+    // The fused append, by the last warp.  Every CTA has read the counters
+    // above; the CTA whose ticket comes last commits the
     // appended counters (no CTA of this launch reads them again).  The new
     // tokens enter the ring slots past the old fill, which no CTA of this
     // launch reads (its copies of those rows come from k_new / v_new).
     if (lane == 0 && atom_add_acq_rel_gpu(&c.state[QS_ST_TICKET], 1) == (int)gridDim.x - 1) {
       for (int b = 0; b < c.B; ++b) {
         int32_t *st = c.state + (size_t)b * QS_STATE_WORDS;
-        if (T.fill[b] != T.fold[b]) {
-          st[QS_ST_FILL] = T.fill[b];
+        int fill, fold;
+        if (CL) {  // (the tables hold this CTA's sequence alone; nobody has changed the counters)
+          const int raw = st[QS_ST_FILL];
+          fold = min(max(raw, 0), kRing);
+          fill = raw >= 0 && raw + prm.n_new <= kRing ? fold + prm.n_new : fold;
+        } else {
+          fill = T.fill[b];
+          fold = T.fold[b];
+        }
+        if (fill != fold) {
+          st[QS_ST_FILL] = fill;
           st[QS_ST_PENDING] += prm.n_new;
         } else {
           atomicOr(&st[QS_ST_ERR], QS_DEV_OVERFLOW);  // as a separate append would: no-op
@@ -928,7 +1130,9 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
       c.state[QS_ST_TICKET] = 0;
     }
     constexpr int kRowVec = kD * 2 / 16;  // uint4 per fp16 row
-    for (int j = p; j < c.B * c.H; j += gridDim.x) {
+    // clustered: the cluster's first CTA writes its own head's tokens
+    const int j0 = CL ? (p % prm.C == 0 ? p / prm.C : c.B * c.H) : p;
+    for (int j = j0; j < c.B * c.H; j += gridDim.x) {
       const int b = j / c.H;
       if (T.fill[b] == T.fold[b]) continue;  // this sequence's append failed
       const int slot0 = T.hb[b] * kG + T.fold[b];
@@ -942,25 +1146,40 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
         bv[slot * kRowVec + e % kRowVec] = sv[e];
       }
     }
-  }
+  };
+  // (listed variants: after the first copies, which the last warp issues too)
+  const bool appends = prm.n_new > 0 && w == NW - 1;
+  if (!IDX && appends) append();
 
   // sequences with n_q > fill see no token: zero outputs, lse = -inf, error
-  for (int b = p; b < c.B; b += prm.P) {
+  for (int b = CL ? seg_cl.b : p; b < c.B; b += prm.P) {
     if (T.len[b] != 0) continue;
-    const size_t nh = (size_t)c.H * R;
-    uint4 *o = reinterpret_cast<uint4 *>(prm.out + (size_t)b * nh * kD);
+    if (CL && p % prm.C != 0) break;  // the cluster's first CTA alone, and for its head alone
+    const size_t nh = CL ? (size_t)R : (size_t)c.H * R;
+    const size_t row0 = CL ? (size_t)(p / prm.C) * R : b * nh;
+    uint4 *o = reinterpret_cast<uint4 *>(prm.out + row0 * kD);
     for (size_t i = threadIdx.x; i < nh * (kD / 8); i += (NW * 32)) o[i] = make_uint4(0, 0, 0, 0);
     if (prm.lse)
-      for (size_t i = threadIdx.x; i < nh; i += (NW * 32)) prm.lse[(size_t)b * nh + i] = -INFINITY;
+      for (size_t i = threadIdx.x; i < nh; i += (NW * 32)) prm.lse[row0 + i] = -INFINITY;
     if (threadIdx.x == 0) atomicOr(&c.state[(size_t)b * QS_STATE_WORDS + QS_ST_ERR], QS_DEV_NQ_GT_FILL);
   }
 
-  const int x0 = (int)range_lo(p, U, prm.P), x1 = (int)range_lo(p + 1, U, prm.P);
-  if (x0 >= x1) return;
+  // clustered: the segment's units from 0 on, and a CTA without any still
+  // meets its cluster at the end
+  const int x0 = CL ? cl_x0 : (int)range_lo(p, U, prm.P);
+  const int x1 = CL ? cl_x0 + cl_n : (int)range_lo(p + 1, U, prm.P);
+  if (CL ? seg_cl.len == 0 : x0 >= x1) {
+    if (IDX && appends) append();
+    return;
+  }
   const int n = x1 - x0;
   Seg first, lastseg;
-  first.seek(x0, T, c.B);
-  lastseg.seek(x1 - 1, T, c.B);
+  if (CL) {
+    first = lastseg = seg_cl;
+  } else {
+    first.seek(x0, T, c.B);
+    lastseg.seek(x1 - 1, T, c.B);
+  }
   const int ord_first = first.ord, ord_last = lastseg.ord;
   // partial slot of warp ww for the piece of segment ordinal o
   auto slot = [&](int o, int ww) {
@@ -1000,6 +1219,10 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
     __syncwarp();
   };
 
+  // clustered: the partials meet in shared memory, so the cluster must have
+  // started by then
+  if (CL) cluster_arrive();
+
   // the warps reach the range's last segment mid-range: start its queries
   // towards L1 now (two 128-byte lines per row; a copy in shared memory was
   // measured no faster)
@@ -1008,37 +1231,34 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
     prefetch_l1(prm.q + (bh * R) * kD + threadIdx.x * 64);
   }
 
-  // Listed variants: where the range's groups lie.  Warp 0's lanes look the
-  // first S up side by side and issue them; meanwhile the other warps put
-  // the next kListMax - S into shared memory, ready for the refills.
+  // units i and i + S share stage i % S; warp 0 issues the first S.  Listed
+  // variants: warp k looks up where unit k lies and issues it, for k < S (warp
+  // 0 alone, one unit after the other, was through 4 us into a call); then all
+  // put the places of the next kListMax - S into shared memory, ready for the
+  // refills.
   int *live = reinterpret_cast<int *>(smem + L::kLiveOff);
   int *list = reinterpret_cast<int *>(smem + L::kListOff);
   auto place_of = [&](const Seg &a) { return a.u < T.ng[a.b] ? unit_place(prm, a.b, a.h, a.u) : 0; };
-  int my_place = 0;
-  if (IDX && w == 0 && lane < min(S, n)) {
-    Seg a;
-    a.seek(x0 + lane, T, c.B);
-    my_place = place_of(a);
-  }
-  // units i and i + S share stage i % S; warp 0 issues the first S
-  if (w == 0 && !prm.no_issue) {
-    Seg a;
-    for (int k = 0; k < S && k < n; ++k) {
-      a.seek(x0 + k, T, c.B);
-      const int place = IDX ? __shfl_sync(0xffffffffu, my_place, k) : 0;
-      if (IDX && lane == 0) live[k] = place >= 0;
+  if ((IDX || w == 0) && !prm.no_issue) {
+    Seg a = first;
+    for (int k = IDX ? w : 0; k < S && k < n; k += IDX ? NW : 1) {
+      a.template seek<CL>(x0 + k, T, c.B);
+      int place = 0;
+      if (IDX && lane == 0) {
+        place = place_of(a);
+        live[k] = place >= 0;
+      }
       if (lane == 0) issued[k] = k;
       issue_unit<MODE, UB, kPadTail, IDX>(prm, T, a, place, sbase + k * L::kStageBytes, full0 + 8 * k,
                                           lane);
     }
   }
+  if (IDX && appends) append();
   if (IDX && n > S) {  // (uniform)
-    if (w > 0) {
-      Seg a;
-      for (int i = S + threadIdx.x - 32; i < min(n, kListMax); i += (NW - 1) * 32) {
-        a.seek(x0 + i, T, c.B);
-        list[i] = place_of(a);
-      }
+    Seg a = first;
+    for (int i = S + threadIdx.x; i < min(n, kListMax); i += NW * 32) {
+      a.template seek<CL>(x0 + i, T, c.B);
+      list[i] = place_of(a);
     }
     __syncthreads();
   }
@@ -1048,7 +1268,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
   uint32_t qp0[8], qp1[8];
   int fill = 0, ng = 0;
   int cur_ord = -1;  // segment ordinal of this warp's softmax state (-1: none yet)
-  Seg cur, ahead;
+  Seg cur = first, ahead = first;
   // Work is claimed in half-units (claim h: unit h / 2, tokens of half h % 2)
   // from one shared counter.  Both halves of a unit go to whichever warps
   // claim them; the stage's release counter joins them again.  Draft claims
@@ -1068,7 +1288,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
     if (hcl >= 2 * n) break;
     if (kAhead) h_next = claim();
     const int i = hcl >> 1, hw = hcl & 1;
-    cur.seek(x0 + i, T, c.B);
+    cur.template seek<CL>(x0 + i, T, c.B);
     if (cur.ord != cur_ord) {
       // a new piece: the finished one's partial (empty ones for pieces this
       // warp skipped), then fresh state and this head's queries
@@ -1429,7 +1649,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
     if (last) {
       if (lane == 0) cnt[stage] = 0;
       if (ok && i + S < n) {
-        ahead.seek(x0 + i + S, T, c.B);
+        ahead.template seek<CL>(x0 + i + S, T, c.B);
         fence_proxy_async_smem();
         int place = 0;
         if (IDX && lane == 0) {
@@ -1488,6 +1708,14 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
   // resets the counter.  Only the first and the last piece of a range can be
   // shared.
   const bool aborted = s_abort != 0;
+  if (CL) {
+    cluster_wait();  // (of the arrival at the start: every CTA runs)
+    finish_cluster<NW>(sm, Centre<MODE, UB>::kScale, PK, smem, sbase, prm.C, p % prm.C, ncg, R,
+                       s_abort == 2, !aborted,
+                       prm.out + (size_t)(p / prm.C) * R * kD,
+                       prm.lse ? prm.lse + (size_t)(p / prm.C) * R : nullptr);
+    return;
+  }
   float *last_part = reinterpret_cast<float *>(smem);  // NW partials, in stage memory (free now)
   chk(smem_in(smem_addr(last_part), (uint32_t)(NW * stride * 4)), 11);
   if (s_abort != 2) {
@@ -1601,25 +1829,34 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
 
 // --------------------------------------------------------------- host side
 struct DevInfo {
-  int ready[32];
-  int grid[32];
+  int ready[48];
+  int grid[48];
 };
 DevInfo g_dev[64];
 
+template <int MODE>
+constexpr int smem_of(int kind) {
+  using L = Layout<MODE>;
+  return kind == kContiguous ? L::kSmemBytes : L::kSmemBytesListed;
+}
+constexpr int smem_bytes(int mode, int kind) {
+  return mode == QS_DRAFT_UPPER4 ? smem_of<QS_DRAFT_UPPER4>(kind) : smem_of<QS_VERIFY_INT8>(kind);
+}
+
 // Resident CTAs of one split-kernel variant on a device (set up once).
-template <int MODE, bool PK, int UB, int NW, bool IDX>
+template <int MODE, bool PK, int UB, int NW, int KIND>
 qs_status grid_for_device(int dev, int &P) {
   DevInfo &di = g_dev[dev];
-  constexpr int v = 2 * MODE + (PK ? 1 : 0) + (UB == 2 ? 4 : 0) + (NW == 8 ? 8 : 0) + (IDX ? 16 : 0);
+  constexpr int v = 2 * MODE + (PK ? 1 : 0) + (UB == 2 ? 4 : 0) + (NW == 8 ? 8 : 0) + 16 * KIND;
   if (!__atomic_load_n(&di.ready[v], __ATOMIC_ACQUIRE)) {
-    const int smem = IDX ? Layout<MODE>::kSmemBytesListed : Layout<MODE>::kSmemBytes;
-    if (cudaFuncSetAttribute(split_kernel<MODE, PK, UB, NW, IDX>,
+    constexpr int smem = smem_bytes(MODE, KIND);
+    if (cudaFuncSetAttribute(split_kernel<MODE, PK, UB, NW, KIND>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
       return QS_ERR_CUDA;
     int sms = 0, occ = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return QS_ERR_CUDA;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, split_kernel<MODE, PK, UB, NW, IDX>,
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, split_kernel<MODE, PK, UB, NW, KIND>,
                                                       NW * 32, smem) != cudaSuccess)
       return QS_ERR_CUDA;
     if (occ < 1) return QS_ERR_CUDA;
@@ -1630,23 +1867,26 @@ qs_status grid_for_device(int dev, int &P) {
   return QS_OK;
 }
 
-template <int UB, bool IDX>
+template <int UB, int KIND>
 qs_status grid_size_ub(int dev, qs_mode mode, bool packed, int ncg, int &P) {
   if (mode == QS_DRAFT_UPPER4)
-    return packed ? grid_for_device<QS_DRAFT_UPPER4, true, UB, kWarps, IDX>(dev, P)
-                  : grid_for_device<QS_DRAFT_UPPER4, false, UB, kWarps, IDX>(dev, P);
-  return ncg <= 2 ? grid_for_device<QS_VERIFY_INT8, false, UB, kVerifyWarps, IDX>(dev, P)
-                  : grid_for_device<QS_VERIFY_INT8, false, UB, kWarps, IDX>(dev, P);
+    return packed ? grid_for_device<QS_DRAFT_UPPER4, true, UB, kWarps, KIND>(dev, P)
+                  : grid_for_device<QS_DRAFT_UPPER4, false, UB, kWarps, KIND>(dev, P);
+  return ncg <= 2 ? grid_for_device<QS_VERIFY_INT8, false, UB, kVerifyWarps, KIND>(dev, P)
+                  : grid_for_device<QS_VERIFY_INT8, false, UB, kWarps, KIND>(dev, P);
 }
 
-template <bool IDX>
+template <int KIND>
 qs_status grid_size(qs_mode mode, bool packed, int upper_bits, int ncg, int &P) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return QS_ERR_CUDA;
   if (dev < 0 || dev >= 64) return QS_ERR_UNSUPPORTED;
-  return upper_bits == 2 ? grid_size_ub<2, IDX>(dev, mode, packed, ncg, P)
-                         : grid_size_ub<4, IDX>(dev, mode, packed, ncg, P);
+  return upper_bits == 2 ? grid_size_ub<2, KIND>(dev, mode, packed, ncg, P)
+                         : grid_size_ub<4, KIND>(dev, mode, packed, ncg, P);
 }
+
+// A draft of at most four query rows takes the packed columns (PK).
+inline bool packed_rows(qs_mode mode, int R) { return mode == QS_DRAFT_UPPER4 && R <= 4; }
 
 // Workspace: (P + B H) x 12 warp slots of R rows (R = group x n_q); an
 // eight-warp launch packs its pieces eight slots apart, inside that size.
@@ -1654,28 +1894,38 @@ size_t ws_bytes(int P, int B, int H, int R) {
   return (size_t)(P + (size_t)B * H) * kWarps * (size_t)(R * kD + 2 * kMaxR) * sizeof(float);
 }
 
-template <int MODE, bool PK, int UB, int NW, bool IDX>
+template <int MODE, bool PK, int UB, int NW, int KIND>
 qs_status launch(const Params &prm, cudaStream_t s) {
-  return launch_pdl(split_kernel<MODE, PK, UB, NW, IDX>, dim3(prm.P), dim3(NW * 32),
-                    IDX ? Layout<MODE>::kSmemBytesListed : Layout<MODE>::kSmemBytes, s, prm);
+  if (KIND == kClustered)
+    return launch_pdl_cluster(split_kernel<MODE, PK, UB, NW, KIND>, dim3(prm.P), dim3(NW * 32), prm.C,
+                              smem_bytes(MODE, KIND), s, prm);
+  return launch_pdl(split_kernel<MODE, PK, UB, NW, KIND>, dim3(prm.P), dim3(NW * 32),
+                    smem_bytes(MODE, KIND), s, prm);
 }
 
-template <int UB, bool IDX>
+template <int UB, int KIND>
 qs_status launch_ub(qs_mode mode, bool packed, const Params &prm, cudaStream_t st) {
   if (mode == QS_VERIFY_INT8)
-    return prm.ncg <= 2 ? launch<QS_VERIFY_INT8, false, UB, kVerifyWarps, IDX>(prm, st)
-                        : launch<QS_VERIFY_INT8, false, UB, kWarps, IDX>(prm, st);
-  return packed ? launch<QS_DRAFT_UPPER4, true, UB, kWarps, IDX>(prm, st)
-                : launch<QS_DRAFT_UPPER4, false, UB, kWarps, IDX>(prm, st);
+    return prm.ncg <= 2 ? launch<QS_VERIFY_INT8, false, UB, kVerifyWarps, KIND>(prm, st)
+                        : launch<QS_VERIFY_INT8, false, UB, kWarps, KIND>(prm, st);
+  return packed ? launch<QS_DRAFT_UPPER4, true, UB, kWarps, KIND>(prm, st)
+                : launch<QS_DRAFT_UPPER4, false, UB, kWarps, KIND>(prm, st);
 }
 
-// What the entry points share: the call's tensors, checked, into a launch.
-// prm holds the cache, the append, the wait limit and, for the listed
-// variants, pages and selection already.
-template <bool IDX>
-qs_status decode(Params &prm, qs_mode mode, const uint16_t *q, int32_t n_q, int32_t group,
-                 float softmax_scale, uint16_t *out, float *lse, void *workspace,
-                 size_t workspace_bytes, qs_stream_t stream) {
+template <int KIND>
+qs_status launch_kind(qs_mode mode, bool packed, const Params &prm, cudaStream_t st) {
+  return prm.c.upper_bits == 2 ? launch_ub<2, KIND>(mode, packed, prm, st)
+                               : launch_ub<4, KIND>(mode, packed, prm, st);
+}
+
+// What the entry points share: the call's tensors, checked, into the kernel's
+// parameters.  prm holds the cache, the append, the wait limit and, for the
+// listed variants, pages and selection already; P: the grid of the variant
+// whose workspace the call needs.
+template <int KIND>
+qs_status fill_params(Params &prm, qs_mode mode, const uint16_t *q, int32_t n_q, int32_t group,
+                      float softmax_scale, uint16_t *out, float *lse, void *workspace,
+                      size_t workspace_bytes) {
   if (!q || !out || n_q < 1 || n_q > kMaxQ || group < 1 || group > kMaxR || group * n_q > kMaxR)
     return QS_ERR_ARG;
   if (mode != QS_DRAFT_UPPER4 && mode != QS_VERIFY_INT8) return QS_ERR_ARG;
@@ -1689,16 +1939,13 @@ qs_status decode(Params &prm, qs_mode mode, const uint16_t *q, int32_t n_q, int3
   prm.ncg = (prm.R + 7) / 8;
   prm.sl2 = softmax_scale * 1.4426950408889634f;
   prm.ws_floats = workspace_bytes / sizeof(float);
-  const bool packed = (mode == QS_DRAFT_UPPER4 && prm.R <= 4);
-  const qs_status s = grid_size<IDX>(mode, packed, prm.c.upper_bits, prm.ncg, prm.P);
+  const qs_status s = grid_size<KIND>(mode, packed_rows(mode, prm.R), prm.c.upper_bits, prm.ncg, prm.P);
   if (s != QS_OK) return s;
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < ws_bytes(prm.P, prm.c.B, prm.c.H, prm.R))
     return QS_ERR_WORKSPACE;
   prm.ws = static_cast<float *>(workspace);
-  cudaStream_t st = (cudaStream_t)stream;
-  return prm.c.upper_bits == 2 ? launch_ub<2, IDX>(mode, packed, prm, st)
-                               : launch_ub<4, IDX>(mode, packed, prm, st);
+  return QS_OK;
 }
 
 }  // namespace

@@ -102,6 +102,26 @@ def test_sparse(torch, k, n_q, group, ub, paged):
     assert np.all(qs.qs_get_errors(cache) == 0)
 
 
+@pytest.mark.parametrize("mode,n_q,group", [(DRAFT, 1, 1), (DRAFT, 1, 8), (VERIFY, 5, 1), (VERIFY, 5, 4),
+                                            (VERIFY, 8, 3)])
+@pytest.mark.parametrize("B,H", [(1, 1), (1, 8), (1, 32), (2, 20), (3, 24), (5, 31)])
+def test_cluster_sizes(torch, B, H, mode, n_q, group):
+    """Eight, four and two CTAs a segment, and the split kernel; sequences
+    with fewer groups than the list, and one with too few buffered tokens."""
+    rng = np.random.default_rng([B, H, n_q, group])
+    ng = [int(x) for x in rng.integers(0, 14, B)]
+    fill = [int(x) for x in rng.integers(1, 257, B)]
+    ng[0], fill[0] = 13, 250
+    oc = _oracle_state(rng, B, H, ng, fill, cap=13)
+    cache = load(torch, oc, rng, paged=False)
+    sel = random_sel(rng, B, H, 9, ng)
+    q = h16(rng, (B, H * group, n_q, 128))
+    got, gl = run(torch, cache, mode, q, group, sel)
+    ref, rl = paging.attention(oc, q, mode == DRAFT, group, sel=sel)
+    assert_close(got, ref, gl, rl)
+    assert list(qs.qs_get_errors(cache)) == [qs.DEV_NQ_GT_FILL if n_q > f else 0 for f in fill]
+
+
 @pytest.mark.parametrize("paged", [False, True])
 def test_every_group_selected_equals_dense(torch, paged):
     """All groups in order give the contiguous kernel's result (within the
