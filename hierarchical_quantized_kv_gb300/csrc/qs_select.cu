@@ -9,11 +9,11 @@
 // the 512 bytes of scales and zeros the attention reads anyway.  A head's
 // score for a group is the maximum over its query rows.
 //
-// Which of two close groups is taken must not depend on rounding, so the order
-// is that of the exact sums: scores come from the tensor cores in fp32 with a
-// bound E on their error; a group more than 2 E above the k-th largest score
-// is in, one more than 2 E below is out, and only what lies between (usually
-// the k-th group alone) is summed again in fp64.
+// Which of two close groups is taken must not depend on rounding: scores come
+// from the tensor cores in fp32 with a bound E on their error; a group more than
+// 2 E above the k-th largest score is in, one more than 2 E below is out, and
+// only what lies between (a few groups) is summed again to about 46 bits, where
+// sums of fp16 products are as good as exact.
 //
 // Bound by latency at one sequence (512 B per group and head: 4 MB for a 32k
 // context of 32 heads) and by HBM for large batches.  A cluster of CTAs per
@@ -33,12 +33,12 @@ namespace {
 constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
 constexpr int kTile = 16;  // groups a warp scores at once (rows of the MMA)
 constexpr int kMaxRows = 24;
-// Groups per sequence: score (4 bytes), fp64 sum (8), list entry (4) and flag
+// Groups per sequence: score (4 bytes), close sum (8), list entry (4) and flag
 // (1) of each lie in shared memory.
 constexpr int kMaxSelectGroups = 12800;
 
 struct SelectSmem {
-  double *exact;   // [n] fp64 score of list entry i
+  double *exact;   // [n] close sum of list entry i
   float *score;    // [n]
   int *list;       // [n] groups near the border, ascending
   uint8_t *flag;   // [n] 1: selected
@@ -60,10 +60,30 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t u = __float_as_uint(x);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+__device__ __forceinline__ float float_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
 __device__ __forceinline__ unsigned long long key_of(double x) {
   x = x == x ? x + 0.0 : -INFINITY;
   const unsigned long long u = __double_as_longlong(x);
   return u >> 63 ? ~u : u | (1ull << 63);
+}
+
+// A number as the sum of two fp32 ones (this GPU adds fp64 numbers at a
+// sixty-fourth of the fp32 rate: the close sums below took 5 us of a 15 us
+// call in fp64).  two_sum is exact (Knuth); a sum of pairs is off by less than
+// 2^-46 of the two numbers' magnitudes, and the same whichever comes first.
+struct Pair {
+  float h, l;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return Pair{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  const Pair s = two_sum(a.h, b.h);
+  const float l = __fadd_rn(s.l, __fadd_rn(a.l, b.l)), h = __fadd_rn(s.h, l);
+  return Pair{h, __fsub_rn(l, __fsub_rn(h, s.h))};  // (|l| is far below |s.h|, or s.h is zero)
 }
 
 struct BlockScratch {
@@ -72,19 +92,20 @@ struct BlockScratch {
   int digit, above;
 };
 
-// Key of the k-th largest of n values (1 <= k <= n), and how many are larger:
-// radix selection from the top byte down, by the whole CTA.
-template <typename T, typename K>
-__device__ K kth_largest(const T *v, int n, int k, int *n_above, BlockScratch &S) {
+// Key of the k-th largest of n keys below 2^BITS (1 <= k <= n), and how many are
+// larger: radix selection from the top byte down, by the whole CTA (0.5 us a
+// byte).
+template <typename K, int BITS, typename KeyOf>
+__device__ __forceinline__ K kth_largest(int n, int k, int *n_above, BlockScratch &S, KeyOf key_at) {
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   K prefix = 0;
   int need = k;
 #pragma unroll 1
-  for (int shift = 8 * (int)sizeof(K) - 8; shift >= 0; shift -= 8) {
+  for (int shift = BITS - 8; shift >= 0; shift -= 8) {
     S.hist[tid] = 0;
     __syncthreads();
     for (int i = tid; i < n; i += kSelThreads) {
-      const K key = key_of(v[i]);
+      const K key = key_at(i);
       // (shifted twice: a shift by the key's whole width is undefined)
       if (((key >> shift) >> 8) == prefix) atomicAdd(&S.hist[(int)(key >> shift) & 255], 1);
     }
@@ -145,15 +166,35 @@ __global__ void __launch_bounds__(kSelThreads)
                   int32_t *__restrict__ sel) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ BlockScratch S;
-  __shared__ float s_err[8];  // largest sum of magnitudes each CTA met
+  // the first CTA's: largest sum of magnitudes, smallest and largest key of a score
   __shared__ int s_mag;
+  __shared__ unsigned s_kmin, s_kmax;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), n_ranks = (int)cluster.num_blocks();
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   const int w = tid >> 5, lane = tid & 31, r = lane >> 2, cq = lane & 3;
   SelectSmem M = SelectSmem::at(smem_raw, c.cap_groups);
-  if (tid == 0) s_mag = 0;
+  if (tid == 0) {
+    s_mag = 0;
+    s_kmin = 0xFFFFFFFFu;
+    s_kmax = 0;
+  }
   pdl_trigger();
+  // While the kernel before still runs: counters, queries, and the first
+  // tile's rows (or its page numbers) towards L2 (L1 would be stale)
+  {
+    const size_t bh = (size_t)b * c.H + h;
+    if (tid == 0) prefetch_l2(c.state + (size_t)b * QS_STATE_WORDS);
+    if (tid < 2 * R) prefetch_l2(q + bh * R * kD + 64 * tid);
+    const int g0 = kTile * (rank * kSelWarps + w) + (lane & 15);
+    if (pg.table) {
+      if (g0 < c.cap_groups && (lane & 15) == lane) prefetch_l2(pg.table + (size_t)b * c.cap_groups + g0);
+    } else if (g0 < c.cap_groups) {  // 512 bytes a group: four lines, two a lane
+      const uint16_t *m = c.meta + (bh * c.cap_groups + g0) * 512 + 128 * (lane >> 4);
+      prefetch_l2(m);
+      prefetch_l2(m + 64);
+    }
+  }
   pdl_wait();
   int32_t *st = c.state + (size_t)b * QS_STATE_WORDS;
   const int n = min(max(st[QS_ST_N_GROUPS], 0), c.cap_groups);
@@ -189,6 +230,7 @@ __global__ void __launch_bounds__(kSelThreads)
   float *score0 = cluster.map_shared_rank(M.score, 0);
   bool started = false;
   float mag = 0.f;
+  unsigned kmin = 0xFFFFFFFFu, kmax = 0;
 #pragma unroll 1
   for (int t = rank * kSelWarps + w; t < n_tiles; t += n_ranks * kSelWarps) {
     uint4 zr[2][4], sr[2][4];  // zero and scale rows of groups r and r + 8
@@ -256,35 +298,44 @@ __global__ void __launch_bounds__(kSelThreads)
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
       const int g = kTile * t + r + 8 * j;
-      if (cq == 0 && g < n) score0[g] = good[j] ? x : -INFINITY;
+      if (cq == 0 && g < n) {
+        x = good[j] ? x : -INFINITY;
+        score0[g] = x;
+        kmin = min(kmin, key_of(x));
+        kmax = max(kmax, key_of(x));
+      }
     }
   }
   if (!started) cluster.barrier_wait();
-  mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
-  mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
-  mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, 4));
-  mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, 8));
-  mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, 16));
-  __syncthreads();
-  if (lane == 0) atomicMax(&s_mag, __float_as_int(mag));  // mag >= 0: ordered as integers
-  __syncthreads();
-  if (tid == 0) *cluster.map_shared_rank(&s_err[rank], 0) = __int_as_float(s_mag);
-  cluster.sync();  // all scores and magnitudes are in the first CTA
+  // (mag >= 0: ordered as integers)
+  const int wmag = __reduce_max_sync(0xffffffffu, __float_as_int(mag));
+  kmin = __reduce_min_sync(0xffffffffu, kmin);
+  kmax = __reduce_max_sync(0xffffffffu, kmax);
+  if (lane == 0 && kmax >= kmin) {
+    atomicMax(cluster.map_shared_rank(&s_mag, 0), wmag);
+    atomicMin(cluster.map_shared_rank(&s_kmin, 0), kmin);
+    atomicMax(cluster.map_shared_rank(&s_kmax, 0), kmax);
+  }
+  cluster.sync();  // all scores are in the first CTA
   if (rank != 0) return;
 
   // ---- selection.  One MMA adds 17 numbers, aligned to the largest and cut
   // no coarser than 2^-23 of it: off by less than 2^-18.9 of the sum of their
   // magnitudes; the eight fp32 additions and the last multiply-add add
   // 9 x 2^-24.  Together under 2^-18.
-  float E = 0.f;
-  for (int i = 0; i < n_ranks; ++i) E = fmaxf(E, s_err[i]);
-  E *= 0x1p-18f;
+  const float E = __int_as_float(s_mag) * 0x1p-18f;
+  // The k-th largest score up to the top 16 bits of the keys' range (a few
+  // rounding steps of a score, below E as a rule): it lies in [t_lo, t_hi].
+  const unsigned k0 = s_kmin, k1 = s_kmax;
+  const int shift = max(0, 16 - __clz(k1 - k0));  // (k1 == k0: clz 32, shift 0)
   int above;
-  const uint32_t key = kth_largest<float, uint32_t>(M.score, n, k_sel, &above, S);
-  const float T = __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+  const unsigned t = kth_largest<unsigned, 16>(n, k_sel, &above, S, [&](int i) {
+    return (key_of(M.score[i]) - k0) >> shift;
+  });
+  const float t_lo = float_of(k0 + (t << shift)), t_hi = float_of(k0 + (t << shift) + ((1u << shift) - 1));
   // (infinite or NaN limits, from queries that are not finite, leave every
-  // group to the fp64 sums)
-  const float hi = __fadd_ru(T, 2.f * E), lo = __fadd_rd(T, -2.f * E);
+  // group to the close sums)
+  const float hi = __fadd_ru(t_hi, 2.f * E), lo = __fadd_rd(t_lo, -2.f * E);
   int m = 0, n_in = 0;
   for (int base = 0; base < n; base += kSelThreads) {
     const int g = base + tid;
@@ -301,46 +352,66 @@ __global__ void __launch_bounds__(kSelThreads)
   if (need >= m) {
     for (int i = tid; i < m; i += kSelThreads) M.flag[M.list[i]] = 1;
   } else if (need > 0) {
-    // fp64 sums: a warp per group, lane l holds positions 4 l .. 4 l + 3
-    for (int i = w; i < m; i += kSelWarps) {
-      const long long place = group_slot(c, pg, b, h, M.list[i]);
-      double best = -INFINITY;
+    // close sums: half a warp per group, lane l of it holds positions 8 l ..
+    // 8 l + 7 of the rows, which are eight channels that lie together
+    const int l = lane & 15, ch = kmeta_channel(8 * l);
+    for (int base = 2 * w; base < m; base += 2 * kSelWarps) {
+      const int i = base + (lane >> 4);
+      const long long place = i < m ? group_slot(c, pg, b, h, M.list[i]) : -1;
+      uint4 sw = make_uint4(0, 0, 0, 0), zw = sw;
       if (place >= 0) {
-        const uint16_t *mt = c.meta + (size_t)place * 4 * 128 + 4 * lane;
-        const uint2 sw = __ldg(reinterpret_cast<const uint2 *>(mt + QS_META_K_SCALE * 128));
-        const uint2 zw = __ldg(reinterpret_cast<const uint2 *>(mt + QS_META_K_ZERO * 128));
-        const float2 s01 = __half22float2(u32_as_h2(sw.x)), s23 = __half22float2(u32_as_h2(sw.y));
-        const float2 z01 = __half22float2(u32_as_h2(zw.x)), z23 = __half22float2(u32_as_h2(zw.y));
-        const float s[4] = {s01.x, s01.y, s23.x, s23.y}, z[4] = {z01.x, z01.y, z23.x, z23.y};
-        for (int row = 0; row < R; ++row) {
-          double d = 0;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const double qv = (double)__half2float(
-                __ushort_as_half(__ldg(qh + (size_t)row * kD + kmeta_channel(4 * lane + x))));
-            // (products of two fp16 numbers, and 255 of them, are exact)
-            d += qv * z[x];
-            d += 255.0 * (qv > 0 ? qv : 0.0) * s[x];
-          }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-          best = fmax(best, d);
-        }
+        const uint16_t *mt = c.meta + (size_t)place * 4 * 128 + 8 * l;
+        sw = ldg16(mt + QS_META_K_SCALE * 128);
+        zw = ldg16(mt + QS_META_K_ZERO * 128);
       }
-      if (lane == 0) M.exact[i] = best;
+      Pair best{-INFINITY, 0.f};
+#pragma unroll 2
+      for (int row = 0; row < R; ++row) {
+        const uint4 qw = ldg16(qh + (size_t)row * kD + ch);
+        // positions 2 x, 2 x + 1 of the eight: channels c, c + 4 with c = 0, 1, 2, 3
+        const uint32_t qp[4] = {prmt(qw.x, qw.z, 0x5410), prmt(qw.x, qw.z, 0x7632),
+                                prmt(qw.y, qw.w, 0x5410), prmt(qw.y, qw.w, 0x7632)};
+        const uint32_t sp[4] = {sw.x, sw.y, sw.z, sw.w}, zp[4] = {zw.x, zw.y, zw.z, zw.w};
+        Pair ds[4], dz[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float2 qv = __half22float2(u32_as_h2(qp[x])), sv = __half22float2(u32_as_h2(sp[x])),
+                       zv = __half22float2(u32_as_h2(zp[x]));
+          // (products of two fp16 numbers are exact in fp32)
+          dz[x] = two_sum(__fmul_rn(qv.x, zv.x), __fmul_rn(qv.y, zv.y));
+          ds[x] = two_sum(__fmul_rn(fmaxf(qv.x, 0.f), sv.x), __fmul_rn(fmaxf(qv.y, 0.f), sv.y));
+        }
+        const Pair sum_s = (ds[0] + ds[1]) + (ds[2] + ds[3]);
+        const float p = __fmul_rn(255.f, sum_s.h), e = __fmaf_rn(255.f, sum_s.h, -p);
+        Pair d = ((dz[0] + dz[1]) + (dz[2] + dz[3])) + Pair{p, __fmaf_rn(255.f, sum_s.l, e)};
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+          d = d + Pair{__shfl_xor_sync(0xffffffffu, d.h, o), __shfl_xor_sync(0xffffffffu, d.l, o)};
+        if (d.h > best.h || (d.h == best.h && d.l > best.l)) best = d;
+      }
+      if (l == 0 && i < m) M.exact[i] = place >= 0 ? (double)best.h + (double)best.l : -INFINITY;
     }
     __syncthreads();
-    const unsigned long long k64 =
-        kth_largest<double, unsigned long long>(M.exact, m, need, &above, S);
-    // those above the need-th, then those equal to it from the lowest index on
-    int equal = 0;
-    for (int base = 0; base < m; base += kSelThreads) {
-      const int i = base + tid;
-      const unsigned long long x = i < m ? key_of(M.exact[i]) : 0;
-      int tot;
-      const int at = equal + block_rank(i < m && x == k64, &tot, S);
-      if (i < m && (x > k64 || (x == k64 && at < need - above))) M.flag[M.list[i]] = 1;
-      equal += tot;
+    if (m <= kSelThreads) {  // a thread an entry counts those before it
+      if (tid < m) {
+        const double x = M.exact[tid] + 0.0;
+        int before = 0;
+        for (int i = 0; i < m; ++i) before += M.exact[i] > x || (M.exact[i] == x && i < tid);
+        if (before < need) M.flag[M.list[tid]] = 1;
+      }
+    } else {
+      const unsigned long long k64 = kth_largest<unsigned long long, 64>(
+          m, need, &above, S, [&](int i) { return key_of(M.exact[i]); });
+      // those above the need-th, then those equal to it from the lowest index on
+      int equal = 0;
+      for (int base = 0; base < m; base += kSelThreads) {
+        const int i = base + tid;
+        const unsigned long long x = i < m ? key_of(M.exact[i]) : 0;
+        int tot;
+        const int at = equal + block_rank(i < m && x == k64, &tot, S);
+        if (i < m && (x > k64 || (x == k64 && at < need - above))) M.flag[M.list[i]] = 1;
+        equal += tot;
+      }
     }
   }
   __syncthreads();
@@ -357,10 +428,12 @@ __global__ void __launch_bounds__(kSelThreads)
 }
 
 // CTAs per (sequence, KV head): one per 128 groups (a tile for each warp), at
-// most 8, as long as the whole grid stays within four CTAs an SM.
+// most 8, as long as the whole grid stays within a CTA an SM (four sequences
+// of 8 KV heads and 1,022 groups: clusters of 4, 8.2 us; of 8, more CTAs than fit
+// beside a call before, 9.6 us).
 int cluster_size(const qs_cache &c, int sms) {
   int n = 1;
-  while (n < 8 && n * kSelWarps * kTile < c.cap_groups && (long long)c.B * c.H * n * 2 <= 4ll * sms) n *= 2;
+  while (n < 8 && n * kSelWarps * kTile < c.cap_groups && (long long)c.B * c.H * n * 2 <= sms) n *= 2;
   return n;
 }
 

@@ -437,8 +437,8 @@ qs_status qs_attn_decode_paged(const qs_cache *c, const qs_pages *pg, qs_mode mo
  * The score of a group is the largest, over the head's query rows, of
  *   sum_d max(q_d z_d, q_d (z_d + 255 s_d)),
  * z_d and s_d being the group's key zero and scale of channel d: no key of the
- * group scores above it (before the softmax scale).  The order is that of the
- * exact sums (close ones are summed in fp64), ties go to the lower index.  The
+ * group scores above it (before the softmax scale).  Close scores are summed to
+ * about 46 bits before they are compared, equal ones go to the lower index.  The
  * selection depends on the quantized groups only, not on the buffer; one
  * selection may serve several draft steps.  With n_groups <= k_sel the scores
  * are not formed.  A group whose page is out of range scores below every other
