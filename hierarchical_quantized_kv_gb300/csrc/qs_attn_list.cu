@@ -10,28 +10,41 @@ using namespace qs;
 
 namespace {
 
-// CTAs that share a segment in the clustered kernel; 1: the split kernel.
-// The clustered kernel starts and ends about 7 us sooner (verify: 11 us), but
-// gives every segment as many CTAs as every other and leaves some of the SMs
-// idle (sizes are powers of two).  So it is for segments of equal length, one
-// sequence or selections, where the longer share of a CTA costs less than
-// that: measured, 0.36 us a unit for a draft and 0.6 us for a verify pass, for
-// every eight query rows.  Split against clustered, in us:
-//   one sequence, 32 heads, 32 selected groups, draft      18.0   12.7
-//   one sequence, 32 heads, 32k tokens, draft / verify     37.9 / 56.0   33.9 / 51.9
-//   one sequence, 8 KV heads of 4, 32k tokens, draft       21.5   20.9
-//   one sequence, 8 KV heads of 4, 128k tokens, draft      37.6   54.8 (not taken)
-int cluster_size(const Params &prm, qs_mode mode) {
+// Clustered kernel: prm.C CTAs to a cluster, prm.K clusters to a segment; C = 1:
+// the split kernel.  The clustered kernel starts and ends about 7 us sooner
+// (verify: 11 us), but gives every segment as many CTAs as every other and
+// leaves some of the SMs idle.  So it is for segments of equal length, one
+// sequence or selections, where the longer share of a CTA costs less than that:
+// measured, 0.36 us a unit for a draft and 0.6 us for a verify pass, for every
+// eight query rows; more clusters cost a segment another 2 us at its end.  All
+// clusters have to be resident at once (this GPU: 76 of 2, 36 of 4, 15 of 8 CTAs;
+// sixteen of 8, in two waves, took 29.7 us where thirty-two of 4 take 18.6).
+qs_status choose_clusters(Params &prm, qs_mode mode) {
   const long long segs = (long long)prm.c.B * prm.c.H;
-  if (prm.c.B > 1 && !prm.sel) return 1;
-  int n = 1;
-  while (n < kMaxCluster && segs * n * 2 <= prm.P) n *= 2;
-  if (n == 1) return 1;
+  const int sms = prm.P;
+  prm.C = prm.K = 1;
+  if (prm.c.B > 1 && !prm.sel) return QS_OK;
+  int grid = 0;
+  const int *resident = nullptr;
+  const qs_status s = grid_size<kClustered>(mode, packed_rows(mode, prm.R), prm.c.upper_bits, prm.ncg,
+                                            grid, &resident);
+  if (s != QS_OK) return s;
   const long long groups = prm.sel && prm.k_sel < prm.c.cap_groups ? prm.k_sel : prm.c.cap_groups;
   const double units = groups + (mode == QS_DRAFT_UPPER4 ? 8 : 4);  // (and a full buffer)
-  const double extra = units / n - units * segs / prm.P;
   const double unit_us = (mode == QS_DRAFT_UPPER4 ? 0.36 : 0.6) * prm.ncg;
-  return extra * unit_us < (mode == QS_DRAFT_UPPER4 ? 7.0 : 11.0) ? n : 1;
+  double best = units * segs / sms * unit_us + (mode == QS_DRAFT_UPPER4 ? 7.0 : 11.0);
+  for (int n = kMaxCluster; n >= 2; n /= 2) {
+    const int k_max = (int)(resident[n] / segs);
+    for (int k = 1; k <= k_max && k <= 16; ++k) {
+      const double us = units / (n * k) * unit_us + (k > 1 ? 2.0 : 0.0);
+      if (us < best) {
+        best = us;
+        prm.C = n;
+        prm.K = k;
+      }
+    }
+  }
+  return QS_OK;
 }
 
 qs_status decode_listed(Params &prm, qs_mode mode, const uint16_t *k_new, const uint16_t *v_new,
@@ -46,17 +59,14 @@ qs_status decode_listed(Params &prm, qs_mode mode, const uint16_t *k_new, const 
   prm.k_new = k_new;
   prm.v_new = v_new;
   prm.n_new = n_new;
-  const qs_status s = fill_params<kListed>(prm, mode, q, n_q, group, softmax_scale, out, lse,
+  qs_status s = fill_params<kListed>(prm, mode, q, n_q, group, softmax_scale, out, lse,
                                            workspace, workspace_bytes);
   if (s != QS_OK) return s;
   const bool packed = packed_rows(mode, prm.R);
   cudaStream_t st = (cudaStream_t)stream;
-  prm.C = cluster_size(prm, mode);
+  if ((s = choose_clusters(prm, mode)) != QS_OK) return s;
   if (prm.C < 2) return launch_kind<kListed>(mode, packed, prm, st);
-  const int grid = prm.c.B * prm.c.H * prm.C;
-  const qs_status g = grid_size<kClustered>(mode, packed, prm.c.upper_bits, prm.ncg, prm.P);
-  if (g != QS_OK) return g;
-  prm.P = grid;
+  prm.P = prm.c.B * prm.c.H * prm.K * prm.C;
   return launch_kind<kClustered>(mode, packed, prm, st);
 }
 

@@ -20,26 +20,30 @@ namespace {
 
 constexpr int kParts = 4;           // CTAs per (head, sequence)
 constexpr int kSlice = kD / kParts;  // key channels / value tokens per CTA
-// Warps per CTA: a flush is one wave of small CTAs, so its time is one
-// CTA's chain of phases, and sixteen warps halve the per-thread work of
-// every phase but the packing (flush 14 -> 11.5 µs); a prefill is many
-// waves, where eight warps keep more CTAs resident (379 against 426 µs).
-constexpr int kFlushWarps = 16, kPrefillWarps = 8;
-// Group quarters per quantizing CTA of a prefill, loads pipelined one ahead.
-#ifndef QS_PREFILL_QUARTERS
-#define QS_PREFILL_QUARTERS 8
-#endif
-constexpr int kPrefillQuarters = QS_PREFILL_QUARTERS;
+// Warps per CTA.  A flush is one wave of small CTAs, so its time is one CTA's
+// chain of phases, and sixteen warps halve the per-thread work of every phase
+// but the packing.  A prefill of many waves is bound by instruction issue, and
+// what a thread does once per quarter (addresses, scales) counts: four warps,
+// twice the elements a thread, 168 us for 32 heads of 32k tokens (eight: 175;
+// 0.71 of the copy bandwidth's time).  A prompt of one quarter per CTA is a
+// chain again: eight warps (two heads of 1k tokens: 5.3 us; four: 7.6).
+constexpr int kFlushWarps = 16, kPrefillWarps = 4, kShortPrefillWarps = 8;
+// Group quarters per quantizing CTA of a prefill, loads pipelined one ahead, at
+// most.
+constexpr int kPrefillQuarters = 8;
 
 // One CTA owns key channels [32p, 32p+32) (one 16-byte column of every key
 // row) and value tokens [32p, 32p+32) (value quarter p).
+// Value codes in shared memory: rows of 144 bytes, so that the four token
+// pairs a group of lanes reads fall into different banks.
+constexpr int kCodeRow = kD + 16;
 template <int QW>
 struct FlushSmem {
-  __half k[kG][kSlice];     // keys of the slice   [token][channel - 32p]
-  __half v[kSlice][kD];     // values of the slice [token - 32p][channel]
-  uint8_t kc[kG][kSlice];   // key codes
-  uint8_t vc[kSlice][kD];   // value codes
-  float kmin[QW][kSlice], kmax[QW][kSlice];
+  __half k[kG][kSlice];          // keys of the slice   [token][channel - 32p]
+  __half v[kSlice][kD];          // values of the slice [token - 32p][channel]
+  uint8_t vc[kSlice][kCodeRow];  // value codes
+  float kzf[kSlice], krf[kSlice];  // key zero, reciprocal of the key scale
+  uint32_t kmin[QW][kSlice / 2], kmax[QW][kSlice / 2];  // half2 per channel pair
   uint16_t ks[kSlice], kz[kSlice], vs[kSlice], vz[kSlice];
   int act, base, g;
 };
@@ -57,54 +61,74 @@ __device__ __forceinline__ void scale_zero(float mn, float mx, uint16_t &s_bits,
 }
 
 // q = clamp(rne(fl((x - z) / s)), 0, 255) with fl the IEEE fp32 quotient, as
-// QS-RN-v1 defines it, without a divide per element: rf = fl(1 / s) is exact
-// to 2^-24, so u' = fl((x - z) * rf) is within 2^-14 of fl((x - z) / s) for
-// every |u| < 256 (u <= 255 (1 + 2^-23) since s >= r / 255).  Both round to
-// the same integer unless u' lies within 2^-12 of a half-integer; there the
-// exact quotient decides (about one element in 2^11).  Four elements at a
-// time, with one warp vote: the exact quotient is computed only when some
-// lane of the warp has an element that close to a tie, and then only for
-// those elements.  Rounding, clamping to [0, 255] and conversion are one
-// saturating conversion.  A zero scale gives code 0 (then rf is +inf and a
-// is 0 or positive: the code is forced).  Called by whole warps.
-__device__ __forceinline__ void codes4(const float (&x)[4], const float (&zf)[4],
-                                       const float (&sf)[4], const float (&rf)[4],
-                                       uint32_t (&q)[4]) {
-  float a[4], ue[4];
-  bool near[4], any = false;
+// QS-RN-v1 defines it, without a divide per element: a = fl(x - z) is never
+// negative (z is the group's minimum), rf = fl(1 / s) is exact to 2^-24, so
+// the exact product a rf is within 2^-15 of fl(a / s) (which is at most 255 (1 +
+// 2^-23), since s >= r / 255).  Adding 1.5 * 2^23 in one fused multiply-add
+// rounds it to the nearest even integer n, which then stands in the low byte of
+// the sum; a second one gives the remainder a rf - n.  The two quotients round
+// alike unless that lies within 2^-12 of a half; there the exact quotient
+// decides (about one element in 2^11).  A zero scale means a zero range: a = 0,
+// and rf is taken as 0, which gives code 0.
+constexpr float kRound = 12582912.f;  // 1.5 * 2^23
+constexpr float kNear = 0.5f - 0x1p-12f;
+
+__device__ __forceinline__ float reciprocal(float sf) { return sf == 0.f ? 0.f : __frcp_rn(sf); }
+
+// Codes of eight values (four half2), one low byte each of t.
+template <typename Scale>  // scale of value i
+__device__ __forceinline__ void codes8(const uint32_t (&x)[4], const float (&zf)[8],
+                                       const float (&rf)[8], Scale scale, uint32_t (&t)[8]) {
+  float a[8], d[8], far = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    a[i] = __fsub_rn(x[i], zf[i]);
-    ue[i] = __fmul_rn(a[i], rf[i]);
-    near[i] = fabsf(__fsub_rn(ue[i], rintf(ue[i]))) > 0.5f - 0x1p-12f;
-    any |= near[i];
-  }
-  if (__any_sync(0xffffffffu, any)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (near[i]) ue[i] = __fdiv_rn(a[i], sf[i]);
+    const float2 f = __half22float2(u32_as_h2(x[i]));
+    a[2 * i] = __fsub_rn(f.x, zf[2 * i]);
+    a[2 * i + 1] = __fsub_rn(f.y, zf[2 * i + 1]);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t v;
-    asm("cvt.rni.sat.u8.f32 %0, %1;" : "=r"(v) : "f"(ue[i]));
-    q[i] = sf[i] == 0.0f ? 0u : v;
+  for (int i = 0; i < 8; ++i) {
+    const float n = __fmaf_rn(a[i], rf[i], kRound);
+    d[i] = __fmaf_rn(a[i], rf[i], -__fsub_rn(n, kRound));
+    far = fmaxf(far, fabsf(d[i]));
+    t[i] = __float_as_uint(n);
+  }
+  if (far > kNear) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (fabsf(d[i]) > kNear) t[i] = __float_as_uint(__fadd_rn(__fdiv_rn(a[i], scale(i)), kRound));
   }
 }
 
-// Two 4-bit planes' bytes from four 8-bit codes per word: words a and b hold
-// codes 4k..4k+3 and 4k+4..4k+7 (channel pairs 2k, 2k+1, 2k+2, 2k+3); the
-// result's byte i holds pair i's two nibbles (the first code's in the low
-// nibble): upper nibbles (hi) or lower nibbles (lo) of the codes.
-__device__ __forceinline__ uint32_t pair_nibbles(uint32_t a, uint32_t b, bool hi) {
-  const uint32_t na = (hi ? a >> 4 : a) & 0x0F0F0F0Fu, nb = (hi ? b >> 4 : b) & 0x0F0F0F0Fu;
-  // byte 0 of (n | n >> 4): nibble of byte 0, then of byte 1; byte 2: of bytes 2, 3
-  return prmt(na | (na >> 4), nb | (nb >> 4), 0x6420);
+// Low bytes of four words, in order.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return prmt(prmt(a, b, 0x0040), prmt(c, d, 0x0040), 0x5410);
 }
 
-// Token held by nibble position p of a 16-byte value row (quarter layout).
-__device__ __forceinline__ int vperm(int p) {
-  return 16 * ((p >> 1) & 1) + 8 * (p & 1) + 2 * (p >> 3) + ((p >> 2) & 1);
+// Eight codes' nibble words: ev holds codes 0, 2, 4, 6 and od 1, 3, 5, 7, a byte
+// each; nibble j of the result belongs to code j.
+__device__ __forceinline__ uint32_t upper_nibbles(uint32_t ev, uint32_t od) {
+  return bitsel(ev >> 4, od, 0x0F0F0F0Fu);
+}
+__device__ __forceinline__ uint32_t lower_nibbles(uint32_t ev, uint32_t od) {
+  return bitsel(ev, od << 4, 0x0F0F0F0Fu);
+}
+
+// Word W of a group's upper plane.  Two-bit draft layout: nibble j of word k of
+// the C_U2 plane (first 4 KB of the group's 8 KB) holds the two-bit field (C_U =
+// 4 C_U2 + M2) of word 2k's nibble j in its low half and of word 2k+1's in its
+// high half, and word k of the M2 plane (second 4 KB) the same of M2; the lanes
+// of words 2k and 2k + 1 are neighbours (W and lane have the same parity, the
+// whole warp calls), the even one writes the C_U2 word, the odd one the M2 word.
+__device__ __forceinline__ void store_upper(uint8_t *base, int W, uint32_t w, bool two_bit) {
+  if (!two_bit) {
+    *reinterpret_cast<uint32_t *>(base + 4 * W) = w;
+    return;
+  }
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 1);
+  const uint32_t v = (W & 1) ? ((other & 0x33333333u) | ((w & 0x33333333u) << 2))
+                             : (((w >> 2) & 0x33333333u) | (other & 0xCCCCCCCCu));
+  *reinterpret_cast<uint32_t *>(base + (W & 1 ? kG * kD / 4 : 0) + 4 * (W >> 1)) = v;
 }
 
 // Position of channel c in a key scale / zero row (inverse of the header's
@@ -118,23 +142,6 @@ __device__ __forceinline__ int kmeta_pos(int c) {
 // p -> 32(p>>5) + ((p>>2)&7) + 16((p>>1)&1) + 8(p&1)).
 __device__ __forceinline__ int vmeta_pos(int t) {
   return ((t >> 3) & 1) | (((t >> 4) & 1) << 1) | ((t & 7) << 2) | ((t >> 5) << 5);
-}
-
-// Two-bit draft layout: four consecutive 32-bit words w[0..3] of a 4-bit
-// upper plane (nibble C_U = 4 C_U2 + M2) become two words of the group's
-// C_U2 plane and two of its M2 plane (second 4 KB of the group's 8 KB).
-// Word k of each holds, in nibble position j, the two-bit field of word 2k's
-// nibble j in bits 4j..4j+1 and of word 2k+1's nibble j in bits 4j+2..4j+3.
-// base: the group's upper plane; off: byte offset of w[0] in the 4-bit plane
-// (a multiple of 16), so the two words go to off / 2.
-__device__ __forceinline__ void store_upper2(uint8_t *base, size_t off, const uint32_t (&w)[4]) {
-  uint2 u, m;
-  u.x = ((w[0] >> 2) & 0x33333333u) | (w[1] & 0xCCCCCCCCu);
-  u.y = ((w[2] >> 2) & 0x33333333u) | (w[3] & 0xCCCCCCCCu);
-  m.x = (w[0] & 0x33333333u) | ((w[1] & 0x33333333u) << 2);
-  m.y = (w[2] & 0x33333333u) | ((w[3] & 0x33333333u) << 2);
-  *reinterpret_cast<uint2 *>(base + off / 2) = u;
-  *reinterpret_cast<uint2 *>(base + (size_t)kG * kD / 4 + off / 2) = m;
 }
 
 // Asynchronous 16-byte copy global -> shared through the load/store path
@@ -178,122 +185,158 @@ __device__ __forceinline__ void load_part(__half (*kt)[kSlice], __half (*vt)[kD]
   if (ASYNC) cp_async_commit();
 }
 
+__device__ __forceinline__ uint32_t hmin2_u32(uint32_t a, uint32_t b) {
+  return h2_as_u32(__hmin2(u32_as_h2(a), u32_as_h2(b)));
+}
+__device__ __forceinline__ uint32_t hmax2_u32(uint32_t a, uint32_t b) {
+  return h2_as_u32(__hmax2(u32_as_h2(a), u32_as_h2(b)));
+}
+__device__ __forceinline__ float half_bits_to_float(uint32_t b) {
+  return __half2float(__ushort_as_half((uint16_t)b));
+}
+
 // Phases 2-7 of a group quarter whose rows are in kt / vt (all loads landed
-// and visible to the CTA).
+// and visible to the CTA).  Bound by instruction issue, so every phase works
+// on as much as a load brings: minima and maxima on pairs of fp16 values
+// (exact), eight codes a thread at a time, planes assembled from words of even
+// and of odd codes by one shift and one bit select each.
 template <int QW>
 __device__ void quantize_loaded(FlushSmem<QW> &S, const __half (*kt)[kSlice],
                                 const __half (*vt)[kD], const qs_cache &c, size_t grp, int part,
                                 int tid) {
   constexpr int kQWarps = QW, kQThreads = 32 * QW;
   const int warp = tid >> 5, lane = tid & 31;
+  const bool two_bit = c.upper_bits == 2;
 
-  // 2. keys: min / max per channel, warp w over tokens kG/kQWarps w onwards
+  // 2. keys: min / max per channel pair.  Thread = pair tid % 16 of every second
+  // token of a run (the two halves of a warp read neighbouring rows).
   {
-    constexpr int kTw = kG / kQWarps;
-    float mn = INFINITY, mx = -INFINITY;
-    for (int t = kTw * warp; t < kTw * warp + kTw; ++t) {
-      const float x = __half2float(kt[t][lane]);
-      mn = fminf(mn, x);
-      mx = fmaxf(mx, x);
+    constexpr int kTs = 16 * kG / kQThreads;  // tokens per thread
+    const int slot = tid >> 4, t0 = 2 * kTs * (slot >> 1) + (slot & 1);
+    uint32_t mn = 0x7C007C00u, mx = 0xFC00FC00u;  // +inf, -inf
+#pragma unroll
+    for (int i = 0; i < kTs; ++i) {
+      const uint32_t x = *reinterpret_cast<const uint32_t *>(&kt[t0 + 2 * i][2 * (tid & 15)]);
+      mn = hmin2_u32(mn, x);
+      mx = hmax2_u32(mx, x);
     }
-    S.kmin[warp][lane] = mn;
-    S.kmax[warp][lane] = mx;
-  }
-  // 3. values: one warp per token, min / max over the 128 channels, codes
-  for (int t = warp; t < kSlice; t += kQWarps) {
-    const __half2 *row = reinterpret_cast<const __half2 *>(&vt[t][4 * lane]);
-    const float2 a = __half22float2(row[0]), bb = __half22float2(row[1]);
-    float mn = fminf(fminf(a.x, a.y), fminf(bb.x, bb.y));
-    float mx = fmaxf(fmaxf(a.x, a.y), fmaxf(bb.x, bb.y));
-    for (int o = 16; o > 0; o >>= 1) {
-      mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mn = hmin2_u32(mn, __shfl_xor_sync(0xffffffffu, mn, 16));
+    mx = hmax2_u32(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+    if (lane < 16) {
+      S.kmin[warp][lane] = mn;
+      S.kmax[warp][lane] = mx;
     }
-    uint16_t sb, zb;
-    float sf, zf;
-    scale_zero(mn, mx, sb, zb, sf, zf);
-    if (lane == 0) {
-      S.vs[t] = sb;
-      S.vz[t] = zb;
-    }
-    const float rf = __frcp_rn(sf);
-    uint32_t q[4];
-    codes4({a.x, a.y, bb.x, bb.y}, {zf, zf, zf, zf}, {sf, sf, sf, sf}, {rf, rf, rf, rf}, q);
-    *reinterpret_cast<uint32_t *>(&S.vc[t][4 * lane]) = q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24);
   }
   __syncthreads();
   if (tid < kSlice) {
-    float mn = S.kmin[0][tid], mx = S.kmax[0][tid];
+    // 3. keys: scale and zero of the channel slice
+    const int sh = 16 * (tid & 1);
+    uint32_t mn = S.kmin[0][tid >> 1], mx = S.kmax[0][tid >> 1];
+#pragma unroll
     for (int w = 1; w < kQWarps; ++w) {
-      mn = fminf(mn, S.kmin[w][tid]);
-      mx = fmaxf(mx, S.kmax[w][tid]);
+      mn = hmin2_u32(mn, S.kmin[w][tid >> 1]);
+      mx = hmax2_u32(mx, S.kmax[w][tid >> 1]);
     }
     uint16_t sb, zb;
     float sf, zf;
-    scale_zero(mn, mx, sb, zb, sf, zf);
+    scale_zero(half_bits_to_float(mn >> sh), half_bits_to_float(mx >> sh), sb, zb, sf, zf);
     S.ks[tid] = sb;
     S.kz[tid] = zb;
+    S.kzf[tid] = zf;
+    S.krf[tid] = reciprocal(sf);
   }
-  __syncthreads();
-
-  // 4. key codes: thread = channel pair j (16 pairs) x kTc tokens
+  // 4. values: kLt threads a token, each kCh runs of eight channels; min / max
+  // (as the pair min, -max, one shuffle for both), scale, codes
   {
-    constexpr int kTc = kG * 16 / kQThreads;
-    const int j = tid & 15, t0 = (tid >> 4) * kTc;
-    const float s0 = __half2float(__ushort_as_half(S.ks[2 * j]));
-    const float s1 = __half2float(__ushort_as_half(S.ks[2 * j + 1]));
-    const float z0 = __half2float(__ushort_as_half(S.kz[2 * j]));
-    const float z1 = __half2float(__ushort_as_half(S.kz[2 * j + 1]));
-    const float r0 = __frcp_rn(s0), r1 = __frcp_rn(s1);
-    static_assert(kTc % 2 == 0, "two tokens per step");
+    constexpr int kLt = kQThreads / kSlice, kCh = kD / 8 / kLt;
+    static_assert(kLt >= 4 && kLt <= 16 && kCh >= 1, "128 to 512 threads");
+    const int t = tid / kLt, lt = tid % kLt;
+    // run i of a thread: with four threads a token, odd tokens take the runs of
+    // a pair the other way round (two rows of 64 bytes otherwise meet in one
+    // half of the banks)
+    auto run = [&](int i) { return 8 * (lt + kLt * (kLt == 4 ? i ^ (t & 1) : i)); };
+    uint4 x[kCh];
+    uint32_t mn = 0x7C007C00u, mx = 0xFC00FC00u;
 #pragma unroll
-    for (int t = t0; t < t0 + kTc; t += 2) {
-      const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&kt[t][2 * j]));
-      const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&kt[t + 1][2 * j]));
-      uint32_t q[4];
-      codes4({x.x, x.y, y.x, y.y}, {z0, z1, z0, z1}, {s0, s1, s0, s1}, {r0, r1, r0, r1}, q);
-      *reinterpret_cast<uint16_t *>(&S.kc[t][2 * j]) = (uint16_t)(q[0] | (q[1] << 8));
-      *reinterpret_cast<uint16_t *>(&S.kc[t + 1][2 * j]) = (uint16_t)(q[2] | (q[3] << 8));
+    for (int i = 0; i < kCh; ++i) {
+      x[i] = *reinterpret_cast<const uint4 *>(&vt[t][run(i)]);
+      mn = hmin2_u32(hmin2_u32(mn, hmin2_u32(x[i].x, x[i].y)), hmin2_u32(x[i].z, x[i].w));
+      mx = hmax2_u32(hmax2_u32(mx, hmax2_u32(x[i].x, x[i].y)), hmax2_u32(x[i].z, x[i].w));
+    }
+    uint32_t mm = prmt(hmin2_u32(mn, prmt(mn, 0, 0x1032)), hmax2_u32(mx, prmt(mx, 0, 0x1032)) ^ 0x80008000u,
+                       0x5410);
+#pragma unroll
+    for (int o = 1; o < kLt; o <<= 1) mm = hmin2_u32(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    uint16_t sb, zb;
+    float sf, zf;
+    scale_zero(half_bits_to_float(mm & 0xFFFFu), -half_bits_to_float(mm >> 16), sb, zb, sf, zf);
+    if (lt == 0) {
+      S.vs[t] = sb;
+      S.vz[t] = zb;
+    }
+    const float rf = reciprocal(sf);
+    const float zs[8] = {zf, zf, zf, zf, zf, zf, zf, zf}, rs[8] = {rf, rf, rf, rf, rf, rf, rf, rf};
+#pragma unroll
+    for (int i = 0; i < kCh; ++i) {
+      uint32_t q[8];
+      codes8({x[i].x, x[i].y, x[i].z, x[i].w}, zs, rs, [&](int) { return sf; }, q);
+      *reinterpret_cast<uint2 *>(&S.vc[t][run(i)]) =
+          make_uint2(low_bytes(q[0], q[1], q[2], q[3]), low_bytes(q[4], q[5], q[6], q[7]));
     }
   }
   __syncthreads();
 
-  if (tid < kG) {
-    // 5. key planes: bytes [16p, 16p+16) of token row tid (channels 2i, 2i+1)
-    // the row's 32 codes in two 16-byte loads; word m of a plane row holds
-    // channel pairs 4m..4m+3 (codes 8m..8m+7)
-    const uint4 ra = *reinterpret_cast<const uint4 *>(&S.kc[tid][0]);
-    const uint4 rb = *reinterpret_cast<const uint4 *>(&S.kc[tid][16]);
-    const uint32_t cw[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
-    uint32_t wu[4], wl[4];
+  if (tid >= kQThreads - kD) {
+    // 5. value planes, by the last four warps: thread = word m (eight tokens of
+    // the quarter) of four channels; nibble j of the word belongs to token
+    // 2 m + j / 4 + 8 (j & 1) + 16 (j / 2 & 1)
+    const int i = tid - (kQThreads - kD), m = i & 3, d0 = 4 * (i >> 2);
+    uint32_t x[8];
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      wu[m] = pair_nibbles(cw[2 * m], cw[2 * m + 1], true);
-      wl[m] = pair_nibbles(cw[2 * m], cw[2 * m + 1], false);
-    }
-    if (c.upper_bits == 2)
-      store_upper2(c.k_upper + grp * kG * (kD / 2), 16 * (4 * tid + part), wu);
-    else
-      reinterpret_cast<uint4 *>(c.k_upper + (grp * kG + tid) * (kD / 2))[part] =
-          make_uint4(wu[0], wu[1], wu[2], wu[3]);
-    reinterpret_cast<uint4 *>(c.k_lower + (grp * kG + tid) * (kD / 2))[part] =
-        make_uint4(wl[0], wl[1], wl[2], wl[3]);
-  } else if (tid < kG + kD) {
-    // 6. value quarter p: row d = 16 bytes, nibble position q holds token vperm(q)
-    const int d = tid - kG;
-    uint32_t wu[4] = {0, 0, 0, 0}, wl[4] = {0, 0, 0, 0};
+    for (int j = 0; j < 8; ++j)
+      x[j] = *reinterpret_cast<const uint32_t *>(
+          &S.vc[2 * m + (j >> 2) + 8 * (j & 1) + 16 * ((j >> 1) & 1)][d0]);
+    // bytes of four rows (even or odd j) to a word per channel
+    uint32_t wrd[2][4];
 #pragma unroll
-    for (int q = 0; q < 32; ++q) {
-      const uint32_t code = S.vc[vperm(q)][d];
-      wu[q >> 3] |= (code >> 4) << (4 * (q & 7));
-      wl[q >> 3] |= (code & 15u) << (4 * (q & 7));
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t a = prmt(x[e], x[2 + e], 0x5140), b = prmt(x[4 + e], x[6 + e], 0x5140);
+      const uint32_t f = prmt(x[e], x[2 + e], 0x7362), g = prmt(x[4 + e], x[6 + e], 0x7362);
+      wrd[e][0] = prmt(a, b, 0x5410);
+      wrd[e][1] = prmt(a, b, 0x7632);
+      wrd[e][2] = prmt(f, g, 0x5410);
+      wrd[e][3] = prmt(f, g, 0x7632);
     }
-    const size_t row = (grp * 4 + part) * kD + d;
-    if (c.upper_bits == 2)
-      store_upper2(c.v_upper + grp * kG * (kD / 2), 16 * (part * kD + d), wu);
-    else
-      reinterpret_cast<uint4 *>(c.v_upper)[row] = make_uint4(wu[0], wu[1], wu[2], wu[3]);
-    reinterpret_cast<uint4 *>(c.v_lower)[row] = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const int W = 4 * (part * kD + d0 + d) + m;
+      store_upper(c.v_upper + grp * kG * (kD / 2), W, upper_nibbles(wrd[0][d], wrd[1][d]), two_bit);
+      *reinterpret_cast<uint32_t *>(c.v_lower + grp * kG * (kD / 2) + 4 * W) =
+          lower_nibbles(wrd[0][d], wrd[1][d]);
+    }
+  }
+  // 6. key codes and planes: thread = eight channels of a token (one word of
+  // each plane), the same channels in every step
+  {
+    const int o = tid & 3;
+    float zf[8], rf[8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 z4 = *reinterpret_cast<const float4 *>(&S.kzf[8 * o + 4 * i]);
+      const float4 r4 = *reinterpret_cast<const float4 *>(&S.krf[8 * o + 4 * i]);
+      zf[4 * i] = z4.x; zf[4 * i + 1] = z4.y; zf[4 * i + 2] = z4.z; zf[4 * i + 3] = z4.w;
+      rf[4 * i] = r4.x; rf[4 * i + 1] = r4.y; rf[4 * i + 2] = r4.z; rf[4 * i + 3] = r4.w;
+    }
+#pragma unroll
+    for (int t = tid >> 2; t < kG; t += kQThreads / 4) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(&kt[t][8 * o]);
+      uint32_t q[8];
+      codes8({x.x, x.y, x.z, x.w}, zf, rf, [&](int i) { return half_bits_to_float(S.ks[8 * o + i]); }, q);
+      const uint32_t ev = low_bytes(q[0], q[2], q[4], q[6]), od = low_bytes(q[1], q[3], q[5], q[7]);
+      const int W = 16 * t + 4 * part + o;
+      store_upper(c.k_upper + grp * kG * (kD / 2), W, upper_nibbles(ev, od), two_bit);
+      *reinterpret_cast<uint32_t *>(c.k_lower + grp * kG * (kD / 2) + 4 * W) = lower_nibbles(ev, od);
+    }
   }
   // 7. metadata: key scale / zero of the channel slice, value scale / zero of the quarter
   if (tid < kSlice) {
@@ -384,18 +427,18 @@ __global__ void __launch_bounds__(32 * kFlushWarps)
 
 // Bulk prefill of empty caches from a prompt (k, v: fp16 [B][H][T][D]).
 // Grid (nq + 2, H, B): block x < nq quantizes group quarters [x Q, x Q + Q)
-// of the sequence's head (quarter i: part i % 4 of group i / 4; Q =
-// kPrefillQuarters), the next quarter's rows copied into the second buffer
+// of the sequence's head (quarter i: part i % 4 of group i / 4; Q = quarters), the next quarter's rows copied into the second buffer
 // while the current one is quantized; the last two blocks copy buffer halves
 // 0 and 1.  The CTA that arrives last on the sequence's ticket writes the
 // counters, so every CTA reads the old (empty) ones first.
-__global__ void __launch_bounds__(32 * kPrefillWarps) prefill_kernel(qs_cache c, Pages pg,
-                                                     const uint16_t *__restrict__ k,
-                                                     const uint16_t *__restrict__ v, int T,
-                                                     const int32_t *__restrict__ len, int nq) {
+template <int QW>
+__global__ void __launch_bounds__(32 * QW, 20 / QW)
+    prefill_kernel(qs_cache c, Pages pg, const uint16_t *__restrict__ k,
+                   const uint16_t *__restrict__ v, int T, const int32_t *__restrict__ len, int nq,
+                   int quarters) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  PrefillSmem<kPrefillWarps> &PS = *reinterpret_cast<PrefillSmem<kPrefillWarps> *>(smem_raw);
-  FlushSmem<kPrefillWarps> &S = PS.f;
+  PrefillSmem<QW> &PS = *reinterpret_cast<PrefillSmem<QW> *>(smem_raw);
+  FlushSmem<QW> &S = PS.f;
   const int x = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   pdl_trigger();
   pdl_wait();
@@ -426,7 +469,7 @@ __global__ void __launch_bounds__(32 * kPrefillWarps) prefill_kernel(qs_cache c,
     // every page the prompt needs, looked at by every CTA alike: a bad one
     // leaves the whole sequence unchanged
     int bad = 0;
-    for (int g = tid; g < ng; g += 32 * kPrefillWarps) bad |= group_slot(c, pg, b, h, g) < 0;
+    for (int g = tid; g < ng; g += 32 * QW) bad |= group_slot(c, pg, b, h, g) < 0;
     if (__syncthreads_or(bad)) {
       if (h == 0 && x == 0 && tid == 0) atomicOr(&st[QS_ST_ERR], QS_DEV_PAGE);
       return;
@@ -435,42 +478,29 @@ __global__ void __launch_bounds__(32 * kPrefillWarps) prefill_kernel(qs_cache c,
   const size_t bh = (size_t)b * c.H + h;
   const uint16_t *kp = k + bh * T * kD, *vp = v + bh * T * kD;
   if (x < nq) {
-    const int q0 = x * kPrefillQuarters, q1 = min(q0 + kPrefillQuarters, 4 * ng);
+    const int q0 = x * quarters, q1 = min(q0 + quarters, 4 * ng);
     const __half *kh = reinterpret_cast<const __half *>(kp), *vh = reinterpret_cast<const __half *>(vp);
-    // the rows of quarter i go to buffer i % 2 (one commit group per quarter:
-    // a quarter whose rows fail the checked build's range check commits an
-    // empty one, so the waits below keep counting quarters)
+    // the rows of quarter i go to buffer i % 2 (a quarter whose rows fail the
+    // checked build's range check is not copied)
     auto load = [&](int i) {
       const int g = i >> 2;
-      if (!chk(in_range(((size_t)g + 1) * kG, 0, (size_t)T), 22))
-        cp_async_commit();
-      else if (i & 1)
-        load_part<kPrefillWarps, true>(PS.k1, PS.v1, kh + (size_t)g * kG * kD,
-                                       vh + (size_t)g * kG * kD, i & 3, tid);
-      else
-        load_part<kPrefillWarps, true>(S.k, S.v, kh + (size_t)g * kG * kD,
+      if (chk(in_range(((size_t)g + 1) * kG, 0, (size_t)T), 22))
+        load_part<QW, true>(i & 1 ? PS.k1 : S.k, i & 1 ? PS.v1 : S.v, kh + (size_t)g * kG * kD,
                                        vh + (size_t)g * kG * kD, i & 3, tid);
     };
     if (q0 < q1) load(q0);
     for (int i = q0; i < q1; ++i) {
-      if (i + 1 < q1) {
-        load(i + 1);  // into the buffer quarter i - 1 used (free since the barrier below)
-        cp_async_wait<1>();
-      } else {
-        cp_async_wait<0>();
-      }
-      __syncthreads();  // quarter i's rows, copied by every thread, are visible
+      cp_async_wait<0>();
+      // quarter i's rows, copied by every thread, are visible; the buffer and
+      // the scratch of quarter i - 1 are free
+      __syncthreads();
+      if (i + 1 < q1) load(i + 1);
       const int g = i >> 2;
       const size_t grp = (size_t)group_slot(c, pg, b, h, g);
       // checked build: the group's prompt rows inside the prompt array
       if (chk(in_range(((size_t)g + 1) * kG, 0, (size_t)T), 22) &&
-          chk(in_range(grp, 1, group_slots(c, pg)), 20)) {
-        if (i & 1)
-          quantize_loaded(S, PS.k1, PS.v1, c, grp, i & 3, tid);
-        else
-          quantize_loaded(S, S.k, S.v, c, grp, i & 3, tid);
-      }
-      __syncthreads();  // the buffer and the scratch are free for the next quarters
+          chk(in_range(grp, 1, group_slots(c, pg)), 20))
+        quantize_loaded(S, i & 1 ? PS.k1 : S.k, i & 1 ? PS.v1 : S.v, c, grp, i & 3, tid);
     }
   } else {
     // buffer half x - nq: tokens i in [G half, G half + G) that are < fill
@@ -480,7 +510,7 @@ __global__ void __launch_bounds__(32 * kPrefillWarps) prefill_kernel(qs_cache c,
     uint4 *kd = reinterpret_cast<uint4 *>(c.buf_k + bh * kRing * kD);
     uint4 *vd = reinterpret_cast<uint4 *>(c.buf_v + bh * kRing * kD);
     if (chk(i1 <= kRing && (size_t)ng * kG + i1 <= (size_t)T, 23))
-      for (int e = i0 * (kD / 8) + tid; e < i1 * (kD / 8); e += 32 * kPrefillWarps) {
+      for (int e = i0 * (kD / 8) + tid; e < i1 * (kD / 8); e += 32 * QW) {
         kd[e] = ks[e];
         vd[e] = vs[e];
       }
@@ -500,22 +530,41 @@ __global__ void __launch_bounds__(32 * kPrefillWarps) prefill_kernel(qs_cache c,
 using namespace qs;
 
 namespace {
-int g_flush_ready = 0, g_prefill_ready = 0;  // one bit per device ordinal below 32
+int g_flush_ready = 0;  // one bit per device ordinal below 32
 }  // namespace
 
 namespace {
+
+// Quarters per CTA: 8 for a prompt that fills the GPU several times over; fewer
+// for a short one, whose time is one CTA's chain of quarters (about 3 us each),
+// so that its quarters spread over five CTAs an SM first.
+int prefill_quarters(long long total) {
+  const long long slots = 5 * 152;
+  int q = 1;
+  while (q < kPrefillQuarters && total > slots * q) q *= 2;
+  return q;
+}
+
+template <int QW>
+qs_status launch_prefill(const qs_cache &c, const Pages &pg, const uint16_t *k, const uint16_t *v, int T,
+                         const int32_t *d_len, int gmax, int quarters, qs_stream_t stream) {
+  static int ready = 0;
+  const int smem = (int)sizeof(PrefillSmem<QW>);
+  const qs_status s = set_smem_once((const void *)prefill_kernel<QW>, smem, &ready);
+  if (s != QS_OK) return s;
+  const int nq = (4 * gmax + quarters - 1) / quarters;
+  return launch_pdl(prefill_kernel<QW>, dim3(nq + 2, c.H, c.B), dim3(32 * QW), smem,
+                    (cudaStream_t)stream, c, pg, k, v, T, d_len, nq, quarters);
+}
 
 qs_status prefill(const qs_cache &c, const Pages &pg, const uint16_t *k, const uint16_t *v, int32_t T,
                   const int32_t *d_len, qs_stream_t stream) {
   if (!k || !v || !d_len || T < 0 || T > (1 << 26)) return QS_ERR_ARG;
   if (!aligned16(k) || !aligned16(v)) return QS_ERR_ALIGN;
-  const int smem = (int)sizeof(PrefillSmem<kPrefillWarps>);
-  const qs_status s = set_smem_once((const void *)prefill_kernel, smem, &g_prefill_ready);
-  if (s != QS_OK) return s;
   const int gmax = T > 2 * kG ? (T - 2 * kG + kG - 1) / kG : 0;
-  const int nq = (4 * gmax + kPrefillQuarters - 1) / kPrefillQuarters;
-  return launch_pdl(prefill_kernel, dim3(nq + 2, c.H, c.B), dim3(32 * kPrefillWarps), smem,
-                    (cudaStream_t)stream, c, pg, k, v, (int)T, d_len, nq);
+  const int quarters = prefill_quarters((long long)4 * gmax * c.H * c.B);
+  return quarters == 1 ? launch_prefill<kShortPrefillWarps>(c, pg, k, v, T, d_len, gmax, 1, stream)
+                       : launch_prefill<kPrefillWarps>(c, pg, k, v, T, d_len, gmax, quarters, stream);
 }
 
 qs_status flush(const qs_cache &c, const Pages &pg, const uint8_t *d_mask, int n_next,

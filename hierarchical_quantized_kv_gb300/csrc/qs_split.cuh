@@ -127,7 +127,7 @@ struct Params {
               // position r % n_q)
   int ncg;    // column groups of eight rows, ceil(R / 8): warp w serves group w % ncg
   int P;      // split-kernel grid size (number of contiguous unit ranges)
-  int C;      // clustered variant: CTAs per cluster (P = B * H * C)
+  int C, K;   // clustered variant: CTAs per cluster, clusters per segment (P = B * H * K * C)
   float sl2;  // softmax_scale * log2(e)
   uint64_t wait_ns;  // limit on each pipeline wait (kWaitLimitNs outside tests)
   int no_issue;      // test entry only: issue no copy, so that every wait runs out
@@ -864,14 +864,17 @@ __device__ __forceinline__ void st_cluster4(uint32_t a, float4 v) {
 //   row_m float [24]: the CTA's maxima of the rows
 //   sum   float [C][R][128], then (l, maximum) [C][R]: the CTAs' sums, in the
 //         first CTA
-// all of them in the stages.  keep: the stages must not be written (copies may
+// all of them in the stages.  With K > 1 clusters a segment, each one's first
+// CTA leaves its merged sums in ws (float [K][R][128 + 4]) and counts on
+// arrive; the last to arrive merges those.  keep: the stages must not be written (copies may
 // still land there; the results are invalid then).  Every CTA takes part in
 // any case: the others count on the barriers, and write to the first one's
 // shared memory.
 template <int NW>
 __device__ __forceinline__ void finish_cluster(Softmax &sm, float oscale, bool pk, uint8_t *smem,
                                                uint32_t sbase, int C, int rank, int ncg, int R,
-                                               bool keep, bool write, uint16_t *out, float *lse) {
+                                               bool keep, bool write, uint16_t *out, float *lse,
+                                               int K, int k_self, float *ws, int *arrive) {
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, cq = lane & 3;
   const int cg = w % ncg, per = NW / ncg, j0 = pk ? cq : 2 * cq;
   cluster_arrive();  // this CTA's stages are free
@@ -936,9 +939,23 @@ __device__ __forceinline__ void finish_cluster(Softmax &sm, float oscale, bool p
   cluster_arrive();
   if (rank != 0) return;  // (the first CTA's shared memory holds all that is still read)
   cluster_wait();
-  if (!write) return;
   const float *sums = reinterpret_cast<const float *>(smem + (sum - sbase));
   const float2 *lm = reinterpret_cast<const float2 *>(smem + (sum_l - sbase));
+  // a row's four channels into the output, or (K > 1) into this cluster's sums
+  float *ws_self = K > 1 ? ws + (size_t)k_self * R * (kD + 4) : nullptr;
+  auto put = [&](int j, int c4, float4 A, float L, float M, float *dst) {
+    if (dst) {
+      reinterpret_cast<float4 *>(dst + j * kD)[c4] = A;
+      if (c4 == 0) *reinterpret_cast<float2 *>(dst + R * kD + 2 * j) = make_float2(L, M);
+      return;
+    }
+    const float Ld = L > 0.f ? L : 1.f;
+    uint2 h;
+    h.x = pack_half2(A.x / Ld, A.y / Ld);
+    h.y = pack_half2(A.z / Ld, A.w / Ld);
+    *reinterpret_cast<uint2 *>(out + j * kD + 4 * c4) = h;
+    if (lse && c4 == 0) lse[j] = (M - kExpShift + log2f(L)) * 0.69314718055994531f;
+  };
   for (int i = threadIdx.x; i < R * 32; i += NW * 32) {
     const int j = i >> 5, c4 = i & 31;
     float M = -INFINITY, L = 0.f;
@@ -952,12 +969,33 @@ __device__ __forceinline__ void finish_cluster(Softmax &sm, float oscale, bool p
       A.z = fmaf(f, x.z, A.z); A.w = fmaf(f, x.w, A.w);
       L = fmaf(f, y.x, L);
     }
-    const float Ld = L > 0.f ? L : 1.f;
-    uint2 h;
-    h.x = pack_half2(A.x / Ld, A.y / Ld);
-    h.y = pack_half2(A.z / Ld, A.w / Ld);
-    *reinterpret_cast<uint2 *>(out + j * kD + 4 * c4) = h;
-    if (lse && c4 == 0) lse[j] = (M - kExpShift + log2f(L)) * 0.69314718055994531f;
+    if (write) put(j, c4, A, L, M, ws_self);
+  }
+  if (K == 1) return;
+  __syncthreads();  // this cluster's sums are written (published by the arrival)
+  int *last = reinterpret_cast<int *>(row_m);
+  if (threadIdx.x == 0) {
+    *last = atom_add_acq_rel_gpu(arrive, 1) == K - 1;
+    if (*last) atomicExch(arrive, 0);  // every other arrival is in: ready for the next call
+  }
+  __syncthreads();
+  if (!*last || !write) return;
+  for (int i = threadIdx.x; i < R * 32; i += NW * 32) {
+    const int j = i >> 5, c4 = i & 31;
+    float M = -INFINITY, L = 0.f;
+    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < K; ++k) {
+      const float *src = ws + (size_t)k * R * (kD + 4);
+      const float4 x = ld_part4(src + j * kD + 4 * c4);
+      const float l = ld_part(src + R * kD + 2 * j), m = ld_part(src + R * kD + 2 * j + 1);
+      const float mn = fmaxf(M, m);
+      const float a = M == -INFINITY ? 0.f : fast_exp2(M - mn), f = m == -INFINITY ? 0.f : fast_exp2(m - mn);
+      A.x = fmaf(A.x, a, f * x.x); A.y = fmaf(A.y, a, f * x.y);
+      A.z = fmaf(A.z, a, f * x.z); A.w = fmaf(A.w, a, f * x.w);
+      L = fmaf(L, a, f * l);
+      M = mn;
+    }
+    put(j, c4, A, L, M, nullptr);
   }
 }
 
@@ -1065,7 +1103,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
   if (CL) {
     // While the kernel before still runs: bring what the start reads one after
     // the other towards L2, and its translations with it (L1 would be stale)
-    const int seg = blockIdx.x / prm.C, b = seg / c.H;
+    const int seg = blockIdx.x / (prm.C * prm.K), b = seg / c.H;
     if (threadIdx.x == 0) prefetch_l2(c.state + (size_t)b * QS_STATE_WORDS);
     if (threadIdx.x - 32 < 2 * prm.R) prefetch_l2(prm.q + (size_t)seg * prm.R * kD + (threadIdx.x - 32) * 64);
     if (prm.sel)
@@ -1081,15 +1119,15 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
   Seg seg_cl;
   int cl_x0 = 0, cl_n = 0;
   if (CL) {
-    const int seg = blockIdx.x / prm.C, rank = blockIdx.x % prm.C;
+    const int per_seg = prm.C * prm.K, seg = blockIdx.x / per_seg, part = blockIdx.x % per_seg;
     seg_cl.b = seg / c.H;
     seg_cl.h = seg % c.H;
     if (threadIdx.x == 0)
       T.len[seg_cl.b] = sequence_entry<TT, IDX>(c, prm.n_q, prm.n_new, n_sel, T, seg_cl.b);
     __syncthreads();
     seg_cl.len = T.len[seg_cl.b];
-    cl_x0 = seg_cl.len * rank / prm.C;
-    cl_n = seg_cl.len * (rank + 1) / prm.C - cl_x0;
+    cl_x0 = (int)((long long)seg_cl.len * part / per_seg);
+    cl_n = (int)((long long)seg_cl.len * (part + 1) / per_seg) - cl_x0;
   } else {
     if (w == 0) {
       const long long tot = build_tables<TT, IDX>(c, prm.n_q, prm.n_new, n_sel, T, lane);
@@ -1130,8 +1168,9 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
       c.state[QS_ST_TICKET] = 0;
     }
     constexpr int kRowVec = kD * 2 / 16;  // uint4 per fp16 row
-    // clustered: the cluster's first CTA writes its own head's tokens
-    const int j0 = CL ? (p % prm.C == 0 ? p / prm.C : c.B * c.H) : p;
+    // clustered: the segment's first CTA writes its own head's tokens
+    const int per_seg = prm.C * prm.K;
+    const int j0 = CL ? (p % per_seg == 0 ? p / per_seg : c.B * c.H) : p;
     for (int j = j0; j < c.B * c.H; j += gridDim.x) {
       const int b = j / c.H;
       if (T.fill[b] == T.fold[b]) continue;  // this sequence's append failed
@@ -1154,9 +1193,10 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
   // sequences with n_q > fill see no token: zero outputs, lse = -inf, error
   for (int b = CL ? seg_cl.b : p; b < c.B; b += prm.P) {
     if (T.len[b] != 0) continue;
-    if (CL && p % prm.C != 0) break;  // the cluster's first CTA alone, and for its head alone
+    // clustered: the segment's first CTA alone, and for its head alone
+    if (CL && p % (prm.C * prm.K) != 0) break;
     const size_t nh = CL ? (size_t)R : (size_t)c.H * R;
-    const size_t row0 = CL ? (size_t)(p / prm.C) * R : b * nh;
+    const size_t row0 = CL ? (size_t)(p / (prm.C * prm.K)) * R : b * nh;
     uint4 *o = reinterpret_cast<uint4 *>(prm.out + row0 * kD);
     for (size_t i = threadIdx.x; i < nh * (kD / 8); i += (NW * 32)) o[i] = make_uint4(0, 0, 0, 0);
     if (prm.lse)
@@ -1710,10 +1750,11 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
   const bool aborted = s_abort != 0;
   if (CL) {
     cluster_wait();  // (of the arrival at the start: every CTA runs)
+    const int q = p / prm.C, seg = q / prm.K;  // (q: the cluster)
     finish_cluster<NW>(sm, Centre<MODE, UB>::kScale, PK, smem, sbase, prm.C, p % prm.C, ncg, R,
-                       s_abort == 2, !aborted,
-                       prm.out + (size_t)(p / prm.C) * R * kD,
-                       prm.lse ? prm.lse + (size_t)(p / prm.C) * R : nullptr);
+                       s_abort == 2, !aborted, prm.out + (size_t)seg * R * kD,
+                       prm.lse ? prm.lse + (size_t)seg * R : nullptr, prm.K, q % prm.K,
+                       prm.ws + (size_t)seg * prm.K * R * (kD + 4), c.arrive + seg);
     return;
   }
   float *last_part = reinterpret_cast<float *>(smem);  // NW partials, in stage memory (free now)
@@ -1831,6 +1872,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
 struct DevInfo {
   int ready[48];
   int grid[48];
+  int clusters[48][kMaxCluster + 1];  // clustered: clusters of 2, 4, 8 CTAs resident at once
 };
 DevInfo g_dev[64];
 
@@ -1845,7 +1887,7 @@ constexpr int smem_bytes(int mode, int kind) {
 
 // Resident CTAs of one split-kernel variant on a device (set up once).
 template <int MODE, bool PK, int UB, int NW, int KIND>
-qs_status grid_for_device(int dev, int &P) {
+qs_status grid_for_device(int dev, int &P, const int **clusters) {
   DevInfo &di = g_dev[dev];
   constexpr int v = 2 * MODE + (PK ? 1 : 0) + (UB == 2 ? 4 : 0) + (NW == 8 ? 8 : 0) + 16 * KIND;
   if (!__atomic_load_n(&di.ready[v], __ATOMIC_ACQUIRE)) {
@@ -1860,29 +1902,47 @@ qs_status grid_for_device(int dev, int &P) {
                                                       NW * 32, smem) != cudaSuccess)
       return QS_ERR_CUDA;
     if (occ < 1) return QS_ERR_CUDA;
+    if (KIND == kClustered)
+      for (int n = 2; n <= kMaxCluster; n *= 2) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(n * sms);
+        cfg.blockDim = dim3(NW * 32);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = n;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&di.clusters[v][n], split_kernel<MODE, PK, UB, NW, KIND>,
+                                           &cfg) != cudaSuccess)
+          return QS_ERR_CUDA;
+      }
     di.grid[v] = sms * occ;
     __atomic_store_n(&di.ready[v], 1, __ATOMIC_RELEASE);
   }
   P = di.grid[v];
+  if (clusters) *clusters = di.clusters[v];
   return QS_OK;
 }
 
 template <int UB, int KIND>
-qs_status grid_size_ub(int dev, qs_mode mode, bool packed, int ncg, int &P) {
+qs_status grid_size_ub(int dev, qs_mode mode, bool packed, int ncg, int &P, const int **cl) {
   if (mode == QS_DRAFT_UPPER4)
-    return packed ? grid_for_device<QS_DRAFT_UPPER4, true, UB, kWarps, KIND>(dev, P)
-                  : grid_for_device<QS_DRAFT_UPPER4, false, UB, kWarps, KIND>(dev, P);
-  return ncg <= 2 ? grid_for_device<QS_VERIFY_INT8, false, UB, kVerifyWarps, KIND>(dev, P)
-                  : grid_for_device<QS_VERIFY_INT8, false, UB, kWarps, KIND>(dev, P);
+    return packed ? grid_for_device<QS_DRAFT_UPPER4, true, UB, kWarps, KIND>(dev, P, cl)
+                  : grid_for_device<QS_DRAFT_UPPER4, false, UB, kWarps, KIND>(dev, P, cl);
+  return ncg <= 2 ? grid_for_device<QS_VERIFY_INT8, false, UB, kVerifyWarps, KIND>(dev, P, cl)
+                  : grid_for_device<QS_VERIFY_INT8, false, UB, kWarps, KIND>(dev, P, cl);
 }
 
 template <int KIND>
-qs_status grid_size(qs_mode mode, bool packed, int upper_bits, int ncg, int &P) {
+qs_status grid_size(qs_mode mode, bool packed, int upper_bits, int ncg, int &P,
+                    const int **clusters = nullptr) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return QS_ERR_CUDA;
   if (dev < 0 || dev >= 64) return QS_ERR_UNSUPPORTED;
-  return upper_bits == 2 ? grid_size_ub<2, KIND>(dev, mode, packed, ncg, P)
-                         : grid_size_ub<4, KIND>(dev, mode, packed, ncg, P);
+  return upper_bits == 2 ? grid_size_ub<2, KIND>(dev, mode, packed, ncg, P, clusters)
+                         : grid_size_ub<4, KIND>(dev, mode, packed, ncg, P, clusters);
 }
 
 // A draft of at most four query rows takes the packed columns (PK).

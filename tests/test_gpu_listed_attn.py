@@ -122,6 +122,23 @@ def test_cluster_sizes(torch, B, H, mode, n_q, group):
     assert list(qs.qs_get_errors(cache)) == [qs.DEV_NQ_GT_FILL if n_q > f else 0 for f in fill]
 
 
+@pytest.mark.parametrize("mode,n_q,group", [(DRAFT, 1, 1), (DRAFT, 1, 4), (DRAFT, 1, 7), (VERIFY, 5, 1),
+                                            (VERIFY, 1, 3), (VERIFY, 5, 4)])
+@pytest.mark.parametrize("H,n", [(8, 130), (1, 200), (3, 100)])
+def test_several_clusters_a_segment(torch, H, n, mode, n_q, group):
+    """Few heads with a long context: two to nineteen clusters a segment,
+    joined through the workspace, twice (the counters are back at zero)."""
+    rng = np.random.default_rng([H, n, n_q, group])
+    oc = _oracle_state(rng, 1, H, [n], [201], cap=n)
+    cache = load(torch, oc, rng, n_pages=n + 2)
+    for _ in range(2):
+        q = h16(rng, (1, H * group, n_q, 128))
+        got, gl = run(torch, cache, mode, q, group)
+        ref, rl = paging.attention(oc, q, mode == DRAFT, group)
+        assert_close(got, ref, gl, rl)
+    assert np.all(qs.qs_get_errors(cache) == 0)
+
+
 @pytest.mark.parametrize("paged", [False, True])
 def test_every_group_selected_equals_dense(torch, paged):
     """All groups in order give the contiguous kernel's result (within the
