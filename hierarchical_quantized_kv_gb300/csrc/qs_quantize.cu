@@ -20,14 +20,16 @@ namespace {
 
 constexpr int kParts = 4;           // CTAs per (head, sequence)
 constexpr int kSlice = kD / kParts;  // key channels / value tokens per CTA
-// Warps per CTA.  A flush is one wave of small CTAs, so its time is one CTA's
-// chain of phases, and sixteen warps halve the per-thread work of every phase
-// but the packing.  A prefill of many waves is bound by instruction issue, and
+// Warps per CTA.  A flush of few heads is one wave of small CTAs, so its time is
+// one CTA's chain of phases, and sixteen warps shorten every phase but the
+// packing (32 heads: 4.6 us; eight warps 5.4, four 6.5); one of many is bound
+// by instruction issue like a prefill, where four are best (8 x 32 heads: 9.7 us;
+// eight 11.3, sixteen 15.1).  A prefill of many waves is bound by instruction issue, and
 // what a thread does once per quarter (addresses, scales) counts: four warps,
 // twice the elements a thread, 168 us for 32 heads of 32k tokens (eight: 175;
 // 0.71 of the copy bandwidth's time).  A prompt of one quarter per CTA is a
 // chain again: eight warps (two heads of 1k tokens: 5.3 us; four: 7.6).
-constexpr int kFlushWarps = 16, kPrefillWarps = 4, kShortPrefillWarps = 8;
+constexpr int kFlushWarps = 16, kBatchFlushWarps = 4, kPrefillWarps = 4, kShortPrefillWarps = 8;
 // Group quarters per quantizing CTA of a prefill, loads pipelined one ahead, at
 // most.
 constexpr int kPrefillQuarters = 8;
@@ -380,10 +382,11 @@ struct PrefillSmem {
 // n_next >= 0: flush the sequences whose buffer cannot take n_next more
 // tokens (qs_need_flush's rule; mask unused); else the masked ones (all
 // without a mask).
-__global__ void __launch_bounds__(32 * kFlushWarps)
+template <int QW>
+__global__ void __launch_bounds__(32 * QW)
     flush_kernel(qs_cache c, Pages pg, const uint8_t *__restrict__ mask, int n_next) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  FlushSmem<kFlushWarps> &S = *reinterpret_cast<FlushSmem<kFlushWarps> *>(smem_raw);
+  FlushSmem<QW> &S = *reinterpret_cast<FlushSmem<QW> *>(smem_raw);
   const int part = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   pdl_trigger();
   pdl_wait();
@@ -530,10 +533,6 @@ __global__ void __launch_bounds__(32 * QW, 20 / QW)
 using namespace qs;
 
 namespace {
-int g_flush_ready = 0;  // one bit per device ordinal below 32
-}  // namespace
-
-namespace {
 
 // Quarters per CTA: 8 for a prompt that fills the GPU several times over; fewer
 // for a short one, whose time is one CTA's chain of quarters (about 3 us each),
@@ -567,13 +566,23 @@ qs_status prefill(const qs_cache &c, const Pages &pg, const uint16_t *k, const u
                        : launch_prefill<kPrefillWarps>(c, pg, k, v, T, d_len, gmax, quarters, stream);
 }
 
+template <int QW>
+qs_status launch_flush(const qs_cache &c, const Pages &pg, const uint8_t *d_mask, int n_next,
+                       qs_stream_t stream) {
+  static int ready = 0;
+  const int smem = (int)sizeof(FlushSmem<QW>);
+  const qs_status s = set_smem_once((const void *)flush_kernel<QW>, smem, &ready);
+  if (s != QS_OK) return s;
+  return launch_pdl(flush_kernel<QW>, dim3(kParts, c.H, c.B), dim3(32 * QW), smem,
+                    (cudaStream_t)stream, c, pg, d_mask, n_next);
+}
+
+// Two CTAs of sixteen warps fit an SM: beyond those the narrow ones win.
 qs_status flush(const qs_cache &c, const Pages &pg, const uint8_t *d_mask, int n_next,
                 qs_stream_t stream) {
-  const int smem = (int)sizeof(FlushSmem<kFlushWarps>);
-  const qs_status s = set_smem_once((const void *)flush_kernel, smem, &g_flush_ready);
-  if (s != QS_OK) return s;
-  return launch_pdl(flush_kernel, dim3(kParts, c.H, c.B), dim3(32 * kFlushWarps), smem,
-                    (cudaStream_t)stream, c, pg, d_mask, n_next);
+  return (long long)kParts * c.H * c.B <= 2 * 152
+             ? launch_flush<kFlushWarps>(c, pg, d_mask, n_next, stream)
+             : launch_flush<kBatchFlushWarps>(c, pg, d_mask, n_next, stream);
 }
 
 }  // namespace

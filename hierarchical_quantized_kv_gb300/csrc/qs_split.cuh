@@ -1280,7 +1280,8 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
   int *list = reinterpret_cast<int *>(smem + L::kListOff);
   auto place_of = [&](const Seg &a) { return a.u < T.ng[a.b] ? unit_place(prm, a.b, a.h, a.u) : 0; };
   if ((IDX || w == 0) && !prm.no_issue) {
-    Seg a = first;
+    Seg a;
+    if (CL) a = first;
     for (int k = IDX ? w : 0; k < S && k < n; k += IDX ? NW : 1) {
       a.template seek<CL>(x0 + k, T, c.B);
       int place = 0;
@@ -1295,7 +1296,8 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
   }
   if (IDX && appends) append();
   if (IDX && n > S) {  // (uniform)
-    Seg a = first;
+    Seg a;
+    if (CL) a = first;
     for (int i = S + threadIdx.x; i < min(n, kListMax); i += NW * 32) {
       a.template seek<CL>(x0 + i, T, c.B);
       list[i] = place_of(a);
@@ -1308,7 +1310,8 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
   uint32_t qp0[8], qp1[8];
   int fill = 0, ng = 0;
   int cur_ord = -1;  // segment ordinal of this warp's softmax state (-1: none yet)
-  Seg cur = first, ahead = first;
+  Seg cur, ahead;
+  if (CL) cur = ahead = first;
   // Work is claimed in half-units (claim h: unit h / 2, tokens of half h % 2)
   // from one shared counter.  Both halves of a unit go to whichever warps
   // claim them; the stage's release counter joins them again.  Draft claims
