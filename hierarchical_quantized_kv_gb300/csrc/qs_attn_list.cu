@@ -50,12 +50,14 @@ qs_status choose_clusters(Params &prm, qs_mode mode) {
 qs_status decode_listed(Params &prm, qs_mode mode, const uint16_t *k_new, const uint16_t *v_new,
                         int32_t n_new, const uint16_t *q, int32_t n_q, int32_t group,
                         float softmax_scale, uint16_t *out, float *lse, void *workspace,
-                        size_t workspace_bytes, qs_stream_t stream) {
+                        size_t workspace_bytes, uint64_t wait_ns, int no_issue,
+                        qs_stream_t stream) {
   if ((k_new != nullptr) != (v_new != nullptr) || n_new < 0 || n_new > kRing ||
       (n_new > 0) != (k_new != nullptr))
     return QS_ERR_ARG;
   if (k_new && (!aligned16(k_new) || !aligned16(v_new))) return QS_ERR_ALIGN;
-  prm.wait_ns = kWaitLimitNs;
+  prm.wait_ns = wait_ns;
+  prm.no_issue = no_issue;
   prm.k_new = k_new;
   prm.v_new = v_new;
   prm.n_new = n_new;
@@ -83,7 +85,7 @@ qs_status qs_attn_decode_paged(const qs_cache *c, const qs_pages *pg, qs_mode mo
   const qs_status s = check_pages(c, pg, true, &prm.c, &prm.pg);
   if (s != QS_OK) return s;
   return decode_listed(prm, mode, k_new, v_new, n_new, q, n_q, group, softmax_scale, out, lse,
-                       workspace, workspace_bytes, stream);
+                       workspace, workspace_bytes, kWaitLimitNs, 0, stream);
 }
 
 qs_status qs_attn_decode_sparse(const qs_cache *c, const qs_pages *pg, qs_mode mode,
@@ -99,7 +101,23 @@ qs_status qs_attn_decode_sparse(const qs_cache *c, const qs_pages *pg, qs_mode m
   prm.sel = sel;
   prm.k_sel = k_sel;
   return decode_listed(prm, mode, k_new, v_new, n_new, q, n_q, group, softmax_scale, out, lse,
-                       workspace, workspace_bytes, stream);
+                       workspace, workspace_bytes, kWaitLimitNs, 0, stream);
+}
+
+// Test entry, not declared in include/qs.h: qs_attn_decode_paged with every
+// pipeline wait limited to wait_ns (1 us .. 100 ms) and no copy ever issued, so
+// the first wait of every warp runs out (as qs_test_attn_decode_timeout does for
+// the contiguous kernel).
+qs_status qs_test_attn_paged_timeout(const qs_cache *c, const qs_pages *pg, qs_mode mode,
+                                     const uint16_t *q, int32_t n_q, int32_t group,
+                                     float softmax_scale, uint16_t *out, float *lse, void *workspace,
+                                     size_t workspace_bytes, uint64_t wait_ns, qs_stream_t stream) {
+  if (wait_ns < 1000ull || wait_ns > 100000000ull) return QS_ERR_ARG;
+  Params prm = {};
+  const qs_status s = check_pages(c, pg, true, &prm.c, &prm.pg);
+  if (s != QS_OK) return s;
+  return decode_listed(prm, mode, nullptr, nullptr, 0, q, n_q, group, softmax_scale, out, lse,
+                       workspace, workspace_bytes, wait_ns, 1, stream);
 }
 
 }  // extern "C"

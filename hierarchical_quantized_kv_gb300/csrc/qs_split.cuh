@@ -934,7 +934,8 @@ __device__ __forceinline__ void finish_cluster(Softmax &sm, float oscale, bool p
     const int j = threadIdx.x;
     float l = 0.f;
     for (int k = 0; k < per; ++k) l += parts[NW * 8 * kD + ((j >> 3) + k * ncg) * 8 + (j & 7)];
-    st_cluster2(mapa(sum_l + (rank * R + j) * 8, 0), l, row_m[j]);
+    // (a NaN maximum: this CTA's part is missing, and nothing is written)
+    st_cluster2(mapa(sum_l + (rank * R + j) * 8, 0), l, write ? row_m[j] : NAN);
   }
   cluster_arrive();
   if (rank != 0) return;  // (the first CTA's shared memory holds all that is still read)
@@ -959,7 +960,12 @@ __device__ __forceinline__ void finish_cluster(Softmax &sm, float oscale, bool p
   for (int i = threadIdx.x; i < R * 32; i += NW * 32) {
     const int j = i >> 5, c4 = i & 31;
     float M = -INFINITY, L = 0.f;
-    for (int k = 0; k < C; ++k) M = fmaxf(M, lm[k * R + j].y);
+    bool whole = true;
+    for (int k = 0; k < C; ++k) {
+      const float m = lm[k * R + j].y;
+      M = fmaxf(M, m);
+      whole &= m == m;
+    }
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = 0; k < C; ++k) {
       const float4 x = *reinterpret_cast<const float4 *>(sums + (k * R + j) * kD + 4 * c4);
@@ -969,7 +975,7 @@ __device__ __forceinline__ void finish_cluster(Softmax &sm, float oscale, bool p
       A.z = fmaf(f, x.z, A.z); A.w = fmaf(f, x.w, A.w);
       L = fmaf(f, y.x, L);
     }
-    if (write) put(j, c4, A, L, M, ws_self);
+    if (whole || K > 1) put(j, c4, A, L, whole ? M : NAN, ws_self);
   }
   if (K == 1) return;
   __syncthreads();  // this cluster's sums are written (published by the arrival)
@@ -979,23 +985,25 @@ __device__ __forceinline__ void finish_cluster(Softmax &sm, float oscale, bool p
     if (*last) atomicExch(arrive, 0);  // every other arrival is in: ready for the next call
   }
   __syncthreads();
-  if (!*last || !write) return;
+  if (!*last) return;
   for (int i = threadIdx.x; i < R * 32; i += NW * 32) {
     const int j = i >> 5, c4 = i & 31;
     float M = -INFINITY, L = 0.f;
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool whole = true;
     for (int k = 0; k < K; ++k) {
       const float *src = ws + (size_t)k * R * (kD + 4);
       const float4 x = ld_part4(src + j * kD + 4 * c4);
       const float l = ld_part(src + R * kD + 2 * j), m = ld_part(src + R * kD + 2 * j + 1);
       const float mn = fmaxf(M, m);
+      whole &= m == m;
       const float a = M == -INFINITY ? 0.f : fast_exp2(M - mn), f = m == -INFINITY ? 0.f : fast_exp2(m - mn);
       A.x = fmaf(A.x, a, f * x.x); A.y = fmaf(A.y, a, f * x.y);
       A.z = fmaf(A.z, a, f * x.z); A.w = fmaf(A.w, a, f * x.w);
       L = fmaf(L, a, f * l);
       M = mn;
     }
-    put(j, c4, A, L, M, nullptr);
+    if (whole) put(j, c4, A, L, M, nullptr);
   }
 }
 
@@ -1107,7 +1115,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
     if (threadIdx.x == 0) prefetch_l2(c.state + (size_t)b * QS_STATE_WORDS);
     if (threadIdx.x - 32 < 2 * prm.R) prefetch_l2(prm.q + (size_t)seg * prm.R * kD + (threadIdx.x - 32) * 64);
     if (prm.sel)
-      for (int i = 32 * threadIdx.x; i < prm.k_sel; i += 32 * NW * 32)
+      for (int i = 32 * threadIdx.x; i < min(prm.k_sel, c.cap_groups); i += 32 * NW * 32)
         prefetch_l2(prm.sel + (size_t)seg * prm.k_sel + i);
     if (prm.pg.table)
       for (int i = 32 * threadIdx.x; i < c.cap_groups; i += 32 * NW * 32)

@@ -213,7 +213,7 @@ qs_status qs_paged_cache_bytes(int32_t B, int32_t H, int32_t D, int32_t G, int32
                                qs_cache_bytes_t *out);
 
 /* Zero every sequence's counters (empty cache) and the attention arrival
- * counters.  Asynchronous memsets.  No counterpart on the pages: it is this
+ * counters.  One launch.  No counterpart on the pages: it is this
  * library's initialisation of its device-resident bookkeeping. */
 qs_status qs_state_reset(const qs_cache *c, qs_stream_t stream);
 
