@@ -375,6 +375,7 @@ struct PrefillSmem {
   __half k1[kG][kSlice];
   __half v1[kSlice][kD];
   FlushSmem<QW> f;
+  int place[kPrefillQuarters / 4 + 1];  // entries of the CTA's groups
 };
 
 }  // namespace
@@ -429,9 +430,10 @@ __global__ void __launch_bounds__(32 * QW)
 }
 
 // Bulk prefill of empty caches from a prompt (k, v: fp16 [B][H][T][D]).
-// Grid (nq + 2, H, B): block x < nq quantizes group quarters [x Q, x Q + Q)
-// of the sequence's head (quarter i: part i % 4 of group i / 4; Q = quarters), the next quarter's rows copied into the second buffer
-// while the current one is quantized; the last two blocks copy buffer halves
+// Grid (nq + 2, H, B), or, into pages, ((nq + 2) H, 1, B) with the heads of a
+// page side by side: block x < nq quantizes group quarters [x Q, x Q + Q) of the
+// sequence's head (quarter i: part i % 4 of group i / 4; Q = quarters), the next
+// quarter's rows copied into the second buffer while the current one is quantized; the last two blocks copy buffer halves
 // 0 and 1.  The CTA that arrives last on the sequence's ticket writes the
 // counters, so every CTA reads the old (empty) ones first.
 template <int QW>
@@ -442,10 +444,13 @@ __global__ void __launch_bounds__(32 * QW, 20 / QW)
   extern __shared__ __align__(128) uint8_t smem_raw[];
   PrefillSmem<QW> &PS = *reinterpret_cast<PrefillSmem<QW> *>(smem_raw);
   FlushSmem<QW> &S = PS.f;
-  const int x = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  const int x = pg.table ? blockIdx.x / c.H : blockIdx.x, h = pg.table ? blockIdx.x % c.H : blockIdx.y;
+  const int b = blockIdx.z, tid = threadIdx.x;
   pdl_trigger();
   pdl_wait();
   int32_t *st = c.state + (size_t)b * QS_STATE_WORDS;
+  if (pg.table)  // (read below, once the prompt's length is known)
+    for (int g = 32 * tid; g < c.cap_groups; g += 32 * 32 * QW) prefetch_l1(pg.table + (size_t)b * c.cap_groups + g);
   if (tid == 0) {
     const int L = len[b];
     const bool lead = (h == 0 && x == 0);
@@ -468,18 +473,18 @@ __global__ void __launch_bounds__(32 * QW, 20 / QW)
   __syncthreads();
   if (!S.act) return;
   const int ng = S.g, fill = S.base;
-  if (pg.table) {
-    // every page the prompt needs, looked at by every CTA alike: a bad one
-    // leaves the whole sequence unchanged
-    int bad = 0;
-    for (int g = tid; g < ng; g += 32 * QW) bad |= group_slot(c, pg, b, h, g) < 0;
-    if (__syncthreads_or(bad)) {
-      if (h == 0 && x == 0 && tid == 0) atomicOr(&st[QS_ST_ERR], QS_DEV_PAGE);
-      return;
-    }
-  }
   const size_t bh = (size_t)b * c.H + h;
   const uint16_t *kp = k + bh * T * kD, *vp = v + bh * T * kD;
+  // Paged: every page the prompt needs, looked at by every CTA alike (while its
+  // first rows are on their way): a bad one leaves the whole sequence unchanged.
+  auto pages_good = [&]() {
+    if (!pg.table) return true;
+    int bad = 0;
+    for (int g = tid; g < ng; g += 32 * QW) bad |= group_slot(c, pg, b, h, g) < 0;
+    if (!__syncthreads_or(bad)) return true;
+    if (h == 0 && x == 0 && tid == 0) atomicOr(&st[QS_ST_ERR], QS_DEV_PAGE);
+    return false;
+  };
   if (x < nq) {
     const int q0 = x * quarters, q1 = min(q0 + quarters, 4 * ng);
     const __half *kh = reinterpret_cast<const __half *>(kp), *vh = reinterpret_cast<const __half *>(vp);
@@ -492,6 +497,13 @@ __global__ void __launch_bounds__(32 * QW, 20 / QW)
                                        vh + (size_t)g * kG * kD, i & 3, tid);
     };
     if (q0 < q1) load(q0);
+    // (looked up once: a table read a quarter, even from L1, cost 9 % of the call)
+    const int g0 = q0 >> 2;
+    if (tid < kPrefillQuarters / 4 + 1 && g0 + tid < ng) PS.place[tid] = (int)group_slot(c, pg, b, h, g0 + tid);
+    if (!pages_good()) {
+      cp_async_wait<0>();
+      return;
+    }
     for (int i = q0; i < q1; ++i) {
       cp_async_wait<0>();
       // quarter i's rows, copied by every thread, are visible; the buffer and
@@ -499,13 +511,14 @@ __global__ void __launch_bounds__(32 * QW, 20 / QW)
       __syncthreads();
       if (i + 1 < q1) load(i + 1);
       const int g = i >> 2;
-      const size_t grp = (size_t)group_slot(c, pg, b, h, g);
+      const size_t grp = (size_t)PS.place[g - g0];
       // checked build: the group's prompt rows inside the prompt array
       if (chk(in_range(((size_t)g + 1) * kG, 0, (size_t)T), 22) &&
           chk(in_range(grp, 1, group_slots(c, pg)), 20))
         quantize_loaded(S, i & 1 ? PS.k1 : S.k, i & 1 ? PS.v1 : S.v, c, grp, i & 3, tid);
     }
   } else {
+    if (!pages_good()) return;
     // buffer half x - nq: tokens i in [G half, G half + G) that are < fill
     const int i0 = (x - nq) * kG, i1 = min(i0 + kG, fill);
     const uint4 *ks = reinterpret_cast<const uint4 *>(kp + (size_t)ng * kG * kD);
@@ -519,7 +532,7 @@ __global__ void __launch_bounds__(32 * QW, 20 / QW)
       }
   }
   __syncthreads();
-  if (tid == 0 && atom_add_acq_rel_gpu(&st[QS_ST_TICKET], 1) == (int)gridDim.x * c.H - 1) {
+  if (tid == 0 && atom_add_acq_rel_gpu(&st[QS_ST_TICKET], 1) == (int)(gridDim.x * gridDim.y) - 1) {
     st[QS_ST_N_GROUPS] = ng;
     st[QS_ST_FILL] = fill;
     st[QS_ST_PENDING] = 0;
@@ -552,8 +565,8 @@ qs_status launch_prefill(const qs_cache &c, const Pages &pg, const uint16_t *k, 
   const qs_status s = set_smem_once((const void *)prefill_kernel<QW>, smem, &ready);
   if (s != QS_OK) return s;
   const int nq = (4 * gmax + quarters - 1) / quarters;
-  return launch_pdl(prefill_kernel<QW>, dim3(nq + 2, c.H, c.B), dim3(32 * QW), smem,
-                    (cudaStream_t)stream, c, pg, k, v, T, d_len, nq, quarters);
+  const dim3 grid = pg.table ? dim3((unsigned)(nq + 2) * c.H, 1, c.B) : dim3(nq + 2, c.H, c.B);
+  return launch_pdl(prefill_kernel<QW>, grid, dim3(32 * QW), smem, (cudaStream_t)stream, c, pg, k, v, T, d_len, nq, quarters);
 }
 
 qs_status prefill(const qs_cache &c, const Pages &pg, const uint16_t *k, const uint16_t *v, int32_t T,

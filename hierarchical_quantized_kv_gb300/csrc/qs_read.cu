@@ -81,8 +81,9 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t r0, ui
                : "memory");
 }
 
-// Grid (128-token units the window touches, H, B): one CTA reads one unit of
-// one head.  Keys are token-major like the output: a thread turns eight
+// Grid (128-token units the window touches, H, B), or, from pages, (units x H,
+// 1, B) with the heads of a page side by side: one CTA reads one unit of one
+// head.  Keys are token-major like the output: a thread turns eight
 // nibbles of a row into 16 output bytes.  Values are stored channel-major: a
 // warp's word holds token pairs of one channel per lane, exactly the 8x8
 // fragments that a transposed matrix store turns into token-major rows of a
@@ -93,8 +94,9 @@ __global__ void __launch_bounds__(kReadThreads)
                 uint16_t *__restrict__ v_out) {
   __shared__ __align__(16) uint8_t tile[kG * kTileRow];
   __shared__ __align__(16) uint16_t ks[kD], kz[kD];
-  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  const int u = tok0 / kG + blockIdx.x;  // unit: tokens [128 u, 128 u + 128)
+  const int h = pg.table ? blockIdx.x % c.H : blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  // unit: tokens [128 u, 128 u + 128)
+  const int u = tok0 / kG + (pg.table ? blockIdx.x / c.H : blockIdx.x);
   pdl_trigger();
   pdl_wait();
   const int32_t *st = c.state + (size_t)b * QS_STATE_WORDS;
@@ -198,7 +200,8 @@ __global__ void __launch_bounds__(kReadThreads)
 template <int MODE>
 qs_status launch_read(const qs_cache &c, const Pages &pg, int tok0, int T, uint16_t *k, uint16_t *v,
                       cudaStream_t s) {
-  const dim3 grid((tok0 + T - 1) / kG - tok0 / kG + 1, c.H, c.B), block(kReadThreads);
+  const unsigned n = (tok0 + T - 1) / kG - tok0 / kG + 1;
+  const dim3 grid = pg.table ? dim3(n * c.H, 1, c.B) : dim3(n, c.H, c.B), block(kReadThreads);
   return c.upper_bits == 2 ? launch_pdl(read_kernel<MODE, 2>, grid, block, 0, s, c, pg, tok0, T, k, v)
                            : launch_pdl(read_kernel<MODE, 4>, grid, block, 0, s, c, pg, tok0, T, k, v);
 }
