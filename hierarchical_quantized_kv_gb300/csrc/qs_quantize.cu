@@ -77,34 +77,49 @@ constexpr float kNear = 0.5f - 0x1p-12f;
 
 __device__ __forceinline__ float reciprocal(float sf) { return sf == 0.f ? 0.f : __frcp_rn(sf); }
 
-// Codes of eight values (four half2), one low byte each of t.
-template <typename Scale>  // scale of value i
-__device__ __forceinline__ void codes8(const uint32_t (&x)[4], const float (&zf)[8],
-                                       const float (&rf)[8], Scale scale, uint32_t (&t)[8]) {
-  float a[8], d[8], far = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(u32_as_h2(x[i]));
-    a[2 * i] = __fsub_rn(f.x, zf[2 * i]);
-    a[2 * i + 1] = __fsub_rn(f.y, zf[2 * i + 1]);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float n = __fmaf_rn(a[i], rf[i], kRound);
-    d[i] = __fmaf_rn(a[i], rf[i], -__fsub_rn(n, kRound));
-    far = fmaxf(far, fabsf(d[i]));
-    t[i] = __float_as_uint(n);
-  }
-  if (far > kNear) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (fabsf(d[i]) > kNear) t[i] = __float_as_uint(__fadd_rn(__fdiv_rn(a[i], scale(i)), kRound));
-  }
-}
-
 // Low bytes of four words, in order.
 __device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return prmt(prmt(a, b, 0x0040), prmt(c, d, 0x0040), 0x5410);
+}
+
+// Codes of eight values that lie together at p in shared memory (x: the same,
+// loaded), a byte each: codes 0..3 and 4..7, or (EVEN_ODD) 0, 2, 4, 6 and 1, 3,
+// 5, 7.  z_at(i), s_at(i): zero and scale of value i, for the rare exact ones,
+// which a loop of their own takes one by one from memory (eight divides in line
+// at every place made a loop body larger than the instruction cache).
+template <bool EVEN_ODD, typename Zero, typename Scale>
+__device__ __forceinline__ uint2 codes8(const __half *p, const uint4 &x, const float (&zf)[8],
+                                        const float (&rf)[8], Zero z_at, Scale s_at) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  float d[8], far = 0.f;
+  uint32_t t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = __half22float2(u32_as_h2(w[i >> 1]));
+    const float a = __fsub_rn(i & 1 ? f.y : f.x, zf[i]);
+    const float n = __fmaf_rn(a, rf[i], kRound);
+    d[i] = __fmaf_rn(a, rf[i], -__fsub_rn(n, kRound));
+    far = fmaxf(far, fabsf(d[i]));
+    t[i] = __float_as_uint(n);
+  }
+  uint2 q = EVEN_ODD ? make_uint2(low_bytes(t[0], t[2], t[4], t[6]), low_bytes(t[1], t[3], t[5], t[7]))
+                     : make_uint2(low_bytes(t[0], t[1], t[2], t[3]), low_bytes(t[4], t[5], t[6], t[7]));
+  if (far > kNear) {
+    unsigned near = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) near |= fabsf(d[i]) > kNear ? 1u << i : 0u;
+#pragma unroll 1
+    while (near) {
+      const int i = __ffs(near) - 1;
+      near &= near - 1;
+      const float a = __fsub_rn(__half2float(p[i]), z_at(i));
+      const uint32_t n = __float_as_uint(__fadd_rn(__fdiv_rn(a, s_at(i)), kRound)) & 0xFFu;
+      const int sh = EVEN_ODD ? 8 * (i >> 1) : 8 * (i & 3);
+      uint32_t &word = (EVEN_ODD ? i & 1 : i >> 2) ? q.y : q.x;
+      word = (word & ~(0xFFu << sh)) | (n << sh);
+    }
+  }
+  return q;
 }
 
 // Eight codes' nibble words: ev holds codes 0, 2, 4, 6 and od 1, 3, 5, 7, a byte
@@ -280,10 +295,8 @@ __device__ void quantize_loaded(FlushSmem<QW> &S, const __half (*kt)[kSlice],
     const float zs[8] = {zf, zf, zf, zf, zf, zf, zf, zf}, rs[8] = {rf, rf, rf, rf, rf, rf, rf, rf};
 #pragma unroll
     for (int i = 0; i < kCh; ++i) {
-      uint32_t q[8];
-      codes8({x[i].x, x[i].y, x[i].z, x[i].w}, zs, rs, [&](int) { return sf; }, q);
-      *reinterpret_cast<uint2 *>(&S.vc[t][run(i)]) =
-          make_uint2(low_bytes(q[0], q[1], q[2], q[3]), low_bytes(q[4], q[5], q[6], q[7]));
+      *reinterpret_cast<uint2 *>(&S.vc[t][run(i)]) = codes8<false>(
+          &vt[t][run(i)], x[i], zs, rs, [&](int) { return zf; }, [&](int) { return sf; });
     }
   }
   __syncthreads();
@@ -329,12 +342,13 @@ __device__ void quantize_loaded(FlushSmem<QW> &S, const __half (*kt)[kSlice],
       zf[4 * i] = z4.x; zf[4 * i + 1] = z4.y; zf[4 * i + 2] = z4.z; zf[4 * i + 3] = z4.w;
       rf[4 * i] = r4.x; rf[4 * i + 1] = r4.y; rf[4 * i + 2] = r4.z; rf[4 * i + 3] = r4.w;
     }
-#pragma unroll
+#pragma unroll 2
     for (int t = tid >> 2; t < kG; t += kQThreads / 4) {
-      const uint4 x = *reinterpret_cast<const uint4 *>(&kt[t][8 * o]);
-      uint32_t q[8];
-      codes8({x.x, x.y, x.z, x.w}, zf, rf, [&](int i) { return half_bits_to_float(S.ks[8 * o + i]); }, q);
-      const uint32_t ev = low_bytes(q[0], q[2], q[4], q[6]), od = low_bytes(q[1], q[3], q[5], q[7]);
+      const uint2 q = codes8<true>(
+          &kt[t][8 * o], *reinterpret_cast<const uint4 *>(&kt[t][8 * o]), zf, rf,
+          [&](int i) { return S.kzf[8 * o + i]; },
+          [&](int i) { return half_bits_to_float(S.ks[8 * o + i]); });
+      const uint32_t ev = q.x, od = q.y;
       const int W = 16 * t + 4 * part + o;
       store_upper(c.k_upper + grp * kG * (kD / 2), W, upper_nibbles(ev, od), two_bit);
       *reinterpret_cast<uint32_t *>(c.k_lower + grp * kG * (kD / 2) + 4 * W) = lower_nibbles(ev, od);
