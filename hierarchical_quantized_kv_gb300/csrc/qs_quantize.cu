@@ -23,13 +23,14 @@ constexpr int kSlice = kD / kParts;  // key channels / value tokens per CTA
 // Warps per CTA.  A flush of few heads is one wave of small CTAs, so its time is
 // one CTA's chain of phases, and sixteen warps shorten every phase but the
 // packing (32 heads: 4.6 us; eight warps 5.4, four 6.5); one of many is bound
-// by instruction issue like a prefill, where four are best (8 x 32 heads: 9.7 us;
-// eight 11.3, sixteen 15.1).  A prefill of many waves is bound by instruction issue, and
-// what a thread does once per quarter (addresses, scales) counts: four warps,
-// twice the elements a thread, 168 us for 32 heads of 32k tokens (eight: 175;
-// 0.71 of the copy bandwidth's time).  A prompt of one quarter per CTA is a
-// chain again: eight warps (two heads of 1k tokens: 5.3 us; four: 7.6).
-constexpr int kFlushWarps = 16, kBatchFlushWarps = 4, kPrefillWarps = 4, kShortPrefillWarps = 8;
+// by instruction issue like a prefill, where four are best (8 x 32 heads: 9.3 us;
+// eight 11.3, sixteen 15.1).  In a prefill of many waves, what a thread does once
+// per quarter (addresses, scales) counts: four warps, twice the elements a
+// thread, 157 us for 32 heads of 32k tokens (0.76 of the copy bandwidth's rate;
+// eight: 177).  A prompt of one or two quarters per CTA is a chain again (four
+// sequences of 1k tokens and 8 heads: eight warps 7.4 us, four 8.7), and a very
+// short one takes sixteen (two heads of 1k tokens: 3.8 us; eight 5.0, four 7.6).
+constexpr int kFlushWarps = 16, kBatchFlushWarps = 4;
 // Group quarters per quantizing CTA of a prefill, loads pipelined one ahead, at
 // most.
 constexpr int kPrefillQuarters = 8;
@@ -562,8 +563,9 @@ using namespace qs;
 namespace {
 
 // Quarters per CTA: 8 for a prompt that fills the GPU several times over; fewer
-// for a short one, whose time is one CTA's chain of quarters (about 3 us each),
-// so that its quarters spread over five CTAs an SM first.
+// for a short one, whose time is one CTA's chain of quarters, so that its
+// quarters spread over five CTAs an SM first (two heads of 1k tokens: 23.5 us
+// with eight quarters a CTA).
 int prefill_quarters(long long total) {
   const long long slots = 5 * 152;
   int q = 1;
@@ -589,8 +591,10 @@ qs_status prefill(const qs_cache &c, const Pages &pg, const uint16_t *k, const u
   if (!aligned16(k) || !aligned16(v)) return QS_ERR_ALIGN;
   const int gmax = T > 2 * kG ? (T - 2 * kG + kG - 1) / kG : 0;
   const int quarters = prefill_quarters((long long)4 * gmax * c.H * c.B);
-  return quarters == 1 ? launch_prefill<kShortPrefillWarps>(c, pg, k, v, T, d_len, gmax, 1, stream)
-                       : launch_prefill<kPrefillWarps>(c, pg, k, v, T, d_len, gmax, quarters, stream);
+  if (quarters > 2) return launch_prefill<4>(c, pg, k, v, T, d_len, gmax, quarters, stream);
+  return (long long)4 * gmax * c.H * c.B <= 2 * 152
+             ? launch_prefill<16>(c, pg, k, v, T, d_len, gmax, quarters, stream)
+             : launch_prefill<8>(c, pg, k, v, T, d_len, gmax, quarters, stream);
 }
 
 template <int QW>

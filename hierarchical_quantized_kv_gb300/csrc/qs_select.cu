@@ -428,12 +428,11 @@ __global__ void __launch_bounds__(kSelThreads)
 }
 
 // CTAs per (sequence, KV head): one per 128 groups (a tile for each warp), at
-// most 8, as long as the whole grid stays within a CTA an SM (four sequences
-// of 8 KV heads and 1,022 groups: clusters of 4, 8.2 us; of 8, more CTAs than fit
-// beside a call before, 9.6 us).
+// most 8, as long as the whole grid stays within two CTAs an SM (four sequences
+// of 8 KV heads and 1,022 groups: clusters of 8, 9.9 us; of 4, 11.4).
 int cluster_size(const qs_cache &c, int sms) {
   int n = 1;
-  while (n < 8 && n * kSelWarps * kTile < c.cap_groups && (long long)c.B * c.H * n * 2 <= sms) n *= 2;
+  while (n < 8 && n * kSelWarps * kTile < c.cap_groups && (long long)c.B * c.H * n * 2 <= 2 * sms) n *= 2;
   return n;
 }
 
