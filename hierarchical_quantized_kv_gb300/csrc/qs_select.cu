@@ -307,6 +307,19 @@ __global__ void __launch_bounds__(kSelThreads)
     }
   }
   if (!started) cluster.barrier_wait();
+  // A product's exponent is taken from the operands' exponent fields, where a
+  // subnormal zero or scale counts as 2^-14: as much again for each channel,
+  // sum |q| (1 + 255) 2^-14 <= 2 max |q|.
+  uint32_t qmax = 0;
+#pragma unroll
+  for (int g = 0; g < NCG; ++g)
+#pragma unroll
+    for (int kb = 0; kb < 8; ++kb)
+      qmax = h2_as_u32(__hmax2_nan(u32_as_h2(qmax), __hmax2_nan(__habs2(u32_as_h2(q0[g][kb])),
+                                                                __habs2(u32_as_h2(q1[g][kb])))));
+  const float2 qm = __half22float2(u32_as_h2(qmax));
+  mag += 2.f * __int_as_float(__reduce_max_sync(
+                   0xffffffffu, max(__float_as_int(qm.x), __float_as_int(qm.y))));
   // (mag >= 0: ordered as integers)
   const int wmag = __reduce_max_sync(0xffffffffu, __float_as_int(mag));
   kmin = __reduce_min_sync(0xffffffffu, kmin);

@@ -285,7 +285,25 @@ __device__ __forceinline__ void pairs_int8(uint32_t wu, uint32_t wl, uint32_t (&
 // bits 4-7 (16 C_U * 2^-24): one shift and four masks per word.  The factor
 // 16 of the odd elements is taken out of their other operand (B = q * s_K / 16
 // for keys, P' / 16 for values), so every product is C_U * 2^-24 * B.
+//
+// HI (listed variants): the same two bits further up (times 4; the scales take it
+// back).  The tensor core seems to align and cut a product by its operands'
+// exponent fields, where a subnormal's leading zeros count: of a code in the low
+// bits that many bits of P' and q s are lost, all in one direction (the error
+// grows fourfold from verify codes to draft codes to two-bit ones).  Measured
+// against 64 bits: draft outputs off by 2.4 to 3.1e-4 (their fp16 rounding alone:
+// 2.1e-4), 5 to 8e-4 in the two-bit layout; with the shift 2.0 to 2.4e-4 in both,
+// for 1 to 3 % of the time of a short call.
+template <bool HI = false>
 __device__ __forceinline__ void pairs_upper(uint32_t w, uint32_t (&e)[4]) {
+  if (HI) {
+    const uint32_t u = w << 2, t = w >> 6;
+    e[0] = u & 0x003C003Cu;
+    e[1] = u & 0x03C003C0u;
+    e[2] = t & 0x003C003Cu;
+    e[3] = t & 0x03C003C0u;
+    return;
+  }
   const uint32_t t = w >> 8;
   e[0] = w & 0x000F000Fu;
   e[1] = w & 0x00F000F0u;
@@ -303,7 +321,7 @@ __device__ __forceinline__ void pairs_upper(uint32_t w, uint32_t (&e)[4]) {
 // Keys need no centring (q * s_K is carried hi + lo to ~2^-22): the bias
 // carries the midpoint alone.
 // UB: the top bits the draft reads (4: 16 C_U + 8; 2: 64 C_U2 + 32).
-template <int MODE, int UB = 4>
+template <int MODE, int UB = 4, bool HI = false>
 struct Centre {
   static constexpr bool kDraft = MODE == QS_DRAFT_UPPER4;
   static constexpr float kStep = UB == 2 ? 64.f : 16.f;  // draft code step
@@ -312,12 +330,13 @@ struct Centre {
   static constexpr float kMid = 128.f;  // taken out of the value product
   // true code sum / tensor-core sum: 2^24 (subnormal codes), times the
   // draft's code step
-  static constexpr float kScale = 16777216.f * (kDraft ? kStep : 1.f);
+  static constexpr float kScale =
+      16777216.f * (kDraft ? kStep / (!HI ? 1.f : UB == 2 ? 16.f : 4.f) : 1.f);
 };
 
-template <int MODE>
+template <int MODE, bool HI>
 __device__ __forceinline__ void pairs(uint32_t wu, uint32_t wl, uint32_t (&e)[4]) {
-  if (MODE == QS_DRAFT_UPPER4) pairs_upper(wu, e);
+  if (MODE == QS_DRAFT_UPPER4) pairs_upper<HI>(wu, e);
   else pairs_int8(wu, wl, e);
 }
 
@@ -326,15 +345,33 @@ __device__ __forceinline__ void pairs(uint32_t wu, uint32_t wl, uint32_t (&e)[4]
 // (bits 4j+2..4j+3).  The draft converts them as pairs_upper converts
 // nibbles, with C_U2 in place of C_U (field sh = 0 for word 2k, 2 for 2k+1):
 // even elements C_U2 * 2^-24, odd ones 16 C_U2 * 2^-24.
-template <int SH>
+// HI: four bits further up (times 16).
+template <int SH, bool HI>
 __device__ __forceinline__ void pairs_upper2(uint32_t x, uint32_t (&e)[4]) {
+  if (HI) {
+    const uint32_t u = x << (4 - SH), v = x >> (4 + SH);
+    e[0] = u & 0x00300030u;
+    e[1] = u & 0x03000300u;
+    e[2] = v & 0x00300030u;
+    e[3] = v & 0x03000300u;
+    return;
+  }
   const uint32_t w = x >> SH, t = x >> (SH + 8);
   e[0] = w & 0x00030003u;
   e[1] = w & 0x00300030u;
   e[2] = t & 0x00030003u;
   e[3] = t & 0x00300030u;
 }
+template <bool HI>
 __device__ __forceinline__ void pairs_upper2_rt(uint32_t x, int sh, uint32_t (&e)[4]) {
+  if (HI) {
+    const uint32_t u = x << (4 - sh), v = x >> (4 + sh);
+    e[0] = u & 0x00300030u;
+    e[1] = u & 0x03000300u;
+    e[2] = v & 0x00300030u;
+    e[3] = v & 0x03000300u;
+    return;
+  }
   const uint32_t w = x >> sh, t = w >> 8;
   e[0] = w & 0x00030003u;
   e[1] = w & 0x00300030u;
@@ -1069,6 +1106,7 @@ __device__ __forceinline__ bool wait_issued(volatile int *issued, int i, uint64_
 template <int MODE, bool PK, int UB, int NW, int KIND>
 __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
   constexpr bool IDX = KIND != kContiguous, CL = KIND == kClustered;
+  using Scales = Centre<MODE, UB, IDX>;  // (IDX: drafts' codes further up, see pairs_upper)
   using C = Cfg<MODE>;
   using L = Layout<MODE>;
   constexpr int TT = C::kTailTok, S = C::kStages;
@@ -1344,7 +1382,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
       // a new piece: the finished one's partial (empty ones for pieces this
       // warp skipped), then fresh state and this head's queries
       if (cur_ord >= 0) {
-        write_partial(sm, Centre<MODE, UB>::kScale, slot(cur_ord, w), R, cg, lane, PK);
+        write_partial(sm, Scales::kScale, slot(cur_ord, w), R, cg, lane, PK);
         leave(cur_ord);
       }
       for (int o = cur_ord >= 0 ? cur_ord + 1 : ord_first; o < cur.ord; ++o) {
@@ -1420,11 +1458,11 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
         }
         // key dequant s * code + (z + kOffK s), code = 16 C_U or C_INT8:
         // bias = sum q z + kOffK sum q s; the code part scales by kScale
-        const float sl2q = prm.sl2 * Centre<MODE, UB>::kScale;
+        const float sl2q = prm.sl2 * Scales::kScale;
         const float bk0 =
-            fmaf(Centre<MODE, UB>::kOffK, bacc[2] + bacc2[2], bacc[0] + bacc2[0]) * prm.sl2;
+            fmaf(Scales::kOffK, bacc[2] + bacc2[2], bacc[0] + bacc2[0]) * prm.sl2;
         const float bk1 =
-            fmaf(Centre<MODE, UB>::kOffK, bacc[3] + bacc2[3], bacc[1] + bacc2[1]) * prm.sl2;
+            fmaf(Scales::kOffK, bacc[3] + bacc2[3], bacc[1] + bacc2[1]) * prm.sl2;
 
         // raw scores (q.k before scale and bias): four m-tiles of 16 tokens
         float s[4][4];
@@ -1466,15 +1504,15 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
             uint32_t a[4], b8[4];
             if (MODE == QS_DRAFT_UPPER4 && UB == 2) {
               if (j & 1) {
-                pairs_upper2<2>(wu0[j], a);
-                pairs_upper2<2>(wu1[j], b8);
+                pairs_upper2<2, IDX>(wu0[j], a);
+                pairs_upper2<2, IDX>(wu1[j], b8);
               } else {
-                pairs_upper2<0>(wu0[j], a);
-                pairs_upper2<0>(wu1[j], b8);
+                pairs_upper2<0, IDX>(wu0[j], a);
+                pairs_upper2<0, IDX>(wu1[j], b8);
               }
             } else {
-              pairs<MODE>(wu0[j], wl0[j], a);
-              pairs<MODE>(wu1[j], wl1[j], b8);
+              pairs<MODE, IDX>(wu0[j], wl0[j], a);
+              pairs<MODE, IDX>(wu1[j], wl1[j], b8);
             }
             mma16816(acc, a[0], b8[0], a[1], b8[1], bh0[2 * j], bh1[2 * j]);
             mma16816(acc2, a[2], b8[2], a[3], b8[3], bh0[2 * j + 1], bh1[2 * j + 1]);
@@ -1531,7 +1569,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
               const float sv = svs[2 * ml + hh];
-              const float zv = fmaf(Centre<MODE, UB>::kOff, sv, zvs[2 * ml + hh]);
+              const float zv = fmaf(Scales::kOff, sv, zvs[2 * ml + hh]);
               const float pa = fast_exp2(fmaf(s[mt][2 * hh], sl2q, c0));
               const float pb = PK ? 0.f : fast_exp2(fmaf(s[mt][2 * hh + 1], sl2q, c1));
               sm.l[0] += pa;
@@ -1562,8 +1600,8 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
           // bias is a per-lane partial summed over the eight row lanes later:
           // one lane per column takes it
           if (r == 0) {
-            sm.bv[0] = fmaf(-Centre<MODE, UB>::kMid, sp[0], sm.bv[0]);
-            sm.bv[1] = fmaf(-Centre<MODE, UB>::kMid, sp[1], sm.bv[1]);
+            sm.bv[0] = fmaf(-Scales::kMid, sp[0], sm.bv[0]);
+            sm.bv[1] = fmaf(-Scales::kMid, sp[1], sm.bv[1]);
           }
         }
         // O^T = a O^T + V^T P'  (values: quarters 2hw and 2hw+1, channel-major)
@@ -1595,11 +1633,11 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
             }
             uint32_t a[4], b8[4];
             if (MODE == QS_DRAFT_UPPER4 && UB == 2) {
-              pairs_upper2_rt(vu0, sh, a);
-              pairs_upper2_rt(vu1, sh, b8);
+              pairs_upper2_rt<IDX>(vu0, sh, a);
+              pairs_upper2_rt<IDX>(vu1, sh, b8);
             } else {
-              pairs<MODE>(vu0, vl0, a);
-              pairs<MODE>(vu1, vl1, b8);
+              pairs<MODE, IDX>(vu0, vl0, a);
+              pairs<MODE, IDX>(vu1, vl1, b8);
             }
             mma16816(d, a[0], b8[0], a[1], b8[1], bp0[2 * qq], bp1[2 * qq]);
             mma16816(d, a[2], b8[2], a[3], b8[3], bp0[2 * qq + 1], bp1[2 * qq + 1]);
@@ -1683,7 +1721,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
             }
             // fp16 values: true units, the accumulators hold O / kScale
 #pragma unroll
-            for (int k = 0; k < 4; ++k) d[k] *= 1.f / Centre<MODE, UB>::kScale;
+            for (int k = 0; k < 4; ++k) d[k] *= 1.f / Scales::kScale;
             sm.merge(md, d, a0, a1);
           }
         }
@@ -1717,7 +1755,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
   // this warp's partials for the pieces after its last unit's piece are empty
   // (all but the range's last piece go to the workspace)
   if (cur_ord >= 0 && cur_ord < ord_last) {
-    write_partial(sm, Centre<MODE, UB>::kScale, slot(cur_ord, w), R, cg, lane, PK);
+    write_partial(sm, Scales::kScale, slot(cur_ord, w), R, cg, lane, PK);
     leave(cur_ord);
   }
   for (int o = cur_ord >= 0 ? cur_ord + 1 : ord_first; o < ord_last; ++o) {
@@ -1762,7 +1800,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
   if (CL) {
     cluster_wait();  // (of the arrival at the start: every CTA runs)
     const int q = p / prm.C, seg = q / prm.K;  // (q: the cluster)
-    finish_cluster<NW>(sm, Centre<MODE, UB>::kScale, PK, smem, sbase, prm.C, p % prm.C, ncg, R,
+    finish_cluster<NW>(sm, Scales::kScale, PK, smem, sbase, prm.C, p % prm.C, ncg, R,
                        s_abort == 2, !aborted, prm.out + (size_t)seg * R * kD,
                        prm.lse ? prm.lse + (size_t)seg * R : nullptr, prm.K, q % prm.K,
                        prm.ws + (size_t)seg * prm.K * R * (kD + 4), c.arrive + seg);
@@ -1772,7 +1810,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
   chk(smem_in(smem_addr(last_part), (uint32_t)(NW * stride * 4)), 11);
   if (s_abort != 2) {
     if (cur_ord == ord_last)
-      write_partial(sm, Centre<MODE, UB>::kScale, last_part + w * stride, R, cg, lane, PK);
+      write_partial(sm, Scales::kScale, last_part + w * stride, R, cg, lane, PK);
     else
       write_empty(last_part + w * stride, R, cg, lane);
   }

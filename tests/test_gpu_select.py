@@ -83,6 +83,19 @@ def test_close_scores(torch, n):
         assert np.array_equal(run(torch, cache, q, k), paging.select(oc, q, k)), k
 
 
+@pytest.mark.parametrize("scale", [1e-4, 2e-6])
+def test_subnormal_boxes(torch, scale):
+    """Zeros and scales below the smallest normal fp16 number."""
+    rng = np.random.default_rng(11)
+    oc = metadata_cache(rng, 1, 3, [400], 400)
+    for x in (oc.kz, oc.ks):
+        x[:] = (x.view(np.float16).astype(np.float64) * scale).astype(np.float16).view(np.uint16)
+    cache = load(torch, oc, rng, paged=False)
+    for q in (h16(rng, (1, 3, 1, 128)), h16(rng, (1, 3, 1, 128), 1e-4), h16(rng, (1, 3, 1, 128), 1e3)):
+        for k in (1, 50, 200):
+            assert np.array_equal(run(torch, cache, q, k), paging.select(oc, q, k))
+
+
 def test_ties_go_to_the_lower_index(torch):
     rng = np.random.default_rng(3)
     oc = metadata_cache(rng, 2, 2, [500, 90], 500)
