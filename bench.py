@@ -44,6 +44,10 @@ G_TOK = 128
 RING = 2 * G_TOK
 
 
+#: --profile kinds of the paged and sparse calls
+LISTED = ["select", "sparse_draft", "paged_draft", "paged_verify", "paged_prefill", "read_verify"]
+
+
 def kernel_source_hash():
     """sha256 over the attention kernel sources (to tell whether a stored ncu
     traffic figure still describes the kernel that runs)."""
@@ -741,6 +745,65 @@ def gqa_calls(torch, qs, synthetic, l2, it):
     return res
 
 
+def paged_32k(torch, qs, synthetic):
+    """The 32k workload in pages of a shuffled pool: (workload, cache, prompt)."""
+    w = synthetic.llama_32k()
+    T, n = w.context[0], w.n_groups[0]
+    k, v = (torch.from_numpy(x[None]).cuda() for x in synthetic.kv_tokens(w, 0, 0, T))
+    lens = torch.tensor([T], dtype=torch.int32, device="cuda")
+    cache = qs.PagedCache(1, w.H, n + 1, n + 8)
+    order = np.random.default_rng(0).permutation(n + 8)[:n + 1].astype(np.int32)
+    cache.table.copy_(torch.from_numpy(order[None]))
+    qs.qs_state_reset(cache)
+    qs.qs_prefill_paged(cache, k, v, lens)
+    return w, cache, (k, v, lens)
+
+
+def listed_ops(torch, qs, synthetic, k_sel=32):
+    """The calls on a paged cache and on selected groups, 32k workload: name ->
+    (call, algorithmic bytes)."""
+    w, cache, (k, v, lens) = paged_32k(torch, qs, synthetic)
+    T, n, fill = w.context[0], w.n_groups[0], w.fill[0]
+    scale = 1 / np.sqrt(w.D)
+    qd, qv = (torch.from_numpy(synthetic.queries(w, i, m)).cuda() for i, m in enumerate((1, GAMMA + 1)))
+    od, ov = torch.empty_like(qd), torch.empty_like(qv)
+    ws = torch.empty(qs.qs_attn_workspace_size(cache, GAMMA + 1), dtype=torch.uint8, device="cuda")
+    sel = torch.empty((1, w.H, k_sel), dtype=torch.int32, device="cuda")
+    kr, vr = (torch.empty_like(x) for x in (k, v))
+    qs.qs_select_groups(cache, qd, sel)
+
+    def prefill():
+        qs.qs_state_reset(cache)
+        qs.qs_prefill_paged(cache, k, v, lens)
+
+    return w, cache, {
+        "select": (lambda: qs.qs_select_groups(cache, qd, sel), n * w.H * 512 + w.H * (256 + 4 * k_sel)),
+        "sparse_draft": (lambda: qs.qs_attn_decode_sparse(cache, qs.QS_DRAFT_UPPER4, sel, qd, scale, od,
+                                                          None, ws),
+                         attn_bytes(k_sel, fill, 1, True, w.H)),
+        "paged_draft": (lambda: qs.qs_attn_decode_paged(cache, qs.QS_DRAFT_UPPER4, qd, scale, od, None, ws),
+                        attn_bytes(n, fill, 1, True, w.H)),
+        "paged_verify": (lambda: qs.qs_attn_decode_paged(cache, qs.QS_VERIFY_INT8, qv, scale, ov, None, ws),
+                         attn_bytes(n, fill, GAMMA + 1, False, w.H)),
+        "paged_prefill": (prefill, prefill_bytes(T, w.H)),
+        "read_verify": (lambda: qs.qs_cache_read(cache, qs.QS_VERIFY_INT8, kr, vr),
+                        prefill_bytes(T, w.H)),
+    }
+
+
+def listed_calls(torch, qs, synthetic, l2, it):
+    """Per-call times and GB/s of the paged and sparse calls (one 32k sequence
+    of 32 heads in pages, 32 groups selected), L2 evicted before each call."""
+    w, cache, ops = listed_ops(torch, qs, synthetic)
+    res = {"workload": w.name + "_paged"}
+    for name, (call, nb) in ops.items():
+        us = time_calls(torch, call, lambda: None, it, l2)
+        res[name + "_us"] = round(us, 2)
+        res[name + "_gbs"] = round(nb / us / 1e3, 1)
+    assert np.all(qs.qs_get_errors(cache) == 0)
+    return res
+
+
 def native(args):
     import torch
     import torch.distributed as dist
@@ -838,6 +901,7 @@ def native(args):
         del kp, vp, pc
     main_32k = w.name == synthetic.llama_32k().name
     gqa = gqa_calls(torch, qs, synthetic, l2, it) if main_32k else None
+    listed = listed_calls(torch, qs, synthetic, l2, it) if main_32k else None
     two_bit = two_bit_calls(torch, qs, synthetic, w, l2, it) if main_32k else None
     # speculative acceptance for the round (synthetic probabilities over a
     # 32,000-token vocabulary): accept/reject, the emitted token, n_drop
@@ -938,6 +1002,7 @@ def native(args):
         "prefill_gbs": None if prefill_gbs is None else round(prefill_gbs, 1),
         "spec_accept_us": round(spec_us, 2),
         "gqa": gqa,
+        "listed": listed,
         "two_bit_draft": two_bit,
         "roofline": {"bound": "hbm", "kernel": "qs_attn_decode %s (split_kernel: split-KV attention + LSE merge, one launch)" % dominant[0],
                      "launch_us": round(dominant[2], 2),
@@ -1097,6 +1162,13 @@ def profile(args):
     from hierarchical_quantized_kv_gb300 import qs, synthetic
     if args.profile.startswith("gqa_"):
         return profile_gqa(args, torch, qs, synthetic)
+    if args.profile in LISTED:
+        w, cache, ops = listed_ops(torch, qs, synthetic)
+        for _ in range(args.profile_calls):
+            ops[args.profile][0]()
+        torch.cuda.synchronize()
+        assert np.all(qs.qs_get_errors(cache) == 0)
+        return print("profile run ok: %d %s calls on %s" % (args.profile_calls, args.profile, w.name))
     w = synthetic.CONFIGS[args.config]()
     r = Round(torch, w, seed=0)
     for i in range(args.warmup if args.profile == "step" else 0):
@@ -1163,7 +1235,7 @@ def main():
     ap.add_argument("--no-configs", action="store_true",
                     help="skip the rounds on the other workloads")
     ap.add_argument("--profile", choices=["draft", "verify", "flush", "prefill", "step", "gqa_draft",
-                                          "gqa_verify"])
+                                          "gqa_verify"] + LISTED)
     ap.add_argument("--profile-calls", type=int, default=3)
     args = ap.parse_args()
     if args.profile:

@@ -873,6 +873,10 @@ __device__ __noinline__ void merge_rows(const float *srcA, int cgA, int kstrideA
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
+// (an arrival that publishes nothing)
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -1307,7 +1311,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
 
   // clustered: the partials meet in shared memory, so the cluster must have
   // started by then
-  if (CL) cluster_arrive();
+  if (CL) cluster_arrive_relaxed();
 
   // the warps reach the range's last segment mid-range: start its queries
   // towards L1 now (two 128-byte lines per row; a copy in shared memory was

@@ -54,7 +54,8 @@ def test_select(torch, k, n_q, group, paged):
 
 
 @pytest.mark.parametrize("B,H,n,k", [(1, 2, 1022, 64), (1, 1, 5000, 300), (2, 3, 1300, 1299),
-                                     (1, 2, 300, 299), (40, 32, 20, 3), (1, 32, 254, 32)])
+                                     (1, 2, 300, 299), (40, 32, 20, 3), (1, 32, 254, 32),
+                                     (1, 1, 12800, 500)])
 def test_sizes(torch, B, H, n, k):
     """Clusters of one to eight CTAs, several passes a warp."""
     rng = np.random.default_rng(n + k)
