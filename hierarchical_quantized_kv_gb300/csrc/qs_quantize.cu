@@ -541,9 +541,25 @@ __global__ void __launch_bounds__(32 * QW, 20 / QW)
     uint4 *kd = reinterpret_cast<uint4 *>(c.buf_k + bh * kRing * kD);
     uint4 *vd = reinterpret_cast<uint4 *>(c.buf_v + bh * kRing * kD);
     if (chk(i1 <= kRing && (size_t)ng * kG + i1 <= (size_t)T, 23))
-      for (int e = i0 * (kD / 8) + tid; e < i1 * (kD / 8); e += 32 * QW) {
-        kd[e] = ks[e];
-        vd[e] = vs[e];
+      // four rows' pieces a thread in flight at once
+      for (int e0 = i0 * (kD / 8) + tid; e0 < i1 * (kD / 8); e0 += 4 * 32 * QW) {
+        uint4 xk[4], xv[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int e = e0 + u * 32 * QW;
+          if (e < i1 * (kD / 8)) {
+            xk[u] = ks[e];
+            xv[u] = vs[e];
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int e = e0 + u * 32 * QW;
+          if (e < i1 * (kD / 8)) {
+            kd[e] = xk[u];
+            vd[e] = xv[u];
+          }
+        }
       }
   }
   __syncthreads();

@@ -108,13 +108,27 @@ __global__ void __launch_bounds__(kReadThreads)
   if (u >= ng) {
     const int fill = min(max(st[QS_ST_FILL], 0), kRing);
     const int i0 = (u - ng) * kG, base = (st[QS_ST_HALF_BASE] & 1) * kG;
-    for (int e = tid; e < kG * (kD / 8); e += kReadThreads) {
-      const int r = e / (kD / 8), col = 8 * (e % (kD / 8));
-      if (r < r_lo || r >= r_hi || u - ng > 1 || i0 + r >= fill) continue;
-      const size_t src = (bh * kRing + ((base + i0 + r) & (kRing - 1))) * kD + col;
-      const long long dst = out0 + (long long)r * kD + col;
-      if (k_out) *reinterpret_cast<uint4 *>(k_out + dst) = *reinterpret_cast<const uint4 *>(c.buf_k + src);
-      if (v_out) *reinterpret_cast<uint4 *>(v_out + dst) = *reinterpret_cast<const uint4 *>(c.buf_v + src);
+    const int hi = min(r_hi, fill - i0);  // rows [r_lo, hi) of the unit
+    if (u - ng > 1) return;
+    // (four rows' pieces a thread in flight at once)
+    for (int e0 = r_lo * (kD / 8) + tid; e0 < hi * (kD / 8); e0 += 4 * kReadThreads) {
+      uint4 xk[4], xv[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int e = e0 + n * kReadThreads, r = e / (kD / 8);
+        if (e >= hi * (kD / 8)) continue;
+        const size_t src = (bh * kRing + ((base + i0 + r) & (kRing - 1))) * kD + 8 * (e % (kD / 8));
+        if (k_out) xk[n] = *reinterpret_cast<const uint4 *>(c.buf_k + src);
+        if (v_out) xv[n] = *reinterpret_cast<const uint4 *>(c.buf_v + src);
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int e = e0 + n * kReadThreads;
+        if (e >= hi * (kD / 8)) continue;
+        const long long dst = out0 + (long long)e * 8;
+        if (k_out) *reinterpret_cast<uint4 *>(k_out + dst) = xk[n];
+        if (v_out) *reinterpret_cast<uint4 *>(v_out + dst) = xv[n];
+      }
     }
     return;
   }

@@ -1,7 +1,8 @@
-// qs_split.cuh -- the kernel of the split-KV decode attention over the hierarchical quantized KV
-// cache (draft: C_U only, or C_U2 in the two-bit layout; verify: INT8 =
-// 16 C_U + C_L) plus the fp16 buffer, with the log-sum-exp combine of the
-// splits in the same kernel.
+// qs_split.cuh -- the kernel of the split-KV decode attention over the
+// hierarchical quantized KV cache (draft: C_U only, or C_U2 in the two-bit
+// layout; verify: INT8 = 16 C_U + C_L) plus the fp16 buffer, with the
+// log-sum-exp combine of the splits in the same kernel.  Its entry points:
+// qs_attn.cu (contiguous caches), qs_attn_list.cu (pages, selected groups).
 //
 // Sources: "QuantSpec Guide: Self-Speculative Decoding & Quantized KV",
 // "1. Hierarchical Two-Level Quantization with Bit-Sharing" (draft loads only
@@ -37,6 +38,11 @@
 //    warps' partials (log-sum-exp); a segment split across CTAs is
 //    finished by whichever of them arrives last on the segment's counter,
 //    so the whole call is one kernel launch.
+//  * Listed variants take a segment's groups from a list (the selected groups,
+//    the page table, or one through the other), looked up beside the first
+//    copies.  Where a few equal segments fill the GPU, a cluster of CTAs takes
+//    each (clustered variant): no tables over the batch, and the partials meet
+//    in distributed shared memory instead of the workspace.
 #pragma once
 
 #include <limits.h>
@@ -1192,10 +1198,10 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
 
   auto append = [&]() {
     // The fused append, by the last warp.  Every CTA has read the counters
-    // above; the CTA whose ticket comes last commits the
-    // appended counters (no CTA of this launch reads them again).  The new
-    // tokens enter the ring slots past the old fill, which no CTA of this
-    // launch reads (its copies of those rows come from k_new / v_new).
+    // above; the CTA whose ticket comes last commits the appended counters (no
+    // CTA of this launch reads them again).  The new tokens enter the ring
+    // slots past the old fill, which no CTA of this launch reads (its copies
+    // of those rows come from k_new / v_new).
     if (lane == 0 && atom_add_acq_rel_gpu(&c.state[QS_ST_TICKET], 1) == (int)gridDim.x - 1) {
       for (int b = 0; b < c.B; ++b) {
         int32_t *st = c.state + (size_t)b * QS_STATE_WORDS;
