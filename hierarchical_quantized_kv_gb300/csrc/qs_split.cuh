@@ -338,6 +338,9 @@ struct Centre {
   // draft's code step
   static constexpr float kScale =
       16777216.f * (kDraft ? kStep / (!HI ? 1.f : UB == 2 ? 16.f : 4.f) : 1.f);
+  // scores of the listed drafts: q s_K is carried fourfold (see kFour)
+  static constexpr bool kFour = kDraft && HI;
+  static constexpr float kScaleK = kFour ? kScale / 4.f : kScale;
 };
 
 template <int MODE, bool HI>
@@ -1447,18 +1450,26 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
           const uint4 sw = lds128(st + kOffMeta + QS_META_K_SCALE * 256 + 16 * (4 * i4 + cq));
           const uint4 zw = lds128(st + kOffMeta + QS_META_K_ZERO * 256 + 16 * (4 * i4 + cq));
           const int k0 = 2 * i4, k1 = 2 * i4 + 1;
-          uint32_t s1 = sw.y, s3 = sw.w;
-          if (MODE == QS_DRAFT_UPPER4) {
+          uint32_t s0 = sw.x, s1 = sw.y, s2 = sw.z, s3 = sw.w;
+          if (Scales::kFour) {
+            // four times q s and q s / 4: the lo parts, subnormal for usual
+            // scales, keep two bits more (log-sum-exp off by under 1e-6 of
+            // itself instead of up to 3e-6), for |q s| below 16,000
+            s0 = hmul2_u32(s0, 0x44004400u);  // fp16 (4, 4)
+            s2 = hmul2_u32(s2, 0x44004400u);
+            s1 = hmul2_u32(s1, 0x34003400u);  // fp16 (1/4, 1/4)
+            s3 = hmul2_u32(s3, 0x34003400u);
+          } else if (MODE == QS_DRAFT_UPPER4) {
             s1 = hmul2_u32(s1, 0x2C002C00u);  // fp16 (1/16, 1/16)
             s3 = hmul2_u32(s3, 0x2C002C00u);
           }
-          bh0[k0] = hmul2_u32(qp0[k0], sw.x);
+          bh0[k0] = hmul2_u32(qp0[k0], s0);
           bh1[k0] = hmul2_u32(qp1[k0], s1);
-          bh0[k1] = hmul2_u32(qp0[k1], sw.z);
+          bh0[k1] = hmul2_u32(qp0[k1], s2);
           bh1[k1] = hmul2_u32(qp1[k1], s3);
-          bl0[k0] = hfma2_neg_u32(qp0[k0], sw.x, bh0[k0]);
+          bl0[k0] = hfma2_neg_u32(qp0[k0], s0, bh0[k0]);
           bl1[k0] = hfma2_neg_u32(qp1[k0], s1, bh1[k0]);
-          bl0[k1] = hfma2_neg_u32(qp0[k1], sw.z, bh0[k1]);
+          bl0[k1] = hfma2_neg_u32(qp0[k1], s2, bh0[k1]);
           bl1[k1] = hfma2_neg_u32(qp1[k1], s3, bh1[k1]);
           if (PK && (r & 1)) {  // odd B columns carry the lo part
             bh0[k0] = bl0[k0]; bh1[k0] = bl1[k0]; bh0[k1] = bl0[k1]; bh1[k1] = bl1[k1];
@@ -1468,7 +1479,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
         }
         // key dequant s * code + (z + kOffK s), code = 16 C_U or C_INT8:
         // bias = sum q z + kOffK sum q s; the code part scales by kScale
-        const float sl2q = prm.sl2 * Scales::kScale;
+        const float sl2q = prm.sl2 * Scales::kScaleK;
         const float bk0 =
             fmaf(Scales::kOffK, bacc[2] + bacc2[2], bacc[0] + bacc2[0]) * prm.sl2;
         const float bk1 =

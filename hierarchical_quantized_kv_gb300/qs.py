@@ -281,6 +281,7 @@ def qs_prefill(cache, k, v, lens, stream=None):
 
 def qs_quantize_flush_paged(cache, mask=None, stream=None):
     """qs_quantize_flush on a PagedCache."""
+    assert mask is None or (mask.numel() == cache.B and mask.element_size() == 1)
     _check("qs_quantize_flush_paged", lib().qs_quantize_flush_paged(
         cache._ref, cache._pages_ref, _ptr(mask), _stream(stream)))
 
@@ -294,6 +295,7 @@ def qs_quantize_flush_due_paged(cache, n_next, stream=None):
 def qs_prefill_paged(cache, k, v, lens, stream=None):
     """qs_prefill on a PagedCache."""
     assert k.is_contiguous() and v.is_contiguous() and k.shape == v.shape
+    assert k.shape[:2] == (cache.B, cache.H) and lens.numel() == cache.B and lens.element_size() == 4
     _check("qs_prefill_paged", lib().qs_prefill_paged(cache._ref, cache._pages_ref, _ptr(k), _ptr(v),
                                                       int(k.shape[2]), _ptr(lens), _stream(stream)))
 
@@ -304,7 +306,8 @@ def qs_cache_read(cache, mode, k, v, tok0=0, stream=None):
     a sequence's last token stay as they were."""
     T = (v if k is None else k).shape[2] if k is not None or v is not None else 0
     for t in (k, v):
-        assert t is None or (t.is_contiguous() and t.shape == (cache.B, cache.H, T, cache.D))
+        assert t is None or (t.is_contiguous() and t.element_size() == 2 and
+                             t.shape == (cache.B, cache.H, T, cache.D))
     _check("qs_cache_read", lib().qs_cache_read(cache._ref, cache._pages_ref, int(mode), int(tok0),
                                                 int(T), _ptr(k), _ptr(v), _stream(stream)))
 
@@ -379,30 +382,53 @@ def qs_attn_decode_append(cache, mode, k_new, v_new, q, softmax_scale, out, lse=
         float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)))
 
 
-def _n_new(k_new, v_new):
+def _n_new(cache, k_new, v_new):
     if k_new is None and v_new is None:
         return 0
     assert k_new.is_contiguous() and v_new.is_contiguous() and k_new.shape == v_new.shape
+    assert k_new.shape[0] == cache.B and k_new.shape[1] == cache.H and k_new.shape[3] == cache.D
     return k_new.shape[2]
+
+
+def _check_queries(cache, q, group, out=None, lse=None):
+    """q (and out) fp16 [B, H * group, n_q, D] contiguous, lse fp32 of the rows."""
+    shape = q.shape
+    b, h, n_q, d = shape
+    assert b == cache.B and h == cache.H * group and d == cache.D
+    assert q.is_contiguous() and q.element_size() == 2
+    if out is not None:
+        assert out.shape == shape and out.is_contiguous() and out.element_size() == 2
+    if lse is not None:
+        assert lse.numel() == b * h * n_q and lse.is_contiguous() and lse.element_size() == 4
+    return n_q
+
+
+def _check_selection(cache, sel):
+    """sel: int32 [B, H, k] contiguous."""
+    b, h, k = sel.shape
+    assert b == cache.B and h == cache.H
+    assert sel.is_contiguous() and sel.element_size() == 4 and not sel.is_floating_point()
+    return k
 
 
 def qs_attn_decode_paged(cache, mode, q, softmax_scale, out, lse=None, workspace=None, group=1,
                          k_new=None, v_new=None, stream=None):
     """qs_attn_decode_gqa on a PagedCache, or with k_new, v_new (fp16 [B, H,
     n_new, D]) qs_attn_decode_append on it."""
+    n_q = _check_queries(cache, q, group, out, lse)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("qs_attn_decode_paged", lib().qs_attn_decode_paged(
-        cache._ref, cache._pages_ref, int(mode), _ptr(k_new), _ptr(v_new), _n_new(k_new, v_new),
-        _ptr(q), q.shape[2], int(group), float(softmax_scale), _ptr(out), _ptr(lse),
+        cache._ref, cache._pages_ref, int(mode), _ptr(k_new), _ptr(v_new), _n_new(cache, k_new, v_new),
+        _ptr(q), n_q, int(group), float(softmax_scale), _ptr(out), _ptr(lse),
         _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 def qs_select_groups(cache, q, sel, group=1, stream=None):
     """For each KV head the sel.shape[2] groups whose keys could score highest
     against q (fp16 [B, H*group, n_q, D]) into sel, int32 [B, H, k]."""
-    assert sel.is_contiguous() and sel.shape[:2] == (cache.B, cache.H)
+    n_q, k = _check_queries(cache, q, group), _check_selection(cache, sel)
     _check("qs_select_groups", lib().qs_select_groups(
-        cache._ref, cache._pages_ref, _ptr(q), q.shape[2], int(group), sel.shape[2], _ptr(sel),
+        cache._ref, cache._pages_ref, _ptr(q), n_q, int(group), k, _ptr(sel),
         _stream(stream)))
 
 
@@ -411,11 +437,11 @@ def qs_attn_decode_sparse(cache, mode, sel, q, softmax_scale, out, lse=None, wor
     """Decode attention (cache: a Cache or a PagedCache) over the groups named
     in sel, int32 [B, H, k] (-1: none), and the buffer; k_new, v_new as for
     qs_attn_decode_paged."""
-    assert sel.is_contiguous() and sel.shape[:2] == (cache.B, cache.H)
+    n_q, k = _check_queries(cache, q, group, out, lse), _check_selection(cache, sel)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("qs_attn_decode_sparse", lib().qs_attn_decode_sparse(
-        cache._ref, cache._pages_ref, int(mode), _ptr(sel), sel.shape[2], _ptr(k_new), _ptr(v_new),
-        _n_new(k_new, v_new), _ptr(q), q.shape[2], int(group), float(softmax_scale), _ptr(out),
+        cache._ref, cache._pages_ref, int(mode), _ptr(sel), k, _ptr(k_new), _ptr(v_new),
+        _n_new(cache, k_new, v_new), _ptr(q), n_q, int(group), float(softmax_scale), _ptr(out),
         _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)))
 
 

@@ -150,3 +150,35 @@ def test_select_arguments(L, paged):
     assert f(q=ctypes.c_void_p(0x20008)) == qs.QS_ERR_ALIGN
     assert f(sel=ctypes.c_void_p(0x20002)) == qs.QS_ERR_ALIGN
     assert f(c=cache(paged, cap_groups=12801)) == qs.QS_ERR_UNSUPPORTED
+
+
+def test_binding_checks_shapes_and_types(L):
+    """The binding turns tensors that do not fit the cache away (no GPU: CPU
+    tensors stand in, nothing is called)."""
+    torch = pytest.importorskip("torch")
+    c = qs.PagedCache(2, 3, 4, 5, device="cpu")
+    f16 = lambda *s: torch.zeros(s, dtype=torch.float16)
+    q, sel = f16(2, 6, 1, 128), torch.zeros((2, 3, 2), dtype=torch.int32)
+    lens = torch.zeros(2, dtype=torch.int32)
+    bad = [
+        lambda: qs.qs_attn_decode_paged(c, 0, q, 0.1, f16(2, 6, 1, 128), group=1),
+        lambda: qs.qs_attn_decode_paged(c, 0, q, 0.1, f16(2, 6, 2, 128), group=2),
+        lambda: qs.qs_attn_decode_paged(c, 0, q.float(), 0.1, q, group=2),
+        lambda: qs.qs_attn_decode_paged(c, 0, f16(2, 6, 128, 2).transpose(2, 3), 0.1, f16(2, 6, 2, 128),
+                                        group=2),
+        lambda: qs.qs_attn_decode_paged(c, 0, q, 0.1, f16(2, 6, 1, 128), torch.zeros(5), group=2),
+        lambda: qs.qs_attn_decode_paged(c, 0, q, 0.1, f16(2, 6, 1, 128), group=2, k_new=f16(2, 6, 1, 128),
+                                        v_new=f16(2, 6, 1, 128)),
+        lambda: qs.qs_attn_decode_sparse(c, 0, sel.long(), q, 0.1, f16(2, 6, 1, 128), group=2),
+        lambda: qs.qs_attn_decode_sparse(c, 0, sel[:1], q, 0.1, f16(2, 6, 1, 128), group=2),
+        lambda: qs.qs_select_groups(c, q, sel.float(), group=2),
+        lambda: qs.qs_select_groups(c, q, sel),
+        lambda: qs.qs_cache_read(c, 1, f16(2, 3, 5, 64), None),
+        lambda: qs.qs_cache_read(c, 1, torch.zeros((2, 3, 5, 128)), None),
+        lambda: qs.qs_prefill_paged(c, f16(2, 6, 5, 128), f16(2, 6, 5, 128), lens),
+        lambda: qs.qs_prefill_paged(c, f16(2, 3, 5, 128), f16(2, 3, 5, 128), lens[:1]),
+        lambda: qs.qs_quantize_flush_paged(c, torch.zeros(3, dtype=torch.uint8)),
+    ]
+    for call in bad:
+        with pytest.raises(AssertionError):
+            call()
