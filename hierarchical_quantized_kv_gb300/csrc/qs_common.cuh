@@ -194,7 +194,9 @@ __device__ __forceinline__ size_t group_slots(const qs_cache &c, const Pages &pg
 __device__ __forceinline__ long long group_slot(const qs_cache &c, const Pages &pg, int b, int h,
                                                 int g) {
   if (!pg.table) return ((long long)b * c.H + h) * c.cap_groups + g;
-  const int page = __ldg(pg.table + (size_t)b * c.cap_groups + g);
+  // (a plain load, not the read-only path: the kernel before this one in the
+  // stream may have written the table while this one was already resident)
+  const int page = pg.table[(size_t)b * c.cap_groups + g];
   return page >= 0 && page < pg.n_pages ? (long long)page * c.H + h : -1;
 }
 

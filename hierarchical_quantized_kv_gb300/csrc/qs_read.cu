@@ -19,9 +19,11 @@ constexpr int kReadThreads = 256;
 // rows of a transposed 8x8 store fall into different banks
 constexpr int kTileRow = 2 * kD + 16;
 
-__device__ __forceinline__ uint32_t ldg_stream(const uint8_t *p) {
+// (not the read-only path: the kernel before may have written the planes while
+// this one was already resident)
+__device__ __forceinline__ uint32_t ld_stream(const uint8_t *p) {
   uint32_t v;
-  asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.b32 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
 
@@ -34,12 +36,12 @@ template <int MODE, int UB>
 __device__ __forceinline__ Raw load_raw(const uint8_t *up, const uint8_t *lo, int W) {
   Raw r{0, 0, 0};
   if (UB == 4) {
-    r.u = ldg_stream(up + 4 * W);
+    r.u = ld_stream(up + 4 * W);
   } else {
-    r.u = ldg_stream(up + 4 * (W >> 1));
-    if (MODE == QS_VERIFY_INT8) r.m = ldg_stream(up + 4096 + 4 * (W >> 1));
+    r.u = ld_stream(up + 4 * (W >> 1));
+    if (MODE == QS_VERIFY_INT8) r.m = ld_stream(up + 4096 + 4 * (W >> 1));
   }
-  if (MODE == QS_VERIFY_INT8) r.l = ldg_stream(lo + 4 * W);
+  if (MODE == QS_VERIFY_INT8) r.l = ld_stream(lo + 4 * W);
   return r;
 }
 

@@ -155,15 +155,16 @@ __device__ __forceinline__ int kmeta_channel(int p) {
   return 32 * ((p >> 3) & 3) + 8 * (p >> 5) + 2 * ((p >> 2) & 1) + ((p >> 1) & 1) + 4 * (p & 1);
 }
 
-__device__ __forceinline__ uint4 ldg16(const uint16_t *p) {
-  return __ldg(reinterpret_cast<const uint4 *>(p));
+// (plain loads: the kernel before may have written what this one reads while it
+// was already resident, which the read-only path does not allow for)
+__device__ __forceinline__ uint4 ld16(const uint16_t *p) {
+  return *reinterpret_cast<const uint4 *>(p);
 }
 
 // Grid (cluster size, H, B).  NCG: column groups of eight query rows.
 template <int NCG>
 __global__ void __launch_bounds__(kSelThreads)
-    select_kernel(qs_cache c, Pages pg, const uint16_t *__restrict__ q, int R, int k_sel,
-                  int32_t *__restrict__ sel) {
+    select_kernel(qs_cache c, Pages pg, const uint16_t *q, int R, int k_sel, int32_t *sel) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ BlockScratch S;
   // the first CTA's: largest sum of magnitudes, smallest and largest key of a score
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kSelThreads)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint4 x = make_uint4(0, 0, 0, 0);
-      if (row < R) x = ldg16(qh + (size_t)row * kD + 32 * cq + 8 * i);
+      if (row < R) x = ld16(qh + (size_t)row * kD + 32 * cq + 8 * i);
       q0[g][2 * i] = prmt(x.x, x.z, 0x5410);
       q1[g][2 * i] = prmt(x.x, x.z, 0x7632);
       q0[g][2 * i + 1] = prmt(x.y, x.w, 0x5410);
@@ -246,8 +247,8 @@ __global__ void __launch_bounds__(kSelThreads)
         zr[j][i] = sr[j][i] = make_uint4(0, 0, 0, 0);
         if (good[j]) {
           const uint16_t *m = c.meta + (size_t)place * 4 * 128 + 8 * (4 * i + cq);
-          sr[j][i] = ldg16(m + QS_META_K_SCALE * 128);
-          zr[j][i] = ldg16(m + QS_META_K_ZERO * 128);
+          sr[j][i] = ld16(m + QS_META_K_SCALE * 128);
+          zr[j][i] = ld16(m + QS_META_K_ZERO * 128);
         }
       }
     }
@@ -374,13 +375,13 @@ __global__ void __launch_bounds__(kSelThreads)
       uint4 sw = make_uint4(0, 0, 0, 0), zw = sw;
       if (place >= 0) {
         const uint16_t *mt = c.meta + (size_t)place * 4 * 128 + 8 * l;
-        sw = ldg16(mt + QS_META_K_SCALE * 128);
-        zw = ldg16(mt + QS_META_K_ZERO * 128);
+        sw = ld16(mt + QS_META_K_SCALE * 128);
+        zw = ld16(mt + QS_META_K_ZERO * 128);
       }
       Pair best{-INFINITY, 0.f};
 #pragma unroll 2
       for (int row = 0; row < R; ++row) {
-        const uint4 qw = ldg16(qh + (size_t)row * kD + ch);
+        const uint4 qw = ld16(qh + (size_t)row * kD + ch);
         // positions 2 x, 2 x + 1 of the eight: channels c, c + 4 with c = 0, 1, 2, 3
         const uint32_t qp[4] = {prmt(qw.x, qw.z, 0x5410), prmt(qw.x, qw.z, 0x7632),
                                 prmt(qw.y, qw.w, 0x5410), prmt(qw.y, qw.w, 0x7632)};

@@ -507,7 +507,7 @@ __device__ __noinline__ int unit_place(const Params &prm, int b, int h, int u) {
   int32_t *st = c.state + (size_t)b * QS_STATE_WORDS;
   int g = u;
   if (prm.sel) {
-    g = __ldg(prm.sel + ((size_t)b * c.H + h) * prm.k_sel + u);
+    g = prm.sel[((size_t)b * c.H + h) * prm.k_sel + u];  // (plain: see group_slot)
     if (g == -1) return -1;
     if (g < 0 || g >= min(max(st[QS_ST_N_GROUPS], 0), c.cap_groups)) {
       atomicOr(&st[QS_ST_ERR], QS_DEV_SELECT);
