@@ -26,8 +26,8 @@ constexpr int kSlice = kD / kParts;  // key channels / value tokens per CTA
 // by instruction issue like a prefill, where four are best (8 x 32 heads: 9.3 us;
 // eight 11.3, sixteen 15.1).  In a prefill of many waves, what a thread does once
 // per quarter (addresses, scales) counts: four warps, twice the elements a
-// thread, 157 us for 32 heads of 32k tokens (0.76 of the copy bandwidth's rate;
-// eight: 177).  A prompt of one or two quarters per CTA is a chain again (four
+// thread, 147 us for 32 heads of 32k tokens (0.82 of the copy bandwidth's rate;
+// eight: 175).  A prompt of one or two quarters per CTA is a chain again (four
 // sequences of 1k tokens and 8 heads: eight warps 7.4 us, four 8.7), and a very
 // short one takes sixteen (two heads of 1k tokens: 3.8 us; eight 5.0, four 7.6).
 constexpr int kFlushWarps = 16, kBatchFlushWarps = 4;
@@ -37,17 +37,25 @@ constexpr int kPrefillQuarters = 8;
 
 // One CTA owns key channels [32p, 32p+32) (one 16-byte column of every key
 // row) and value tokens [32p, 32p+32) (value quarter p).
-// Value codes in shared memory: rows of 144 bytes, so that the four token
-// pairs a group of lanes reads fall into different banks.
-constexpr int kCodeRow = kD + 16;
+// Value codes in shared memory: blocks of 32 bytes of a row swapped by its
+// number, so that the four token pairs a group of lanes reads (and the four
+// tokens half a warp writes) fall into different banks.
+__device__ __forceinline__ int code_col(int row, int col) { return col ^ (32 * ((row >> 1) & 3)); }
 template <int QW>
 struct FlushSmem {
   __half k[kG][kSlice];          // keys of the slice   [token][channel - 32p]
   __half v[kSlice][kD];          // values of the slice [token - 32p][channel]
-  uint8_t vc[kSlice][kCodeRow];  // value codes
-  float kzf[kSlice], krf[kSlice];  // key zero, reciprocal of the key scale
-  uint32_t kmin[QW][kSlice / 2], kmax[QW][kSlice / 2];  // half2 per channel pair
-  uint16_t ks[kSlice], kz[kSlice], vs[kSlice], vz[kSlice];
+  uint8_t vc[kSlice][kD];        // value codes
+  union {
+    struct {
+      uint32_t kmin[QW][kSlice / 2], kmax[QW][kSlice / 2];  // half2 per channel pair
+    };
+    struct {  // (written by the warp that has read those)
+      float kzf[kSlice], krf[kSlice];  // key zero, reciprocal of the key scale
+      uint16_t ks[kSlice], kz[kSlice];
+    };
+  };
+  uint16_t vs[kSlice], vz[kSlice];
   int act, base, g;
 };
 
@@ -147,6 +155,24 @@ __device__ __forceinline__ void store_upper(uint8_t *base, int W, uint32_t w, bo
   const uint32_t v = (W & 1) ? ((other & 0x33333333u) | ((w & 0x33333333u) << 2))
                              : (((w >> 2) & 0x33333333u) | (other & 0xCCCCCCCCu));
   *reinterpret_cast<uint32_t *>(base + (W & 1 ? kG * kD / 4 : 0) + 4 * (W >> 1)) = v;
+}
+
+// Transposes the 4 x 4 words of four neighbouring lanes (m = lane % 4): word j of
+// lane m goes to word m of lane j.
+__device__ __forceinline__ void transpose4(uint32_t (&x)[4], int m) {
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    const bool hi = m & o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j & o) continue;
+      const uint32_t y = __shfl_xor_sync(0xffffffffu, hi ? x[j] : x[j | o], o);
+      if (hi)
+        x[j] = y;
+      else
+        x[j | o] = y;
+    }
+  }
 }
 
 // Position of channel c in a key scale / zero row (inverse of the header's
@@ -258,6 +284,8 @@ __device__ void quantize_loaded(FlushSmem<QW> &S, const __half (*kt)[kSlice],
     uint16_t sb, zb;
     float sf, zf;
     scale_zero(half_bits_to_float(mn >> sh), half_bits_to_float(mx >> sh), sb, zb, sf, zf);
+    static_assert(kSlice == 32, "one warp");
+    __syncwarp();
     S.ks[tid] = sb;
     S.kz[tid] = zb;
     S.kzf[tid] = zf;
@@ -269,10 +297,10 @@ __device__ void quantize_loaded(FlushSmem<QW> &S, const __half (*kt)[kSlice],
     constexpr int kLt = kQThreads / kSlice, kCh = kD / 8 / kLt;
     static_assert(kLt >= 4 && kLt <= 16 && kCh >= 1, "128 to 512 threads");
     const int t = tid / kLt, lt = tid % kLt;
-    // run i of a thread: with four threads a token, odd tokens take the runs of
-    // a pair the other way round (two rows of 64 bytes otherwise meet in one
-    // half of the banks)
-    auto run = [&](int i) { return 8 * (lt + kLt * (kLt == 4 ? i ^ (t & 1) : i)); };
+    // run i of a thread: with four threads a token, odd tokens take the runs from
+    // the last one down (two rows of 64 bytes otherwise meet in one half of the
+    // banks)
+    auto run = [&](int i) { return 8 * (lt + kLt * (kLt == 4 ? i ^ (3 * (t & 1)) : i)); };
     uint4 x[kCh];
     uint32_t mn = 0x7C007C00u, mx = 0xFC00FC00u;
 #pragma unroll
@@ -296,7 +324,7 @@ __device__ void quantize_loaded(FlushSmem<QW> &S, const __half (*kt)[kSlice],
     const float zs[8] = {zf, zf, zf, zf, zf, zf, zf, zf}, rs[8] = {rf, rf, rf, rf, rf, rf, rf, rf};
 #pragma unroll
     for (int i = 0; i < kCh; ++i) {
-      *reinterpret_cast<uint2 *>(&S.vc[t][run(i)]) = codes8<false>(
+      *reinterpret_cast<uint2 *>(&S.vc[t][code_col(t, run(i))]) = codes8<false>(
           &vt[t][run(i)], x[i], zs, rs, [&](int) { return zf; }, [&](int) { return sf; });
     }
   }
@@ -309,9 +337,10 @@ __device__ void quantize_loaded(FlushSmem<QW> &S, const __half (*kt)[kSlice],
     const int i = tid - (kQThreads - kD), m = i & 3, d0 = 4 * (i >> 2);
     uint32_t x[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      x[j] = *reinterpret_cast<const uint32_t *>(
-          &S.vc[2 * m + (j >> 2) + 8 * (j & 1) + 16 * ((j >> 1) & 1)][d0]);
+    for (int j = 0; j < 8; ++j) {
+      const int t = 2 * m + (j >> 2) + 8 * (j & 1) + 16 * ((j >> 1) & 1);
+      x[j] = *reinterpret_cast<const uint32_t *>(&S.vc[t][code_col(t, d0)]);
+    }
     // bytes of four rows (even or odd j) to a word per channel
     uint32_t wrd[2][4];
 #pragma unroll
@@ -323,13 +352,29 @@ __device__ void quantize_loaded(FlushSmem<QW> &S, const __half (*kt)[kSlice],
       wrd[e][2] = prmt(f, g, 0x5410);
       wrd[e][3] = prmt(f, g, 0x7632);
     }
+    uint32_t up[4], lo[4];
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-      const int W = 4 * (part * kD + d0 + d) + m;
-      store_upper(c.v_upper + grp * kG * (kD / 2), W, upper_nibbles(wrd[0][d], wrd[1][d]), two_bit);
-      *reinterpret_cast<uint32_t *>(c.v_lower + grp * kG * (kD / 2) + 4 * W) =
-          lower_nibbles(wrd[0][d], wrd[1][d]);
+      up[d] = upper_nibbles(wrd[0][d], wrd[1][d]);
+      lo[d] = lower_nibbles(wrd[0][d], wrd[1][d]);
     }
+    // word m of four channels to the four words of channel d0 + m, which lie
+    // together (a store of 16 bytes a lane; words stored one by one fill half a
+    // sector each: 32 heads of 32k tokens 156 us, two-bit layout 172, against 152 and
+    // 159)
+    transpose4(up, m);
+    transpose4(lo, m);
+    const int W = 4 * (part * kD + d0 + m);
+    uint8_t *vu = c.v_upper + grp * kG * (kD / 2);
+    if (two_bit) {
+      *reinterpret_cast<uint2 *>(vu + 2 * W) =
+          make_uint2(bitsel(up[0] >> 2, up[1], 0x33333333u), bitsel(up[2] >> 2, up[3], 0x33333333u));
+      *reinterpret_cast<uint2 *>(vu + kG * kD / 4 + 2 * W) =
+          make_uint2(bitsel(up[0], up[1] << 2, 0x33333333u), bitsel(up[2], up[3] << 2, 0x33333333u));
+    } else {
+      *reinterpret_cast<uint4 *>(vu + 4 * W) = make_uint4(up[0], up[1], up[2], up[3]);
+    }
+    *reinterpret_cast<uint4 *>(c.v_lower + grp * kG * (kD / 2) + 4 * W) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
   // 6. key codes and planes: thread = eight channels of a token (one word of
   // each plane), the same channels in every step
@@ -392,6 +437,9 @@ struct PrefillSmem {
   FlushSmem<QW> f;
   int place[kPrefillQuarters / 4 + 1];  // entries of the CTA's groups
 };
+// Six CTAs of four warps fit an SM (with five, 152 us where six take 147): 227 KB,
+// and a KB of each CTA is the system's.
+static_assert(6 * (sizeof(PrefillSmem<4>) + 1024) <= 227 * 1024, "six CTAs an SM");
 
 }  // namespace
 
@@ -452,7 +500,7 @@ __global__ void __launch_bounds__(32 * QW)
 // 0 and 1.  The CTA that arrives last on the sequence's ticket writes the
 // counters, so every CTA reads the old (empty) ones first.
 template <int QW>
-__global__ void __launch_bounds__(32 * QW, 20 / QW)
+__global__ void __launch_bounds__(32 * QW, 24 / QW)
     prefill_kernel(qs_cache c, Pages pg, const uint16_t *__restrict__ k,
                    const uint16_t *__restrict__ v, int T, const int32_t *__restrict__ len, int nq,
                    int quarters) {
@@ -578,15 +626,15 @@ using namespace qs;
 
 namespace {
 
-// Quarters per CTA: 8 for a prompt that fills the GPU several times over; fewer
-// for a short one, whose time is one CTA's chain of quarters, so that its
-// quarters spread over five CTAs an SM first (two heads of 1k tokens: 23.5 us
-// with eight quarters a CTA).
+// Quarters per CTA: 8 for a prompt of many waves of CTAs (32 heads of 32k tokens:
+// 147 us; four 150); 4 where eight leave the last wave half empty (32 heads of 9k
+// tokens: 48 us; eight 55); fewer for a short one, whose time is one CTA's chain of
+// quarters, so that its quarters spread over five CTAs an SM first (two heads of
+// 1k tokens: 23.5 us with eight quarters a CTA).
 int prefill_quarters(long long total) {
   const long long slots = 5 * 152;
-  int q = 1;
-  while (q < kPrefillQuarters && total > slots * q) q *= 2;
-  return q;
+  if (total > slots * 3 * kPrefillQuarters) return kPrefillQuarters;
+  return total > slots * 2 ? 4 : total > slots ? 2 : 1;
 }
 
 template <int QW>
