@@ -36,7 +36,7 @@ def prompt(rng, H, T):
 
 
 @pytest.mark.parametrize("ub", [4, 2])
-@pytest.mark.parametrize("H,T", [(3, 700), (40, 640), (40, 1000), (80, 900), (80, 2300)])
+@pytest.mark.parametrize("H,T", [(3, 700), (40, 640), (40, 1000), (80, 900), (80, 2300), (150, 4200)])
 def test_prefill(torch, H, T, ub):
     rng = np.random.default_rng([H, T, ub])
     k, v = prompt(rng, H, T)
