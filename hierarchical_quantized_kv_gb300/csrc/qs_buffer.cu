@@ -16,8 +16,8 @@
 namespace qs {
 
 // One CTA per (head, sequence): copy n_new rows of K and V into the ring.
-__global__ void __launch_bounds__(256) append_kernel(qs_cache c, const uint4 *__restrict__ k_new,
-                                                     const uint4 *__restrict__ v_new, int n_new) {
+__global__ void __launch_bounds__(256) append_kernel(qs_cache c, const uint4 *k_new,
+                                                     const uint4 *v_new, int n_new) {
   const int h = blockIdx.x, b = blockIdx.y;
   pdl_trigger();
   pdl_wait();
@@ -39,11 +39,26 @@ __global__ void __launch_bounds__(256) append_kernel(qs_cache c, const uint4 *__
   uint4 *bv = reinterpret_cast<uint4 *>(c.buf_v) + bh * kRing * kRowVec;
   const uint4 *sk = k_new + bh * n_new * kRowVec;
   const uint4 *sv = v_new + bh * n_new * kRowVec;
-  for (int e = threadIdx.x; e < n_new * kRowVec; e += blockDim.x) {
-    const int i = e / kRowVec, col = e % kRowVec;
-    const int slot = (base * kG + fill + i) & (kRing - 1);
-    bk[slot * kRowVec + col] = sk[e];
-    bv[slot * kRowVec + col] = sv[e];
+  // (four pieces a thread in flight at once)
+  for (int e0 = threadIdx.x; e0 < n_new * kRowVec; e0 += 4 * blockDim.x) {
+    uint4 xk[4], xv[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = e0 + u * blockDim.x;
+      if (e < n_new * kRowVec) {
+        xk[u] = sk[e];
+        xv[u] = sv[e];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = e0 + u * blockDim.x, i = e / kRowVec, col = e % kRowVec;
+      const int slot = (base * kG + fill + i) & (kRing - 1);
+      if (e < n_new * kRowVec) {
+        bk[slot * kRowVec + col] = xk[u];
+        bv[slot * kRowVec + col] = xv[u];
+      }
+    }
   }
   __syncthreads();
   // every head has read the old counters once the ticket reaches H - 1
@@ -68,7 +83,7 @@ __global__ void __launch_bounds__(256) reset_kernel(qs_cache c) {
   }
 }
 
-__global__ void rollback_kernel(qs_cache c, const int32_t *__restrict__ n_drop) {
+__global__ void rollback_kernel(qs_cache c, const int32_t *n_drop) {
   pdl_trigger();
   pdl_wait();
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
@@ -83,7 +98,7 @@ __global__ void rollback_kernel(qs_cache c, const int32_t *__restrict__ n_drop) 
   st[QS_ST_PENDING] = 0;
 }
 
-__global__ void need_flush_kernel(qs_cache c, int n_next, uint8_t *__restrict__ mask) {
+__global__ void need_flush_kernel(qs_cache c, int n_next, uint8_t *mask) {
   pdl_trigger();
   pdl_wait();
   const int b = blockIdx.x * blockDim.x + threadIdx.x;

@@ -139,6 +139,12 @@ inline qs_status launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 bl
 // Programmatic dependent launch: let the next kernel in the stream start its
 // launch now / wait until the previous kernel has completed and its writes
 // are visible (returns at once when there is no programmatic predecessor).
+// What that kernel may have written is read by plain loads, never through the
+// read-only path (__ldg, const __restrict__ parameters, ld.global.nc): every
+// kernel here triggers its successor at its start, so several calls of a stream
+// can be resident together, and a read-only line that an SM fetched for an
+// earlier one is not dropped by this wait.  Any argument can be such data: a
+// mask from qs_need_flush, counts from qs_spec_accept, rows from qs_cache_read.
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -194,8 +200,6 @@ __device__ __forceinline__ size_t group_slots(const qs_cache &c, const Pages &pg
 __device__ __forceinline__ long long group_slot(const qs_cache &c, const Pages &pg, int b, int h,
                                                 int g) {
   if (!pg.table) return ((long long)b * c.H + h) * c.cap_groups + g;
-  // (a plain load, not the read-only path: the kernel before this one in the
-  // stream may have written the table while this one was already resident)
   const int page = pg.table[(size_t)b * c.cap_groups + g];
   return page >= 0 && page < pg.n_pages ? (long long)page * c.H + h : -1;
 }

@@ -448,7 +448,7 @@ static_assert(6 * (sizeof(PrefillSmem<4>) + 1024) <= 227 * 1024, "six CTAs an SM
 // without a mask).
 template <int QW>
 __global__ void __launch_bounds__(32 * QW)
-    flush_kernel(qs_cache c, Pages pg, const uint8_t *__restrict__ mask, int n_next) {
+    flush_kernel(qs_cache c, Pages pg, const uint8_t *mask, int n_next) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   FlushSmem<QW> &S = *reinterpret_cast<FlushSmem<QW> *>(smem_raw);
   const int part = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
@@ -501,9 +501,8 @@ __global__ void __launch_bounds__(32 * QW)
 // counters, so every CTA reads the old (empty) ones first.
 template <int QW>
 __global__ void __launch_bounds__(32 * QW, 24 / QW)
-    prefill_kernel(qs_cache c, Pages pg, const uint16_t *__restrict__ k,
-                   const uint16_t *__restrict__ v, int T, const int32_t *__restrict__ len, int nq,
-                   int quarters) {
+    prefill_kernel(qs_cache c, Pages pg, const uint16_t *k, const uint16_t *v, int T,
+                   const int32_t *len, int nq, int quarters) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   PrefillSmem<QW> &PS = *reinterpret_cast<PrefillSmem<QW> *>(smem_raw);
   FlushSmem<QW> &S = PS.f;

@@ -19,8 +19,7 @@ constexpr int kReadThreads = 256;
 // rows of a transposed 8x8 store fall into different banks
 constexpr int kTileRow = 2 * kD + 16;
 
-// (not the read-only path: the kernel before may have written the planes while
-// this one was already resident)
+// (a plain load but for L1: see pdl_wait)
 __device__ __forceinline__ uint32_t ld_stream(const uint8_t *p) {
   uint32_t v;
   asm volatile("ld.global.L1::no_allocate.b32 %0, [%1];" : "=r"(v) : "l"(p));
@@ -92,8 +91,7 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t r0, ui
 // shared tile.
 template <int MODE, int UB>
 __global__ void __launch_bounds__(kReadThreads)
-    read_kernel(qs_cache c, Pages pg, int tok0, int T, uint16_t *__restrict__ k_out,
-                uint16_t *__restrict__ v_out) {
+    read_kernel(qs_cache c, Pages pg, int tok0, int T, uint16_t *k_out, uint16_t *v_out) {
   __shared__ __align__(16) uint8_t tile[kG * kTileRow];
   __shared__ __align__(16) uint16_t ks[kD], kz[kD];
   const int h = pg.table ? blockIdx.x % c.H : blockIdx.y, b = blockIdx.z, tid = threadIdx.x;

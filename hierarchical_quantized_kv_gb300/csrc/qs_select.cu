@@ -155,8 +155,6 @@ __device__ __forceinline__ int kmeta_channel(int p) {
   return 32 * ((p >> 3) & 3) + 8 * (p >> 5) + 2 * ((p >> 2) & 1) + ((p >> 1) & 1) + 4 * (p & 1);
 }
 
-// (plain loads: the kernel before may have written what this one reads while it
-// was already resident, which the read-only path does not allow for)
 __device__ __forceinline__ uint4 ld16(const uint16_t *p) {
   return *reinterpret_cast<const uint4 *>(p);
 }

@@ -36,9 +36,8 @@ __device__ __forceinline__ bool before(float k1, int x1, float k2, int x2) {
 
 // This CTA's best (key, index) over x in [x0, x1) of the weights p (minus q
 // when q is given, clamped at 0): block reduction into s_key[0], s_idx[0].
-__device__ void race_block(const float *__restrict__ wp, const float *__restrict__ wq,
-                           const float *__restrict__ eb, int x0, int x1, float *s_key,
-                           int *s_idx) {
+__device__ void race_block(const float *wp, const float *wq, const float *eb, int x0, int x1,
+                           float *s_key, int *s_idx) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   float key = 0.f;
   int idx = -1;
@@ -86,10 +85,9 @@ __device__ void race_block(const float *__restrict__ wp, const float *__restrict
 // over its slice of the vocabulary, and the slices' winners meet through
 // distributed shared memory.
 __global__ void __cluster_dims__(kSpecCluster, 1, 1) __launch_bounds__(kSpecThreads)
-    spec_accept_kernel(const float *__restrict__ p, const float *__restrict__ q,
-                       const int32_t *__restrict__ draft, const float *__restrict__ u,
-                       const float *__restrict__ e, int gamma, int V, int32_t *n_accept,
-                       int32_t *token, int32_t *n_drop) {
+    spec_accept_kernel(const float *p, const float *q, const int32_t *draft, const float *u,
+                       const float *e, int gamma, int V, int32_t *n_accept, int32_t *token,
+                       int32_t *n_drop) {
   __shared__ int s_a;
   __shared__ float s_key[kSpecThreads / 32];
   __shared__ int s_idx[kSpecThreads / 32];

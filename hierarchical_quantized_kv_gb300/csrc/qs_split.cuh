@@ -473,13 +473,13 @@ __device__ __forceinline__ float warp_sum8(float v) {
 
 // q row of query r as tensor-core B pairs in the key-plane channel order:
 // k-block kb, first register {q(ch0), q(ch0+4)}, second {q(ch0+1), q(ch0+5)},
-// ch0 = 32c + 8 (kb >> 1) + 2 (kb & 1).
+// ch0 = 32c + 8 (kb >> 1) + 2 (kb & 1).  (Plain loads: see pdl_wait.)
 __device__ __forceinline__ void load_q_pairs(const uint16_t *qrow, bool valid, int c,
                                              uint32_t (&q0)[8], uint32_t (&q1)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint4 w = make_uint4(0, 0, 0, 0);
-    if (valid) w = __ldg(reinterpret_cast<const uint4 *>(qrow + 32 * c) + i);
+    if (valid) w = reinterpret_cast<const uint4 *>(qrow + 32 * c)[i];
     q0[2 * i] = prmt(w.x, w.z, 0x5410);
     q1[2 * i] = prmt(w.x, w.z, 0x7632);
     q0[2 * i + 1] = prmt(w.y, w.w, 0x5410);
@@ -507,7 +507,7 @@ __device__ __noinline__ int unit_place(const Params &prm, int b, int h, int u) {
   int32_t *st = c.state + (size_t)b * QS_STATE_WORDS;
   int g = u;
   if (prm.sel) {
-    g = prm.sel[((size_t)b * c.H + h) * prm.k_sel + u];  // (plain: see group_slot)
+    g = prm.sel[((size_t)b * c.H + h) * prm.k_sel + u];
     if (g == -1) return -1;
     if (g < 0 || g >= min(max(st[QS_ST_N_GROUPS], 0), c.cap_groups)) {
       atomicOr(&st[QS_ST_ERR], QS_DEV_SELECT);
