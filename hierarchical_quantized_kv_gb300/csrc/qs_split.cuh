@@ -338,10 +338,27 @@ struct Centre {
   // draft's code step
   static constexpr float kScale =
       16777216.f * (kDraft ? kStep / (!HI ? 1.f : UB == 2 ? 16.f : 4.f) : 1.f);
-  // scores of the listed drafts: q s_K is carried fourfold (see kFour)
+  // scores of the listed drafts: q s_K is carried fourfold, unless the queries
+  // are too large for that (kWideQ)
   static constexpr bool kFour = kDraft && HI;
-  static constexpr float kScaleK = kFour ? kScale / 4.f : kScale;
 };
+
+// A scale that this library stores is at most 514 (the range of finite fp16
+// numbers over 255, rounded up), so 4 q s_K stays finite for every |q| up to this:
+// 4 * 31.75 * 514 = 65,278.  Rows with a larger query carry q s_K itself, as the
+// contiguous kernel does.
+constexpr uint32_t kWideQ = 0x4FF0;  // fp16 31.75
+
+// Whether a query of the warp's rows (its q pairs) is larger, or not a number.
+__device__ __forceinline__ bool wide_queries(const uint32_t (&q0)[8], const uint32_t (&q1)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    constexpr uint32_t kAbs = 0x7FFF7FFFu;  // (magnitudes are ordered as integers)
+    m = __vmaxu2(m, __vmaxu2(q0[i] & kAbs, q1[i] & kAbs));
+  }
+  return __any_sync(0xffffffffu, (m & 0xFFFFu) > kWideQ || (m >> 16) > kWideQ);
+}
 
 template <int MODE, bool HI>
 __device__ __forceinline__ void pairs(uint32_t wu, uint32_t wl, uint32_t (&e)[4]) {
@@ -1368,6 +1385,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
   sm.reset();
   uint32_t qp0[8], qp1[8];
   int fill = 0, ng = 0;
+  bool wide = false;  // kFour: the segment's queries are carried onefold (wide_queries)
   int cur_ord = -1;  // segment ordinal of this warp's softmax state (-1: none yet)
   Seg cur, ahead;
   if (CL) cur = ahead = first;
@@ -1408,6 +1426,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
       const bool q_ok =  // (rows qi >= R are not read)
           qi >= R || chk(in_range((bh * R + qi) * kD, kD, (size_t)c.B * c.H * R * kD), 9);
       load_q_pairs(prm.q + (q_ok ? (bh * R + qi) * kD : 0), qi < R, cq, qp0, qp1);
+      if (Scales::kFour) wide = wide_queries(qp0, qp1);
       sm.reset();
       fill = T.fill[cur.b];
       ng = T.ng[cur.b];
@@ -1454,11 +1473,13 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
           if (Scales::kFour) {
             // four times q s and q s / 4: the lo parts, subnormal for usual
             // scales, keep two bits more (log-sum-exp off by under 1e-6 of
-            // itself instead of up to 3e-6), for |q s| below 16,000
-            s0 = hmul2_u32(s0, 0x44004400u);  // fp16 (4, 4)
-            s2 = hmul2_u32(s2, 0x44004400u);
-            s1 = hmul2_u32(s1, 0x34003400u);  // fp16 (1/4, 1/4)
-            s3 = hmul2_u32(s3, 0x34003400u);
+            // itself instead of up to 3e-6).  Wide queries: q s and q s / 16
+            const uint32_t f = wide ? 0x3C003C00u : 0x44004400u;   // fp16 (1, 1) or (4, 4)
+            const uint32_t fo = wide ? 0x2C002C00u : 0x34003400u;  // (1/16, 1/16) or (1/4, 1/4)
+            s0 = hmul2_u32(s0, f);
+            s2 = hmul2_u32(s2, f);
+            s1 = hmul2_u32(s1, fo);
+            s3 = hmul2_u32(s3, fo);
           } else if (MODE == QS_DRAFT_UPPER4) {
             s1 = hmul2_u32(s1, 0x2C002C00u);  // fp16 (1/16, 1/16)
             s3 = hmul2_u32(s3, 0x2C002C00u);
@@ -1478,8 +1499,10 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
           mma16816(bacc2, zw.z, sw.z, zw.w, sw.w, qp0[k1], qp1[k1]);
         }
         // key dequant s * code + (z + kOffK s), code = 16 C_U or C_INT8:
-        // bias = sum q z + kOffK sum q s; the code part scales by kScale
-        const float sl2q = prm.sl2 * Scales::kScaleK;
+        // bias = sum q z + kOffK sum q s; the code part scales by kScale (a
+        // quarter of it where q s is carried fourfold)
+        const float sl2q =
+            prm.sl2 * (Scales::kFour && !wide ? Scales::kScale / 4.f : Scales::kScale);
         const float bk0 =
             fmaf(Scales::kOffK, bacc[2] + bacc2[2], bacc[0] + bacc2[0]) * prm.sl2;
         const float bk1 =

@@ -364,6 +364,9 @@ qs_status qs_attn_workspace_size(const qs_cache *c, int32_t n_q, size_t *bytes);
  *   workspace  device scratch of at least qs_attn_workspace_size bytes, 16-byte
  *          aligned; it holds split partials and is not read across calls.
  * Sequences with n_q > fill get QS_DEV_NQ_GT_FILL, zero output, lse = -inf.
+ * Here and in every other attention call the product of a query and a key scale
+ * is an fp16 number: |q_d| times the scale of a group's channel d has to stay
+ * below 65,504 (a key range of 65,504 * 255 / |q_d|), or the row is NaN.
  * One kernel launch: a persistent split-KV pass over a balanced partition of
  * all (sequence, head, group) units, whose log-sum-exp merge of the splits
  * runs in the same kernel.  Errors: QS_ERR_ARG (null q/out, n_q outside 1..8,
@@ -413,8 +416,10 @@ qs_status qs_attn_decode_append(const qs_cache *c, qs_mode mode, const uint16_t 
                                 qs_stream_t stream);
 
 /* Decode attention over a paged cache: qs_attn_decode_gqa, with the groups
- * where the page table puts them (the same results as a contiguous cache of
- * the same content).  With n_new > 0 the tokens k_new, v_new are appended
+ * where the page table puts them (the same attention as over a contiguous cache
+ * of the same content; a draft rounds less: its output is 2.0 to 2.4e-4 of itself
+ * from 64 bits, there 2.4 to 3.1e-4, and 5 to 8e-4 with upper_bits 2; its scores
+ * are as exact as there where a query is larger than 31.75, else more so).  With n_new > 0 the tokens k_new, v_new are appended
  * first, as in qs_attn_decode_append; without an append pass NULL, NULL, 0.
  * A group whose page is out of range is left out of the softmax and flags
  * QS_DEV_PAGE.  Arguments, workspace (qs_attn_workspace_size_gqa) and errors
