@@ -80,9 +80,18 @@ __device__ __forceinline__ void scale_zero(float mn, float mx, uint16_t &s_bits,
 // the sum; a second one gives the remainder a rf - n.  The two quotients round
 // alike unless that lies within 2^-12 of a half; there the exact quotient
 // decides (about one element in 2^11).  A zero scale means a zero range: a = 0,
-// and rf is taken as 0, which gives code 0.
+// and rf is taken as 0, which gives code 0.  A quotient that is not a number (an
+// element that is not one, or a range that is infinite) has code 0; its remainder
+// is not a number either and takes the element the exact quotient's way.
 constexpr float kRound = 12582912.f;  // 1.5 * 2^23
 constexpr float kNear = 0.5f - 0x1p-12f;
+
+// The larger number, NaN if either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 
 __device__ __forceinline__ float reciprocal(float sf) { return sf == 0.f ? 0.f : __frcp_rn(sf); }
 
@@ -108,21 +117,22 @@ __device__ __forceinline__ uint2 codes8(const __half *p, const uint4 &x, const f
     const float a = __fsub_rn(i & 1 ? f.y : f.x, zf[i]);
     const float n = __fmaf_rn(a, rf[i], kRound);
     d[i] = __fmaf_rn(a, rf[i], -__fsub_rn(n, kRound));
-    far = fmaxf(far, fabsf(d[i]));
+    far = max_nan(far, fabsf(d[i]));
     t[i] = __float_as_uint(n);
   }
   uint2 q = EVEN_ODD ? make_uint2(low_bytes(t[0], t[2], t[4], t[6]), low_bytes(t[1], t[3], t[5], t[7]))
                      : make_uint2(low_bytes(t[0], t[1], t[2], t[3]), low_bytes(t[4], t[5], t[6], t[7]));
-  if (far > kNear) {
+  if (!(far <= kNear)) {
     unsigned near = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) near |= fabsf(d[i]) > kNear ? 1u << i : 0u;
+    for (int i = 0; i < 8; ++i) near |= fabsf(d[i]) <= kNear ? 0u : 1u << i;
 #pragma unroll 1
     while (near) {
       const int i = __ffs(near) - 1;
       near &= near - 1;
       const float a = __fsub_rn(__half2float(p[i]), z_at(i));
-      const uint32_t n = __float_as_uint(__fadd_rn(__fdiv_rn(a, s_at(i)), kRound)) & 0xFFu;
+      const float u = __fdiv_rn(a, s_at(i));
+      const uint32_t n = u == u ? __float_as_uint(__fadd_rn(u, kRound)) & 0xFFu : 0u;
       const int sh = EVEN_ODD ? 8 * (i >> 1) : 8 * (i & 3);
       uint32_t &word = (EVEN_ODD ? i & 1 : i >> 2) ? q.y : q.x;
       word = (word & ~(0xFFu << sh)) | (n << sh);
