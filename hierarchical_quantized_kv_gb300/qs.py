@@ -214,7 +214,8 @@ class PagedCache(Cache):
     """A cache whose groups lie in a pool of n_pages pages (include/qs.h,
     qs_pages): the group arrays are [n_pages, H, ...], ``table`` (int32 [B,
     cap_groups], filled with -1) names the page of each sequence's groups and
-    is the caller's to fill.  The calls for contiguous caches refuse it."""
+    is the caller's to fill or to replace.  The calls for contiguous caches
+    refuse it."""
 
     def __init__(self, B, H, cap_groups, n_pages, device="cuda", D=128, G=128, upper_bits=4):
         import torch
@@ -222,11 +223,27 @@ class PagedCache(Cache):
         qs_paged_cache_bytes(B, H, n_pages, D, G)
         self.n_pages = n_pages
         self._alloc(B, H, cap_groups, device, D, G, upper_bits, (n_pages, H))
+        self.pages_struct = QsPagesStruct(None, n_pages)
+        self._pages_ref = ctypes.byref(self.pages_struct)
         self.table = torch.full((B, cap_groups), -1, dtype=torch.int32, device=device)
         self.struct = self._struct(upper_bits | QS_PAGED)
         self._ref = ctypes.byref(self.struct)
-        self.pages_struct = QsPagesStruct(self.table.data_ptr(), n_pages)
-        self._pages_ref = ctypes.byref(self.pages_struct)
+
+    @property
+    def table(self):
+        """The page table: write into it, or assign another int32 [B,
+        cap_groups] tensor (a captured graph keeps the one it was captured
+        with)."""
+        return self._table
+
+    @table.setter
+    def table(self, t):
+        if (t.dtype != self.state.dtype or t.device != self.state.device or
+                tuple(t.shape) != (self.B, self.cap) or not t.is_contiguous()):
+            raise ValueError("the page table is a contiguous int32 [%d, %d] tensor on %s"
+                             % (self.B, self.cap, self.state.device))
+        self._table = t
+        self.pages_struct.table = t.data_ptr()
 
     def nbytes(self):
         return super().nbytes() + self.table.numel() * self.table.element_size()
