@@ -51,6 +51,10 @@ class QsError(RuntimeError):
         super().__init__("%s failed: %s (%d)" % (fn, status_string(status), status))
 
 
+class QsArgumentError(AssertionError, ValueError):
+    """A tensor that does not fit the call: its shape, type, device or layout."""
+
+
 _lib = None
 
 # exported entry points and their argument types
@@ -181,6 +185,7 @@ class Cache:
         import torch
         self.B, self.H, self.D, self.G, self.cap = B, H, D, G, cap_groups
         self.upper_bits = upper_bits
+        self._f32 = torch.float32
         u8 = dict(dtype=torch.uint8, device=device)
         f16 = dict(dtype=torch.float16, device=device)
         self.k_upper = torch.zeros(slots + (G, D // 2), **u8)
@@ -192,6 +197,7 @@ class Cache:
         self.buf_v = torch.zeros((B, H, 2 * G, D), **f16)
         self.state = torch.zeros((B, STATE_WORDS), dtype=torch.int32, device=device)
         self.arrive = torch.zeros((B, H), dtype=torch.int32, device=device)
+        self._f16, self._i32, self._dev = self.buf_k.dtype, self.state.dtype, self.state.get_device()
 
     def _struct(self, upper_bits):
         return QsCacheStruct(self.B, self.H, self.D, self.G, self.cap, upper_bits,
@@ -298,7 +304,9 @@ def qs_prefill(cache, k, v, lens, stream=None):
 
 def qs_quantize_flush_paged(cache, mask=None, stream=None):
     """qs_quantize_flush on a PagedCache."""
-    assert mask is None or (mask.numel() == cache.B and mask.element_size() == 1)
+    if mask is not None and not (mask.numel() == cache.B and mask.element_size() == 1 and
+                                 mask.is_contiguous() and mask.get_device() == cache._dev):
+        raise QsArgumentError("mask: uint8 [B] on the cache's device")
     _check("qs_quantize_flush_paged", lib().qs_quantize_flush_paged(
         cache._ref, cache._pages_ref, _ptr(mask), _stream(stream)))
 
@@ -309,10 +317,21 @@ def qs_quantize_flush_due_paged(cache, n_next, stream=None):
         cache._ref, cache._pages_ref, int(n_next), _stream(stream)))
 
 
+def _check_f16(cache, t, name):
+    if not (t.dtype is cache._f16 and t.is_contiguous() and t.get_device() == cache._dev):
+        raise QsArgumentError("%s: contiguous float16 on the cache's device" % name)
+
+
 def qs_prefill_paged(cache, k, v, lens, stream=None):
     """qs_prefill on a PagedCache."""
-    assert k.is_contiguous() and v.is_contiguous() and k.shape == v.shape
-    assert k.shape[:2] == (cache.B, cache.H) and lens.numel() == cache.B and lens.element_size() == 4
+    if not (k.shape == v.shape and k.dim() == 4 and k.shape[:2] == (cache.B, cache.H) and
+            k.shape[3] == cache.D):
+        raise QsArgumentError("k, v: [B, H, T, D]")
+    _check_f16(cache, k, "k")
+    _check_f16(cache, v, "v")
+    if not (lens.numel() == cache.B and lens.dtype is cache._i32 and lens.is_contiguous() and
+            lens.get_device() == cache._dev):
+        raise QsArgumentError("lens: int32 [B] on the cache's device")
     _check("qs_prefill_paged", lib().qs_prefill_paged(cache._ref, cache._pages_ref, _ptr(k), _ptr(v),
                                                       int(k.shape[2]), _ptr(lens), _stream(stream)))
 
@@ -322,9 +341,11 @@ def qs_cache_read(cache, mode, k, v, tok0=0, stream=None):
     [B, H, T, D] contiguous device tensors, one of them may be None.  Rows past
     a sequence's last token stay as they were."""
     T = (v if k is None else k).shape[2] if k is not None or v is not None else 0
-    for t in (k, v):
-        assert t is None or (t.is_contiguous() and t.element_size() == 2 and
-                             t.shape == (cache.B, cache.H, T, cache.D))
+    for name, t in (("k", k), ("v", v)):
+        if t is not None:
+            if t.shape != (cache.B, cache.H, T, cache.D):
+                raise QsArgumentError("%s: [B, H, T, D]" % name)
+            _check_f16(cache, t, name)
     _check("qs_cache_read", lib().qs_cache_read(cache._ref, cache._pages_ref, int(mode), int(tok0),
                                                 int(T), _ptr(k), _ptr(v), _stream(stream)))
 
@@ -400,32 +421,54 @@ def qs_attn_decode_append(cache, mode, k_new, v_new, q, softmax_scale, out, lse=
 
 
 def _n_new(cache, k_new, v_new):
+    """The appended tokens: k_new and v_new fp16 [B, H, n_new, D], or neither."""
     if k_new is None and v_new is None:
         return 0
-    assert k_new.is_contiguous() and v_new.is_contiguous() and k_new.shape == v_new.shape
-    assert k_new.shape[0] == cache.B and k_new.shape[1] == cache.H and k_new.shape[3] == cache.D
-    return k_new.shape[2]
+    if k_new is None or v_new is None:
+        raise QsArgumentError("k_new and v_new go together")
+    shape = k_new.shape
+    if not (len(shape) == 4 and v_new.shape == shape and shape[0] == cache.B and
+            shape[1] == cache.H and shape[3] == cache.D):
+        raise QsArgumentError("k_new, v_new: [B, H, n_new, D]")
+    _check_f16(cache, k_new, "k_new")
+    _check_f16(cache, v_new, "v_new")
+    return shape[2]
 
 
 def _check_queries(cache, q, group, out=None, lse=None):
     """q (and out) fp16 [B, H * group, n_q, D] contiguous, lse fp32 of the rows."""
     shape = q.shape
+    if len(shape) != 4:
+        raise QsArgumentError("q: [B, H * group, n_q, D]")
     b, h, n_q, d = shape
-    assert b == cache.B and h == cache.H * group and d == cache.D
-    assert q.is_contiguous() and q.element_size() == 2
+    if b != cache.B or h != cache.H * group or d != cache.D:
+        raise QsArgumentError("q: [B, H * group, n_q, D]")
+    _check_f16(cache, q, "q")
     if out is not None:
-        assert out.shape == shape and out.is_contiguous() and out.element_size() == 2
-    if lse is not None:
-        assert lse.numel() == b * h * n_q and lse.is_contiguous() and lse.element_size() == 4
+        if out.shape != shape:
+            raise QsArgumentError("out: the shape of q")
+        _check_f16(cache, out, "out")
+    if lse is not None and not (lse.numel() == b * h * n_q and lse.dtype is cache._f32 and
+                                lse.is_contiguous() and lse.get_device() == cache._dev):
+        raise QsArgumentError("lse: contiguous float32 [B, H * group, n_q] on the cache's device")
     return n_q
+
+
+def _ws_bytes(cache, workspace):
+    if workspace is None:
+        return 0
+    if not workspace.is_contiguous() or workspace.get_device() != cache._dev:
+        raise QsArgumentError("workspace: contiguous, on the cache's device")
+    return workspace.nbytes
 
 
 def _check_selection(cache, sel):
     """sel: int32 [B, H, k] contiguous."""
-    b, h, k = sel.shape
-    assert b == cache.B and h == cache.H
-    assert sel.is_contiguous() and sel.element_size() == 4 and not sel.is_floating_point()
-    return k
+    shape = sel.shape
+    if not (len(shape) == 3 and shape[0] == cache.B and shape[1] == cache.H and
+            sel.dtype is cache._i32 and sel.is_contiguous() and sel.get_device() == cache._dev):
+        raise QsArgumentError("sel: contiguous int32 [B, H, k] on the cache's device")
+    return shape[2]
 
 
 def qs_attn_decode_paged(cache, mode, q, softmax_scale, out, lse=None, workspace=None, group=1,
@@ -433,7 +476,7 @@ def qs_attn_decode_paged(cache, mode, q, softmax_scale, out, lse=None, workspace
     """qs_attn_decode_gqa on a PagedCache, or with k_new, v_new (fp16 [B, H,
     n_new, D]) qs_attn_decode_append on it."""
     n_q = _check_queries(cache, q, group, out, lse)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _ws_bytes(cache, workspace)
     _check("qs_attn_decode_paged", lib().qs_attn_decode_paged(
         cache._ref, cache._pages_ref, int(mode), _ptr(k_new), _ptr(v_new), _n_new(cache, k_new, v_new),
         _ptr(q), n_q, int(group), float(softmax_scale), _ptr(out), _ptr(lse),
@@ -455,7 +498,7 @@ def qs_attn_decode_sparse(cache, mode, sel, q, softmax_scale, out, lse=None, wor
     in sel, int32 [B, H, k] (-1: none), and the buffer; k_new, v_new as for
     qs_attn_decode_paged."""
     n_q, k = _check_queries(cache, q, group, out, lse), _check_selection(cache, sel)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _ws_bytes(cache, workspace)
     _check("qs_attn_decode_sparse", lib().qs_attn_decode_sparse(
         cache._ref, cache._pages_ref, int(mode), _ptr(sel), k, _ptr(k_new), _ptr(v_new),
         _n_new(cache, k_new, v_new), _ptr(q), n_q, int(group), float(softmax_scale), _ptr(out),
