@@ -100,24 +100,32 @@ qs_status qs_test_attn_decode_timeout(const qs_cache *c, qs_mode mode, const uin
 #if QS_CHECKED
 extern "C" int qs_checked_failures_quantize(unsigned long long *out2, int reset);
 extern "C" int qs_checked_failures_listed(unsigned long long *out2, int reset);
+extern "C" int qs_checked_failures_select(unsigned long long *out2, int reset);
+extern "C" int qs_checked_failures_read(unsigned long long *out2, int reset);
 
 // Checked build only (-DQS_CHECKED=1): the number of failed bounds checks of
-// the attention and quantization kernels since the last reset, and the tag of
-// the first (1 shared-memory load, 2 copy destination, 3 group index, 4 buffer
-// row, 6 ldmatrix row, 7 partial slot, 8 merge source, 9 query row, 10 output
-// head, 11 tail partials, 20 flush group, 21 metadata position, 22 prefill
-// group rows, 23 prefill buffer rows).  reset != 0 zeroes the counts.
-// Returns 0, or 1 if a CUDA call failed.
+// the kernels since the last reset, and the tag of the first (attention: 1
+// shared-memory load, 2 copy destination, 3 group index, 4 buffer row, 6 ldmatrix
+// row, 7 partial slot, 8 merge source, 9 query row, 10 output head, 11 tail
+// partials; quantizer: 20 flush group, 21 metadata position, 22 prefill group
+// rows, 23 prefill buffer rows; listed attention: 30 page table entry, 31 entry of
+// the selection, 32 place of a unit, 33 a cluster's sums in shared memory, 34 its
+// sums in the workspace; selection: 40 score, 41 list of close groups, 42 output,
+// 43 scales and zeros, 44 query row; read back: 50 group, 51 buffer row, 52 output
+// row, 53 tile row).  reset != 0 zeroes the counts.  Returns 0, or 1 if a CUDA call
+// failed.
 extern "C" int qs_checked_failures(unsigned long long *count, unsigned int *first_tag, int reset) {
-  unsigned long long a[2], q[2], l[2];
-  if (cudaMemcpyFromSymbol(a, g_check_fail, sizeof(a)) != cudaSuccess) return 1;
-  if (qs_checked_failures_quantize(q, reset) || qs_checked_failures_listed(l, reset)) return 1;
-  if (reset) {
-    const unsigned long long z[2] = {0, 0};
-    if (cudaMemcpyToSymbol(g_check_fail, z, sizeof(z)) != cudaSuccess) return 1;
+  unsigned long long f[5][2];
+  if (read_check_failures(f[0], reset) || qs_checked_failures_quantize(f[1], reset) ||
+      qs_checked_failures_listed(f[2], reset) || qs_checked_failures_select(f[3], reset) ||
+      qs_checked_failures_read(f[4], reset))
+    return 1;
+  *count = 0;
+  *first_tag = 0;
+  for (const auto &x : f) {
+    if (*count == 0 && x[0]) *first_tag = (unsigned int)x[1];
+    *count += x[0];
   }
-  *count = a[0] + q[0] + l[0];
-  *first_tag = (unsigned int)(a[0] ? a[1] : q[0] ? q[1] : l[1]);
   return 0;
 }
 #endif

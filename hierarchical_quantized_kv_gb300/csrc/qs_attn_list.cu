@@ -125,11 +125,6 @@ qs_status qs_test_attn_paged_timeout(const qs_cache *c, const qs_pages *pg, qs_m
 #if QS_CHECKED
 // Checked build only: this file's failure count and first failing tag.
 extern "C" int qs_checked_failures_listed(unsigned long long *out2, int reset) {
-  if (cudaMemcpyFromSymbol(out2, g_check_fail, sizeof(g_check_fail)) != cudaSuccess) return 1;
-  if (reset) {
-    const unsigned long long z[2] = {0, 0};
-    if (cudaMemcpyToSymbol(g_check_fail, z, sizeof(z)) != cudaSuccess) return 1;
-  }
-  return 0;
+  return read_check_failures(out2, reset);
 }
 #endif

@@ -161,8 +161,9 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 }
 
 // ---- checked build (-DQS_CHECKED=1): the kernels check the bounds of their
-// shared-memory and global indexing on the device.  A failing access is
-// skipped (a load reads zero) and counted with a tag naming it, never
+// shared-memory and global indexing on the device (attention, quantizer,
+// selection, read back; the tags are listed at qs_checked_failures).  A failing
+// access is skipped (a load reads zero) and counted with a tag naming it, never
 // trapped; the checked library exports qs_checked_failures to read the
 // counts.  The ordinary build compiles every check away.
 #ifndef QS_CHECKED
@@ -170,11 +171,18 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 #endif
 #if QS_CHECKED
 static __device__ unsigned long long g_check_fail[2];  // count, first failing tag (per file)
+// This file's count and first failing tag (out2), zeroed after the reading if reset.
+static int read_check_failures(unsigned long long *out2, int reset) {
+  const unsigned long long z[2] = {0, 0};
+  if (cudaMemcpyFromSymbol(out2, g_check_fail, sizeof(g_check_fail)) != cudaSuccess) return 1;
+  return reset && cudaMemcpyToSymbol(g_check_fail, z, sizeof(z)) != cudaSuccess;
+}
 __device__ __forceinline__ bool chk(bool ok, uint32_t tag) {
   if (!ok && atomicAdd(&g_check_fail[0], 1ull) == 0ull) g_check_fail[1] = tag;
   return ok;
 }
-// [a, a + n) inside this CTA's dynamic shared memory (shared-window address)
+// [a, a + n) inside this CTA's dynamic shared memory (shared-window address); the
+// kernels declare theirs with this alignment, or it would start elsewhere
 __device__ __forceinline__ bool smem_in(uint32_t a, uint32_t n) {
   extern __shared__ __align__(128) uint8_t qs_dyn_smem[];
   uint32_t dyn;
@@ -200,7 +208,9 @@ __device__ __forceinline__ size_t group_slots(const qs_cache &c, const Pages &pg
 __device__ __forceinline__ long long group_slot(const qs_cache &c, const Pages &pg, int b, int h,
                                                 int g) {
   if (!pg.table) return ((long long)b * c.H + h) * c.cap_groups + g;
-  const int page = pg.table[(size_t)b * c.cap_groups + g];
+  const size_t at = (size_t)b * c.cap_groups + g;
+  if (!chk(g >= 0 && g < c.cap_groups && in_range(at, 1, (size_t)c.B * c.cap_groups), 30)) return -1;
+  const int page = pg.table[at];
   return page >= 0 && page < pg.n_pages ? (long long)page * c.H + h : -1;
 }
 

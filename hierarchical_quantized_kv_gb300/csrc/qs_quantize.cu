@@ -742,11 +742,6 @@ qs_status qs_quantize_flush_due_paged(const qs_cache *c, const qs_pages *pg, int
 #if QS_CHECKED
 // Checked build only: this file's failure count and first failing tag.
 extern "C" int qs_checked_failures_quantize(unsigned long long *out2, int reset) {
-  if (cudaMemcpyFromSymbol(out2, g_check_fail, sizeof(g_check_fail)) != cudaSuccess) return 1;
-  if (reset) {
-    const unsigned long long z[2] = {0, 0};
-    if (cudaMemcpyToSymbol(g_check_fail, z, sizeof(z)) != cudaSuccess) return 1;
-  }
-  return 0;
+  return read_check_failures(out2, reset);
 }
 #endif

@@ -105,6 +105,11 @@ __global__ void __launch_bounds__(kReadThreads)
   // output row r of the unit is token 128 u + r, row 128 u + r - tok0 of out
   const int r_lo = max(0, tok0 - u * kG), r_hi = (int)min((long long)kG, (long long)tok0 + T - (long long)u * kG);
   const long long out0 = ((long long)bh * T + ((long long)u * kG - tok0)) * kD;
+  // checked build: the 16 bytes at dst are in the output and in this head's rows
+  auto row_ok = [&](long long dst) {
+    return dst >= (long long)bh * T * kD && dst + 8 <= (long long)(bh + 1) * T * kD &&
+           bh < (size_t)c.B * c.H;
+  };
   if (u >= ng) {
     const int fill = min(max(st[QS_ST_FILL], 0), kRing);
     const int i0 = (u - ng) * kG, base = (st[QS_ST_HALF_BASE] & 1) * kG;
@@ -117,7 +122,12 @@ __global__ void __launch_bounds__(kReadThreads)
       for (int n = 0; n < 4; ++n) {
         const int e = e0 + n * kReadThreads, r = e / (kD / 8);
         if (e >= hi * (kD / 8)) continue;
-        const size_t src = (bh * kRing + ((base + i0 + r) & (kRing - 1))) * kD + 8 * (e % (kD / 8));
+        const size_t row = bh * kRing + ((base + i0 + r) & (kRing - 1));
+        const size_t src = row * kD + 8 * (e % (kD / 8));
+        if (!chk(in_range(row, 1, (size_t)c.B * c.H * kRing), 51)) {
+          xk[n] = xv[n] = make_uint4(0, 0, 0, 0);
+          continue;
+        }
         if (k_out) xk[n] = *reinterpret_cast<const uint4 *>(c.buf_k + src);
         if (v_out) xv[n] = *reinterpret_cast<const uint4 *>(c.buf_v + src);
       }
@@ -126,6 +136,7 @@ __global__ void __launch_bounds__(kReadThreads)
         const int e = e0 + n * kReadThreads;
         if (e >= hi * (kD / 8)) continue;
         const long long dst = out0 + (long long)e * 8;
+        if (!chk(row_ok(dst), 52)) continue;
         if (k_out) *reinterpret_cast<uint4 *>(k_out + dst) = xk[n];
         if (v_out) *reinterpret_cast<uint4 *>(v_out + dst) = xv[n];
       }
@@ -137,6 +148,7 @@ __global__ void __launch_bounds__(kReadThreads)
     if (h == 0 && tid == 0) atomicOr(&c.state[(size_t)b * QS_STATE_WORDS + QS_ST_ERR], QS_DEV_PAGE);
     return;
   }
+  if (!chk(in_range((size_t)grp, 1, group_slots(c, pg)), 50)) return;
   constexpr int kPlane = kG * kD / 2, kIter = kPlane / 4 / kReadThreads;
   const uint16_t *meta = c.meta + (size_t)grp * 4 * 128;
   const int w = tid >> 5, lane = tid & 31, r = lane >> 2, cq = lane & 3;
@@ -176,7 +188,8 @@ __global__ void __launch_bounds__(kReadThreads)
       const int md = (w & 1) * kIter + i;
       // matrix m: tokens 8 m .. 8 m + 7 of the quarter; this lane names row
       // lane % 8 of matrix lane / 8
-      const uint32_t addr = smem_addr(tile) + (32 * (w >> 1) + lane) * kTileRow + 16 * md;
+      uint32_t addr = smem_addr(tile) + (32 * (w >> 1) + lane) * kTileRow + 16 * md;
+      if (!chk(addr + 16 <= smem_addr(tile) + (uint32_t)sizeof(tile), 53)) addr = smem_addr(tile);
       stmatrix_x4_trans(addr, dequant2(prmt(ev, kMagic, 0x4240), s[0], z[0]),
                         dequant2(prmt(od, kMagic, 0x4240), s[1], z[1]),
                         dequant2(prmt(ev, kMagic, 0x4341), s[2], z[2]),
@@ -198,7 +211,8 @@ __global__ void __launch_bounds__(kReadThreads)
       x.y = dequant2(prmt(a, kMagic, 0x4342), s4.y, z4.y);
       x.z = dequant2(prmt(d, kMagic, 0x4140), s4.z, z4.z);
       x.w = dequant2(prmt(d, kMagic, 0x4342), s4.w, z4.w);
-      if (row >= r_lo && row < r_hi) *reinterpret_cast<uint4 *>(k_out + out0 + row * kD + col) = x;
+      if (row >= r_lo && row < r_hi && chk(row_ok(out0 + row * kD + col), 52))
+        *reinterpret_cast<uint4 *>(k_out + out0 + row * kD + col) = x;
     }
   }
   if (v_out) {
@@ -206,7 +220,8 @@ __global__ void __launch_bounds__(kReadThreads)
     for (int i = 0; i < kIter; ++i) {
       const int e = tid + kReadThreads * i, row = e >> 4, col = 8 * (e & 15);
       const uint4 x = *reinterpret_cast<const uint4 *>(tile + row * kTileRow + 2 * col);
-      if (row >= r_lo && row < r_hi) *reinterpret_cast<uint4 *>(v_out + out0 + row * kD + col) = x;
+      if (row >= r_lo && row < r_hi && chk(row_ok(out0 + row * kD + col), 52))
+        *reinterpret_cast<uint4 *>(v_out + out0 + row * kD + col) = x;
     }
   }
 }
@@ -238,3 +253,10 @@ extern "C" qs_status qs_cache_read(const qs_cache *c, const qs_pages *pg, qs_mod
              ? launch_read<QS_DRAFT_UPPER4>(cc, pages, tok0, T, k, v, (cudaStream_t)stream)
              : launch_read<QS_VERIFY_INT8>(cc, pages, tok0, T, k, v, (cudaStream_t)stream);
 }
+
+#if QS_CHECKED
+// Checked build only: this file's failure count and first failing tag.
+extern "C" int qs_checked_failures_read(unsigned long long *out2, int reset) {
+  return read_check_failures(out2, reset);
+}
+#endif

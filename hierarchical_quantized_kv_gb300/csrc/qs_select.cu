@@ -163,7 +163,7 @@ __device__ __forceinline__ uint4 ld16(const uint16_t *p) {
 template <int NCG>
 __global__ void __launch_bounds__(kSelThreads)
     select_kernel(qs_cache c, Pages pg, const uint16_t *q, int R, int k_sel, int32_t *sel) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ BlockScratch S;
   // the first CTA's: largest sum of magnitudes, smallest and largest key of a score
   __shared__ int s_mag;
@@ -218,7 +218,8 @@ __global__ void __launch_bounds__(kSelThreads)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint4 x = make_uint4(0, 0, 0, 0);
-      if (row < R) x = ld16(qh + (size_t)row * kD + 32 * cq + 8 * i);
+      if (row < R && chk(in_range((bh * R + row) * kD, kD, (size_t)c.B * c.H * R * kD), 44))
+        x = ld16(qh + (size_t)row * kD + 32 * cq + 8 * i);
       q0[g][2 * i] = prmt(x.x, x.z, 0x5410);
       q1[g][2 * i] = prmt(x.x, x.z, 0x7632);
       q0[g][2 * i + 1] = prmt(x.y, x.w, 0x5410);
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kSelThreads)
     for (int j = 0; j < 2; ++j) {
       const int g = kTile * t + r + 8 * j;
       const long long place = g < n ? group_slot(c, pg, b, h, g) : -1;
-      good[j] = place >= 0;
+      good[j] = place >= 0 && chk(in_range((size_t)place, 1, group_slots(c, pg)), 43);
       if (g < n && place < 0 && h == 0 && cq == 0) atomicOr(&st[QS_ST_ERR], QS_DEV_PAGE);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -299,7 +300,8 @@ __global__ void __launch_bounds__(kSelThreads)
       const int g = kTile * t + r + 8 * j;
       if (cq == 0 && g < n) {
         x = good[j] ? x : -INFINITY;
-        score0[g] = x;
+        // (the first CTA's shared memory is laid out as this one's)
+        if (chk(smem_in(smem_addr(M.score + g), 4) && M.score + g < (float *)M.list, 40)) score0[g] = x;
         kmin = min(kmin, key_of(x));
         kmax = max(kmax, key_of(x));
       }
@@ -355,21 +357,27 @@ __global__ void __launch_bounds__(kSelThreads)
     const bool in = g < n && x > hi, near = g < n && !in && !(x < lo);
     int tot;
     const int at = m + block_rank(near, &tot, S);
-    if (g < n) M.flag[g] = in;
-    if (near) M.list[at] = g;
+    if (g < n && chk(smem_in(smem_addr(M.flag + g), 1), 40)) M.flag[g] = in;
+    if (near && chk(smem_in(smem_addr(M.list + at), 4) && (uint8_t *)(M.list + at) < M.flag, 41))
+      M.list[at] = g;
     m += tot;
     n_in += __syncthreads_count(in);
   }
   const int need = k_sel - n_in;  // of the m groups near the border
+  auto take = [&](int i) {        // the i-th of them is selected
+    const int g = M.list[i];
+    if (chk(i < c.cap_groups && g >= 0 && g < n, 41)) M.flag[g] = 1;
+  };
   if (need >= m) {
-    for (int i = tid; i < m; i += kSelThreads) M.flag[M.list[i]] = 1;
+    for (int i = tid; i < m; i += kSelThreads) take(i);
   } else if (need > 0) {
     // close sums: half a warp per group, lane l of it holds positions 8 l ..
     // 8 l + 7 of the rows, which are eight channels that lie together
     const int l = lane & 15, ch = kmeta_channel(8 * l);
     for (int base = 2 * w; base < m; base += 2 * kSelWarps) {
       const int i = base + (lane >> 4);
-      const long long place = i < m ? group_slot(c, pg, b, h, M.list[i]) : -1;
+      long long place = i < m ? group_slot(c, pg, b, h, M.list[i]) : -1;
+      if (place >= 0 && !chk(in_range((size_t)place, 1, group_slots(c, pg)), 43)) place = -1;
       uint4 sw = make_uint4(0, 0, 0, 0), zw = sw;
       if (place >= 0) {
         const uint16_t *mt = c.meta + (size_t)place * 4 * 128 + 8 * l;
@@ -401,7 +409,8 @@ __global__ void __launch_bounds__(kSelThreads)
           d = d + Pair{__shfl_xor_sync(0xffffffffu, d.h, o), __shfl_xor_sync(0xffffffffu, d.l, o)};
         if (d.h > best.h || (d.h == best.h && d.l > best.l)) best = d;
       }
-      if (l == 0 && i < m) M.exact[i] = place >= 0 ? (double)best.h + (double)best.l : -INFINITY;
+      if (l == 0 && i < m && chk((float *)(M.exact + i) < M.score, 41))
+        M.exact[i] = place >= 0 ? (double)best.h + (double)best.l : -INFINITY;
     }
     __syncthreads();
     if (m <= kSelThreads) {  // a thread an entry counts those before it
@@ -409,7 +418,7 @@ __global__ void __launch_bounds__(kSelThreads)
         const double x = M.exact[tid] + 0.0;
         int before = 0;
         for (int i = 0; i < m; ++i) before += M.exact[i] > x || (M.exact[i] == x && i < tid);
-        if (before < need) M.flag[M.list[tid]] = 1;
+        if (before < need) take(tid);
       }
     } else {
       const unsigned long long k64 = kth_largest<unsigned long long, 64>(
@@ -421,7 +430,7 @@ __global__ void __launch_bounds__(kSelThreads)
         const unsigned long long x = i < m ? key_of(M.exact[i]) : 0;
         int tot;
         const int at = equal + block_rank(i < m && x == k64, &tot, S);
-        if (i < m && (x > k64 || (x == k64 && at < need - above))) M.flag[M.list[i]] = 1;
+        if (i < m && (x > k64 || (x == k64 && at < need - above))) take(i);
         equal += tot;
       }
     }
@@ -433,7 +442,7 @@ __global__ void __launch_bounds__(kSelThreads)
     const bool in = g < n && M.flag[g];
     int tot;
     const int at = done + block_rank(in, &tot, S);
-    if (in && at < k_sel) out[at] = g;
+    if (in && at < k_sel && chk(in_range(bh * k_sel + at, 1, (size_t)c.B * c.H * k_sel), 42)) out[at] = g;
     done += tot;
   }
   for (int i = done + tid; i < k_sel; i += kSelThreads) out[i] = -1;  // (never with finite queries)
@@ -488,3 +497,10 @@ extern "C" qs_status qs_select_groups(const qs_cache *c, const qs_pages *pg, con
   return R <= 16 ? launch_select<2>(cc, pages, q, R, k_sel, sel, st)
                  : launch_select<3>(cc, pages, q, R, k_sel, sel, st);
 }
+
+#if QS_CHECKED
+// Checked build only: this file's failure count and first failing tag.
+extern "C" int qs_checked_failures_select(unsigned long long *out2, int reset) {
+  return read_check_failures(out2, reset);
+}
+#endif

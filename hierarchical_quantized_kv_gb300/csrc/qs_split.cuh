@@ -524,7 +524,9 @@ __device__ __noinline__ int unit_place(const Params &prm, int b, int h, int u) {
   int32_t *st = c.state + (size_t)b * QS_STATE_WORDS;
   int g = u;
   if (prm.sel) {
-    g = prm.sel[((size_t)b * c.H + h) * prm.k_sel + u];
+    const size_t at = ((size_t)b * c.H + h) * prm.k_sel + u;
+    if (!chk(u >= 0 && u < prm.k_sel && in_range(at, 1, (size_t)c.B * c.H * prm.k_sel), 31)) return -1;
+    g = prm.sel[at];
     if (g == -1) return -1;
     if (g < 0 || g >= min(max(st[QS_ST_N_GROUPS], 0), c.cap_groups)) {
       atomicOr(&st[QS_ST_ERR], QS_DEV_SELECT);
@@ -931,6 +933,7 @@ __device__ __forceinline__ void st_cluster4(uint32_t a, float4 v) {
 //   row_m float [24]: the CTA's maxima of the rows
 //   sum   float [C][R][128], then (l, maximum) [C][R]: the CTAs' sums, in the
 //         first CTA
+//   ws_len  floats from ws on (for the checked build)
 // all of them in the stages.  With K > 1 clusters a segment, each one's first
 // CTA leaves its merged sums in ws (float [K][R][128 + 4]) and counts on
 // arrive; the last to arrive merges those.  keep: the stages must not be written (copies may
@@ -941,7 +944,8 @@ template <int NW>
 __device__ __forceinline__ void finish_cluster(Softmax &sm, float oscale, bool pk, uint8_t *smem,
                                                uint32_t sbase, int C, int rank, int ncg, int R,
                                                bool keep, bool write, uint16_t *out, float *lse,
-                                               int K, int k_self, float *ws, int *arrive) {
+                                               int K, int k_self, float *ws, size_t ws_len,
+                                               int *arrive) {
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, cq = lane & 3;
   const int cg = w % ncg, per = NW / ncg, j0 = pk ? cq : 2 * cq;
   cluster_arrive();  // this CTA's stages are free
@@ -985,6 +989,9 @@ __device__ __forceinline__ void finish_cluster(Softmax &sm, float oscale, bool p
     }
   }
   const uint32_t sum = sbase + kFinishBytes<NW>, sum_l = sum + C * R * kD * 4;
+  chk(smem_in(smem_addr(part), 8 * kD * 4) && smem_in(smem_addr(part_l), 8 * 4) &&
+          smem_in(smem_addr(mx), NW * 8 * 4) && smem_addr(mx + NW * 8) <= sum,
+      33);
   __syncthreads();
   cluster_wait();  // the first CTA's stages are free
   for (int i = threadIdx.x; i < R * 32; i += NW * 32) {
@@ -995,14 +1002,16 @@ __device__ __forceinline__ void finish_cluster(Softmax &sm, float oscale, bool p
           parts + (((j >> 3) + k * ncg) * 8 + (j & 7)) * kD + 4 * c4);
       A.x += x.x; A.y += x.y; A.z += x.z; A.w += x.w;
     }
-    st_cluster4(mapa(sum + ((rank * R + j) * kD + 4 * c4) * 4, 0), A);
+    const uint32_t dst = sum + ((rank * R + j) * kD + 4 * c4) * 4;
+    if (chk(rank < C && dst + 16 <= sum_l && smem_in(dst, 16), 33)) st_cluster4(mapa(dst, 0), A);
   }
   if (threadIdx.x < R) {
     const int j = threadIdx.x;
     float l = 0.f;
     for (int k = 0; k < per; ++k) l += parts[NW * 8 * kD + ((j >> 3) + k * ncg) * 8 + (j & 7)];
     // (a NaN maximum: this CTA's part is missing, and nothing is written)
-    st_cluster2(mapa(sum_l + (rank * R + j) * 8, 0), l, write ? row_m[j] : NAN);
+    const uint32_t dst = sum_l + (rank * R + j) * 8;
+    if (chk(rank < C && smem_in(dst, 8), 33)) st_cluster2(mapa(dst, 0), l, write ? row_m[j] : NAN);
   }
   cluster_arrive();
   if (rank != 0) return;  // (the first CTA's shared memory holds all that is still read)
@@ -1013,6 +1022,7 @@ __device__ __forceinline__ void finish_cluster(Softmax &sm, float oscale, bool p
   float *ws_self = K > 1 ? ws + (size_t)k_self * R * (kD + 4) : nullptr;
   auto put = [&](int j, int c4, float4 A, float L, float M, float *dst) {
     if (dst) {
+      if (!chk(k_self < K && in_range((size_t)(dst - ws), R * (kD + 4), ws_len), 34)) return;
       reinterpret_cast<float4 *>(dst + j * kD)[c4] = A;
       if (c4 == 0) *reinterpret_cast<float2 *>(dst + R * kD + 2 * j) = make_float2(L, M);
       return;
@@ -1060,6 +1070,7 @@ __device__ __forceinline__ void finish_cluster(Softmax &sm, float oscale, bool p
     bool whole = true;
     for (int k = 0; k < K; ++k) {
       const float *src = ws + (size_t)k * R * (kD + 4);
+      if (!chk(in_range((size_t)(src - ws), R * (kD + 4), ws_len), 34)) continue;
       const float4 x = ld_part4(src + j * kD + 4 * c4);
       const float l = ld_part(src + R * kD + 2 * j), m = ld_part(src + R * kD + 2 * j + 1);
       const float mn = fmaxf(M, m);
@@ -1376,7 +1387,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
     if (CL) a = first;
     for (int i = S + threadIdx.x; i < min(n, kListMax); i += NW * 32) {
       a.template seek<CL>(x0 + i, T, c.B);
-      list[i] = place_of(a);
+      if (chk(smem_in(smem_addr(list + i), 4), 32)) list[i] = place_of(a);
     }
     __syncthreads();
   }
@@ -1786,7 +1797,8 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
         fence_proxy_async_smem();
         int place = 0;
         if (IDX && lane == 0) {
-          place = i + S < kListMax ? list[i + S] : place_of(ahead);
+          place = i + S < kListMax && chk(smem_in(smem_addr(list + i + S), 4), 32) ? list[i + S]
+                                                                                   : place_of(ahead);
           live[stage] = place >= 0;
         }
         if (lane == 0) issued[stage] = i + S;
@@ -1844,10 +1856,13 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
   if (CL) {
     cluster_wait();  // (of the arrival at the start: every CTA runs)
     const int q = p / prm.C, seg = q / prm.K;  // (q: the cluster)
+    if (!chk(seg < c.B * c.H, 10)) return;     // (the whole cluster alike)
+    const size_t ws_off = (size_t)seg * prm.K * R * (kD + 4);
     finish_cluster<NW>(sm, Scales::kScale, PK, smem, sbase, prm.C, p % prm.C, ncg, R,
                        s_abort == 2, !aborted, prm.out + (size_t)seg * R * kD,
                        prm.lse ? prm.lse + (size_t)seg * R : nullptr, prm.K, q % prm.K,
-                       prm.ws + (size_t)seg * prm.K * R * (kD + 4), c.arrive + seg);
+                       prm.ws + ws_off, prm.ws_floats > ws_off ? prm.ws_floats - ws_off : 0,
+                       c.arrive + seg);
     return;
   }
   float *last_part = reinterpret_cast<float *>(smem);  // NW partials, in stage memory (free now)
