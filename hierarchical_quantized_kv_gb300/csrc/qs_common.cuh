@@ -79,6 +79,15 @@ inline qs_status launch_status() {
   return e == cudaSuccess ? QS_OK : QS_ERR_CUDA;
 }
 
+// SMs of the current device (the dispatch rules below count CTAs per SM).
+inline qs_status sm_count(int *sms) {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess &&
+                 cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess
+             ? QS_OK
+             : QS_ERR_CUDA;
+}
+
 // Opt a kernel into its dynamic shared memory once per device (mask: one bit per
 // device ordinal below 32).
 inline qs_status set_smem_once(const void *kernel, int smem, int *mask) {

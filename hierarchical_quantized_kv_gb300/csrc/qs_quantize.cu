@@ -635,15 +635,14 @@ using namespace qs;
 
 namespace {
 
-// Quarters per CTA: 8 for a prompt of many waves of CTAs (32 heads of 32k tokens:
-// 147 us; four 150); 4 where eight leave the last wave half empty (32 heads of 9k
-// tokens: 48 us; eight 55); fewer for a short one, whose time is one CTA's chain of
-// quarters, so that its quarters spread over five CTAs an SM first (two heads of
-// 1k tokens: 23.5 us with eight quarters a CTA).
-int prefill_quarters(long long total) {
-  const long long slots = 5 * 152;
-  if (total > slots * 3 * kPrefillQuarters) return kPrefillQuarters;
-  return total > slots * 2 ? 4 : total > slots ? 2 : 1;
+// Quarters per CTA, by the prompt's quarters per SM: 8 for a prompt of many waves
+// of CTAs (more than 120 an SM; 32 heads of 32k tokens: 147 us, four 150); 4 where
+// eight leave the last wave half empty (32 heads of 9k tokens: 48 us; eight 55);
+// fewer for a short one, whose time is one CTA's chain of quarters: 2 up to ten an
+// SM, 1 up to five (two heads of 1k tokens: 23.5 us with eight quarters a CTA).
+int prefill_quarters(long long total, int sms) {
+  if (total > 120ll * sms) return kPrefillQuarters;
+  return total > 10ll * sms ? 4 : total > 5ll * sms ? 2 : 1;
 }
 
 template <int QW>
@@ -663,9 +662,14 @@ qs_status prefill(const qs_cache &c, const Pages &pg, const uint16_t *k, const u
   if (!k || !v || !d_len || T < 0 || T > (1 << 26)) return QS_ERR_ARG;
   if (!aligned16(k) || !aligned16(v)) return QS_ERR_ALIGN;
   const int gmax = T > 2 * kG ? (T - 2 * kG + kG - 1) / kG : 0;
-  const int quarters = prefill_quarters((long long)4 * gmax * c.H * c.B);
+  const long long total = (long long)4 * gmax * c.H * c.B;
+  int sms = 0;
+  const qs_status s = sm_count(&sms);
+  if (s != QS_OK) return s;
+  const int quarters = prefill_quarters(total, sms);
   if (quarters > 2) return launch_prefill<4>(c, pg, k, v, T, d_len, gmax, quarters, stream);
-  return (long long)4 * gmax * c.H * c.B <= 2 * 152
+  // (one CTA of sixteen warps a quarter, at most two an SM; else eight warps)
+  return total <= 2ll * sms
              ? launch_prefill<16>(c, pg, k, v, T, d_len, gmax, quarters, stream)
              : launch_prefill<8>(c, pg, k, v, T, d_len, gmax, quarters, stream);
 }
@@ -684,7 +688,10 @@ qs_status launch_flush(const qs_cache &c, const Pages &pg, const uint8_t *d_mask
 // Two CTAs of sixteen warps fit an SM: beyond those the narrow ones win.
 qs_status flush(const qs_cache &c, const Pages &pg, const uint8_t *d_mask, int n_next,
                 qs_stream_t stream) {
-  return (long long)kParts * c.H * c.B <= 2 * 152
+  int sms = 0;
+  const qs_status s = sm_count(&sms);
+  if (s != QS_OK) return s;
+  return (long long)kParts * c.H * c.B <= 2ll * sms
              ? launch_flush<kFlushWarps>(c, pg, d_mask, n_next, stream)
              : launch_flush<kBatchFlushWarps>(c, pg, d_mask, n_next, stream);
 }

@@ -462,12 +462,11 @@ int g_sel_ready[3] = {0, 0, 0};  // one bit per device ordinal below 32
 template <int NCG>
 qs_status launch_select(const qs_cache &c, const Pages &pg, const uint16_t *q, int R, int k_sel,
                         int32_t *sel, cudaStream_t stream) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return QS_ERR_CUDA;
-  const qs_status s = set_smem_once((const void *)select_kernel<NCG>,
-                                    (int)select_smem(kMaxSelectGroups), &g_sel_ready[NCG - 1]);
+  int sms = 0;
+  qs_status s = sm_count(&sms);
+  if (s != QS_OK) return s;
+  s = set_smem_once((const void *)select_kernel<NCG>, (int)select_smem(kMaxSelectGroups),
+                    &g_sel_ready[NCG - 1]);
   if (s != QS_OK) return s;
   const int cl = cluster_size(c, sms);
   return launch_pdl_cluster(select_kernel<NCG>, dim3(cl, c.H, c.B), dim3(kSelThreads), cl,
