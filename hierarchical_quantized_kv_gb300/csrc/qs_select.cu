@@ -159,14 +159,16 @@ __device__ __forceinline__ uint4 ld16(const uint16_t *p) {
   return *reinterpret_cast<const uint4 *>(p);
 }
 
-// Grid (cluster size, H, B).  NCG: column groups of eight query rows.
+// Grid (cluster size, H, B).  NCG: column groups of eight query rows.  (Two CTAs an
+// SM asked for in the usual variant, or the compiler stops at 108 registers with
+// fewer rows in flight: 16 x 32 heads of 512 groups 41.7 us; so 30.3.)
 template <int NCG>
-__global__ void __launch_bounds__(kSelThreads)
+__global__ void __launch_bounds__(kSelThreads, NCG == 1 ? 2 : 1)
     select_kernel(qs_cache c, Pages pg, const uint16_t *q, int R, int k_sel, int32_t *sel) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ BlockScratch S;
   // the first CTA's: largest sum of magnitudes, smallest and largest key of a score
-  __shared__ int s_mag;
+  __shared__ int s_mag, s_n;
   __shared__ unsigned s_kmin, s_kmax;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), n_ranks = (int)cluster.num_blocks();
@@ -195,15 +197,27 @@ __global__ void __launch_bounds__(kSelThreads)
     }
   }
   pdl_wait();
+  // Should somebody change the counter meanwhile (against the rule that calls on a
+  // cache are ordered), warps and CTAs may differ in it.  The selection is then
+  // worth nothing, but a CTA goes one way, all meet the cluster's barriers and the
+  // first CTA leaves last, so that no store goes to one that has gone; and that CTA
+  // selects by the one number that its first thread read.
   int32_t *st = c.state + (size_t)b * QS_STATE_WORDS;
-  const int n = min(max(st[QS_ST_N_GROUPS], 0), c.cap_groups);
+  const int n_warp = min(max(st[QS_ST_N_GROUPS], 0), c.cap_groups);
+  if (tid == 0) s_n = n_warp;
   const size_t bh = (size_t)b * c.H + h;
   int32_t *out = sel + bh * k_sel;
-  if (n <= k_sel) {  // all of them (the whole cluster alike)
+  if (__syncthreads_and(n_warp <= k_sel)) {  // all of them
     if (rank == 0)
-      for (int i = tid; i < k_sel; i += kSelThreads) out[i] = i < n ? i : -1;
+      for (int i = tid; i < k_sel; i += kSelThreads) out[i] = i < s_n ? i : -1;
+    if (n_ranks > 1) {
+      cluster.barrier_arrive();
+      cluster.barrier_wait();
+      cluster.sync();
+    }
     return;
   }
+  int n = n_warp;
   // the first CTA's shared memory is written below: it must have started
   cluster.barrier_arrive();
 
@@ -332,6 +346,7 @@ __global__ void __launch_bounds__(kSelThreads)
   }
   cluster.sync();  // all scores are in the first CTA
   if (rank != 0) return;
+  n = s_n;
 
   // ---- selection.  One MMA adds 17 numbers, aligned to the largest and cut
   // no coarser than 2^-23 of it: off by less than 2^-18.9 of the sum of their

@@ -1291,11 +1291,13 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
     if (threadIdx.x == 0) atomicOr(&c.state[(size_t)b * QS_STATE_WORDS + QS_ST_ERR], QS_DEV_NQ_GT_FILL);
   }
 
-  // clustered: the segment's units from 0 on, and a CTA without any still
-  // meets its cluster at the end
+  // clustered: the segment's units from 0 on, and a CTA without any still meets
+  // its cluster at the end, also where the segment has none: should its counters
+  // change meanwhile (against the rule that calls on a cache are ordered), another
+  // CTA may have seen some, and stores to the first one's shared memory
   const int x0 = CL ? cl_x0 : (int)range_lo(p, U, prm.P);
   const int x1 = CL ? cl_x0 + cl_n : (int)range_lo(p + 1, U, prm.P);
-  if (CL ? seg_cl.len == 0 : x0 >= x1) {
+  if (!CL && x0 >= x1) {
     if (IDX && appends) append();
     return;
   }
@@ -1859,7 +1861,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
     if (!chk(seg < c.B * c.H, 10)) return;     // (the whole cluster alike)
     const size_t ws_off = (size_t)seg * prm.K * R * (kD + 4);
     finish_cluster<NW>(sm, Scales::kScale, PK, smem, sbase, prm.C, p % prm.C, ncg, R,
-                       s_abort == 2, !aborted, prm.out + (size_t)seg * R * kD,
+                       s_abort == 2, !aborted && seg_cl.len > 0, prm.out + (size_t)seg * R * kD,
                        prm.lse ? prm.lse + (size_t)seg * R : nullptr, prm.K, q % prm.K,
                        prm.ws + ws_off, prm.ws_floats > ws_off ? prm.ws_floats - ws_off : 0,
                        c.arrive + seg);
