@@ -56,7 +56,7 @@ struct FlushSmem {
     };
   };
   uint16_t vs[kSlice], vz[kSlice];
-  int act, base, g;
+  int act, base, g, place;
 };
 
 __device__ __forceinline__ void scale_zero(float mn, float mx, uint16_t &s_bits, uint16_t &z_bits,
@@ -475,10 +475,14 @@ __global__ void __launch_bounds__(32 * QW)
     } else if (act && (ng < 0 || ng >= c.cap_groups)) {
       if (lead) atomicOr(&st[QS_ST_ERR], QS_DEV_CAPACITY);
       act = 0;
-    } else if (act && group_slot(c, pg, b, h, ng) < 0) {
+    }
+    // (the page is looked up once: the entry that was found good is the one used)
+    const long long place = act ? group_slot(c, pg, b, h, ng) : 0;
+    if (place < 0) {
       if (lead) atomicOr(&st[QS_ST_ERR], QS_DEV_PAGE);
       act = 0;
     }
+    S.place = (int)place;  // a group takes 33 KB: places stay far below 2^31
     S.act = act;
     S.base = st[QS_ST_HALF_BASE] & 1;
     S.g = ng;
@@ -490,7 +494,7 @@ __global__ void __launch_bounds__(32 * QW)
   const __half *gk = reinterpret_cast<const __half *>(c.buf_k) + (bh * kRing + base * kG) * kD;
   const __half *gv = reinterpret_cast<const __half *>(c.buf_v) + (bh * kRing + base * kG) * kD;
 
-  quantize_part(S, gk, gv, c, group_slots(c, pg), (size_t)group_slot(c, pg, b, h, g), part, tid);
+  quantize_part(S, gk, gv, c, group_slots(c, pg), (size_t)S.place, part, tid);
   __syncthreads();
   // every CTA of the sequence has read the old counters once the ticket
   // reaches kParts H - 1 (the planes are published by the kernel's end)
@@ -506,9 +510,10 @@ __global__ void __launch_bounds__(32 * QW)
 // Grid (nq + 2, H, B), or, into pages, ((nq + 2) H, 1, B) with the heads of a
 // page side by side: block x < nq quantizes group quarters [x Q, x Q + Q) of the
 // sequence's head (quarter i: part i % 4 of group i / 4; Q = quarters), the next
-// quarter's rows copied into the second buffer while the current one is quantized; the last two blocks copy buffer halves
-// 0 and 1.  The CTA that arrives last on the sequence's ticket writes the
-// counters, so every CTA reads the old (empty) ones first.
+// quarter's rows copied into the second buffer while the current one is quantized;
+// the last two blocks copy buffer halves 0 and 1.  The CTA that arrives last on
+// the sequence's ticket writes the counters, so every CTA reads the old (empty)
+// ones first.
 template <int QW>
 __global__ void __launch_bounds__(32 * QW, 24 / QW)
     prefill_kernel(qs_cache c, Pages pg, const uint16_t *k, const uint16_t *v, int T,
@@ -549,9 +554,10 @@ __global__ void __launch_bounds__(32 * QW, 24 / QW)
   const uint16_t *kp = k + bh * T * kD, *vp = v + bh * T * kD;
   // Paged: every page the prompt needs, looked at by every CTA alike (while its
   // first rows are on their way): a bad one leaves the whole sequence unchanged.
-  auto pages_good = [&]() {
+  // bad_own: an entry that this thread has read already and will use is a bad one.
+  auto pages_good = [&](bool bad_own) {
     if (!pg.table) return true;
-    int bad = 0;
+    int bad = bad_own;
     for (int g = tid; g < ng; g += 32 * QW) bad |= group_slot(c, pg, b, h, g) < 0;
     if (!__syncthreads_or(bad)) return true;
     if (h == 0 && x == 0 && tid == 0) atomicOr(&st[QS_ST_ERR], QS_DEV_PAGE);
@@ -571,8 +577,12 @@ __global__ void __launch_bounds__(32 * QW, 24 / QW)
     if (q0 < q1) load(q0);
     // (looked up once: a table read a quarter, even from L1, cost 9 % of the call)
     const int g0 = q0 >> 2;
-    if (tid < kPrefillQuarters / 4 + 1 && g0 + tid < ng) PS.place[tid] = (int)group_slot(c, pg, b, h, g0 + tid);
-    if (!pages_good()) {
+    long long own = 0;
+    if (tid < kPrefillQuarters / 4 + 1 && g0 + tid < ng) {
+      own = group_slot(c, pg, b, h, g0 + tid);
+      PS.place[tid] = (int)own;
+    }
+    if (!pages_good(own < 0)) {
       cp_async_wait<0>();
       return;
     }
@@ -590,7 +600,7 @@ __global__ void __launch_bounds__(32 * QW, 24 / QW)
         quantize_loaded(S, i & 1 ? PS.k1 : S.k, i & 1 ? PS.v1 : S.v, c, grp, i & 3, tid);
     }
   } else {
-    if (!pages_good()) return;
+    if (!pages_good(false)) return;
     // buffer half x - nq: tokens i in [G half, G half + G) that are < fill
     const int i0 = (x - nq) * kG, i1 = min(i0 + kG, fill);
     const uint4 *ks = reinterpret_cast<const uint4 *>(kp + (size_t)ng * kG * kD);
