@@ -22,14 +22,14 @@ constexpr int kParts = 4;           // CTAs per (head, sequence)
 constexpr int kSlice = kD / kParts;  // key channels / value tokens per CTA
 // Warps per CTA.  A flush of few heads is one wave of small CTAs, so its time is
 // one CTA's chain of phases, and sixteen warps shorten every phase but the
-// packing (32 heads: 4.6 us; eight warps 5.4, four 6.5); one of many is bound
-// by instruction issue like a prefill, where four are best (8 x 32 heads: 9.3 us;
-// eight 11.3, sixteen 15.1).  In a prefill of many waves, what a thread does once
+// packing (32 heads: 4.2 us; eight warps 5.2, four 6.2); one of many is bound
+// by instruction issue like a prefill, where four are best (8 x 32 heads: 9.4 us;
+// eight 10.5, sixteen 12.4).  In a prefill of many waves, what a thread does once
 // per quarter (addresses, scales) counts: four warps, twice the elements a
 // thread, 147 us for 32 heads of 32k tokens (0.82 of the copy bandwidth's rate;
 // eight: 175).  A prompt of one or two quarters per CTA is a chain again (four
-// sequences of 1k tokens and 8 heads: eight warps 7.4 us, four 8.7), and a very
-// short one takes sixteen (two heads of 1k tokens: 3.8 us; eight 5.0, four 7.6).
+// sequences of 1k tokens and 8 heads: eight warps 7.3 us, four 8.5), and a very
+// short one takes sixteen (two heads of 1k tokens: 3.6 us; eight 3.8, four 4.1).
 constexpr int kFlushWarps = 16, kBatchFlushWarps = 4;
 // Group quarters per quantizing CTA of a prefill, loads pipelined one ahead, at
 // most.
@@ -647,9 +647,10 @@ namespace {
 
 // Quarters per CTA, by the prompt's quarters per SM: 8 for a prompt of many waves
 // of CTAs (more than 120 an SM; 32 heads of 32k tokens: 147 us, four 150); 4 where
-// eight leave the last wave half empty (32 heads of 9k tokens: 48 us; eight 55);
+// eight leave the last wave half empty (32 heads of 9k tokens: 48 us; eight 52);
 // fewer for a short one, whose time is one CTA's chain of quarters: 2 up to ten an
-// SM, 1 up to five (two heads of 1k tokens: 23.5 us with eight quarters a CTA).
+// SM, 1 up to five (two heads of 1k tokens: 15.6 us with eight quarters of four
+// warps a CTA).
 int prefill_quarters(long long total, int sms) {
   if (total > 120ll * sms) return kPrefillQuarters;
   return total > 10ll * sms ? 4 : total > 5ll * sms ? 2 : 1;

@@ -5,8 +5,9 @@
 // its tokens lies in [z_d, z_d + 255 s_d] (zero and scale of the per-channel
 // quantization).  The largest score a key in that box can have with a query q,
 //   sum_d max(q_d z_d, q_d (z_d + 255 s_d)) = q . z + 255 relu(q) . s,
-// bounds the score of every token of the group, and is two dot products with
-// the 512 bytes of scales and zeros the attention reads anyway.  A head's
+// bounds the score of every token of the group (the criterion of Quest, 2024, for
+// blocks of keys), and is two dot products with the 512 bytes of scales and zeros
+// the attention reads anyway.  A head's
 // score for a group is the maximum over its query rows.
 //
 // Which of two close groups is taken must not depend on rounding: scores come

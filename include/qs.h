@@ -191,8 +191,8 @@ qs_status qs_cache_bytes(int32_t B, int32_t H, int32_t D, int32_t G, int32_t cap
  * (the most groups a sequence may have).  Buffers, state and arrive are as for
  * a contiguous cache.  The table (int32 [B][cap_groups], device memory,
  * 4-byte aligned) is the caller's: entries below n_groups must be valid, the
- * entry of a group about to be written before the call that writes it, the
- * rest is not read.  Sequences may share pages (a common prefix); a page that
+ * entry of a group about to be written before the call that writes it, and both
+ * stay as they are while a call runs; the rest is not read.  Sequences may share pages (a common prefix); a page that
  * is written (flush, prefill) must belong to one sequence alone.  An entry in
  * use outside [0, n_pages) gives QS_DEV_PAGE: a write leaves the sequence
  * unchanged, a read leaves the group out.
@@ -451,9 +451,13 @@ qs_status qs_attn_decode_paged(const qs_cache *c, const qs_pages *pg, qs_mode mo
  * selection.  One launch.  Errors: QS_ERR_ARG (null q or sel, n_q, group or
  * k_sel out of range, pg missing or not wanted), QS_ERR_UNSUPPORTED
  * (cap_groups > 12800, a context of 1.6 million tokens), QS_ERR_ALIGN.
- * Source: Pith review page (sparse-KV drafting named as work to combine with
- * this cache) and Appendix D (keys quantized per channel, whose zero and scale
- * are the box); the score is this library's. */
+ * A flush makes a group that an earlier selection does not name: select again
+ * after it.  Source: Pith review page (sparse-KV drafting named as work to combine
+ * with this cache) and Appendix D (keys quantized per channel, whose zero and scale
+ * are the box).  An upper bound on a block's scores from the minima and maxima of
+ * its keys' channels is a published criterion for choosing blocks (Quest:
+ * query-aware sparsity for long-context inference, 2024); taking it from the
+ * quantizer's own metadata is this library's. */
 qs_status qs_select_groups(const qs_cache *c, const qs_pages *pg, const uint16_t *q, int32_t n_q,
                            int32_t group, int32_t k_sel, int32_t *sel, qs_stream_t stream);
 
