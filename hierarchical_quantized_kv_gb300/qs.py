@@ -324,8 +324,8 @@ def _check_f16(cache, t, name):
 
 def qs_prefill_paged(cache, k, v, lens, stream=None):
     """qs_prefill on a PagedCache."""
-    if not (k.shape == v.shape and k.dim() == 4 and k.shape[:2] == (cache.B, cache.H) and
-            k.shape[3] == cache.D):
+    if k is None or v is None or not (k.shape == v.shape and k.dim() == 4 and
+                                      k.shape[:2] == (cache.B, cache.H) and k.shape[3] == cache.D):
         raise QsArgumentError("k, v: [B, H, T, D]")
     _check_f16(cache, k, "k")
     _check_f16(cache, v, "v")
@@ -340,7 +340,8 @@ def qs_cache_read(cache, mode, k, v, tok0=0, stream=None):
     """Tokens [tok0, tok0 + T) of each sequence as fp16 rows into k, v: fp16
     [B, H, T, D] contiguous device tensors, one of them may be None.  Rows past
     a sequence's last token stay as they were."""
-    T = (v if k is None else k).shape[2] if k is not None or v is not None else 0
+    shape = () if k is None and v is None else (v if k is None else k).shape
+    T = shape[2] if len(shape) == 4 else 0
     for name, t in (("k", k), ("v", v)):
         if t is not None:
             if t.shape != (cache.B, cache.H, T, cache.D):

@@ -88,6 +88,8 @@ BAD = [
     (select, dict(q=half(*Q, dtype=BF))), (select, dict(q=half(*Q, away=True))),
     (select, dict(sel=zeros(2, 3, 2, dtype=I32, away=True))),
     (read, dict(k_new=half(*KV, dtype=BF))), (read, dict(v_new=half(*KV, away=True))),
+    (read, dict(k_new=half(2, 3))), (read, dict(k_new=None, v_new=half(2, 3, 128))),
+    (prefill, dict(v_new=None)), (prefill, dict(k_new=half(2, 3, 128), v_new=half(2, 3, 128))),
     (prefill, dict(k_new=half(*KV, dtype=BF), v_new=half(*KV, dtype=BF))),
     (prefill, dict(v_new=half(*KV, away=True))), (prefill, dict(lens=torch.zeros(2))),
     (prefill, dict(lens=zeros(2, dtype=I32, away=True))),
