@@ -35,8 +35,9 @@ __device__ __forceinline__ bool before(float k1, int x1, float k2, int x2) {
 }
 
 // This CTA's best (key, index) over x in [x0, x1) of the weights p (minus q
-// when q is given, clamped at 0): block reduction into s_key[0], s_idx[0].
-__device__ void race_block(const float *wp, const float *wq, const float *eb, int x0, int x1,
+// when q is given, clamped at 0): block reduction into s_key[0], s_idx[0] (none, a
+// negative number, where no weight is positive).
+__device__ void race_block(const float *wp, const float *wq, const float *eb, int x0, int x1, int none,
                            float *s_key, int *s_idx) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   float key = 0.f;
@@ -76,7 +77,7 @@ __device__ void race_block(const float *wp, const float *wq, const float *eb, in
         idx = s_idx[w2];
       }
     s_key[0] = key;
-    s_idx[0] = idx;
+    s_idx[0] = idx < 0 ? none : idx;
   }
 }
 
@@ -127,24 +128,29 @@ __global__ void __cluster_dims__(kSpecCluster, 1, 1) __launch_bounds__(kSpecThre
   const int chunk = (V + kSpecCluster - 1) / kSpecCluster;
   const int x0 = min(V, rank * chunk), x1 = min(V, x0 + chunk);
   // pass 0: the residual (p_a - q_a)_+ after a rejection, else p_gamma;
-  // pass 1 (a residual that is zero everywhere): p_a
+  // pass 1 (a residual that is zero everywhere): p_a.  Whether there is one is read
+  // off the eight CTAs' winners (-1: none, from a residual; -2: none, from p_gamma),
+  // not off each CTA's own count, so that all go the same way even if somebody
+  // changes the inputs meanwhile: none may leave while another reads its winner.
   int idx = -1;
   for (int pass = 0; pass < 2; ++pass) {
     const float *wq = (a < gamma && pass == 0) ? qb + (size_t)a * V : nullptr;
-    race_block(pb + (size_t)a * V, wq, eb, x0, x1, s_key, s_idx);
+    race_block(pb + (size_t)a * V, wq, eb, x0, x1, a < gamma ? -1 : -2, s_key, s_idx);
     cluster.sync();  // every slice's winner is in its CTA's shared memory
     float key = 0.f;
     idx = -1;
+    bool again = false;
     for (int r = 0; r < kSpecCluster; ++r) {  // in rank order: ties to the smaller index
       const float k2 = *cluster.map_shared_rank(&s_key[0], r);
       const int i2 = *cluster.map_shared_rank(&s_idx[0], r);
+      again |= i2 == -1;
       if (before(k2, i2, key, idx)) {
         key = k2;
         idx = i2;
       }
     }
     cluster.sync();  // no CTA overwrites its winner while another still reads it
-    if (idx >= 0 || a == gamma) break;
+    if (idx >= 0 || !again) break;
   }
   if (rank == 0 && tid == 0) {
     n_accept[b] = a;

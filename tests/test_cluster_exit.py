@@ -26,6 +26,13 @@ def test_selection_meets_every_barrier():
     assert re.match(r"cluster\.sync\(\);\s*if \(rank != 0\) return;\s*n = s_n;", text[text.rindex("cluster.sync()"):])
 
 
+def test_acceptance_decides_its_second_pass_together():
+    text = body(code("qs_spec.cu"), "spec_accept_kernel")
+    loop = text[text.index("for (int pass = 0"):]
+    assert "if (idx >= 0 || !again) break;" in loop and loop.count("break;") == 1
+    assert loop.count("cluster.sync()") == 2 and "return" not in text
+
+
 def test_clustered_attention_meets_every_barrier():
     text = body(code("qs_split.cuh"), "split_kernel")
     start = text[:text.index("finish_cluster<NW>(")]
