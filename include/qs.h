@@ -366,7 +366,10 @@ qs_status qs_attn_workspace_size(const qs_cache *c, int32_t n_q, size_t *bytes);
  * Sequences with n_q > fill get QS_DEV_NQ_GT_FILL, zero output, lse = -inf.
  * Here and in every other attention call the product of a query and a key scale
  * is an fp16 number: |q_d| times the scale of a group's channel d has to stay
- * below 65,504 (a key range of 65,504 * 255 / |q_d|), or the row is NaN.
+ * below 65,504 (a key range of 65,504 * 255 / |q_d|), or the row is NaN.  Which
+ * warp takes which tokens varies from run to run, and with it the rounding: the
+ * same call twice gives outputs that differ by about 2e-4 of their size (fp16
+ * steps), the log-sum-exp by fp32 steps.
  * One kernel launch: a persistent split-KV pass over a balanced partition of
  * all (sequence, head, group) units, whose log-sum-exp merge of the splits
  * runs in the same kernel.  Errors: QS_ERR_ARG (null q/out, n_q outside 1..8,
