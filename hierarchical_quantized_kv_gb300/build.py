@@ -17,7 +17,8 @@ LIB = os.path.join(HERE, "libqs.so")
 BUILD_CHECKED = os.path.join(HERE, "_build_checked")
 LIB_CHECKED = os.path.join(HERE, "libqs_checked.so")
 SOURCES = ["qs_buffer.cu", "qs_quantize.cu", "qs_attn.cu", "qs_attn_static.cu", "qs_spec.cu",
-           "qs_read.cu", "qs_attn_list.cu", "qs_select.cu"]
+           "qs_read.cu", "qs_attn_list.cu", "qs_select.cu", "qs_attn_tree.cu", "qs_tree.cu",
+           "qs_sample.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "nvcc")
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

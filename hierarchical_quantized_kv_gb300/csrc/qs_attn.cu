@@ -102,6 +102,7 @@ extern "C" int qs_checked_failures_quantize(unsigned long long *out2, int reset)
 extern "C" int qs_checked_failures_listed(unsigned long long *out2, int reset);
 extern "C" int qs_checked_failures_select(unsigned long long *out2, int reset);
 extern "C" int qs_checked_failures_read(unsigned long long *out2, int reset);
+extern "C" int qs_checked_failures_tree(unsigned long long *out2, int reset);
 
 // Checked build only (-DQS_CHECKED=1): the number of failed bounds checks of
 // the kernels since the last reset, and the tag of the first (attention: 1
@@ -115,10 +116,10 @@ extern "C" int qs_checked_failures_read(unsigned long long *out2, int reset);
 // row, 53 tile row).  reset != 0 zeroes the counts.  Returns 0, or 1 if a CUDA call
 // failed.
 extern "C" int qs_checked_failures(unsigned long long *count, unsigned int *first_tag, int reset) {
-  unsigned long long f[5][2];
+  unsigned long long f[6][2];
   if (read_check_failures(f[0], reset) || qs_checked_failures_quantize(f[1], reset) ||
       qs_checked_failures_listed(f[2], reset) || qs_checked_failures_select(f[3], reset) ||
-      qs_checked_failures_read(f[4], reset))
+      qs_checked_failures_read(f[4], reset) || qs_checked_failures_tree(f[5], reset))
     return 1;
   *count = 0;
   *first_tag = 0;

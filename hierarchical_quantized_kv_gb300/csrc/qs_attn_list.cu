@@ -10,43 +10,6 @@ using namespace qs;
 
 namespace {
 
-// Clustered kernel: prm.C CTAs to a cluster, prm.K clusters to a segment; C = 1:
-// the split kernel.  The clustered kernel starts and ends about 7 us sooner
-// (verify: 11 us), but gives every segment as many CTAs as every other and
-// leaves some of the SMs idle.  So it is for segments of equal length, one
-// sequence or selections, where the longer share of a CTA costs less than that:
-// measured, 0.36 us a unit for a draft and 0.6 us for a verify pass, for every
-// eight query rows; more clusters cost a segment another 2 us at its end.  All
-// clusters have to be resident at once (this GPU: 76 of 2, 36 of 4, 15 of 8 CTAs;
-// sixteen of 8, in two waves, took 29.7 us where thirty-two of 4 take 18.6).
-qs_status choose_clusters(Params &prm, qs_mode mode) {
-  const long long segs = (long long)prm.c.B * prm.c.H;
-  const int sms = prm.P;
-  prm.C = prm.K = 1;
-  if (prm.c.B > 1 && !prm.sel) return QS_OK;
-  int grid = 0;
-  const int *resident = nullptr;
-  const qs_status s = grid_size<kClustered>(mode, packed_rows(mode, prm.R), prm.c.upper_bits, prm.ncg,
-                                            grid, &resident);
-  if (s != QS_OK) return s;
-  const long long groups = prm.sel && prm.k_sel < prm.c.cap_groups ? prm.k_sel : prm.c.cap_groups;
-  const double units = groups + (mode == QS_DRAFT_UPPER4 ? 8 : 4);  // (and a full buffer)
-  const double unit_us = (mode == QS_DRAFT_UPPER4 ? 0.36 : 0.6) * prm.ncg;
-  double best = units * segs / sms * unit_us + (mode == QS_DRAFT_UPPER4 ? 7.0 : 11.0);
-  for (int n = kMaxCluster; n >= 2; n /= 2) {
-    const int k_max = (int)(resident[n] / segs);
-    for (int k = 1; k <= k_max && k <= 16; ++k) {
-      const double us = units / (n * k) * unit_us + (k > 1 ? 2.0 : 0.0);
-      if (us < best) {
-        best = us;
-        prm.C = n;
-        prm.K = k;
-      }
-    }
-  }
-  return QS_OK;
-}
-
 qs_status decode_listed(Params &prm, qs_mode mode, const uint16_t *k_new, const uint16_t *v_new,
                         int32_t n_new, const uint16_t *q, int32_t n_q, int32_t group,
                         float softmax_scale, uint16_t *out, float *lse, void *workspace,
@@ -66,7 +29,7 @@ qs_status decode_listed(Params &prm, qs_mode mode, const uint16_t *k_new, const 
   if (s != QS_OK) return s;
   const bool packed = packed_rows(mode, prm.R);
   cudaStream_t st = (cudaStream_t)stream;
-  if ((s = choose_clusters(prm, mode)) != QS_OK) return s;
+  if ((s = choose_clusters<0>(prm, mode)) != QS_OK) return s;
   if (prm.C < 2) return launch_kind<kListed>(mode, packed, prm, st);
   prm.P = prm.c.B * prm.c.H * prm.K * prm.C;
   return launch_kind<kClustered>(mode, packed, prm, st);

@@ -70,8 +70,8 @@ template <bool PAD>
 constexpr int tail_row() { return PAD ? 272 : 256; }
 constexpr int kOffKU = 0, kOffVU = 8192, kOffMeta = 16384, kOffKL = 17408, kOffVL = 25600;
 
-// The kernel's variants (see split_kernel).
-enum { kContiguous = 0, kListed = 1, kClustered = 2 };
+// The kernel's variants (see split_kernel); kTree is added to one of the last two.
+enum { kContiguous = 0, kListed = 1, kClustered = 2, kTree = 4 };
 
 template <int MODE>
 struct Cfg;
@@ -146,6 +146,10 @@ struct Params {
   Pages pg;
   const int32_t *sel;
   int k_sel;
+  // tree variants: parents of the last n_tree buffer tokens, int32 [B][n_tree]; the
+  // queries are the last n_q of those
+  const int32_t *parent;
+  int n_tree;
   size_t ws_floats;  // workspace size (the checked build bounds its indexing by it)
 };
 
@@ -1125,6 +1129,67 @@ __device__ __forceinline__ void write_empty(float *dst, int R, int cg, int lane)
   }
 }
 
+// ---- trees -----------------------------------------------------------------
+// A node's parent as the kernels take it: one that is not an earlier node counts
+// as -1 (and is flagged by the caller).
+__device__ __forceinline__ int node_parent(const int32_t *parent, int j, bool &bad) {
+  const int up = parent[j];
+  const bool ok = up >= -1 && up < j;
+  bad |= !ok;
+  return ok ? up : -1;
+}
+
+// Ancestors (bit j: node j, the node itself among them) of nodes lane and lane + 32
+// of a tree of n <= 64, by a whole warp: each round every node takes over what its
+// furthest known ancestor has gathered, which doubles the reach.
+__device__ __forceinline__ void tree_ancestors(const int32_t *parent, int n, int lane, uint64_t (&m)[2],
+                                               bool &bad) {
+  int up[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int j = lane + 32 * k;
+    up[k] = j < n ? node_parent(parent, j, bad) : -1;
+    m[k] = 1ull << j;
+  }
+  for (int reach = 1; reach < n; reach *= 2) {
+    uint64_t got[2];
+    int next[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int src = up[k] & 31;
+      const uint64_t a = __shfl_sync(0xffffffffu, m[0], src), b = __shfl_sync(0xffffffffu, m[1], src);
+      const int ua = __shfl_sync(0xffffffffu, up[0], src), ub = __shfl_sync(0xffffffffu, up[1], src);
+      got[k] = up[k] < 0 ? 0 : up[k] < 32 ? a : b;
+      next[k] = up[k] < 0 ? -1 : up[k] < 32 ? ua : ub;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      m[k] |= got[k];
+      up[k] = next[k];
+    }
+  }
+}
+// The ancestors of node j (0 <= j < 64), from the lane that has them.
+__device__ __forceinline__ uint64_t ancestors_of(const uint64_t (&m)[2], int j) {
+  const uint64_t a = __shfl_sync(0xffffffffu, m[0], j & 31), b = __shfl_sync(0xffffffffu, m[1], j & 31);
+  return j < 32 ? a : b;
+}
+
+// The halves of a pair that are infinite or not numbers become 0; bit 0 and 1 say which.
+__device__ __forceinline__ unsigned drop_nonfinite(uint32_t &x) {
+  const unsigned lo = (x & 0x7C00u) == 0x7C00u, hi = (x & 0x7C000000u) == 0x7C000000u;
+  if (lo) x &= 0xFFFF0000u;
+  if (hi) x &= 0x0000FFFFu;
+  return lo | hi << 1;
+}
+
+// The same for the upper half alone (a pair across the tree's start): bit 0.
+__device__ __forceinline__ unsigned drop_high(uint32_t &x) {
+  const unsigned hi = (x & 0x7C000000u) == 0x7C000000u;
+  if (hi) x &= 0x0000FFFFu;
+  return hi;
+}
+
 // Wait (at most limit_ns) until a stage's copy of unit i has been issued.
 __device__ __forceinline__ bool wait_issued(volatile int *issued, int i, uint64_t limit_ns) {
   if (*issued == i) return true;
@@ -1142,11 +1207,12 @@ __device__ __forceinline__ bool wait_issued(volatile int *issued, int i, uint64_
 // NW: warps per CTA (12, or kVerifyWarps for a verify tile of <= 16 rows).
 // KIND: kContiguous; kListed: groups lie where a page table and / or a list of
 // selected groups puts them (unit_place); kClustered: listed, each segment
-// shared by one cluster of CTAs.  Variants of their own, so that the
-// contiguous kernel carries nothing of the others.
+// shared by one cluster of CTAs; either with kTree: the queries are nodes of a tree,
+// which see their ancestors among the last n_tree buffer tokens.  Variants of
+// their own, so that the contiguous kernel carries nothing of the others.
 template <int MODE, bool PK, int UB, int NW, int KIND>
 __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
-  constexpr bool IDX = KIND != kContiguous, CL = KIND == kClustered;
+  constexpr bool IDX = KIND != kContiguous, CL = (KIND & 3) == kClustered, TREE = (KIND & kTree) != 0;
   using Scales = Centre<MODE, UB, IDX>;  // (IDX: drafts' codes further up, see pairs_upper)
   using C = Cfg<MODE>;
   using L = Layout<MODE>;
@@ -1202,6 +1268,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
   }
   pdl_wait();  // counters, cache and queries are written by earlier kernels
   const int n_sel = IDX && prm.sel ? prm.k_sel : INT_MAX;
+  const int n_tail = TREE ? prm.n_tree : prm.n_q;  // buffer tokens that the mask is about
   // clustered: this CTA's segment and its share of it, and its sequence's counters
   Seg seg_cl;
   int cl_x0 = 0, cl_n = 0;
@@ -1210,14 +1277,14 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
     seg_cl.b = seg / c.H;
     seg_cl.h = seg % c.H;
     if (threadIdx.x == 0)
-      T.len[seg_cl.b] = sequence_entry<TT, IDX>(c, prm.n_q, prm.n_new, n_sel, T, seg_cl.b);
+      T.len[seg_cl.b] = sequence_entry<TT, IDX>(c, n_tail, prm.n_new, n_sel, T, seg_cl.b);
     __syncthreads();
     seg_cl.len = T.len[seg_cl.b];
     cl_x0 = (int)((long long)seg_cl.len * part / per_seg);
     cl_n = (int)((long long)seg_cl.len * (part + 1) / per_seg) - cl_x0;
   } else {
     if (w == 0) {
-      const long long tot = build_tables<TT, IDX>(c, prm.n_q, prm.n_new, n_sel, T, lane);
+      const long long tot = build_tables<TT, IDX>(c, n_tail, prm.n_new, n_sel, T, lane);
       if (lane == 0) s_total = tot;
     }
     __syncthreads();
@@ -1716,6 +1783,17 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
           const int row0 = PK ? cq : 8 * cg + 2 * cq;
           const int lim0 = fill - prm.n_q + row0 % prm.n_q;
           const int lim1 = fill - prm.n_q + (row0 + 1) % prm.n_q;
+          // tree: the ancestors of the two columns' nodes, and where the tree starts
+          uint64_t anc0 = 0, anc1 = 0, nonfinite = 0;
+          const int tree0 = fill - n_tail;
+          if (TREE) {
+            uint64_t m[2];
+            bool bad = false;
+            tree_ancestors(prm.parent + (size_t)cur.b * n_tail, n_tail, lane, m, bad);
+            anc0 = ancestors_of(m, n_tail - prm.n_q + row0 % prm.n_q);
+            anc1 = ancestors_of(m, n_tail - prm.n_q + (row0 + 1) % prm.n_q);
+            if (bad) atomicOr(&c.state[(size_t)cur.b * QS_STATE_WORDS + QS_ST_ERR], QS_DEV_TREE);
+          }
           float sv[kTailTiles][4];
           float g0 = -INFINITY, g1 = -INFINITY;
 #pragma unroll
@@ -1741,7 +1819,12 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int tok = mr + r + 8 * (k >> 1);
-              const bool vis = tok < rows && (i0 + tok) <= ((k & 1) ? lim1 : lim0) && !(PK && (k & 1));
+              bool seen = (i0 + tok) <= ((k & 1) ? lim1 : lim0);
+              if (TREE) {
+                const int j = i0 + tok - tree0;  // (below 64 for a token that there is)
+                seen = j < 0 || ((((k & 1) ? anc1 : anc0) >> (j & 63)) & 1);
+              }
+              const bool vis = tok < rows && seen && !(PK && (k & 1));
               sv[tl][k] = vis ? acc[k] * prm.sl2 : -INFINITY;
             }
             g0 = fmaxf(g0, fmaxf(sv[tl][0], sv[tl][2]));
@@ -1774,12 +1857,29 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
               if (!chk(smem_in(addr, 16), 6)) addr = zero_row;
               uint32_t f0, f1, f2, f3;
               ldmatrix_x4_trans(addr, f0, f1, f2, f3);
+              if (TREE) {
+                // a node's values meet the zero weights of the rows that do not see
+                // it: infinities are taken out, and given to the rows that do below
+                const int j = i0 + mr0 + 16 * tl + 2 * cq - tree0;
+                if (j >= 0) nonfinite |= (uint64_t)(drop_nonfinite(f0) | drop_nonfinite(f1)) << (j & 63);
+                if (j == -1) nonfinite |= (drop_high(f0) | drop_high(f1));
+                if (j + 8 >= 0)
+                  nonfinite |= (uint64_t)(drop_nonfinite(f2) | drop_nonfinite(f3)) << ((j + 8) & 63);
+                if (j + 8 == -1) nonfinite |= (drop_high(f2) | drop_high(f3));
+              }
               mma16816(d, f0, f1, f2, f3, bq0[tl], bq1[tl]);
             }
             // fp16 values: true units, the accumulators hold O / kScale
 #pragma unroll
             for (int k = 0; k < 4; ++k) d[k] *= 1.f / Scales::kScale;
             sm.merge(md, d, a0, a1);
+          }
+          if (TREE) {
+            const uint64_t all =
+                (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(nonfinite >> 32)) << 32 |
+                __reduce_or_sync(0xffffffffu, (uint32_t)nonfinite);
+            if (anc0 & all) sm.l[0] = sm.bv[0] = NAN;
+            if (anc1 & all) sm.l[1] = sm.bv[1] = NAN;
           }
         }
       }
@@ -1980,9 +2080,9 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const Params prm) {
 
 // --------------------------------------------------------------- host side
 struct DevInfo {
-  int ready[48];
-  int grid[48];
-  int clusters[48][kMaxCluster + 1];  // clustered: clusters of 2, 4, 8 CTAs resident at once
+  int ready[112];
+  int grid[112];
+  int clusters[112][kMaxCluster + 1];  // clustered: clusters of 2, 4, 8 CTAs resident at once
 };
 DevInfo g_dev[64];
 
@@ -2012,7 +2112,7 @@ qs_status grid_for_device(int dev, int &P, const int **clusters) {
                                                       NW * 32, smem) != cudaSuccess)
       return QS_ERR_CUDA;
     if (occ < 1) return QS_ERR_CUDA;
-    if (KIND == kClustered)
+    if ((KIND & 3) == kClustered)
       for (int n = 2; n <= kMaxCluster; n *= 2) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(n * sms);
@@ -2066,7 +2166,7 @@ size_t ws_bytes(int P, int B, int H, int R) {
 
 template <int MODE, bool PK, int UB, int NW, int KIND>
 qs_status launch(const Params &prm, cudaStream_t s) {
-  if (KIND == kClustered)
+  if ((KIND & 3) == kClustered)
     return launch_pdl_cluster(split_kernel<MODE, PK, UB, NW, KIND>, dim3(prm.P), dim3(NW * 32), prm.C,
                               smem_bytes(MODE, KIND), s, prm);
   return launch_pdl(split_kernel<MODE, PK, UB, NW, KIND>, dim3(prm.P), dim3(NW * 32),
@@ -2088,6 +2188,23 @@ qs_status launch_kind(qs_mode mode, bool packed, const Params &prm, cudaStream_t
                                : launch_ub<4, KIND>(mode, packed, prm, st);
 }
 
+inline qs_status check_queries(qs_mode mode, const uint16_t *q, float softmax_scale, const uint16_t *out,
+                               const float *lse) {
+  if (!q || !out || (mode != QS_DRAFT_UPPER4 && mode != QS_VERIFY_INT8)) return QS_ERR_ARG;
+  if (!(softmax_scale > 0.f) || !isfinite(softmax_scale)) return QS_ERR_ARG;
+  return aligned16(q) && aligned16(out) && (!lse || aligned16(lse)) ? QS_OK : QS_ERR_ALIGN;
+}
+inline void set_queries(Params &prm, const uint16_t *q, int32_t n_q, int32_t group, float softmax_scale,
+                        uint16_t *out, float *lse) {
+  prm.q = q;
+  prm.out = out;
+  prm.lse = lse;
+  prm.n_q = n_q;
+  prm.R = group * n_q;
+  prm.ncg = (prm.R + 7) / 8;
+  prm.sl2 = softmax_scale * 1.4426950408889634f;
+}
+
 // What the entry points share: the call's tensors, checked, into the kernel's
 // parameters.  prm holds the cache, the append, the wait limit and, for the
 // listed variants, pages and selection already; P: the grid of the variant
@@ -2096,25 +2213,57 @@ template <int KIND>
 qs_status fill_params(Params &prm, qs_mode mode, const uint16_t *q, int32_t n_q, int32_t group,
                       float softmax_scale, uint16_t *out, float *lse, void *workspace,
                       size_t workspace_bytes) {
-  if (!q || !out || n_q < 1 || n_q > kMaxQ || group < 1 || group > kMaxR || group * n_q > kMaxR)
-    return QS_ERR_ARG;
-  if (mode != QS_DRAFT_UPPER4 && mode != QS_VERIFY_INT8) return QS_ERR_ARG;
-  if (!(softmax_scale > 0.f) || !isfinite(softmax_scale)) return QS_ERR_ARG;
-  if (!aligned16(q) || !aligned16(out) || (lse && !aligned16(lse))) return QS_ERR_ALIGN;
-  prm.q = q;
-  prm.out = out;
-  prm.lse = lse;
-  prm.n_q = n_q;
-  prm.R = group * n_q;
-  prm.ncg = (prm.R + 7) / 8;
-  prm.sl2 = softmax_scale * 1.4426950408889634f;
+  constexpr int kMostQ = (KIND & kTree) ? QS_MAX_TREE : kMaxQ;
+  if (n_q < 1 || n_q > kMostQ || group < 1 || group > kMaxR || group * n_q > kMaxR) return QS_ERR_ARG;
+  qs_status s = check_queries(mode, q, softmax_scale, out, lse);
+  if (s != QS_OK) return s;
+  set_queries(prm, q, n_q, group, softmax_scale, out, lse);
   prm.ws_floats = workspace_bytes / sizeof(float);
-  const qs_status s = grid_size<KIND>(mode, packed_rows(mode, prm.R), prm.c.upper_bits, prm.ncg, prm.P);
+  s = grid_size<KIND>(mode, packed_rows(mode, prm.R), prm.c.upper_bits, prm.ncg, prm.P);
   if (s != QS_OK) return s;
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < ws_bytes(prm.P, prm.c.B, prm.c.H, prm.R))
     return QS_ERR_WORKSPACE;
   prm.ws = static_cast<float *>(workspace);
+  return QS_OK;
+}
+
+// Clustered kernel: prm.C CTAs to a cluster, prm.K clusters to a segment; C = 1:
+// the split kernel.  The clustered kernel starts and ends about 7 us sooner
+// (verify: 11 us), but gives every segment as many CTAs as every other and
+// leaves some of the SMs idle.  So it is for segments of equal length, one
+// sequence or selections, where the longer share of a CTA costs less than that:
+// measured, 0.36 us a unit for a draft and 0.6 us for a verify pass, for every
+// eight query rows; more clusters cost a segment another 2 us at its end.  All
+// clusters have to be resident at once (this GPU: 76 of 2, 36 of 4, 15 of 8 CTAs;
+// sixteen of 8, in two waves, took 29.7 us where thirty-two of 4 take 18.6).
+// TREE: 0, or kTree for the variants of trees.
+template <int TREE>
+qs_status choose_clusters(Params &prm, qs_mode mode) {
+  const long long segs = (long long)prm.c.B * prm.c.H;
+  const int sms = prm.P;
+  prm.C = prm.K = 1;
+  if (prm.c.B > 1 && !prm.sel) return QS_OK;
+  int grid = 0;
+  const int *resident = nullptr;
+  const qs_status s = grid_size<kClustered | TREE>(mode, packed_rows(mode, prm.R), prm.c.upper_bits,
+                                                   prm.ncg, grid, &resident);
+  if (s != QS_OK) return s;
+  const long long groups = prm.sel && prm.k_sel < prm.c.cap_groups ? prm.k_sel : prm.c.cap_groups;
+  const double units = groups + (mode == QS_DRAFT_UPPER4 ? 8 : 4);  // (and a full buffer)
+  const double unit_us = (mode == QS_DRAFT_UPPER4 ? 0.36 : 0.6) * prm.ncg;
+  double best = units * segs / sms * unit_us + (mode == QS_DRAFT_UPPER4 ? 7.0 : 11.0);
+  for (int n = kMaxCluster; n >= 2; n /= 2) {
+    const int k_max = (int)(resident[n] / segs);
+    for (int k = 1; k <= k_max && k <= 16; ++k) {
+      const double us = units / (n * k) * unit_us + (k > 1 ? 2.0 : 0.0);
+      if (us < best) {
+        best = us;
+        prm.C = n;
+        prm.K = k;
+      }
+    }
+  }
   return QS_OK;
 }
 

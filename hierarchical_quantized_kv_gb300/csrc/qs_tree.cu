@@ -1,0 +1,312 @@
+// qs_tree.cu -- what a round over a tree of drafted tokens does to the buffer:
+// the append with position rotation, and the acceptance of a path.  (The attention
+// of the nodes: qs_attn_tree.cu.)
+//
+// Source: "QuantSpec: Self-Speculative Decoding with Hierarchical Quantized KV
+// Cache" (Pith review), "What carries the argument": new tokens enter the double
+// full-precision buffer, rejected speculative ones are dropped before
+// quantization -- here the ones off the accepted path.
+#include "qs_common.cuh"
+
+namespace qs {
+namespace {
+
+constexpr int kVec = kD / 8;  // uint4 of eight fp16 per row
+
+// ------------------------------------------------------------------ rotation
+
+constexpr int kRotThreads = 256;
+constexpr int kRotTokens = 4;     // tokens per CTA at most
+constexpr int kMaxHalf = kD / 2;  // pairs per row at most
+
+struct RotArgs {
+  qs_cache c;
+  qs_rows k, v, q;
+  uint16_t *q_out;
+  const int32_t *offset;
+  const float *inv_freq;
+  int hq, n_new, rot, inter;
+  int tokens, splits;  // tokens per CTA; CTAs that share a token tile's rows
+};
+
+// p * inv_freq in turns without loss: a turn is 2^64, so the product by the
+// (signed) position wraps by itself.  inv_freq / 2 pi carries the 53 bits of a
+// double: 2^-23 turns at the last position of 32 bits, 2^-38 at 65k.
+__device__ __forceinline__ unsigned long long turns(float inv_freq) {
+  const double t = (double)inv_freq * 0.15915494309189533577;
+  return (unsigned long long)((t - floor(t)) * 18446744073709551616.0);
+}
+
+// Eight pairs (x_i, y_i): x cos - y sin, y cos + x sin.
+__device__ __forceinline__ void turn(uint4 &a, uint4 &b, const float2 *cs, bool inter) {
+  uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (inter) {  // a pair a word
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 v = __half22float2(u32_as_h2(x[i])), t = cs[i];
+      x[i] = pack_half2(v.x * t.x - v.y * t.y, v.y * t.x + v.x * t.y);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 u = __half22float2(u32_as_h2(x[i])), v = __half22float2(u32_as_h2(x[4 + i]));
+      const float2 t0 = cs[2 * i], t1 = cs[2 * i + 1];
+      x[i] = pack_half2(u.x * t0.x - v.x * t0.y, u.y * t1.x - v.y * t1.y);
+      x[4 + i] = pack_half2(v.x * t0.x + u.x * t0.y, v.y * t1.x + u.y * t1.y);
+    }
+  }
+  a = make_uint4(x[0], x[1], x[2], x[3]);
+  b = make_uint4(x[4], x[5], x[6], x[7]);
+}
+
+// CTA (tile, split, sequence): up to kRotTokens tokens of the sequence, and every
+// splits-th part of their H + H + hq rows (keys, values, queries).  An item is two
+// 16-byte vectors of a row, eight items a row: a pair of vectors that turn
+// together, or two that stay.  The CTA's angles go through shared memory, so
+// their sines are formed once for all heads.
+__global__ void __launch_bounds__(kRotThreads) append_rotary_kernel(const RotArgs a) {
+  __shared__ float2 s_cs[kRotTokens * kMaxHalf];
+  const qs_cache &c = a.c;
+  const int b = blockIdx.z, j0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.n_new - j0);
+  pdl_trigger();
+  pdl_wait();
+  int32_t *st = c.state + (size_t)b * QS_STATE_WORDS;
+  const int ng = st[QS_ST_N_GROUPS], fill = st[QS_ST_FILL], pending = st[QS_ST_PENDING];
+  const int base = st[QS_ST_HALF_BASE] & 1;
+  const bool room = fill >= 0 && fill + a.n_new <= kRing;
+  const int half = a.rot / 2;
+  for (int i = threadIdx.x; i < nt * half; i += kRotThreads) {
+    const int j = i / half, f = i % half;
+    const int pos = ng * kG + fill +
+                    (a.offset ? a.offset[(size_t)b * a.n_new + j0 + j] - pending : j0 + j);
+    // the signed fraction of a turn, in half turns
+    const long long p = (long long)((unsigned long long)(long long)pos * turns(a.inv_freq[f]));
+    float2 cs;
+    sincospif((float)(int)(p >> 32) * 4.656612873077393e-10f, &cs.y, &cs.x);
+    s_cs[j * kMaxHalf + f] = cs;
+  }
+  __syncthreads();
+  const int rows = 2 * c.H + a.hq, per = (rows + a.splits - 1) / a.splits;
+  const int r0 = blockIdx.y * per, r1 = min(rows, r0 + per);
+  const int n_items = (r1 - r0) * nt * 8;
+  constexpr int U = 4;  // items in flight per thread
+  for (int e0 = threadIdx.x; e0 < n_items; e0 += U * kRotThreads) {
+    uint4 x[U], y[U];
+    uint4 *dst[U];
+    int vx[U], vy[U], tj[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int e = e0 + u * kRotThreads;
+      dst[u] = nullptr;
+      if (e >= n_items) continue;
+      const int i = e & 7, j = (e >> 3) % nt, row = r0 + (e >> 3) / nt;
+      const bool is_q = row >= 2 * c.H, is_v = !is_q && row >= c.H;
+      const int h = is_q ? row - 2 * c.H : is_v ? row - c.H : row;
+      const qs_rows &s = is_q ? a.q : is_v ? a.v : a.k;
+      // item i of a row: the vectors of pairs 8 i .. 8 i + 7 while those turn,
+      // then the rest two by two
+      const bool turns = !is_v && 16 * i < a.rot;
+      vx[u] = turns && !a.inter ? i : 2 * i;
+      vy[u] = turns && !a.inter ? i + a.rot / 16 : 2 * i + 1;
+      tj[u] = turns ? j * kMaxHalf + 8 * i : -1;
+      const uint4 *src = reinterpret_cast<const uint4 *>(s.data + b * s.stride_b + h * s.stride_h +
+                                                         (j0 + j) * s.stride_t);
+      x[u] = src[vx[u]];
+      y[u] = src[vy[u]];
+      if (is_q) {
+        dst[u] = reinterpret_cast<uint4 *>(a.q_out) + (((size_t)b * a.hq + h) * a.n_new + j0 + j) * kVec;
+      } else if (room) {
+        const int slot = (base * kG + fill + j0 + j) & (kRing - 1);
+        dst[u] = reinterpret_cast<uint4 *>(is_v ? c.buf_v : c.buf_k) +
+                 (((size_t)b * c.H + h) * kRing + slot) * kVec;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!dst[u]) continue;
+      if (tj[u] >= 0) turn(x[u], y[u], s_cs + tj[u], a.inter);
+      dst[u][vx[u]] = x[u];
+      dst[u][vy[u]] = y[u];
+    }
+  }
+  if (!room) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(&st[QS_ST_ERR], QS_DEV_OVERFLOW);
+    return;
+  }
+  __syncthreads();
+  // every CTA of the sequence has read the old counters once the last one arrives
+  if (threadIdx.x == 0 &&
+      atom_add_acq_rel_gpu(&st[QS_ST_TICKET], 1) == (int)(gridDim.x * gridDim.y) - 1) {
+    st[QS_ST_FILL] = fill + a.n_new;
+    st[QS_ST_PENDING] = pending + a.n_new;
+    st[QS_ST_TICKET] = 0;
+  }
+}
+
+// ---------------------------------------------------------------- acceptance
+
+constexpr int kAccThreads = 256;
+
+// One CTA per (head, sequence).  Its first warp walks the tree, two nodes a lane:
+// a step is a shuffle (the target's token of the current node) and two votes (the
+// nodes that hang from it with that token).  Then the CTA reads the rows of the
+// path that have to move, all before the first is written: they only move
+// forward, so one may lie where an earlier one goes.
+__global__ void __launch_bounds__(kAccThreads)
+    tree_accept_kernel(qs_cache c, const int32_t *parent, const int32_t *draft, const int32_t *target,
+                       int n, int32_t *n_keep, int32_t *path, int32_t *emitted) {
+  __shared__ int s_path[QS_MAX_TREE], s_keep, s_fill, s_base;
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  pdl_trigger();
+  pdl_wait();
+  int32_t *st = c.state + (size_t)b * QS_STATE_WORDS;
+  if (tid < 32) {
+    const int fill = st[QS_ST_FILL], pending = st[QS_ST_PENDING], base = st[QS_ST_HALF_BASE] & 1;
+    int up[2], tok[2], tgt[2];
+    bool bad = fill > kRing || pending > fill || n > pending;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int j = tid + 32 * k;
+      const size_t at = (size_t)b * n + j;
+      up[k] = tok[k] = tgt[k] = -1;
+      if (j < n) {
+        up[k] = parent[at];
+        tok[k] = draft[at];
+        tgt[k] = target[at];
+        bad |= up[k] < -1 || up[k] >= j;
+      }
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    int keep = 0;
+    int mine[2] = {-1, -1}, out[2] = {-1, -1};  // entries tid and tid + 32 of path and emitted
+    if (!bad) {
+      int at = 0;
+      for (; keep < n;) {
+        const int a0 = __shfl_sync(0xffffffffu, tgt[0], at & 31), a1 = __shfl_sync(0xffffffffu, tgt[1], at & 31);
+        const int t = at < 32 ? a0 : a1;
+        if (tid == (keep & 31)) {
+          mine[keep >> 5] = at;
+          out[keep >> 5] = t;
+        }
+        ++keep;
+        const unsigned m0 = __ballot_sync(0xffffffffu, up[0] == at && tok[0] == t && tok[0] >= 0);
+        const unsigned m1 = __ballot_sync(0xffffffffu, up[1] == at && tok[1] == t && tok[1] >= 0);
+        if (!(m0 | m1)) break;
+        at = m0 ? __ffs(m0) - 1 : 31 + __ffs(m1);
+      }
+    }
+    s_path[tid] = mine[0];
+    s_path[tid + 32] = mine[1];
+    if (tid == 0) {
+      s_keep = keep;
+      s_fill = fill;
+      s_base = base;
+    }
+    if (h == 0) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (tid + 32 * k < n) {
+          path[(size_t)b * n + tid + 32 * k] = mine[k];
+          emitted[(size_t)b * n + tid + 32 * k] = out[k];
+        }
+      if (tid == 0) {
+        n_keep[b] = keep;
+        if (bad) atomicOr(&st[QS_ST_ERR], QS_DEV_TREE);
+      }
+    }
+  }
+  __syncthreads();
+  const int keep = s_keep;
+  if (keep == 0) return;
+  const int first = s_base * kG + s_fill - n;
+  const size_t row0 = ((size_t)b * c.H + h) * kRing;
+  uint4 *bk = reinterpret_cast<uint4 *>(c.buf_k) + row0 * kVec, *bv = reinterpret_cast<uint4 *>(c.buf_v) + row0 * kVec;
+  constexpr int U = QS_MAX_TREE * kVec / kAccThreads;
+  uint4 xk[U], xv[U];
+  const int col = tid % kVec;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int i = tid / kVec + u * (kAccThreads / kVec);
+    if (i < keep && s_path[i] != i) {
+      const int src = (first + s_path[i]) & (kRing - 1);
+      xk[u] = bk[src * kVec + col];
+      xv[u] = bv[src * kVec + col];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int i = tid / kVec + u * (kAccThreads / kVec);
+    if (i < keep && s_path[i] != i) {
+      const int dst = (first + i) & (kRing - 1);
+      bk[dst * kVec + col] = xk[u];
+      bv[dst * kVec + col] = xv[u];
+    }
+  }
+  // every head has read the old counters once the ticket reaches H - 1
+  if (tid == 0 && atom_add_acq_rel_gpu(&st[QS_ST_TICKET], 1) == c.H - 1) {
+    st[QS_ST_FILL] = s_fill - n + keep;
+    st[QS_ST_PENDING] = 0;
+    st[QS_ST_TICKET] = 0;
+  }
+}
+
+qs_status check_rows(const qs_rows *r) {
+  if (!r->data) return QS_ERR_ARG;
+  if (r->stride_b % 8 || r->stride_h % 8 || r->stride_t % 8) return QS_ERR_SHAPE;
+  return aligned16(r->data) ? QS_OK : QS_ERR_ALIGN;
+}
+
+}  // namespace
+}  // namespace qs
+
+using namespace qs;
+
+extern "C" {
+
+qs_status qs_buffer_append_rotary(const qs_cache *c, const qs_rows *k, const qs_rows *v,
+                                  const qs_rows *q, uint16_t *q_out, int32_t group, int32_t n_new,
+                                  const int32_t *offset, const float *inv_freq, int32_t rot,
+                                  int32_t interleaved, qs_stream_t stream) {
+  qs_status s = check_cache_any(c);
+  if (s != QS_OK) return s;
+  if (!k || !v || !inv_freq || (q != nullptr) != (q_out != nullptr)) return QS_ERR_ARG;
+  if (n_new < 1 || n_new > kRing || (q && (group < 1 || group > 1024))) return QS_ERR_ARG;
+  if (rot < 16 || rot > kD || rot % 16) return QS_ERR_ARG;
+  const qs_rows none = {nullptr, 0, 0, 0};
+  const qs_rows *rows[] = {k, v, q};
+  for (const qs_rows *r : rows)
+    if (r && (s = check_rows(r)) != QS_OK) return s;
+  if (!aligned16(q_out) || reinterpret_cast<uintptr_t>(inv_freq) % 4 ||
+      reinterpret_cast<uintptr_t>(offset) % 4)
+    return QS_ERR_ALIGN;
+  RotArgs a = {*c, *k, *v, q ? *q : none, q_out, offset, inv_freq, q ? c->H * group : 0, n_new, rot,
+               interleaved != 0, 1, 1};
+  const long long n_rows = 2ll * c->H + a.hq;
+  a.tokens = n_new < kRotTokens ? n_new : kRotTokens;
+  int sms = 0;
+  if ((s = sm_count(&sms)) != QS_OK) return s;
+  const long long tiles = (long long)((n_new + a.tokens - 1) / a.tokens) * c->B;
+  // few token tiles: their rows split over CTAs, 32 items of 8 lanes each at least
+  long long split = (2ll * sms + tiles - 1) / tiles, most = (n_rows * a.tokens + 31) / 32;
+  if (split > most) split = most;
+  a.splits = (int)(split < 1 ? 1 : split > 65535 ? 65535 : split);
+  return launch_pdl(append_rotary_kernel, dim3((n_new + a.tokens - 1) / a.tokens, a.splits, c->B),
+                    dim3(kRotThreads), 0, (cudaStream_t)stream, a);
+}
+
+qs_status qs_tree_accept(const qs_cache *c, const int32_t *parent, const int32_t *draft,
+                         const int32_t *target, int32_t n_tree, int32_t *n_keep, int32_t *path,
+                         int32_t *emitted, qs_stream_t stream) {
+  const qs_status s = check_cache_any(c);
+  if (s != QS_OK) return s;
+  if (!parent || !draft || !target || !n_keep || !path || !emitted) return QS_ERR_ARG;
+  if (n_tree < 1 || n_tree > QS_MAX_TREE) return QS_ERR_ARG;
+  const void *ptrs[] = {parent, draft, target, n_keep, path, emitted};
+  for (const void *p : ptrs)
+    if (reinterpret_cast<uintptr_t>(p) % 4) return QS_ERR_ALIGN;
+  return launch_pdl(tree_accept_kernel, dim3(c->H, c->B), dim3(kAccThreads), 0, (cudaStream_t)stream,
+                    *c, parent, draft, target, (int)n_tree, n_keep, path, emitted);
+}
+
+}  // extern "C"

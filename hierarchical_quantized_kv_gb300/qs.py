@@ -19,10 +19,12 @@ QS_DRAFT_UPPER4, QS_VERIFY_INT8 = 0, 1
 QS_STATIC_WS_BYTES = 8 << 20
 DEV_OVERFLOW, DEV_OVER_ROLLBACK, DEV_FLUSH_UNCOMMITTED, DEV_CAPACITY, DEV_NQ_GT_FILL, DEV_TIMEOUT = (
     1, 2, 4, 8, 16, 32)
-DEV_PREFILL, DEV_PAGE, DEV_SELECT = 64, 128, 256
+DEV_PREFILL, DEV_PAGE, DEV_SELECT, DEV_TREE = 64, 128, 256, 512
 QS_PAGED = 0x100
 ST_N_GROUPS, ST_FILL, ST_PENDING, ST_HALF_BASE, ST_ERR, ST_TICKET = range(6)
 STATE_WORDS = 8
+QS_FP16, QS_BF16, QS_FP32 = range(3)
+QS_MAX_TREE, QS_MAX_VOCAB = 64, 393216
 META_K_SCALE, META_K_ZERO, META_V_SCALE, META_V_ZERO = range(4)
 
 _P = ctypes.c_void_p
@@ -37,6 +39,11 @@ class QsCacheStruct(ctypes.Structure):
 
 class QsPagesStruct(ctypes.Structure):
     _fields_ = [("table", _P), ("n_pages", _I32)]
+
+
+class QsRowsStruct(ctypes.Structure):
+    _fields_ = [("data", _P), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_t", ctypes.c_int64)]
 
 
 class QsCacheBytes(ctypes.Structure):
@@ -96,6 +103,15 @@ _SIGS = {
                                  ctypes.c_float, _P, _P, _P],
     "qs_attn_decode_append": [ctypes.POINTER(QsCacheStruct), ctypes.c_int, _P, _P, _I32, _P, _I32,
                               _I32, ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P],
+    "qs_buffer_append_rotary": [ctypes.POINTER(QsCacheStruct), ctypes.POINTER(QsRowsStruct),
+                                ctypes.POINTER(QsRowsStruct), ctypes.POINTER(QsRowsStruct), _P, _I32,
+                                _I32, _P, _P, _I32, _I32, _P],
+    "qs_attn_tree_workspace_size": [ctypes.POINTER(QsCacheStruct), _I32, _I32,
+                                    ctypes.POINTER(ctypes.c_size_t)],
+    "qs_attn_decode_tree": [ctypes.POINTER(QsCacheStruct), ctypes.POINTER(QsPagesStruct), ctypes.c_int,
+                            _P, _I32, _P, _I32, _I32, ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P],
+    "qs_tree_accept": [ctypes.POINTER(QsCacheStruct), _P, _P, _P, _I32, _P, _P, _P, _P],
+    "qs_sample": [_P, ctypes.c_int, _I32, _I32, ctypes.c_int64, _P, _P, _P, _P, _P, _P, _P, _P],
 }
 
 
@@ -504,6 +520,136 @@ def qs_attn_decode_sparse(cache, mode, sel, q, softmax_scale, out, lse=None, wor
         cache._ref, cache._pages_ref, int(mode), _ptr(sel), k, _ptr(k_new), _ptr(v_new),
         _n_new(cache, k_new, v_new), _ptr(q), n_q, int(group), float(softmax_scale), _ptr(out),
         _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+# ------------------------------------- a round over a tree of drafted tokens
+
+def _current_device():
+    import torch
+    return torch.cuda.current_device()
+
+
+def _check_device(dev):
+    """The library launches on the current device."""
+    if dev >= 0 and dev != _current_device():
+        raise QsArgumentError("the tensors lie on cuda:%d, which is not the current device" % dev)
+
+
+def _rows_struct(cache, t, name, heads, n):
+    """fp16 [B, heads, n, D] with any strides, the last one 1."""
+    shape = t.shape
+    if not (len(shape) == 4 and shape[0] == cache.B and shape[1] == heads and shape[2] == n and
+            shape[3] == cache.D and t.dtype is cache._f16 and t.get_device() == cache._dev):
+        raise QsArgumentError("%s: float16 [%d, %d, %d, %d] on the cache's device"
+                              % (name, cache.B, heads, n, cache.D))
+    s = t.stride()
+    if s[3] != 1:
+        raise QsArgumentError("%s: the elements of a row lie side by side" % name)
+    # (the stride of a dimension of one is of no account)
+    return QsRowsStruct(t.data_ptr(), *(s[i] if shape[i] > 1 else 0 for i in range(3)))
+
+
+def qs_buffer_append_rotary(cache, k, v, inv_freq, q=None, q_out=None, offset=None, interleaved=False,
+                            stream=None):
+    """qs_buffer_append with the position rotation.  k, v: fp16 [B, H, n, D], q:
+    fp16 [B, H * group, n, D] or None, all with any strides but the last (slices
+    of a projection's output, say); q_out: contiguous, the shape of q; inv_freq:
+    float32 [rot / 2]; offset: int32 [B, n] or None."""
+    _check_device(cache._dev)
+    n = k.shape[2] if k.dim() == 4 else 0
+    ks, vs = _rows_struct(cache, k, "k", cache.H, n), _rows_struct(cache, v, "v", cache.H, n)
+    if (q is None) != (q_out is None):
+        raise QsArgumentError("q and q_out go together")
+    group, q_ref = 1, None
+    if q is not None:
+        group = q.shape[1] // cache.H if q.dim() == 4 else 0
+        qrows = _rows_struct(cache, q, "q", cache.H * group, n)
+        q_ref = ctypes.byref(qrows)
+        if q_out.shape != q.shape:
+            raise QsArgumentError("q_out: the shape of q")
+        _check_f16(cache, q_out, "q_out")
+    if not (inv_freq.dim() == 1 and inv_freq.dtype is cache._f32 and inv_freq.is_contiguous() and
+            inv_freq.get_device() == cache._dev):
+        raise QsArgumentError("inv_freq: contiguous float32 [rot / 2] on the cache's device")
+    if offset is not None:
+        _check_i32(cache, offset, "offset", (cache.B, n))
+    _check("qs_buffer_append_rotary", lib().qs_buffer_append_rotary(
+        cache._ref, ctypes.byref(ks), ctypes.byref(vs), q_ref, _ptr(q_out), group, n, _ptr(offset),
+        _ptr(inv_freq), 2 * inv_freq.shape[0], int(bool(interleaved)), _stream(stream)))
+
+
+def _check_i32(cache, t, name, shape):
+    if not (tuple(t.shape) == tuple(shape) and t.dtype is cache._i32 and t.is_contiguous() and
+            t.get_device() == cache._dev):
+        raise QsArgumentError("%s: contiguous int32 %s on the cache's device" % (name, list(shape)))
+
+
+def qs_attn_tree_workspace_size(cache, n_q, group=1):
+    n = ctypes.c_size_t()
+    _check("qs_attn_tree_workspace_size", lib().qs_attn_tree_workspace_size(
+        cache._ref, int(n_q), int(group), ctypes.byref(n)))
+    return n.value
+
+
+def qs_attn_decode_tree(cache, mode, parent, q, softmax_scale, out, lse=None, workspace=None, group=1,
+                        stream=None):
+    """Decode attention (cache: a Cache or a PagedCache) of the last n_q nodes of
+    a tree, parent int32 [B, n_tree]; q, out: fp16 [B, H * group, n_q, D]."""
+    _check_device(cache._dev)
+    n_q = _check_queries(cache, q, group, out, lse)
+    n_tree = parent.shape[1] if parent.dim() == 2 else 0
+    _check_i32(cache, parent, "parent", (cache.B, n_tree))
+    ws_bytes = _ws_bytes(cache, workspace)
+    _check("qs_attn_decode_tree", lib().qs_attn_decode_tree(
+        cache._ref, cache._pages_ref, int(mode), _ptr(parent), n_tree, _ptr(q), n_q, int(group),
+        float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def qs_tree_accept(cache, parent, draft, target, n_keep, path, emitted, stream=None):
+    """parent, draft, target, and the outputs path, emitted: int32 [B, n_tree];
+    n_keep (out): int32 [B]."""
+    _check_device(cache._dev)
+    n_tree = parent.shape[1] if parent.dim() == 2 else 0
+    for name, t in (("parent", parent), ("draft", draft), ("target", target), ("path", path),
+                    ("emitted", emitted)):
+        _check_i32(cache, t, name, (cache.B, n_tree))
+    _check_i32(cache, n_keep, "n_keep", (cache.B,))
+    _check("qs_tree_accept", lib().qs_tree_accept(
+        cache._ref, _ptr(parent), _ptr(draft), _ptr(target), n_tree, _ptr(n_keep), _ptr(path),
+        _ptr(emitted), _stream(stream)))
+
+
+def qs_sample(logits, u, token, probs=None, temperature=None, top_k=None, top_p=None, min_p=None,
+              stream=None):
+    """A token (int32 [rows]) for each row of logits, fp16, bf16 or fp32
+    [rows, V] with any row stride, by u, float32 [rows]; probs: float32 [rows, V]
+    or None; temperature, top_p, min_p: float32 [rows], top_k: int32 [rows], or
+    None."""
+    import torch
+    types = {torch.float16: QS_FP16, torch.bfloat16: QS_BF16, torch.float32: QS_FP32}
+    if logits.dim() != 2 or logits.dtype not in types:
+        raise QsArgumentError("logits: fp16, bf16 or fp32 [rows, V]")
+    rows, V = logits.shape
+    dev = logits.get_device()
+    if dev < 0:
+        raise QsArgumentError("logits: on a CUDA device")
+    _check_device(dev)
+    if logits.stride(1) != 1 and V > 1:
+        raise QsArgumentError("logits: the elements of a row lie side by side")
+    for name, t, dtype, shape in (("u", u, torch.float32, (rows,)), ("token", token, torch.int32, (rows,)),
+                                  ("probs", probs, torch.float32, (rows, V)),
+                                  ("temperature", temperature, torch.float32, (rows,)),
+                                  ("top_k", top_k, torch.int32, (rows,)),
+                                  ("top_p", top_p, torch.float32, (rows,)),
+                                  ("min_p", min_p, torch.float32, (rows,))):
+        if t is None and name not in ("u", "token"):
+            continue
+        if not (t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev):
+            raise QsArgumentError("%s: contiguous %s %s on the logits' device" % (name, dtype, list(shape)))
+    _check("qs_sample", lib().qs_sample(
+        _ptr(logits), types[logits.dtype], rows, V, logits.stride(0) if rows > 1 else V,
+        _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(token), _ptr(probs),
+        _stream(stream)))
 
 
 def qs_get_errors(cache, stream=None):

@@ -93,8 +93,10 @@ enum {
                                     length outside [0, T] */
   QS_DEV_PAGE = 128,             /* a page table entry in use outside
                                     [0, n_pages) */
-  QS_DEV_SELECT = 256            /* a selected group that the sequence does not
+  QS_DEV_SELECT = 256,           /* a selected group that the sequence does not
                                     have */
+  QS_DEV_TREE = 512              /* a node's parent is not an earlier node, or
+                                    fewer pending tokens than nodes */
 };
 
 /* Per-sequence counters: int32 state[B][QS_STATE_WORDS]. */
@@ -482,6 +484,151 @@ qs_status qs_attn_decode_sparse(const qs_cache *c, const qs_pages *pg, qs_mode m
                                 const uint16_t *v_new, int32_t n_new, const uint16_t *q, int32_t n_q,
                                 int32_t group, float softmax_scale, uint16_t *out, float *lse,
                                 void *workspace, size_t workspace_bytes, qs_stream_t stream);
+
+/* ---- a speculative round over a tree of drafted tokens -------------------
+ * A tree has n_tree nodes (1..QS_MAX_TREE); they are the last n_tree tokens of
+ * the buffer, node j at buffer position fill - n_tree + j, appended in that
+ * order (in one call or level by level).  parent, int32 [B][n_tree] on the
+ * device, names each node's parent: an earlier node (0 <= parent[j] < j), or -1
+ * for a node that follows the tokens in front of the tree.  A node sees all
+ * those tokens, its ancestors and itself.  Sequences whose tree is smaller pad
+ * it with nodes whose parent is -1: nothing else sees those, whatever their keys
+ * and values hold.  A parent that is neither flags QS_DEV_TREE.  A round:
+ * qs_buffer_append_rotary and qs_attn_decode_tree for each level that is drafted,
+ * the same two for the verification (after a rollback of the drafted tokens),
+ * qs_sample for the target's token at every node, qs_tree_accept.
+ * Source: Pith review page, "What carries the argument" (drafts enter the
+ * double full-precision buffer, rejected ones are dropped from it): there a
+ * chain; trees of drafts, verified in one pass under the mask of their
+ * ancestors, are a published method (SpecInfer, 2023). */
+#define QS_MAX_TREE 64
+
+/* Rows of D fp16 elements for (sequence, head, token), the row's elements side
+ * by side: row (b, h, t) starts at data + b * stride_b + h * stride_h +
+ * t * stride_t elements.  So the heads of a projection's output, [B][n][heads][D],
+ * need no copy.  data is 16-byte aligned, the strides are multiples of 8 (0 and
+ * negative ones too). */
+typedef struct {
+  const uint16_t *data;
+  int64_t stride_b, stride_h, stride_t;
+} qs_rows;
+
+/* Append n_new tokens per sequence to the buffer, as qs_buffer_append, with the
+ * position rotation applied to the keys on the way, and to the queries.
+ *   k, v    rows of H heads and n_new tokens (v is not rotated);
+ *   q       rows of H * group heads and n_new tokens, or NULL (with q_out NULL);
+ *   q_out   fp16 [B][H*group][n_new][D]: the rotated queries, as the attention
+ *           calls take them (may be q itself where that has this layout);
+ *   offset  int32 [B][n_new], 4-byte aligned, or NULL: token j stands at position
+ *             n_groups * G + fill - pending + offset[j]
+ *           (the committed tokens, and the depth of a node in a tree), with NULL
+ *           at the position after the tokens there are,
+ *             n_groups * G + fill + j;
+ *   inv_freq  float [rot / 2], finite: angle i of a token at position p is
+ *           p * inv_freq[i] (whole turns are taken out exactly, so far positions
+ *           lose nothing);
+ *   rot     channels that turn, a multiple of 16 from 16 to D; the others stay;
+ *   interleaved  0: channel i turns with channel i + rot / 2; 1: channel 2 i with
+ *           2 i + 1.
+ * A pair (x, y) becomes (x cos - y sin, y cos + x sin), in fp32, rounded once.
+ * A sequence without room for the tokens gets QS_DEV_OVERFLOW: its buffer and
+ * counters stay, its queries are written all the same.  Errors: QS_ERR_ARG
+ * (null pointers, n_new outside 1..2G, group < 1 with q, q without q_out or the
+ * other way round, rot out of range), QS_ERR_SHAPE (a stride that is no multiple
+ * of 8), QS_ERR_ALIGN.  The inputs must not overlap the buffers.  Source: as
+ * qs_buffer_append; rotary positions are a published method (RoFormer, 2021). */
+qs_status qs_buffer_append_rotary(const qs_cache *c, const qs_rows *k, const qs_rows *v,
+                                  const qs_rows *q, uint16_t *q_out, int32_t group, int32_t n_new,
+                                  const int32_t *offset, const float *inv_freq, int32_t rot,
+                                  int32_t interleaved, qs_stream_t stream);
+
+/* Bytes of device workspace qs_attn_decode_tree needs for n_q queries and
+ * `group` query heads per KV head.  Errors: as qs_attn_decode_tree. */
+qs_status qs_attn_tree_workspace_size(const qs_cache *c, int32_t n_q, int32_t group, size_t *bytes);
+
+/* Decode attention of a tree's nodes: as qs_attn_decode_gqa (pg NULL: a
+ * contiguous cache; else the pages of a paged one, as qs_attn_decode_paged), but
+ * a query sees, of the tree's tokens, only its ancestors and itself.
+ *   parent  int32 [B][n_tree], 4-byte aligned: the tree (see above);
+ *   q, out  fp16 [B][H*group][n_q][D], lse float [B][H*group][n_q] or NULL:
+ *           query j is node n_tree - n_q + j (the last n_q nodes; all of them for
+ *           a verification, a level of the tree for a draft);
+ *           1 <= n_q <= n_tree <= QS_MAX_TREE, group * n_q <= 512.
+ * Sequences with n_tree > fill get QS_DEV_NQ_GT_FILL, zero output, lse = -inf.
+ * A parent that is not allowed flags QS_DEV_TREE and counts as -1.  A node whose
+ * value row holds an infinity or a NaN makes the rows that see it NaN, and no
+ * other row (in front of the tree such values reach every row, as in the other
+ * attention calls).  Up to 24 rows per KV head (group * n_q) run as
+ * qs_attn_decode_paged does; more of them go through the tensor cores 128 at a
+ * time, their keys and values rounded to fp16 once.  Errors as qs_attn_decode_gqa,
+ * QS_ERR_ARG also for a null parent and sizes out of range. */
+qs_status qs_attn_decode_tree(const qs_cache *c, const qs_pages *pg, qs_mode mode,
+                              const int32_t *parent, int32_t n_tree, const uint16_t *q, int32_t n_q,
+                              int32_t group, float softmax_scale, uint16_t *out, float *lse,
+                              void *workspace, size_t workspace_bytes, qs_stream_t stream);
+
+/* Accept a path of the tree: from node 0, which always stays (the last token
+ * emitted before the round), on to the lowest-numbered child whose draft token is
+ * the target's token of the node it hangs from, as long as there is one.  With
+ * target tokens drawn from the target's distribution (qs_sample) the emitted
+ * tokens are distributed as the target's own; with the likeliest ones (temperature
+ * 0) they are its greedy tokens.
+ *   parent    int32 [B][n_tree] (parent[b][0] = -1);
+ *   draft     int32 [B][n_tree]: token of each node (a negative one never matches);
+ *   target    int32 [B][n_tree]: the target's token after each node;
+ *   n_keep    int32 [B] (out): nodes on the path, at least 1;
+ *   path      int32 [B][n_tree] (out): those nodes in order, -1 behind;
+ *   emitted   int32 [B][n_tree] (out): the target's token after each of them (the
+ *             n_keep tokens this round adds to the text), -1 behind.
+ * The path's rows move to the front of the tree's place in the buffer, the
+ * others are dropped: fill becomes fill - n_tree + n_keep, pending 0 (older pending
+ * tokens are committed with the path).  A sequence with fewer than n_tree pending
+ * tokens or a parent that is not allowed gets QS_DEV_TREE: n_keep 0, path and
+ * emitted -1, buffer and counters as they were.  All arrays are the caller's,
+ * 4-byte aligned.  Errors: QS_ERR_ARG (null pointers, n_tree out of range),
+ * QS_ERR_ALIGN.  Source: Pith review page, referee report on Algorithm 1 (verify,
+ * keep what the target confirms, roll back the rest), here along a tree. */
+qs_status qs_tree_accept(const qs_cache *c, const int32_t *parent, const int32_t *draft,
+                         const int32_t *target, int32_t n_tree, int32_t *n_keep, int32_t *path,
+                         int32_t *emitted, qs_stream_t stream);
+
+typedef enum { QS_FP16 = 0, QS_BF16 = 1, QS_FP32 = 2 } qs_dtype;
+
+/* Largest vocabulary of qs_sample. */
+#define QS_MAX_VOCAB 393216
+
+/* A token for each row of logits, and the probabilities it is drawn from.
+ *   logits  [rows][V] of the given type, row r at logits + r * row_stride elements
+ *           (row_stride >= V, or any for one row), aligned to the type;
+ *   temperature, top_k, top_p, min_p  per row (float, int32, float, float [rows]),
+ *           each may be NULL: 1, off, off, off;
+ *   u       float [rows]: uniform numbers in [0, 1);
+ *   token   int32 [rows] (out);
+ *   probs   float [rows][V] (out) or NULL.
+ * With x the row's logits and m the largest, token i weighs w_i = exp((x_i - m) /
+ * temperature).  The tokens in order of falling logits, equal ones by rising index:
+ *   top_k   keeps the first top_k (0 or less, or V and more: all);
+ *   top_p   of those, keeps each one in front of which less than top_p of their
+ *           weight stands, so the first always (1 and more, or NaN: all);
+ *   min_p   of those, keeps the ones with w_i >= min_p (0 and less, or NaN: all;
+ *           above 1 counts as 1).
+ * probs_i is w_i over the sum of the kept weights, 0 for the others.  The token is
+ * the first one, by index, at which the running sum of the kept weights exceeds u
+ * times their sum (u below 0 or NaN counts as 0, 1 and more takes the last kept
+ * token).  Weights are formed to about 2^-37 of themselves and added as 64-bit
+ * integers, so a result does not depend on an order of summation.  A temperature
+ * of 0 (of less than 2^-60, or NaN) takes the largest logit, the lowest index among
+ * equal ones.  Logits of -inf or NaN are never kept; where one is +inf, those with
+ * +inf weigh 1 and all others 0.  A row without any token to keep gives token -1 and
+ * zero probs.  One launch.  Errors: QS_ERR_ARG (null pointers, bad type, rows or V
+ * < 1, a row_stride below V), QS_ERR_UNSUPPORTED (V > QS_MAX_VOCAB), QS_ERR_ALIGN.
+ * Source: "QuantSpec Guide", "The Self-Speculative Verification Loop" (tokens are
+ * drawn from draft and target distributions, which qs_spec_accept takes); the
+ * filters are those in common use. */
+qs_status qs_sample(const void *logits, qs_dtype dtype, int32_t rows, int32_t V, int64_t row_stride,
+                    const float *temperature, const int32_t *top_k, const float *top_p,
+                    const float *min_p, const float *u, int32_t *token, float *probs,
+                    qs_stream_t stream);
 
 /* Size of the fixed scratch array behind qs_attn_decode_static_ws. */
 #define QS_STATIC_WS_BYTES (8u << 20)
