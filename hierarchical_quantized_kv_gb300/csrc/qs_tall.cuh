@@ -1,0 +1,913 @@
+// qs_tall.cuh -- decode attention of many query rows per KV head (the nodes of a tree
+// times the query heads that share a KV head): both products on the fifth-generation
+// tensor cores, 128 rows at a time.
+//
+// Mathematics.  S = Q K^T and O = P V over tiles of 128 tokens, a group of the cache
+// or half of the buffer, with a running maximum m and sum l per row:
+//   P = 2^(S c - m),  O <- O a + P V,  l <- l a + sum P,  a = 2^(m_old - m),
+// where m only moves when a row's maximum rises by more than 2^kRaise, so that O,
+// which lives in tensor memory, is rescaled a few times in a call and not in every
+// tile.  A token's mask (what a node of the tree sees) concerns the buffer alone.
+//
+// Design (GB300).
+//  * One CTA per SM takes an equal range of (sequence, KV head, unit)s, as the split
+//    kernel does, and writes a partial (O, m, l) for each segment it touches; a second
+//    kernel joins them.
+//  * Roles: one warp starts the bulk copies of planes and scales into a ring; eight
+//    warps make fp16 operand tiles of them (128 rows of 128 fp16, the 128-byte swizzle
+//    of K-major operands) in a ring of three; one thread issues the MMAs; two groups
+//    of four warps do the softmax, a row per thread.
+//  * Two streams alternate on the tensor core, so that one multiplies while the other's
+//    softmax runs.  With more than 128 rows they are two row tiles over the same keys
+//    and values; else they take every other unit.
+//  * S (fp32) and O lie in tensor memory; P replaces S there as fp16 and is the second
+//    product's A operand, so scores never touch shared memory.
+//  * The planes' layouts fit: keys are stored by token, channels side by side, and
+//    values by channel, tokens side by side, both K-major as they are.  Within
+//    eight channels the keys' nibbles come out as 0 4 1 5 2 6 3 7; the queries are
+//    stored in that order too.
+#pragma once
+
+#include "qs_split.cuh"
+
+namespace qs {
+namespace {
+
+constexpr int kTile = 128;                 // rows, tokens and channels of a tile
+constexpr int kTileBytes = kTile * kTile * 2;
+constexpr int kOpTiles = 3;                // operand tiles (keys or values) in the ring
+constexpr int kSoftWarps = 8, kDeqWarps = 8;
+constexpr int kMmaWarp = kSoftWarps + kDeqWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kTallThreads = 32 * (kLoadWarp + 1);
+constexpr float kRaise = 8.f;              // log2 by which a maximum may be behind
+constexpr int kFlags = 8;                  // units whose flags are kept
+constexpr int kMaxTreeRows = 512;
+
+// A piece of a unit in the ring of raw copies: keys or values.
+template <int MODE>
+struct TallCfg {
+  static constexpr bool kDraft = MODE == QS_DRAFT_UPPER4;
+  static constexpr int kUpOff = 0, kLowOff = 8192, kMetaOff = kDraft ? 8192 : 16384;
+  static constexpr int kRawBytes = kMetaOff + 512;
+};
+template <int MODE, int MT>
+struct TallLayout {
+  static constexpr int kQOff = 0;
+  static constexpr int kOpOff = MT * kTileBytes;
+  static constexpr int kRawOff = kOpOff + kOpTiles * kTileBytes;
+  static constexpr int kRest = 227 * 1024 - 1024 - kRawOff - 7 * kMaxB * 4 - 512;
+  static constexpr int kRawFit = kRest / TallCfg<MODE>::kRawBytes;
+  static constexpr int kRaw = kRawFit < 10 ? kRawFit : 10;
+  static constexpr int kTabOff = kRawOff + kRaw * TallCfg<MODE>::kRawBytes;
+  static constexpr int kSmem = kTabOff + 7 * kMaxB * 4;  // (+ up to 1 KB of alignment)
+  static_assert(kRaw >= 3, "");
+};
+
+struct TallParams {
+  qs_cache c;
+  Pages pg;
+  const uint16_t *q;
+  uint16_t *out;
+  float *lse, *ws;
+  const int32_t *parent;
+  int n_tree, n_q, R;
+  int n_mp;    // pairs of row tiles per KV head
+  int rows;    // rows of a partial
+  int P;       // CTAs
+  float sl2;
+  uint64_t wait_ns;
+  int no_issue;
+  size_t ws_floats;
+};
+
+// ------------------------------------------------------------------ tcgen05
+
+// K-major operand tile with the 128-byte swizzle: rows of 128 bytes, eight of them to
+// a 1024-byte pattern.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | 1ull << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// fp16 operands, fp32 sums, 128 x 128
+constexpr uint32_t kMmaDesc = 1u << 4 | (kTile / 8) << 17 | (kTile / 16) << 24;
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(kMmaDesc), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(kMmaDesc), "r"(add)
+      : "memory");
+}
+// An arrival on bar when every MMA issued so far is done.
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void tc_before_sync() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_after_sync() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+#define QS_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
+#define QS_S8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
+// 32 columns of the warp's 32 lanes; the load's wait is part of the statement, so
+// that nothing can use the registers before it
+__device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : QS_R8(v, 0), QS_R8(v, 8), QS_R8(v, 16), QS_R8(v, 24)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::QS_S8(v, 0),
+      QS_S8(v, 8), QS_S8(v, 16), QS_S8(v, 24), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::
+          QS_S8(v, 0),
+      QS_S8(v, 8), "r"(addr)
+      : "memory");
+}
+
+// ------------------------------------------------------- operand conversion
+
+// Eight codes of a word pair as four fp16 pairs (elements j and j + 4), exact: the
+// code goes into the mantissa of 1024 (or 1024 and the draft's midpoint), which is
+// taken off again; then scale and zero in one rounding.
+template <int MODE>
+__device__ __forceinline__ void code_pairs(uint32_t wu, uint32_t wl, uint32_t (&e)[4]) {
+  if (MODE == QS_VERIFY_INT8) {
+    const uint32_t ev = bitsel(wl, wu << 4, 0x0F0F0F0Fu), od = bitsel(wl >> 4, wu, 0x0F0F0F0Fu);
+    constexpr uint32_t k64 = 0x64646464u;
+    e[0] = prmt(ev, k64, 0x4240);
+    e[1] = prmt(od, k64, 0x4240);
+    e[2] = prmt(ev, k64, 0x4341);
+    e[3] = prmt(od, k64, 0x4341);
+  } else {
+    constexpr uint32_t m = 0x00F000F0u, k = 0x64086408u;
+    e[0] = ((wu << 4) & m) | k;
+    e[1] = (wu & m) | k;
+    e[2] = ((wu >> 4) & m) | k;
+    e[3] = ((wu >> 8) & m) | k;
+  }
+}
+// The two-bit draft: field sh (0 or 2) of each nibble of a C_U2 word.
+template <int SH>
+__device__ __forceinline__ void code_pairs2(uint32_t x, uint32_t (&e)[4]) {
+  constexpr uint32_t m = 0x00C000C0u, k = 0x64206420u;
+  e[0] = ((x << (6 - SH)) & m) | k;
+  e[1] = (SH <= 2 ? ((x << (2 - SH)) & m) : 0) | k;
+  e[2] = ((x >> (2 + SH)) & m) | k;
+  e[3] = ((x >> (6 + SH)) & m) | k;
+}
+__device__ __forceinline__ uint32_t dequant2(uint32_t e, uint32_t s, uint32_t z) {
+  const __half2 k1024 = __half2half2(__ushort_as_half(0x6400));
+  return h2_as_u32(__hfma2(__hsub2(u32_as_h2(e), k1024), u32_as_h2(s), u32_as_h2(z)));
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  if (!chk(smem_in(a, 16), 60)) return;
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+// Chunk c (eight elements) of row r of an operand tile.
+__device__ __forceinline__ uint32_t tile_at(uint32_t tile, int r, int c) {
+  return tile + (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+// Eight channels in the order of the key codes.
+__device__ __forceinline__ void sts_permuted(uint32_t a, uint4 x) {
+  sts128(a, prmt(x.x, x.z, 0x5410), prmt(x.x, x.z, 0x7632), prmt(x.y, x.w, 0x5410), prmt(x.y, x.w, 0x7632));
+}
+
+// The four words of upper codes (and of lower ones) of 16-byte piece i of a plane; a
+// two-bit draft gets its two C_U2 words doubled.
+template <int MODE, int UB>
+__device__ __forceinline__ void raw_words(uint32_t raw, int i, uint32_t (&u)[4], uint32_t (&l)[4]) {
+  using C = TallCfg<MODE>;
+  if (UB == 4) {
+    const uint4 x = lds128(raw + C::kUpOff + 16 * i);
+    u[0] = x.x; u[1] = x.y; u[2] = x.z; u[3] = x.w;
+  } else {
+    const uint2 a = lds64(raw + C::kUpOff + 8 * i);
+    if (C::kDraft) {
+      u[0] = u[1] = a.x;
+      u[2] = u[3] = a.y;
+    } else {
+      const uint2 m = lds64(raw + C::kUpOff + 4096 + 8 * i);
+      u[0] = upper_from2(a.x, m.x, 0); u[1] = upper_from2(a.x, m.x, 2);
+      u[2] = upper_from2(a.y, m.y, 0); u[3] = upper_from2(a.y, m.y, 2);
+    }
+  }
+  if (!C::kDraft) {
+    const uint4 x = lds128(raw + C::kLowOff + 16 * i);
+    l[0] = x.x; l[1] = x.y; l[2] = x.z; l[3] = x.w;
+  } else {
+    l[0] = l[1] = l[2] = l[3] = 0;
+  }
+}
+template <int MODE, int UB, int W>
+__device__ __forceinline__ void word_pairs(uint32_t u, uint32_t l, uint32_t (&e)[4]) {
+  if (UB == 2 && MODE == QS_DRAFT_UPPER4) code_pairs2<2 * (W & 1)>(u, e);
+  else code_pairs<MODE>(u, l, e);
+}
+
+// A group's keys into an operand tile, by the dequantizing warps (dw of 0 .. 7): a
+// lane takes 32 channels of a token; its scales and zeros stay in registers.  The
+// lanes of a quarter-warp write all eight 16-byte columns of the swizzle.
+template <int MODE, int UB>
+__device__ __forceinline__ void keys_tile(uint32_t raw, uint32_t tile, int dw, int lane) {
+  const int p = (lane & 1) | ((lane >> 2) & 2), tl = ((lane >> 1) & 3) | ((lane >> 4) << 2);
+  uint32_t s[4][4], z[4][4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint4 a = lds128(raw + TallCfg<MODE>::kMetaOff + 16 * (p + 4 * w));
+    const uint4 b = lds128(raw + TallCfg<MODE>::kMetaOff + 256 + 16 * (p + 4 * w));
+    s[w][0] = a.x; s[w][1] = a.y; s[w][2] = a.z; s[w][3] = a.w;
+    z[w][0] = b.x; z[w][1] = b.y; z[w][2] = b.z; z[w][3] = b.w;
+  }
+#pragma unroll
+  for (int pass = 0; pass < 2; ++pass) {
+    const int t = 16 * dw + 8 * pass + tl;
+    uint32_t u[4], l[4], e[4] = {};
+    raw_words<MODE, UB>(raw, 4 * t + p, u, l);
+    auto put = [&](int w) {
+      sts128(tile_at(tile, t, 4 * p + w), dequant2(e[0], s[w][0], z[w][0]), dequant2(e[1], s[w][1], z[w][1]),
+             dequant2(e[2], s[w][2], z[w][2]), dequant2(e[3], s[w][3], z[w][3]));
+    };
+    word_pairs<MODE, UB, 0>(u[0], l[0], e);
+    put(0);
+    word_pairs<MODE, UB, 1>(u[1], l[1], e);
+    put(1);
+    word_pairs<MODE, UB, 2>(u[2], l[2], e);
+    put(2);
+    word_pairs<MODE, UB, 3>(u[3], l[3], e);
+    put(3);
+  }
+}
+
+// A group's values: a lane takes a quarter's 32 tokens of a channel.  Word w's pair j
+// is tokens 8 j + 2 w and the next, so pair j of the four words is eight tokens in
+// order.
+template <int MODE, int UB>
+__device__ __forceinline__ void values_tile(uint32_t raw, uint32_t tile, int dw, int lane) {
+  const int q = dw >> 1;
+  uint32_t s[4][4], z[4][4];  // [word][pair]
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint4 a = lds128(raw + TallCfg<MODE>::kMetaOff + 64 * q + 16 * w);
+    const uint4 b = lds128(raw + TallCfg<MODE>::kMetaOff + 256 + 64 * q + 16 * w);
+    // (a token's four entries: tokens t, t + 8, t + 16, t + 24)
+    s[w][0] = prmt(a.x, a.z, 0x5410); s[w][1] = prmt(a.x, a.z, 0x7632);
+    s[w][2] = prmt(a.y, a.w, 0x5410); s[w][3] = prmt(a.y, a.w, 0x7632);
+    z[w][0] = prmt(b.x, b.z, 0x5410); z[w][1] = prmt(b.x, b.z, 0x7632);
+    z[w][2] = prmt(b.y, b.w, 0x5410); z[w][3] = prmt(b.y, b.w, 0x7632);
+  }
+#pragma unroll
+  for (int pass = 0; pass < 2; ++pass) {
+    const int d = 64 * (dw & 1) + 32 * pass + lane;
+    uint32_t u[4], l[4], e[4][4];
+    raw_words<MODE, UB>(raw, kTile * q + d, u, l);
+    word_pairs<MODE, UB, 0>(u[0], l[0], e[0]);
+    word_pairs<MODE, UB, 1>(u[1], l[1], e[1]);
+    word_pairs<MODE, UB, 2>(u[2], l[2], e[2]);
+    word_pairs<MODE, UB, 3>(u[3], l[3], e[3]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      sts128(tile_at(tile, d, 4 * q + j), dequant2(e[0][j], s[0][j], z[0][j]), dequant2(e[1][j], s[1][j], z[1][j]),
+             dequant2(e[2][j], s[2][j], z[2][j]), dequant2(e[3][j], s[3][j], z[3][j]));
+  }
+}
+
+// ------------------------------------------------------------------- kernel
+
+// Item o of a CTA's 2 n operand tiles, in the order the MMAs take them: unit and
+// whether it is the values.  MT = 2: K0 V0 K1 V1 ..; MT = 1: K0 K1 V0 K2 V1 .. .
+template <int MT>
+__device__ __forceinline__ void item_of(int o, int n, int &unit, bool &values) {
+  if (MT == 2) {
+    unit = o >> 1;
+    values = o & 1;
+  } else if (o == 0) {
+    unit = 0;
+    values = false;
+  } else if (o == 2 * n - 1) {
+    unit = n - 1;
+    values = true;
+  } else {
+    values = !(o & 1);
+    unit = values ? (o - 2) >> 1 : (o + 1) >> 1;
+  }
+}
+template <int MT>
+__device__ __forceinline__ int key_item(int g) {
+  return MT == 2 ? 2 * g : g == 0 ? 0 : 2 * g - 1;
+}
+template <int MT>
+__device__ __forceinline__ int value_item(int g, int n) {
+  return MT == 2 ? 2 * g + 1 : g == n - 1 ? 2 * n - 1 : 2 * g + 2;
+}
+
+struct TallShared {
+  uint64_t raw_full[10], raw_empty[10], op_full[kOpTiles], op_empty[kOpTiles];
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], q_full, q_empty, drain;
+  uint64_t bad[8];        // nodes with values that are not finite, per piece
+  long long total;
+  uint32_t tmem;
+  int abort;
+  int raw_dead[10], dead[kFlags];
+};
+
+// bar's phase with the given parity, or false when the time is up or another role
+// gave up.  (The clock is asked late: reading it takes longer than most waits.)
+__device__ __forceinline__ bool tall_wait(TallShared &s, const uint64_t &bar, uint32_t parity, uint64_t ns) {
+  const uint32_t a = smem_addr(&bar);
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(a, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(a, parity)) return true;
+    if (*reinterpret_cast<volatile int *>(&s.abort)) return false;
+    if (globaltimer_ns() - t0 > ns) {
+      *reinterpret_cast<volatile int *>(&s.abort) = 1;
+      return false;
+    }
+  }
+}
+
+// The same for a whole warp: all lanes agree.
+__device__ __forceinline__ bool warp_wait(TallShared &s, const uint64_t &bar, uint32_t parity, uint64_t ns) {
+  return __all_sync(0xffffffffu, tall_wait(s, bar, parity, ns));
+}
+
+template <int MODE, int UB, int MT>
+__global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const TallParams prm) {
+  using L = TallLayout<MODE, MT>;
+  using C = TallCfg<MODE>;
+  constexpr int NR = L::kRaw;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  __shared__ TallShared sh;
+  // tiles start at multiples of 1024 bytes
+  uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  const uint32_t sbase = smem_addr(smem);
+  const qs_cache &c = prm.c;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, p = blockIdx.x;
+  Tables T = tables_at(smem, L::kTabOff);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(smem_addr(&sh.raw_full[i]), 1);
+      mbar_init(smem_addr(&sh.raw_empty[i]), kDeqWarps);
+    }
+    for (int i = 0; i < kOpTiles; ++i) {
+      mbar_init(smem_addr(&sh.op_full[i]), kDeqWarps);
+      mbar_init(smem_addr(&sh.op_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sh.s_full[i]), 1);
+      mbar_init(smem_addr(&sh.p_full[i]), 4);
+      mbar_init(smem_addr(&sh.o_full[i]), 1);
+      mbar_init(smem_addr(&sh.o_empty[i]), 4);
+    }
+    mbar_init(smem_addr(&sh.q_full), kDeqWarps);
+    mbar_init(smem_addr(&sh.q_empty), 1);
+    mbar_init(smem_addr(&sh.drain), 1);
+    fence_mbar_init();
+    sh.abort = 0;
+    for (int i = 0; i < 8; ++i) sh.bad[i] = 0;
+  }
+  if (w == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    tc_before_sync();
+  }
+  pdl_trigger();
+  pdl_wait();
+  if (w == 0) {
+    qs_cache ct = c;  // segments: (sequence, KV head, pair of row tiles)
+    ct.H = c.H * prm.n_mp;
+    const long long tot = build_tables<kTile, true>(ct, prm.n_tree, 0, INT_MAX, T, lane);
+    if (lane == 0) sh.total = tot;
+  }
+  __syncthreads();
+  tc_after_sync();
+  const long long U = sh.total;
+  const int x0 = (int)range_lo(p, U, prm.P), x1 = (int)range_lo(p + 1, U, prm.P), n = x1 - x0;
+  const uint32_t tmem = sh.tmem;  // columns: S (and P) of stream s at 128 s, O at 256 + 128 s
+  const uint64_t ns = prm.wait_ns;
+  auto bar = [&](const uint64_t &b) { return smem_addr(&b); };
+  auto tile = [&](int o) { return sbase + L::kOpOff + (o % kOpTiles) * kTileBytes; };
+  auto raw_at = [&](int r) { return sbase + L::kRawOff + (r % NR) * C::kRawBytes; };
+
+  if (n <= 0) {
+  } else if (w == kLoadWarp) {
+    // ------------------------------------------------------------- copies
+    Seg cur;
+    int r = 0;  // raw pieces so far
+    for (int o = 0; o < 2 * n; ++o) {
+      int g;
+      bool values;
+      item_of<MT>(o, n, g, values);
+      cur.seek(x0 + g, T, c.B);
+      if (cur.u >= T.ng[cur.b]) continue;  // the buffer is read by the warps that use it
+      if (r >= NR && !warp_wait(sh, sh.raw_empty[r % NR], (r / NR - 1) & 1, ns)) break;
+      if (lane == 0 && !prm.no_issue) {
+        const long long place = group_slot(c, prm.pg, cur.b, cur.h / prm.n_mp, cur.u);
+        const uint32_t dst = raw_at(r), b = bar(sh.raw_full[r % NR]);
+        sh.raw_dead[r % NR] = place < 0;
+        if (place < 0 || !chk(in_range(place, 1, group_slots(c, prm.pg)) && smem_in(dst, C::kRawBytes), 61)) {
+          if (!values) atomicOr(&c.state[(size_t)cur.b * QS_STATE_WORDS + QS_ST_ERR], QS_DEV_PAGE);
+          mbar_arrive(b);
+        } else {
+          constexpr int kUp = C::kDraft && UB == 2 ? 4096 : 8192;
+          const uint64_t pol = l2_evict_first_policy();
+          mbar_arrive_expect_tx(b, kUp + (C::kDraft ? 0 : 8192) + 512);
+          const uint8_t *up = values ? c.v_upper : c.k_upper, *low = values ? c.v_lower : c.k_lower;
+          if (prm.n_mp == 1) {
+            bulk_g2s_hint(dst + C::kUpOff, up + place * 8192, kUp, b, pol);
+            if (!C::kDraft) bulk_g2s_hint(dst + C::kLowOff, low + place * 8192, 8192, b, pol);
+          } else {  // (the next pair of row tiles reads them again)
+            bulk_g2s(dst + C::kUpOff, up + place * 8192, kUp, b);
+            if (!C::kDraft) bulk_g2s(dst + C::kLowOff, low + place * 8192, 8192, b);
+          }
+          bulk_g2s(dst + C::kMetaOff, c.meta + place * 512 + (values ? 256 : 0), 512, b);
+        }
+      }
+      ++r;
+    }
+    // after a timeout nothing may still land in shared memory when the CTA ends
+    // (raw_full completes for every piece that was issued)
+    if (*reinterpret_cast<volatile int *>(&sh.abort) && lane == 0 && !prm.no_issue) {
+      const uint64_t t0 = globaltimer_ns();
+      for (int k = max(0, r - NR); k < r; ++k)
+        while (!mbar_try_wait(bar(sh.raw_full[k % NR]), (k / NR) & 1))
+          if (globaltimer_ns() - t0 > ns) break;
+    }
+  } else if (w == kMmaWarp) {
+    // --------------------------------------------------------------- MMAs
+    if (lane == 0) {
+      Seg cur;
+      int n_s[2] = {0, 0}, n_e[2] = {0, 0}, piece = -1;  // S issued; sums handed over; pieces begun
+      bool ok = true;
+      auto first_of = [&](int g) {  // g starts a piece / its last unit
+        cur.seek(x0 + g, T, c.B);
+        return g == 0 || cur.u == 0;
+      };
+      auto last_of = [&](int g) {
+        cur.seek(x0 + g, T, c.B);
+        return g == n - 1 || cur.u == cur.len - 1;
+      };
+      auto same_piece = [&](int g, int g2) {
+        if (g2 >= n) return false;
+        cur.seek(x0 + g, T, c.B);
+        return x0 + g2 < cur.s0 + cur.len;
+      };
+      auto scores = [&](int s, int g) {
+        const int o = key_item<MT>(g);
+        ok = ok && tall_wait(sh, sh.op_full[o % kOpTiles], (o / kOpTiles) & 1, ns);
+        if (first_of(g) && (MT == 1 || s == 0)) ++piece;
+        if (first_of(g)) ok = ok && tall_wait(sh, sh.q_full, piece & 1, ns);
+        if (!ok) return;
+        tc_after_sync();
+        const uint32_t a = sbase + L::kQOff + (MT == 2 ? s * kTileBytes : 0), b = tile(o);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t off = (k >> 2) * (kTile * 128) + (k & 3) * 32;
+          mma_ss(tmem + 128 * s, operand_desc(a + off), operand_desc(b + off), k > 0);
+        }
+        mma_commit(bar(sh.s_full[s]));
+        if (MT == 1 || s == 1) {
+          mma_commit(bar(sh.op_empty[o % kOpTiles]));
+          if (last_of(g)) mma_commit(bar(sh.q_empty));
+        }
+        ++n_s[s];
+      };
+      // first: the stream's first unit of a piece (the sums start anew)
+      auto sums = [&](int s, int g, bool first, bool last) {
+        const int o = value_item<MT>(g, n);
+        ok = ok && tall_wait(sh, sh.p_full[s], (n_s[s] - 1) & 1, ns) &&
+             tall_wait(sh, sh.op_full[o % kOpTiles], (o / kOpTiles) & 1, ns);
+        if (first && n_e[s] > 0) ok = ok && tall_wait(sh, sh.o_empty[s], (n_e[s] - 1) & 1, ns);
+        if (!ok) return;
+        tc_after_sync();
+        const uint32_t b = tile(o);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ts(tmem + 256 + 128 * s, tmem + 128 * s + 8 * k,
+                 operand_desc(b + (k >> 2) * (kTile * 128) + (k & 3) * 32), !first || k > 0);
+        if (MT == 1 || s == 1) mma_commit(bar(sh.op_empty[o % kOpTiles]));
+        if (last) {
+          mma_commit(bar(sh.o_full[s]));
+          ++n_e[s];
+        }
+      };
+      if (MT == 2) {
+        scores(0, 0);
+        scores(1, 0);
+        for (int g = 0; ok && g < n; ++g) {
+          const bool f = first_of(g), l = last_of(g);
+          for (int s = 0; s < 2; ++s) {
+            sums(s, g, f, l);
+            if (g + 1 < n) scores(s, g + 1);
+          }
+        }
+      } else {
+        scores(0, 0);
+        if (n > 1) scores(1, 1);
+        for (int g = 0; ok && g < n; ++g) {
+          cur.seek(x0 + g, T, c.B);
+          const bool f = g < 2 || x0 + g - 2 < cur.s0, l = !same_piece(g, g + 2);
+          sums(g & 1, g, f, l);
+          if (g + 2 < n) scores(g & 1, g + 2);
+        }
+      }
+      // no MMA may be in flight when the CTA gives its tensor memory back
+      mma_commit(bar(sh.drain));
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(bar(sh.drain), 0))
+        if (globaltimer_ns() - t0 > ns) break;
+    }
+    __syncwarp();
+  } else if (w >= kSoftWarps) {
+    // ----------------------------------------------------- operand tiles
+    const int dw = w - kSoftWarps, dt = dw * 32 + lane;
+    Seg cur;
+    int r = 0, piece = -1;
+    for (int o = 0; o < 2 * n; ++o) {
+      int g;
+      bool values;
+      item_of<MT>(o, n, g, values);
+      cur.seek(x0 + g, T, c.B);
+      const int h = cur.h / prm.n_mp, mp = cur.h % prm.n_mp, ng = T.ng[cur.b];
+      const size_t bh = (size_t)cur.b * c.H + h;
+      if (!values && (g == 0 || cur.u == 0)) {
+        // a piece begins: its queries, once no MMA reads the last piece's any more
+        ++piece;
+        if (piece > 0 && !warp_wait(sh, sh.q_empty, (piece - 1) & 1, ns)) break;
+        // (an entry that no warp here can have reached again, nor the softmax
+        // still reads: each is within three pieces of this one)
+        if (dt == 0) sh.bad[(piece + 4) & 7] = 0;
+        const uint4 *src = reinterpret_cast<const uint4 *>(prm.q + bh * prm.R * kD);
+#pragma unroll 1
+        for (int i0 = dt; i0 < MT * kTile * 16; i0 += 4 * 32 * kDeqWarps) {
+          uint4 x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int i = i0 + k * 32 * kDeqWarps, row = mp * 2 * kTile + (i >> 4);
+            x[k] = row < prm.R ? src[(size_t)row * 16 + (i & 15)] : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int i = i0 + k * 32 * kDeqWarps, row = i >> 4;
+            sts_permuted(tile_at(sbase + L::kQOff + (row / kTile) * kTileBytes, row % kTile, i & 15), x[k]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh.q_full));
+      }
+      if (o >= kOpTiles && !warp_wait(sh, sh.op_empty[o % kOpTiles], (o / kOpTiles - 1) & 1, ns)) break;
+      const uint32_t dst = tile(o);
+      if (cur.u < ng) {
+        if (!warp_wait(sh, sh.raw_full[r % NR], (r / NR) & 1, ns)) break;
+        const bool dead = *reinterpret_cast<volatile int *>(&sh.raw_dead[r % NR]) != 0;
+        if (dead) {  // a group that is left out: nothing that could disturb the sums
+#pragma unroll 1
+          for (int i = dt; i < kTileBytes / 16; i += 32 * kDeqWarps) sts128(dst + 16 * i, 0, 0, 0, 0);
+        } else if (values) {
+          values_tile<MODE, UB>(raw_at(r), dst, dw, lane);
+        } else {
+          keys_tile<MODE, UB>(raw_at(r), dst, dw, lane);
+        }
+        if (!values && dt == 0) *reinterpret_cast<volatile int *>(&sh.dead[g % kFlags]) = dead;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh.raw_empty[r % NR]));
+        ++r;
+      } else {
+        const int i0 = (cur.u - ng) * kTile, fill = T.fill[cur.b], tree0 = fill - prm.n_tree;
+        const size_t row0 = bh * kRing;
+        const int base = T.hb[cur.b] * kG + i0;
+        if (!values) {
+          const uint4 *src = reinterpret_cast<const uint4 *>(c.buf_k);
+          uint4 x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int t = (dt >> 4) + 16 * k;
+            x[k] = i0 + t < fill ? src[(row0 + ((base + t) & (kRing - 1))) * 16 + (dt & 15)] : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sts_permuted(tile_at(dst, (dt >> 4) + 16 * k, dt & 15), x[k]);
+          if (dt == 0) *reinterpret_cast<volatile int *>(&sh.dead[g % kFlags]) = 0;
+        } else {
+          // eight tokens of eight channels per thread, turned in registers
+          const int tc = (dt & 7) | ((dt >> 4) & 8), dc = (dt >> 3) & 15;
+          const uint4 *src = reinterpret_cast<const uint4 *>(c.buf_v);
+          // (MT = 1: the next unit's keys come before these values)
+          const int of = MT == 1 && g + 1 < n && cur.u == cur.len - 1 ? piece - 1 : piece;
+          uint4 x[8];
+          uint64_t bad = 0;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int t = 8 * tc + k;
+            x[k] = i0 + t < fill ? src[(row0 + ((base + t) & (kRing - 1))) * 16 + dc] : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            // a node's values meet the zero weights of rows that do not see it
+            const int j = i0 + 8 * tc + k - tree0;
+            if (j < 0) continue;
+            unsigned f = drop_nonfinite(x[k].x);
+            f |= drop_nonfinite(x[k].y);
+            f |= drop_nonfinite(x[k].z);
+            f |= drop_nonfinite(x[k].w);
+            if (f) bad |= 1ull << (j & 63);
+          }
+          if (bad) atomicOr(reinterpret_cast<unsigned long long *>(&sh.bad[of & 7]), bad);
+          const uint32_t *xs = reinterpret_cast<const uint32_t *>(x);
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {
+            const uint32_t sel = d & 1 ? 0x7632 : 0x5410;
+            const int k = d >> 1;
+            sts128(tile_at(dst, 8 * dc + d, tc), prmt(xs[k], xs[4 + k], sel), prmt(xs[8 + k], xs[12 + k], sel),
+                   prmt(xs[16 + k], xs[20 + k], sel), prmt(xs[24 + k], xs[28 + k], sel));
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sh.op_full[o % kOpTiles]));
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int s = w >> 2, lanes = 32 * (w & 3), row_t = lanes + lane;  // stream; row in the tile
+    const uint32_t t_s = tmem + 128 * s + ((uint32_t)lanes << 16);
+    const uint32_t t_o = tmem + 256 + 128 * s + ((uint32_t)lanes << 16);
+    int n_s = 0, n_e = 0;
+    bool ok = true;
+    Seg cur;
+    for (int x = x0, piece = 0; ok && x < x1; ++piece) {
+      cur.seek(x, T, c.B);
+      const int end = min(x1, cur.s0 + cur.len), b = cur.b, mp = cur.h % prm.n_mp, ng = T.ng[b];
+      const int fill = T.fill[b], tree0 = fill - prm.n_tree;
+      const int row = 2 * kTile * mp + (MT == 2 ? s * kTile : 0) + row_t;
+      const bool live_warp = row - lane < prm.R;
+      uint64_t sees = 0;
+      bool known = false;
+      float m = -INFINITY, l = 0.f;
+      int done = 0;
+      // the stream's units of the piece
+      for (int y = MT == 2 ? x : x + ((x - x0 + s) & 1); ok && y < end; y += MT == 2 ? 1 : 2) {
+        const int u = y - cur.s0;
+        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+        if (u >= ng) {  // the buffer: which of the 128 tokens this row sees
+          if (!known) {
+            uint64_t mm[2];
+            bool bad = false;
+            tree_ancestors(prm.parent + (size_t)b * prm.n_tree, prm.n_tree, lane, mm, bad);
+            if (bad) atomicOr(&c.state[(size_t)b * QS_STATE_WORDS + QS_ST_ERR], QS_DEV_TREE);
+            sees = ancestors_of(mm, prm.n_tree - prm.n_q + row % prm.n_q);
+            known = true;
+          }
+          const int i0 = (u - ng) * kTile;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int i = i0 + 32 * k, before = tree0 - i;  // tokens of the word in front of the tree
+            uint32_t v = before >= 32 ? ~0u : before <= 0 ? 0u : (1u << before) - 1;
+            if (before < 32) {
+              const uint64_t node = before >= 0 ? sees << before : -before < 64 ? sees >> -before : 0;
+              v |= (uint32_t)node;
+            }
+            const int have = fill - i;
+            if (have < 32) v &= have <= 0 ? 0u : (1u << have) - 1;
+            vis[k] = v;
+          }
+        }
+        ok = warp_wait(sh, sh.s_full[s], n_s & 1, ns);
+        if (!ok) break;
+        ++n_s;
+        tc_after_sync();
+        if (live_warp) {
+          if (u < ng && *reinterpret_cast<volatile int *>(&sh.dead[(y - x0) % kFlags]))
+            vis[0] = vis[1] = vis[2] = vis[3] = 0;
+          const bool masked = (vis[0] & vis[1] & vis[2] & vis[3]) != ~0u;
+          uint32_t v[32];
+          float mx = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            tc_ld32(t_s + 32 * k, v);
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) mx = fmaxf(mx, vis[k] >> i & 1 ? __uint_as_float(v[i]) : -INFINITY);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(v[i]));
+            }
+          }
+          const float mn = mx * prm.sl2;
+          const bool raise = mn > m + kRaise || (m == -INFINITY && mn > -INFINITY);
+          if (__any_sync(0xffffffffu, raise)) {
+            const float a = raise ? (m == -INFINITY ? 0.f : fast_exp2(m - mn)) : 1.f;
+            if (done > 0) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                tc_ld32(t_o + 32 * k, v);
+    #pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a);
+                tc_st32(t_o + 32 * k, v);
+              }
+            }
+            l *= a;
+            if (raise) m = mn;
+          }
+          const float off = m == -INFINITY ? 0.f : kExpShift - m;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            tc_ld32(t_s + 32 * k, v);
+            uint32_t ph[16];
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float a = fast_exp2(fmaf(__uint_as_float(v[2 * i]), prm.sl2, off));
+              float e = fast_exp2(fmaf(__uint_as_float(v[2 * i + 1]), prm.sl2, off));
+              if (masked) {
+                if (!(vis[k] >> (2 * i) & 1)) a = 0.f;
+                if (!(vis[k] >> (2 * i + 1) & 1)) e = 0.f;
+              }
+              sum += a + e;
+              ph[i] = pack_half2(a, e);
+            }
+            l += sum;
+            tc_st16(t_s + 16 * k, ph);
+          }
+          tc_wait_st();
+        }
+        ++done;
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh.p_full[s]));
+      }
+      if (!ok) break;
+      // the piece's partial: rows side by side, four channels each
+      float *part = prm.ws + ((size_t)(cur.ord + p) * 2 + s) * prm.rows * (kD + 2);
+      const bool mine = live_warp && row < prm.R &&
+                        chk(in_range((size_t)(part - prm.ws), (size_t)prm.rows * (kD + 2), prm.ws_floats), 62);
+      if (done > 0) {
+        ok = warp_wait(sh, sh.o_full[s], n_e & 1, ns);
+        if (!ok) break;
+        ++n_e;
+        tc_after_sync();
+        if (live_warp) {
+          if (known && (sees & *reinterpret_cast<volatile uint64_t *>(&sh.bad[piece & 7]))) l = NAN;
+          const float poison = l == l ? 0.f : NAN;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t v[32];
+            tc_ld32(t_o + 32 * k, v);
+            if (mine)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                reinterpret_cast<float4 *>(part)[(8 * k + i) * prm.rows + row_t] =
+                    make_float4(__uint_as_float(v[4 * i]) + poison, __uint_as_float(v[4 * i + 1]) + poison,
+                                __uint_as_float(v[4 * i + 2]) + poison, __uint_as_float(v[4 * i + 3]) + poison);
+          }
+        }
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh.o_empty[s]));
+      }
+      if (mine) {
+        part[prm.rows * kD + row_t] = m;
+        part[prm.rows * (kD + 1) + row_t] = l;
+      }
+      x = end;
+    }
+  }
+  __syncthreads();
+  if (sh.abort && threadIdx.x == 0)
+    for (int b = 0; b < c.B; ++b) atomicOr(&c.state[(size_t)b * QS_STATE_WORDS + QS_ST_ERR], QS_DEV_TIMEOUT);
+  if (w == kMmaWarp) {
+    tc_after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+// Joins the partials: a thread takes four channels of a row (eight rows side by
+// side), its loads in flight four at a time.  The CTAs that hold a segment, and where
+// their partials lie, follow from the counters as in the kernel above.
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads) tall_join_kernel(const TallParams prm, int MT) {
+  __shared__ int tab[7 * kMaxB];
+  __shared__ long long s_total;
+  const qs_cache &c = prm.c;
+  Tables T = tables_at(reinterpret_cast<uint8_t *>(tab), 0);
+  pdl_trigger();
+  pdl_wait();
+  if (threadIdx.x < 32) {
+    qs_cache ct = c;
+    ct.H = c.H * prm.n_mp;
+    const long long tot = build_tables<kTile, true>(ct, prm.n_tree, 0, INT_MAX, T, threadIdx.x);
+    if (threadIdx.x == 0) s_total = tot;
+  }
+  __syncthreads();
+  const long long at = (long long)blockIdx.x * 8 + (threadIdx.x & 7);
+  const int c4 = threadIdx.x >> 3;
+  if (at >= (long long)c.B * c.H * prm.R) return;
+  const int row = (int)(at % prm.R), bh = (int)(at / prm.R), b = bh / c.H, h = bh % c.H;
+  uint2 *out = reinterpret_cast<uint2 *>(prm.out + (size_t)at * kD + 4 * c4);
+  const int len = T.len[b];
+  if (len == 0) {  // n_tree > fill
+    *out = make_uint2(0, 0);
+    if (c4 == 0) {
+      if (prm.lse) prm.lse[at] = -INFINITY;
+      atomicOr(&c.state[(size_t)b * QS_STATE_WORDS + QS_ST_ERR], QS_DEV_NQ_GT_FILL);
+    }
+    return;
+  }
+  const long long U = s_total;
+  const int seg = h * prm.n_mp + row / (2 * kTile), s0 = T.base[b] + seg * len, ord = T.ord0[b] + seg;
+  const int plo = cta_of(s0, U, prm.P), phi = cta_of(s0 + len - 1, U, prm.P);
+  const int row_t = row % kTile, s_at = MT == 2 ? (row / kTile) & 1 : 0, per = MT == 2 ? 1 : 2;
+  const size_t size = (size_t)prm.rows * (kD + 2);
+  float M = -INFINITY, Ls = 0.f;
+  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int np = (phi - plo + 1) * per;
+  for (int k0 = 0; k0 < np; k0 += 4) {
+    float m[4], l[4];
+    float4 o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = k0 + i;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+      if (k >= np) continue;
+      const size_t off = ((size_t)(ord + plo + k / per) * 2 + s_at + k % per) * size;
+      if (!chk(in_range(off, size, prm.ws_floats), 63)) continue;
+      const float *part = prm.ws + off;
+      m[i] = part[prm.rows * kD + row_t];
+      l[i] = part[prm.rows * (kD + 1) + row_t];
+      o[i] = reinterpret_cast<const float4 *>(part)[c4 * prm.rows + row_t];
+    }
+    float mn = M;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mn = fmaxf(mn, m[i]);
+    const float a = M == -INFINITY ? 0.f : fast_exp2(M - mn);
+    A.x *= a; A.y *= a; A.z *= a; A.w *= a;
+    Ls *= a;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (l[i] == 0.f) continue;  // nothing seen there (its sums were not written)
+      const float f = m[i] == -INFINITY ? 1.f : fast_exp2(m[i] - mn);  // (no maximum: all NaN)
+      A.x = fmaf(f, o[i].x, A.x); A.y = fmaf(f, o[i].y, A.y);
+      A.z = fmaf(f, o[i].z, A.z); A.w = fmaf(f, o[i].w, A.w);
+      Ls = fmaf(f, l[i], Ls);
+    }
+    M = mn;
+  }
+  const float inv = 1.f / Ls;
+  *out = make_uint2(pack_half2(A.x * inv, A.y * inv), pack_half2(A.z * inv, A.w * inv));
+  if (prm.lse && c4 == 0) prm.lse[at] = (M - kExpShift + log2f(Ls)) * 0.69314718055994531f;
+}
+
+// --------------------------------------------------------------- host side
+
+// Rows of a partial: a row tile's, in eights (its four channels lie 16-byte aligned).
+inline int tall_rows(int R) { return R < kTile ? (R + 7) / 8 * 8 : kTile; }
+inline size_t tall_ws_bytes(int P, int B, int H, int R) {
+  const int n_mp = (R + 2 * kTile - 1) / (2 * kTile), rows = tall_rows(R);
+  return ((size_t)P + (size_t)B * H * n_mp) * 2 * rows * (kD + 2) * sizeof(float);
+}
+
+template <int MODE, int UB, int MT>
+qs_status launch_tall(const TallParams &prm, cudaStream_t st) {
+  constexpr int smem = TallLayout<MODE, MT>::kSmem + 1024;
+  static int mask = 0;
+  qs_status s = set_smem_once((const void *)tall_kernel<MODE, UB, MT>, smem, &mask);
+  if (s != QS_OK) return s;
+  s = launch_pdl(tall_kernel<MODE, UB, MT>, dim3(prm.P), dim3(kTallThreads), smem, st, prm);
+  if (s != QS_OK) return s;
+  const long long rows = (long long)prm.c.B * prm.c.H * prm.R;
+  return launch_pdl(tall_join_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(kJoinThreads), 0, st, prm, MT);
+}
+template <int MODE>
+qs_status launch_tall_mode(const TallParams &prm, cudaStream_t st) {
+  const bool two = prm.R > kTile;
+  if (prm.c.upper_bits == 2) return two ? launch_tall<MODE, 2, 2>(prm, st) : launch_tall<MODE, 2, 1>(prm, st);
+  return two ? launch_tall<MODE, 4, 2>(prm, st) : launch_tall<MODE, 4, 1>(prm, st);
+}
+
+}  // namespace
+}  // namespace qs
