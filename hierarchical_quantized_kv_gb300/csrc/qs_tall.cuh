@@ -14,9 +14,12 @@
 //    kernel does, and writes a partial (O, m, l) for each segment it touches; a second
 //    kernel joins them.
 //  * Roles: one warp starts the bulk copies of planes and scales into a ring; eight
-//    warps make fp16 operand tiles of them (128 rows of 128 fp16, the 128-byte swizzle
-//    of K-major operands) in a ring of three; one thread issues the MMAs; two groups
-//    of four warps do the softmax, a row per thread.
+//    warps make fp16 operand tiles of the keys (128 rows of 128 fp16, the 128-byte
+//    swizzle of K-major operands), eight of the values, in a ring of three; one thread
+//    issues the MMAs; two groups of four warps do the softmax, a row per thread.
+//  * 26 warps in five roles share the instruction caches: the loops are kept short
+//    (unrolled over whole tiles, with the segments' bookkeeping inside, the same
+//    kernel had 188 KB of code and took 102 us instead of 62 for 240 rows of 32k).
 //  * Two streams alternate on the tensor core, so that one multiplies while the other's
 //    softmax runs.  With more than 128 rows they are two row tiles over the same keys
 //    and values; else they take every other unit.
@@ -36,8 +39,8 @@ namespace {
 constexpr int kTile = 128;                 // rows, tokens and channels of a tile
 constexpr int kTileBytes = kTile * kTile * 2;
 constexpr int kOpTiles = 3;                // operand tiles (keys or values) in the ring
-constexpr int kSoftWarps = 8, kDeqWarps = 8;
-constexpr int kMmaWarp = kSoftWarps + kDeqWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kSoftWarps = 8, kDeqWarps = 8;  // (of the latter for keys, and for values)
+constexpr int kMmaWarp = kSoftWarps + 2 * kDeqWarps, kLoadWarp = kMmaWarp + 1;
 constexpr int kTallThreads = 32 * (kLoadWarp + 1);
 constexpr float kRaise = 8.f;              // log2 by which a maximum may be behind
 constexpr int kFlags = 8;                  // units whose flags are kept
@@ -103,6 +106,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(kMmaDesc), "r"(add)
       : "memory");
+}
+// True in one lane of a converged warp (the same one every time, as an arrival
+// covers the MMAs of its own thread).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 // An arrival on bar when every MMA issued so far is done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
@@ -238,7 +248,7 @@ __device__ __forceinline__ void keys_tile(uint32_t raw, uint32_t tile, int dw, i
     s[w][0] = a.x; s[w][1] = a.y; s[w][2] = a.z; s[w][3] = a.w;
     z[w][0] = b.x; z[w][1] = b.y; z[w][2] = b.z; z[w][3] = b.w;
   }
-#pragma unroll
+#pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     const int t = 16 * dw + 8 * pass + tl;
     uint32_t u[4], l[4], e[4] = {};
@@ -275,7 +285,7 @@ __device__ __forceinline__ void values_tile(uint32_t raw, uint32_t tile, int dw,
     z[w][0] = prmt(b.x, b.z, 0x5410); z[w][1] = prmt(b.x, b.z, 0x7632);
     z[w][2] = prmt(b.y, b.w, 0x5410); z[w][3] = prmt(b.y, b.w, 0x7632);
   }
-#pragma unroll
+#pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     const int d = 64 * (dw & 1) + 32 * pass + lane;
     uint32_t u[4], l[4], e[4][4];
@@ -293,23 +303,16 @@ __device__ __forceinline__ void values_tile(uint32_t raw, uint32_t tile, int dw,
 
 // ------------------------------------------------------------------- kernel
 
-// Item o of a CTA's 2 n operand tiles, in the order the MMAs take them: unit and
+// Item i of a piece's 2 n operand tiles, in the order the MMAs take them: unit and
 // whether it is the values.  MT = 2: K0 V0 K1 V1 ..; MT = 1: K0 K1 V0 K2 V1 .. .
 template <int MT>
-__device__ __forceinline__ void item_of(int o, int n, int &unit, bool &values) {
+__device__ __forceinline__ int item_of(int i, int n, bool &values) {
   if (MT == 2) {
-    unit = o >> 1;
-    values = o & 1;
-  } else if (o == 0) {
-    unit = 0;
-    values = false;
-  } else if (o == 2 * n - 1) {
-    unit = n - 1;
-    values = true;
-  } else {
-    values = !(o & 1);
-    unit = values ? (o - 2) >> 1 : (o + 1) >> 1;
+    values = i & 1;
+    return i >> 1;
   }
+  values = i > 0 && (!(i & 1) || i == 2 * n - 1);
+  return i == 2 * n - 1 ? n - 1 : values ? (i - 2) >> 1 : (i + 1) >> 1;
 }
 template <int MT>
 __device__ __forceinline__ int key_item(int g) {
@@ -319,6 +322,24 @@ template <int MT>
 __device__ __forceinline__ int value_item(int g, int n) {
   return MT == 2 ? 2 * g + 1 : g == n - 1 ? 2 * n - 1 : 2 * g + 2;
 }
+
+// A place in a ring of N and the parity of its turn.
+template <int N>
+struct Ring {
+  int slot = 0, par = 0;
+  __device__ __forceinline__ void add(int by) {  // up to N
+    slot += by;
+    if (slot >= N) {
+      slot -= N;
+      par ^= 1;
+    }
+  }
+  __device__ __forceinline__ void add_any(int by) {
+    const int x = slot + by;
+    par ^= (x / N) & 1;
+    slot = x % N;
+  }
+};
 
 struct TallShared {
   uint64_t raw_full[10], raw_empty[10], op_full[kOpTiles], op_empty[kOpTiles];
@@ -330,12 +351,31 @@ struct TallShared {
   int raw_dead[10], dead[kFlags];
 };
 
+// A CTA's part of one segment.
+struct Piece {
+  int b, h, mp, ord;     // sequence, KV head, pair of row tiles, ordinal of the segment
+  int u0, n;             // first unit in the segment, units
+  int ng, fill, hb;      // of the sequence
+};
+// (Not inlined, as it runs once a piece in four places: the loops of this kernel
+// have to share the instruction caches.)
+__device__ __noinline__ void piece_at(int B, int n_mp, const Tables &T, int x, int x1, Piece &pc) {
+  Seg cur;
+  cur.seek(x, T, B);
+  pc.b = cur.b;
+  pc.h = n_mp == 1 ? cur.h : cur.h >> 1;
+  pc.mp = n_mp == 1 ? 0 : cur.h & 1;
+  pc.ord = cur.ord;
+  pc.u0 = cur.u;
+  pc.n = min(x1, cur.s0 + cur.len) - x;
+  pc.ng = T.ng[cur.b];
+  pc.fill = T.fill[cur.b];
+  pc.hb = T.hb[cur.b];
+}
+
 // bar's phase with the given parity, or false when the time is up or another role
 // gave up.  (The clock is asked late: reading it takes longer than most waits.)
-__device__ __forceinline__ bool tall_wait(TallShared &s, const uint64_t &bar, uint32_t parity, uint64_t ns) {
-  const uint32_t a = smem_addr(&bar);
-  for (int i = 0; i < 64; ++i)
-    if (mbar_try_wait(a, parity)) return true;
+__device__ __noinline__ bool tall_wait_long(TallShared &s, uint32_t a, uint32_t parity, uint64_t ns) {
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
     for (int i = 0; i < 64; ++i)
@@ -347,14 +387,109 @@ __device__ __forceinline__ bool tall_wait(TallShared &s, const uint64_t &bar, ui
     }
   }
 }
-
+__device__ __forceinline__ bool tall_wait(TallShared &s, const uint64_t &bar, uint32_t parity, uint64_t ns) {
+  const uint32_t a = smem_addr(&bar);
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(a, parity)) return true;
+  return tall_wait_long(s, a, parity, ns);
+}
 // The same for a whole warp: all lanes agree.
 __device__ __forceinline__ bool warp_wait(TallShared &s, const uint64_t &bar, uint32_t parity, uint64_t ns) {
   return __all_sync(0xffffffffu, tall_wait(s, bar, parity, ns));
 }
 
+// 128 buffer tokens from i0 on into an operand tile, straight from memory: keys...
+__device__ __noinline__ void buffer_keys_tile(const uint4 *src, int base, int i0, int fill, uint32_t tile, int dt) {
+  uint4 x[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int t = (dt >> 4) + 16 * k;
+    x[k] = i0 + t < fill ? src[((base + t) & (kRing - 1)) * 16 + (dt & 15)] : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) sts_permuted(tile_at(tile, (dt >> 4) + 16 * k, dt & 15), x[k]);
+}
+// ... and values, eight tokens of eight channels per thread, turned in registers.
+// Values of nodes (from token tree0 on) that are not finite become 0 (they meet the
+// zero weights of rows that do not see the node); returns those nodes' bits.
+__device__ __noinline__ uint64_t buffer_values_tile(const uint4 *src, int base, int i0, int fill, int tree0,
+                                                    uint32_t tile, int dt) {
+  const int tc = (dt & 7) | ((dt >> 4) & 8), dc = (dt >> 3) & 15;
+  uint4 x[8];
+  uint64_t bad = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int t = 8 * tc + k;
+    x[k] = i0 + t < fill ? src[((base + t) & (kRing - 1)) * 16 + dc] : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int j = i0 + 8 * tc + k - tree0;
+    if (j < 0) continue;
+    unsigned f = drop_nonfinite(x[k].x);
+    f |= drop_nonfinite(x[k].y);
+    f |= drop_nonfinite(x[k].z);
+    f |= drop_nonfinite(x[k].w);
+    if (f) bad |= 1ull << (j & 63);
+  }
+  const uint32_t *xs = reinterpret_cast<const uint32_t *>(x);
+#pragma unroll
+  for (int d = 0; d < 8; ++d) {
+    const uint32_t sel = d & 1 ? 0x7632 : 0x5410;
+    const int k = d >> 1;
+    sts128(tile_at(tile, 8 * dc + d, tc), prmt(xs[k], xs[4 + k], sel), prmt(xs[8 + k], xs[12 + k], sel),
+           prmt(xs[16 + k], xs[20 + k], sel), prmt(xs[24 + k], xs[28 + k], sel));
+  }
+  return bad;
+}
+
+// A piece's queries into their operand tiles (rows past the last: zeros).
+template <int MT>
+__device__ __noinline__ void query_tiles(const uint4 *src, int row0, int R, uint32_t tiles, int dt) {
+#pragma unroll 1
+  for (int i0 = dt; i0 < MT * kTile * 16; i0 += 4 * 32 * kDeqWarps) {
+    uint4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * 32 * kDeqWarps, row = row0 + (i >> 4);
+      x[k] = row < R ? src[(size_t)row * 16 + (i & 15)] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * 32 * kDeqWarps, row = i >> 4;
+      sts_permuted(tile_at(tiles + (row / kTile) * kTileBytes, row % kTile, i & 15), x[k]);
+    }
+  }
+}
+
+// The tokens i0 .. i0 + 127 of the buffer that a row sees, a bit each: those in front
+// of the tree, and of the tree the bits of sees.  The scores of the others become
+// -inf.
+__device__ __noinline__ void mask_scores(uint32_t t_s, int i0, int fill, int tree0, uint64_t sees, bool dead) {
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    const int i = i0 + 32 * k, before = tree0 - i;  // tokens of the word in front of the tree
+    uint32_t vis = before >= 32 ? ~0u : before <= 0 ? 0u : (1u << before) - 1;
+    if (before < 32) {
+      const uint64_t node = before >= 0 ? sees << before : -before < 64 ? sees >> -before : 0;
+      vis |= (uint32_t)node;
+    }
+    const int have = fill - i;
+    if (have < 32) vis &= have <= 0 ? 0u : (1u << have) - 1;
+    if (dead) vis = 0;
+    uint32_t v[32];
+    tc_ld32(t_s + 32 * k, v);
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (!(vis >> j & 1)) v[j] = 0xFF800000u;
+    tc_st32(t_s + 32 * k, v);
+  }
+  tc_wait_st();
+}
+
 template <int MODE, int UB, int MT>
-__global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const TallParams prm) {
+__global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_constant__ TallParams prm) {
   using L = TallLayout<MODE, MT>;
   using C = TallCfg<MODE>;
   constexpr int NR = L::kRaw;
@@ -367,14 +502,17 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const TallParams 
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, p = blockIdx.x;
   Tables T = tables_at(smem, L::kTabOff);
   if (threadIdx.x == 0) {
+#pragma unroll 1
     for (int i = 0; i < NR; ++i) {
       mbar_init(smem_addr(&sh.raw_full[i]), 1);
       mbar_init(smem_addr(&sh.raw_empty[i]), kDeqWarps);
     }
+#pragma unroll 1
     for (int i = 0; i < kOpTiles; ++i) {
       mbar_init(smem_addr(&sh.op_full[i]), kDeqWarps);
       mbar_init(smem_addr(&sh.op_empty[i]), 1);
     }
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&sh.s_full[i]), 1);
       mbar_init(smem_addr(&sh.p_full[i]), 4);
@@ -386,6 +524,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const TallParams 
     mbar_init(smem_addr(&sh.drain), 1);
     fence_mbar_init();
     sh.abort = 0;
+#pragma unroll 1
     for (int i = 0; i < 8; ++i) sh.bad[i] = 0;
   }
   if (w == kMmaWarp) {
@@ -405,137 +544,154 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const TallParams 
   __syncthreads();
   tc_after_sync();
   const long long U = sh.total;
-  const int x0 = (int)range_lo(p, U, prm.P), x1 = (int)range_lo(p + 1, U, prm.P), n = x1 - x0;
+  const int x0 = (int)range_lo(p, U, prm.P), x1 = (int)range_lo(p + 1, U, prm.P);
   const uint32_t tmem = sh.tmem;  // columns: S (and P) of stream s at 128 s, O at 256 + 128 s
   const uint64_t ns = prm.wait_ns;
   auto bar = [&](const uint64_t &b) { return smem_addr(&b); };
-  auto tile = [&](int o) { return sbase + L::kOpOff + (o % kOpTiles) * kTileBytes; };
-  auto raw_at = [&](int r) { return sbase + L::kRawOff + (r % NR) * C::kRawBytes; };
+  auto tile = [&](int slot) { return sbase + L::kOpOff + slot * kTileBytes; };
+  auto raw_at = [&](int slot) { return sbase + L::kRawOff + slot * C::kRawBytes; };
+  Piece pc;
 
-  if (n <= 0) {
-  } else if (w == kLoadWarp) {
+  if (w == kLoadWarp) {
     // ------------------------------------------------------------- copies
-    Seg cur;
-    int r = 0;  // raw pieces so far
-    for (int o = 0; o < 2 * n; ++o) {
-      int g;
-      bool values;
-      item_of<MT>(o, n, g, values);
-      cur.seek(x0 + g, T, c.B);
-      if (cur.u >= T.ng[cur.b]) continue;  // the buffer is read by the warps that use it
-      if (r >= NR && !warp_wait(sh, sh.raw_empty[r % NR], (r / NR - 1) & 1, ns)) break;
-      if (lane == 0 && !prm.no_issue) {
-        const long long place = group_slot(c, prm.pg, cur.b, cur.h / prm.n_mp, cur.u);
-        const uint32_t dst = raw_at(r), b = bar(sh.raw_full[r % NR]);
-        sh.raw_dead[r % NR] = place < 0;
-        if (place < 0 || !chk(in_range(place, 1, group_slots(c, prm.pg)) && smem_in(dst, C::kRawBytes), 61)) {
-          if (!values) atomicOr(&c.state[(size_t)cur.b * QS_STATE_WORDS + QS_ST_ERR], QS_DEV_PAGE);
-          mbar_arrive(b);
-        } else {
-          constexpr int kUp = C::kDraft && UB == 2 ? 4096 : 8192;
-          const uint64_t pol = l2_evict_first_policy();
-          mbar_arrive_expect_tx(b, kUp + (C::kDraft ? 0 : 8192) + 512);
-          const uint8_t *up = values ? c.v_upper : c.k_upper, *low = values ? c.v_lower : c.k_lower;
-          if (prm.n_mp == 1) {
-            bulk_g2s_hint(dst + C::kUpOff, up + place * 8192, kUp, b, pol);
-            if (!C::kDraft) bulk_g2s_hint(dst + C::kLowOff, low + place * 8192, 8192, b, pol);
-          } else {  // (the next pair of row tiles reads them again)
-            bulk_g2s(dst + C::kUpOff, up + place * 8192, kUp, b);
-            if (!C::kDraft) bulk_g2s(dst + C::kLowOff, low + place * 8192, 8192, b);
+    int r = 0, slot = 0, round = 0;  // raw pieces so far, the next one's place
+    const uint64_t pol = l2_evict_first_policy();
+    bool ok = true;
+#pragma unroll 1
+    for (int x = x0; ok && x < x1; x += pc.n) {
+      piece_at(c.B, prm.n_mp, T, x, x1, pc);
+      const int n = pc.n;
+      int at0 = -64, places = 0;  // lane k: the place of unit at0 + k
+#pragma unroll 1
+      for (int i = 0; i < 2 * n; ++i) {
+        bool values;
+        const int g = item_of<MT>(i, n, values), u = pc.u0 + g;
+        if (u >= pc.ng) continue;  // the buffer is read by the warps that use it
+        if (!values && g >= at0 + 32) {
+          // (values come one unit behind the keys: keep one)
+          at0 = max(0, g - 1);
+          places = pc.u0 + at0 + lane < pc.ng
+                       ? (int)group_slot(c, prm.pg, pc.b, pc.h, pc.u0 + at0 + lane) : -1;
+        }
+        const int place = __shfl_sync(0xffffffffu, places, (g - at0) & 31);
+        if (round > 0 && !warp_wait(sh, sh.raw_empty[slot], (round - 1) & 1, ns)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0 && !prm.no_issue) {
+          const uint32_t dst = raw_at(slot), b = bar(sh.raw_full[slot]);
+          sh.raw_dead[slot] = place < 0;
+          if (place < 0 || !chk(in_range(place, 1, group_slots(c, prm.pg)) && smem_in(dst, C::kRawBytes), 61)) {
+            if (!values) atomicOr(&c.state[(size_t)pc.b * QS_STATE_WORDS + QS_ST_ERR], QS_DEV_PAGE);
+            mbar_arrive(b);
+          } else {
+            constexpr int kUp = C::kDraft && UB == 2 ? 4096 : 8192;
+            mbar_arrive_expect_tx(b, kUp + (C::kDraft ? 0 : 8192) + 512);
+            const size_t off = (size_t)place * 8192;
+            // (with two pairs of row tiles the other one reads them again)
+            if (prm.n_mp == 1)
+              bulk_g2s_hint(dst + C::kUpOff, (values ? c.v_upper : c.k_upper) + off, kUp, b, pol);
+            else
+              bulk_g2s(dst + C::kUpOff, (values ? c.v_upper : c.k_upper) + off, kUp, b);
+            if (!C::kDraft) {
+              if (prm.n_mp == 1)
+                bulk_g2s_hint(dst + C::kLowOff, (values ? c.v_lower : c.k_lower) + off, 8192, b, pol);
+              else
+                bulk_g2s(dst + C::kLowOff, (values ? c.v_lower : c.k_lower) + off, 8192, b);
+            }
+            bulk_g2s(dst + C::kMetaOff, c.meta + (size_t)place * 512 + (values ? 256 : 0), 512, b);
           }
-          bulk_g2s(dst + C::kMetaOff, c.meta + place * 512 + (values ? 256 : 0), 512, b);
+        }
+        ++r;
+        if (++slot == NR) {
+          slot = 0;
+          ++round;
         }
       }
-      ++r;
     }
     // after a timeout nothing may still land in shared memory when the CTA ends
     // (raw_full completes for every piece that was issued)
     if (*reinterpret_cast<volatile int *>(&sh.abort) && lane == 0 && !prm.no_issue) {
       const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
       for (int k = max(0, r - NR); k < r; ++k)
         while (!mbar_try_wait(bar(sh.raw_full[k % NR]), (k / NR) & 1))
           if (globaltimer_ns() - t0 > ns) break;
     }
   } else if (w == kMmaWarp) {
     // --------------------------------------------------------------- MMAs
-    if (lane == 0) {
-      Seg cur;
-      int n_s[2] = {0, 0}, n_e[2] = {0, 0}, piece = -1;  // S issued; sums handed over; pieces begun
+    // The whole warp goes along, so that addresses and conditions are uniform; one
+    // elected lane issues.
+    {
+      int n_s = 0, n_e = 0, piece = 0;  // bits 0, 1: parities of the streams' S, and of their sums
+      int begun = 0;                    // bits: the stream has handed over sums before
+      Ring<kOpTiles> start;             // the piece's first operand tile
       bool ok = true;
-      auto first_of = [&](int g) {  // g starts a piece / its last unit
-        cur.seek(x0 + g, T, c.B);
-        return g == 0 || cur.u == 0;
-      };
-      auto last_of = [&](int g) {
-        cur.seek(x0 + g, T, c.B);
-        return g == n - 1 || cur.u == cur.len - 1;
-      };
-      auto same_piece = [&](int g, int g2) {
-        if (g2 >= n) return false;
-        cur.seek(x0 + g, T, c.B);
-        return x0 + g2 < cur.s0 + cur.len;
-      };
-      auto scores = [&](int s, int g) {
-        const int o = key_item<MT>(g);
-        ok = ok && tall_wait(sh, sh.op_full[o % kOpTiles], (o / kOpTiles) & 1, ns);
-        if (first_of(g) && (MT == 1 || s == 0)) ++piece;
-        if (first_of(g)) ok = ok && tall_wait(sh, sh.q_full, piece & 1, ns);
-        if (!ok) return;
-        tc_after_sync();
-        const uint32_t a = sbase + L::kQOff + (MT == 2 ? s * kTileBytes : 0), b = tile(o);
+      const uint64_t q_desc = operand_desc(sbase + L::kQOff), op_desc = operand_desc(sbase + L::kOpOff);
+#pragma unroll 1
+      for (int x = x0; ok && x < x1; ++piece) {
+        piece_at(c.B, prm.n_mp, T, x, x1, pc);
+        const int n = pc.n, steps = MT == 2 ? 2 * n + 2 : n + 2;
+        x += n;
+        Ring<kOpTiles> rk = start, rv = start;  // the next keys' tile, the next values'
+        rv.add(value_item<MT>(0, n));
+#pragma unroll 1
+        for (int t = 0; t < steps; ++t) {
+          const int s = t & 1, g = MT == 2 ? t >> 1 : t;  // stream; unit whose scores are next
+          const int gv = MT == 2 ? g - 1 : g - 2;         // unit whose values are next
+          if (gv >= 0) {
+            ok = warp_wait(sh, sh.p_full[s], ((n_s >> s) & 1) ^ 1, ns) &&
+                 warp_wait(sh, sh.op_full[rv.slot], rv.par, ns);
+            const bool first = MT == 2 ? gv == 0 : gv < 2;
+            if (ok && first && (begun >> s & 1)) ok = warp_wait(sh, sh.o_empty[s], ((n_e >> s) & 1) ^ 1, ns);
+            if (!ok) break;
+            tc_after_sync();
+            const uint64_t b = op_desc + rv.slot * (kTileBytes >> 4);
+            const bool last = MT == 2 ? gv == n - 1 : gv >= n - 2;  // the stream's last unit here
+            if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t off = (k >> 2) * (kTile * 128) + (k & 3) * 32;
-          mma_ss(tmem + 128 * s, operand_desc(a + off), operand_desc(b + off), k > 0);
-        }
-        mma_commit(bar(sh.s_full[s]));
-        if (MT == 1 || s == 1) {
-          mma_commit(bar(sh.op_empty[o % kOpTiles]));
-          if (last_of(g)) mma_commit(bar(sh.q_empty));
-        }
-        ++n_s[s];
-      };
-      // first: the stream's first unit of a piece (the sums start anew)
-      auto sums = [&](int s, int g, bool first, bool last) {
-        const int o = value_item<MT>(g, n);
-        ok = ok && tall_wait(sh, sh.p_full[s], (n_s[s] - 1) & 1, ns) &&
-             tall_wait(sh, sh.op_full[o % kOpTiles], (o / kOpTiles) & 1, ns);
-        if (first && n_e[s] > 0) ok = ok && tall_wait(sh, sh.o_empty[s], (n_e[s] - 1) & 1, ns);
-        if (!ok) return;
-        tc_after_sync();
-        const uint32_t b = tile(o);
+              for (int k = 0; k < 8; ++k)
+                mma_ts(tmem + 256 + 128 * s, tmem + 128 * s + 8 * k, b + ((k >> 2) * (kTile * 8) + (k & 3) * 2),
+                       !first || k > 0);
+              if (MT == 1 || s == 1) mma_commit(bar(sh.op_empty[rv.slot]));
+              if (last) mma_commit(bar(sh.o_full[s]));
+            }
+            __syncwarp();
+            if (MT == 1 || s == 1) rv.add(MT == 1 && gv == n - 2 ? 1 : 2);
+            if (last) {
+              n_e ^= 1 << s;
+              begun |= 1 << s;
+            }
+          }
+          if (g < n) {
+            ok = warp_wait(sh, sh.op_full[rk.slot], rk.par, ns);
+            if (ok && g == 0) ok = warp_wait(sh, sh.q_full, piece & 1, ns);
+            if (!ok) break;
+            tc_after_sync();
+            const uint64_t a = q_desc + (MT == 2 ? s * (kTileBytes >> 4) : 0);
+            const uint64_t b = op_desc + rk.slot * (kTileBytes >> 4);
+            if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ts(tmem + 256 + 128 * s, tmem + 128 * s + 8 * k,
-                 operand_desc(b + (k >> 2) * (kTile * 128) + (k & 3) * 32), !first || k > 0);
-        if (MT == 1 || s == 1) mma_commit(bar(sh.op_empty[o % kOpTiles]));
-        if (last) {
-          mma_commit(bar(sh.o_full[s]));
-          ++n_e[s];
-        }
-      };
-      if (MT == 2) {
-        scores(0, 0);
-        scores(1, 0);
-        for (int g = 0; ok && g < n; ++g) {
-          const bool f = first_of(g), l = last_of(g);
-          for (int s = 0; s < 2; ++s) {
-            sums(s, g, f, l);
-            if (g + 1 < n) scores(s, g + 1);
+              for (int k = 0; k < 8; ++k) {
+                const uint32_t off = (k >> 2) * (kTile * 8) + (k & 3) * 2;  // (in units of 16 bytes)
+                mma_ss(tmem + 128 * s, a + off, b + off, k > 0);
+              }
+              mma_commit(bar(sh.s_full[s]));
+              if (MT == 1 || s == 1) {
+                mma_commit(bar(sh.op_empty[rk.slot]));
+                if (g == n - 1) mma_commit(bar(sh.q_empty));
+              }
+            }
+            __syncwarp();
+            n_s ^= 1 << s;
+            if (MT == 1 || s == 1) rk.add(MT == 1 && g == 0 ? 1 : 2);
           }
         }
-      } else {
-        scores(0, 0);
-        if (n > 1) scores(1, 1);
-        for (int g = 0; ok && g < n; ++g) {
-          cur.seek(x0 + g, T, c.B);
-          const bool f = g < 2 || x0 + g - 2 < cur.s0, l = !same_piece(g, g + 2);
-          sums(g & 1, g, f, l);
-          if (g + 2 < n) scores(g & 1, g + 2);
-        }
+        start.add_any(2 * n);
       }
       // no MMA may be in flight when the CTA gives its tensor memory back
-      mma_commit(bar(sh.drain));
+      if (elect_one()) mma_commit(bar(sh.drain));
+      __syncwarp();
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_try_wait(bar(sh.drain), 0))
         if (globaltimer_ns() - t0 > ns) break;
@@ -543,188 +699,143 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const TallParams 
     __syncwarp();
   } else if (w >= kSoftWarps) {
     // ----------------------------------------------------- operand tiles
-    const int dw = w - kSoftWarps, dt = dw * 32 + lane;
-    Seg cur;
-    int r = 0, piece = -1;
-    for (int o = 0; o < 2 * n; ++o) {
-      int g;
-      bool values;
-      item_of<MT>(o, n, g, values);
-      cur.seek(x0 + g, T, c.B);
-      const int h = cur.h / prm.n_mp, mp = cur.h % prm.n_mp, ng = T.ng[cur.b];
-      const size_t bh = (size_t)cur.b * c.H + h;
-      if (!values && (g == 0 || cur.u == 0)) {
-        // a piece begins: its queries, once no MMA reads the last piece's any more
-        ++piece;
-        if (piece > 0 && !warp_wait(sh, sh.q_empty, (piece - 1) & 1, ns)) break;
-        // (an entry that no warp here can have reached again, nor the softmax
-        // still reads: each is within three pieces of this one)
-        if (dt == 0) sh.bad[(piece + 4) & 7] = 0;
-        const uint4 *src = reinterpret_cast<const uint4 *>(prm.q + bh * prm.R * kD);
+    const bool values = w >= kSoftWarps + kDeqWarps;
+    const int dw = (w - kSoftWarps) & (kDeqWarps - 1), dt = dw * 32 + lane;
+    Ring<kOpTiles> start;
+    Ring<NR> raw_start;
+    int piece = 0, unit0 = 0, o0 = 0;
+    bool ok = true;
 #pragma unroll 1
-        for (int i0 = dt; i0 < MT * kTile * 16; i0 += 4 * 32 * kDeqWarps) {
-          uint4 x[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int i = i0 + k * 32 * kDeqWarps, row = mp * 2 * kTile + (i >> 4);
-            x[k] = row < prm.R ? src[(size_t)row * 16 + (i & 15)] : make_uint4(0, 0, 0, 0);
+    for (int x = x0; ok && x < x1; ++piece) {
+      piece_at(c.B, prm.n_mp, T, x, x1, pc);
+      const int n = pc.n, n_grp = min(n, max(0, pc.ng - pc.u0));  // units; groups among them
+      const size_t bh = (size_t)pc.b * c.H + pc.h;
+      x += n;
+      if (!values) {
+        // the piece's queries, once no MMA reads the last one's any more
+        if (piece > 0 && !warp_wait(sh, sh.q_empty, (piece - 1) & 1, ns)) break;
+        query_tiles<MT>(reinterpret_cast<const uint4 *>(prm.q + bh * prm.R * kD), pc.mp * 2 * kTile, prm.R,
+                        sbase + L::kQOff, dt);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh.q_full));
+      } else if (dt == 0) {
+        // (an entry that no warp here can have reached again, nor the softmax still
+        // reads: each is within three pieces of this one)
+        sh.bad[(piece + 4) & 7] = 0;
+      }
+      Ring<kOpTiles> op = start;
+      Ring<NR> raw = raw_start;
+      if (values) {
+        op.add(value_item<MT>(0, n));
+        raw.add(value_item<MT>(0, n_grp));
+      }
+      int o = o0 + (values ? value_item<MT>(0, n) : 0);  // operand tiles before this one
+#pragma unroll 1
+      for (int g = 0; g < n; ++g) {
+        if (o >= kOpTiles && !warp_wait(sh, sh.op_empty[op.slot], op.par ^ 1, ns)) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = tile(op.slot);
+        if (g < n_grp) {
+          if (!warp_wait(sh, sh.raw_full[raw.slot], raw.par, ns)) {
+            ok = false;
+            break;
           }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int i = i0 + k * 32 * kDeqWarps, row = i >> 4;
-            sts_permuted(tile_at(sbase + L::kQOff + (row / kTile) * kTileBytes, row % kTile, i & 15), x[k]);
+          const bool dead = *reinterpret_cast<volatile int *>(&sh.raw_dead[raw.slot]) != 0;
+          if (dead) {  // a group that is left out: nothing that could disturb the sums
+#pragma unroll 1
+            for (int k = dt; k < kTileBytes / 16; k += 32 * kDeqWarps) sts128(dst + 16 * k, 0, 0, 0, 0);
+          } else if (values) {
+            values_tile<MODE, UB>(raw_at(raw.slot), dst, dw, lane);
+          } else {
+            keys_tile<MODE, UB>(raw_at(raw.slot), dst, dw, lane);
+          }
+          if (!values && dt == 0) *reinterpret_cast<volatile int *>(&sh.dead[(unit0 + g) % kFlags]) = dead;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(sh.raw_empty[raw.slot]));
+          raw.add(values ? (MT == 1 && g == n_grp - 2 ? 1 : 2) : (MT == 1 && g == 0 ? 1 : 2));
+        } else {
+          const int i0 = (pc.u0 + g - pc.ng) * kTile, base = pc.hb * kG + i0;
+          const size_t row0 = bh * kRing * 16;
+          if (!values) {
+            buffer_keys_tile(reinterpret_cast<const uint4 *>(c.buf_k) + row0, base, i0, pc.fill, dst, dt);
+          } else {
+            const uint64_t bad = buffer_values_tile(reinterpret_cast<const uint4 *>(c.buf_v) + row0, base, i0,
+                                                    pc.fill, pc.fill - prm.n_tree, dst, dt);
+            if (bad) atomicOr(reinterpret_cast<unsigned long long *>(&sh.bad[piece & 7]), bad);
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(sh.q_full));
+        if (lane == 0) mbar_arrive(bar(sh.op_full[op.slot]));
+        const int by = values ? (MT == 1 && g == n - 2 ? 1 : 2) : (MT == 1 && g == 0 ? 1 : 2);
+        op.add(by);
+        o += by;
       }
-      if (o >= kOpTiles && !warp_wait(sh, sh.op_empty[o % kOpTiles], (o / kOpTiles - 1) & 1, ns)) break;
-      const uint32_t dst = tile(o);
-      if (cur.u < ng) {
-        if (!warp_wait(sh, sh.raw_full[r % NR], (r / NR) & 1, ns)) break;
-        const bool dead = *reinterpret_cast<volatile int *>(&sh.raw_dead[r % NR]) != 0;
-        if (dead) {  // a group that is left out: nothing that could disturb the sums
-#pragma unroll 1
-          for (int i = dt; i < kTileBytes / 16; i += 32 * kDeqWarps) sts128(dst + 16 * i, 0, 0, 0, 0);
-        } else if (values) {
-          values_tile<MODE, UB>(raw_at(r), dst, dw, lane);
-        } else {
-          keys_tile<MODE, UB>(raw_at(r), dst, dw, lane);
-        }
-        if (!values && dt == 0) *reinterpret_cast<volatile int *>(&sh.dead[g % kFlags]) = dead;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(sh.raw_empty[r % NR]));
-        ++r;
-      } else {
-        const int i0 = (cur.u - ng) * kTile, fill = T.fill[cur.b], tree0 = fill - prm.n_tree;
-        const size_t row0 = bh * kRing;
-        const int base = T.hb[cur.b] * kG + i0;
-        if (!values) {
-          const uint4 *src = reinterpret_cast<const uint4 *>(c.buf_k);
-          uint4 x[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int t = (dt >> 4) + 16 * k;
-            x[k] = i0 + t < fill ? src[(row0 + ((base + t) & (kRing - 1))) * 16 + (dt & 15)] : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) sts_permuted(tile_at(dst, (dt >> 4) + 16 * k, dt & 15), x[k]);
-          if (dt == 0) *reinterpret_cast<volatile int *>(&sh.dead[g % kFlags]) = 0;
-        } else {
-          // eight tokens of eight channels per thread, turned in registers
-          const int tc = (dt & 7) | ((dt >> 4) & 8), dc = (dt >> 3) & 15;
-          const uint4 *src = reinterpret_cast<const uint4 *>(c.buf_v);
-          // (MT = 1: the next unit's keys come before these values)
-          const int of = MT == 1 && g + 1 < n && cur.u == cur.len - 1 ? piece - 1 : piece;
-          uint4 x[8];
-          uint64_t bad = 0;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int t = 8 * tc + k;
-            x[k] = i0 + t < fill ? src[(row0 + ((base + t) & (kRing - 1))) * 16 + dc] : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            // a node's values meet the zero weights of rows that do not see it
-            const int j = i0 + 8 * tc + k - tree0;
-            if (j < 0) continue;
-            unsigned f = drop_nonfinite(x[k].x);
-            f |= drop_nonfinite(x[k].y);
-            f |= drop_nonfinite(x[k].z);
-            f |= drop_nonfinite(x[k].w);
-            if (f) bad |= 1ull << (j & 63);
-          }
-          if (bad) atomicOr(reinterpret_cast<unsigned long long *>(&sh.bad[of & 7]), bad);
-          const uint32_t *xs = reinterpret_cast<const uint32_t *>(x);
-#pragma unroll
-          for (int d = 0; d < 8; ++d) {
-            const uint32_t sel = d & 1 ? 0x7632 : 0x5410;
-            const int k = d >> 1;
-            sts128(tile_at(dst, 8 * dc + d, tc), prmt(xs[k], xs[4 + k], sel), prmt(xs[8 + k], xs[12 + k], sel),
-                   prmt(xs[16 + k], xs[20 + k], sel), prmt(xs[24 + k], xs[28 + k], sel));
-          }
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(sh.op_full[o % kOpTiles]));
+      start.add_any(2 * n);
+      raw_start.add_any(2 * n_grp);
+      o0 += 2 * n;
+      unit0 += n;
     }
   } else {
     // ------------------------------------------------------------ softmax
     const int s = w >> 2, lanes = 32 * (w & 3), row_t = lanes + lane;  // stream; row in the tile
     const uint32_t t_s = tmem + 128 * s + ((uint32_t)lanes << 16);
     const uint32_t t_o = tmem + 256 + 128 * s + ((uint32_t)lanes << 16);
-    int n_s = 0, n_e = 0;
+    int n_s = 0, n_e = 0, unit0 = 0;
     bool ok = true;
-    Seg cur;
-    for (int x = x0, piece = 0; ok && x < x1; ++piece) {
-      cur.seek(x, T, c.B);
-      const int end = min(x1, cur.s0 + cur.len), b = cur.b, mp = cur.h % prm.n_mp, ng = T.ng[b];
-      const int fill = T.fill[b], tree0 = fill - prm.n_tree;
-      const int row = 2 * kTile * mp + (MT == 2 ? s * kTile : 0) + row_t;
+#pragma unroll 1
+    for (int x = x0, piece = 0; ok && x < x1; x += pc.n, ++piece) {
+      piece_at(c.B, prm.n_mp, T, x, x1, pc);
+      const int n = pc.n;
+      const int row = 2 * kTile * pc.mp + (MT == 2 ? s * kTile : 0) + row_t;
       const bool live_warp = row - lane < prm.R;
       uint64_t sees = 0;
-      bool known = false;
+      if (pc.u0 + n > pc.ng && live_warp) {  // the buffer: the nodes that this row sees
+        uint64_t mm[2];
+        bool bad = false;
+        tree_ancestors(prm.parent + (size_t)pc.b * prm.n_tree, prm.n_tree, lane, mm, bad);
+        if (bad) atomicOr(&c.state[(size_t)pc.b * QS_STATE_WORDS + QS_ST_ERR], QS_DEV_TREE);
+        sees = ancestors_of(mm, prm.n_tree - prm.n_q + row % prm.n_q);
+      }
       float m = -INFINITY, l = 0.f;
       int done = 0;
       // the stream's units of the piece
-      for (int y = MT == 2 ? x : x + ((x - x0 + s) & 1); ok && y < end; y += MT == 2 ? 1 : 2) {
-        const int u = y - cur.s0;
-        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-        if (u >= ng) {  // the buffer: which of the 128 tokens this row sees
-          if (!known) {
-            uint64_t mm[2];
-            bool bad = false;
-            tree_ancestors(prm.parent + (size_t)b * prm.n_tree, prm.n_tree, lane, mm, bad);
-            if (bad) atomicOr(&c.state[(size_t)b * QS_STATE_WORDS + QS_ST_ERR], QS_DEV_TREE);
-            sees = ancestors_of(mm, prm.n_tree - prm.n_q + row % prm.n_q);
-            known = true;
-          }
-          const int i0 = (u - ng) * kTile;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int i = i0 + 32 * k, before = tree0 - i;  // tokens of the word in front of the tree
-            uint32_t v = before >= 32 ? ~0u : before <= 0 ? 0u : (1u << before) - 1;
-            if (before < 32) {
-              const uint64_t node = before >= 0 ? sees << before : -before < 64 ? sees >> -before : 0;
-              v |= (uint32_t)node;
-            }
-            const int have = fill - i;
-            if (have < 32) v &= have <= 0 ? 0u : (1u << have) - 1;
-            vis[k] = v;
-          }
-        }
+#pragma unroll 1
+      for (int g = MT == 2 ? 0 : s; g < n; g += MT == 2 ? 1 : 2) {
+        const int u = pc.u0 + g;
         ok = warp_wait(sh, sh.s_full[s], n_s & 1, ns);
         if (!ok) break;
         ++n_s;
         tc_after_sync();
         if (live_warp) {
-          if (u < ng && *reinterpret_cast<volatile int *>(&sh.dead[(y - x0) % kFlags]))
-            vis[0] = vis[1] = vis[2] = vis[3] = 0;
-          const bool masked = (vis[0] & vis[1] & vis[2] & vis[3]) != ~0u;
+          const bool dead = u < pc.ng && *reinterpret_cast<volatile int *>(&sh.dead[(unit0 + g) % kFlags]);
+          if (dead || u >= pc.ng)
+            mask_scores(t_s, (u - pc.ng) * kTile, pc.fill, pc.fill - prm.n_tree, sees, dead);
           uint32_t v[32];
           float mx = -INFINITY;
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < 4; ++k) {
             tc_ld32(t_s + 32 * k, v);
-            if (masked) {
+            float a = __uint_as_float(v[0]), e = __uint_as_float(v[1]);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) mx = fmaxf(mx, vis[k] >> i & 1 ? __uint_as_float(v[i]) : -INFINITY);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(v[i]));
+            for (int i = 2; i < 32; i += 2) {
+              a = fmaxf(a, __uint_as_float(v[i]));
+              e = fmaxf(e, __uint_as_float(v[i + 1]));
             }
+            mx = fmaxf(mx, fmaxf(a, e));
           }
           const float mn = mx * prm.sl2;
           const bool raise = mn > m + kRaise || (m == -INFINITY && mn > -INFINITY);
           if (__any_sync(0xffffffffu, raise)) {
             const float a = raise ? (m == -INFINITY ? 0.f : fast_exp2(m - mn)) : 1.f;
             if (done > 0) {
-#pragma unroll
+#pragma unroll 1
               for (int k = 0; k < 4; ++k) {
                 tc_ld32(t_o + 32 * k, v);
-    #pragma unroll
+#pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a);
                 tc_st32(t_o + 32 * k, v);
               }
@@ -733,23 +844,20 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const TallParams 
             if (raise) m = mn;
           }
           const float off = m == -INFINITY ? 0.f : kExpShift - m;
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < 4; ++k) {
             tc_ld32(t_s + 32 * k, v);
             uint32_t ph[16];
-            float sum = 0.f;
+            float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              float a = fast_exp2(fmaf(__uint_as_float(v[2 * i]), prm.sl2, off));
-              float e = fast_exp2(fmaf(__uint_as_float(v[2 * i + 1]), prm.sl2, off));
-              if (masked) {
-                if (!(vis[k] >> (2 * i) & 1)) a = 0.f;
-                if (!(vis[k] >> (2 * i + 1) & 1)) e = 0.f;
-              }
-              sum += a + e;
+              const float a = fast_exp2(fmaf(__uint_as_float(v[2 * i]), prm.sl2, off));
+              const float e = fast_exp2(fmaf(__uint_as_float(v[2 * i + 1]), prm.sl2, off));
+              sum0 += a;
+              sum1 += e;
               ph[i] = pack_half2(a, e);
             }
-            l += sum;
+            l += sum0 + sum1;
             tc_st16(t_s + 16 * k, ph);
           }
           tc_wait_st();
@@ -761,7 +869,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const TallParams 
       }
       if (!ok) break;
       // the piece's partial: rows side by side, four channels each
-      float *part = prm.ws + ((size_t)(cur.ord + p) * 2 + s) * prm.rows * (kD + 2);
+      float *part = prm.ws + ((size_t)(pc.ord + p) * 2 + s) * prm.rows * (kD + 2);
       const bool mine = live_warp && row < prm.R &&
                         chk(in_range((size_t)(part - prm.ws), (size_t)prm.rows * (kD + 2), prm.ws_floats), 62);
       if (done > 0) {
@@ -770,9 +878,9 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const TallParams 
         ++n_e;
         tc_after_sync();
         if (live_warp) {
-          if (known && (sees & *reinterpret_cast<volatile uint64_t *>(&sh.bad[piece & 7]))) l = NAN;
+          if (sees & *reinterpret_cast<volatile uint64_t *>(&sh.bad[piece & 7])) l = NAN;
           const float poison = l == l ? 0.f : NAN;
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < 4; ++k) {
             uint32_t v[32];
             tc_ld32(t_o + 32 * k, v);
@@ -792,7 +900,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const TallParams 
         part[prm.rows * kD + row_t] = m;
         part[prm.rows * (kD + 1) + row_t] = l;
       }
-      x = end;
+      unit0 += n;
     }
   }
   __syncthreads();
