@@ -24,7 +24,7 @@ QS_PAGED = 0x100
 ST_N_GROUPS, ST_FILL, ST_PENDING, ST_HALF_BASE, ST_ERR, ST_TICKET = range(6)
 STATE_WORDS = 8
 QS_FP16, QS_BF16, QS_FP32 = range(3)
-QS_MAX_TREE, QS_MAX_VOCAB = 64, 393216
+QS_MAX_TREE, QS_MAX_VOCAB = 64, 368640
 META_K_SCALE, META_K_ZERO, META_V_SCALE, META_V_ZERO = range(4)
 
 _P = ctypes.c_void_p

@@ -595,7 +595,7 @@ qs_status qs_tree_accept(const qs_cache *c, const int32_t *parent, const int32_t
 typedef enum { QS_FP16 = 0, QS_BF16 = 1, QS_FP32 = 2 } qs_dtype;
 
 /* Largest vocabulary of qs_sample. */
-#define QS_MAX_VOCAB 393216
+#define QS_MAX_VOCAB 368640
 
 /* A token for each row of logits, and the probabilities it is drawn from.
  *   logits  [rows][V] of the given type, row r at logits + r * row_stride elements
