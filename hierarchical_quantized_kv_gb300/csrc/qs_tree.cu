@@ -26,7 +26,7 @@ struct RotArgs {
   const int32_t *offset;
   const float *inv_freq;
   int hq, n_new, rot, inter;
-  int tokens, splits;  // tokens per CTA; CTAs that share a token tile's rows
+  int log_tokens, splits;  // tokens per CTA, as a power of 2; CTAs that share a tile's rows
 };
 
 // p * inv_freq in turns without loss: a turn is 2^64, so the product by the
@@ -37,82 +37,86 @@ __device__ __forceinline__ unsigned long long turns(float inv_freq) {
   return (unsigned long long)((t - floor(t)) * 18446744073709551616.0);
 }
 
-// Eight pairs (x_i, y_i): x cos - y sin, y cos + x sin.
-__device__ __forceinline__ void turn(uint4 &a, uint4 &b, const float2 *cs, bool inter) {
-  uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  if (inter) {  // a pair a word
+// Four neighbouring pairs (x, y) of a vector, a pair a word: x cos - y sin, y cos + x sin.
+__device__ __forceinline__ void turn_neighbours(uint4 &a, const float2 *cs) {
+  uint32_t x[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 v = __half22float2(u32_as_h2(x[i])), t = cs[i];
-      x[i] = pack_half2(v.x * t.x - v.y * t.y, v.y * t.x + v.x * t.y);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 u = __half22float2(u32_as_h2(x[i])), v = __half22float2(u32_as_h2(x[4 + i]));
-      const float2 t0 = cs[2 * i], t1 = cs[2 * i + 1];
-      x[i] = pack_half2(u.x * t0.x - v.x * t0.y, u.y * t1.x - v.y * t1.y);
-      x[4 + i] = pack_half2(v.x * t0.x + u.x * t0.y, v.y * t1.x + u.y * t1.y);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = __half22float2(u32_as_h2(x[i])), t = cs[i];
+    x[i] = pack_half2(v.x * t.x - v.y * t.y, v.y * t.x + v.x * t.y);
   }
   a = make_uint4(x[0], x[1], x[2], x[3]);
-  b = make_uint4(x[4], x[5], x[6], x[7]);
+}
+// Eight pairs whose halves lie in two vectors.
+__device__ __forceinline__ void turn_halves(uint4 &a, uint4 &b, const float2 *cs) {
+  uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 u = __half22float2(u32_as_h2(x[i])), v = __half22float2(u32_as_h2(y[i]));
+    const float2 t0 = cs[2 * i], t1 = cs[2 * i + 1];
+    x[i] = pack_half2(u.x * t0.x - v.x * t0.y, u.y * t1.x - v.y * t1.y);
+    y[i] = pack_half2(v.x * t0.x + u.x * t0.y, v.y * t1.x + u.y * t1.y);
+  }
+  a = make_uint4(x[0], x[1], x[2], x[3]);
+  b = make_uint4(y[0], y[1], y[2], y[3]);
 }
 
-// CTA (tile, split, sequence): up to kRotTokens tokens of the sequence, and every
+// CTA (tile, split, sequence): 1 << a.log_tokens tokens of the sequence, and every
 // splits-th part of their H + H + hq rows (keys, values, queries).  An item is two
-// 16-byte vectors of a row, eight items a row: a pair of vectors that turn
-// together, or two that stay.  The CTA's angles go through shared memory, so
-// their sines are formed once for all heads.
+// 16-byte vectors of a row, eight items a row, whose lanes' vectors lie side by side:
+// a pair of vectors that turn together, or two on their own.  The CTA's angles go
+// through shared memory, so their sines are formed once for all heads.
+template <bool INTER>
 __global__ void __launch_bounds__(kRotThreads) append_rotary_kernel(const RotArgs a) {
   __shared__ float2 s_cs[kRotTokens * kMaxHalf];
+  __shared__ unsigned long long s_turns[kMaxHalf];
   const qs_cache &c = a.c;
-  const int b = blockIdx.z, j0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.n_new - j0);
+  const int b = blockIdx.z, j0 = blockIdx.x << a.log_tokens, nt = min(1 << a.log_tokens, a.n_new - j0);
+  const int half = a.rot / 2;
   pdl_trigger();
   pdl_wait();
   int32_t *st = c.state + (size_t)b * QS_STATE_WORDS;
   const int ng = st[QS_ST_N_GROUPS], fill = st[QS_ST_FILL], pending = st[QS_ST_PENDING];
   const int base = st[QS_ST_HALF_BASE] & 1;
+  if (threadIdx.x < half) s_turns[threadIdx.x] = turns(a.inv_freq[threadIdx.x]);
   const bool room = fill >= 0 && fill + a.n_new <= kRing;
-  const int half = a.rot / 2;
-  for (int i = threadIdx.x; i < nt * half; i += kRotThreads) {
-    const int j = i / half, f = i % half;
-    const int pos = ng * kG + fill +
-                    (a.offset ? a.offset[(size_t)b * a.n_new + j0 + j] - pending : j0 + j);
+  __syncthreads();
+  for (int i = threadIdx.x; i < nt * kMaxHalf; i += kRotThreads) {
+    const int j = i / kMaxHalf, f = i % kMaxHalf;
+    if (f >= half) continue;
+    const int pos = ng * kG + fill + (a.offset ? a.offset[(size_t)b * a.n_new + j0 + j] - pending : j0 + j);
     // the signed fraction of a turn, in half turns
-    const long long p = (long long)((unsigned long long)(long long)pos * turns(a.inv_freq[f]));
+    const long long p = (long long)((unsigned long long)(long long)pos * s_turns[f]);
     float2 cs;
     sincospif((float)(int)(p >> 32) * 4.656612873077393e-10f, &cs.y, &cs.x);
-    s_cs[j * kMaxHalf + f] = cs;
+    s_cs[i] = cs;
   }
   __syncthreads();
   const int rows = 2 * c.H + a.hq, per = (rows + a.splits - 1) / a.splits;
   const int r0 = blockIdx.y * per, r1 = min(rows, r0 + per);
-  const int n_items = (r1 - r0) * nt * 8;
+  const int n_items = (r1 - r0) << (a.log_tokens + 3);
+  const int turning = INTER ? 0 : a.rot / 16;  // items of a row whose vectors turn together
   constexpr int U = 4;  // items in flight per thread
+#pragma unroll 1
   for (int e0 = threadIdx.x; e0 < n_items; e0 += U * kRotThreads) {
     uint4 x[U], y[U];
     uint4 *dst[U];
-    int vx[U], vy[U], tj[U];
+    const int i = e0 & 7;  // (the same for all U)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int e = e0 + u * kRotThreads;
+      const int j = (e >> 3) & ((1 << a.log_tokens) - 1), row = r0 + (e >> (a.log_tokens + 3));
       dst[u] = nullptr;
-      if (e >= n_items) continue;
-      const int i = e & 7, j = (e >> 3) % nt, row = r0 + (e >> 3) / nt;
+      if (e >= n_items || j >= nt) continue;
       const bool is_q = row >= 2 * c.H, is_v = !is_q && row >= c.H;
       const int h = is_q ? row - 2 * c.H : is_v ? row - c.H : row;
       const qs_rows &s = is_q ? a.q : is_v ? a.v : a.k;
-      // item i of a row: the vectors of pairs 8 i .. 8 i + 7 while those turn,
-      // then the rest two by two
-      const bool turns = !is_v && 16 * i < a.rot;
-      vx[u] = turns && !a.inter ? i : 2 * i;
-      vy[u] = turns && !a.inter ? i + a.rot / 16 : 2 * i + 1;
-      tj[u] = turns ? j * kMaxHalf + 8 * i : -1;
+      const bool together = !is_v && i < turning;
+      const int vx = is_v || together ? i : i + turning, vy = together ? i + turning : i + 8;
       const uint4 *src = reinterpret_cast<const uint4 *>(s.data + b * s.stride_b + h * s.stride_h +
                                                          (j0 + j) * s.stride_t);
-      x[u] = src[vx[u]];
-      y[u] = src[vy[u]];
+      x[u] = src[vx];
+      y[u] = src[vy];
       if (is_q) {
         dst[u] = reinterpret_cast<uint4 *>(a.q_out) + (((size_t)b * a.hq + h) * a.n_new + j0 + j) * kVec;
       } else if (room) {
@@ -124,9 +128,18 @@ __global__ void __launch_bounds__(kRotThreads) append_rotary_kernel(const RotArg
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (!dst[u]) continue;
-      if (tj[u] >= 0) turn(x[u], y[u], s_cs + tj[u], a.inter);
-      dst[u][vx[u]] = x[u];
-      dst[u][vy[u]] = y[u];
+      const int e = e0 + u * kRotThreads;
+      const int j = (e >> 3) & ((1 << a.log_tokens) - 1), row = r0 + (e >> (a.log_tokens + 3));
+      const bool is_v = row >= c.H && row < 2 * c.H, together = !is_v && i < turning;
+      const float2 *cs = s_cs + j * kMaxHalf;
+      if (INTER) {
+        if (!is_v && 8 * i < a.rot) turn_neighbours(x[u], cs + 4 * i);
+        if (!is_v && 8 * i + 64 < a.rot) turn_neighbours(y[u], cs + 4 * i + 32);
+      } else if (together) {
+        turn_halves(x[u], y[u], cs + 8 * i);
+      }
+      dst[u][is_v || together ? i : i + turning] = x[u];
+      dst[u][together ? i + turning : i + 8] = y[u];
     }
   }
   if (!room) {
@@ -281,17 +294,20 @@ qs_status qs_buffer_append_rotary(const qs_cache *c, const qs_rows *k, const qs_
       reinterpret_cast<uintptr_t>(offset) % 4)
     return QS_ERR_ALIGN;
   RotArgs a = {*c, *k, *v, q ? *q : none, q_out, offset, inv_freq, q ? c->H * group : 0, n_new, rot,
-               interleaved != 0, 1, 1};
+               interleaved != 0, 0, 1};
   const long long n_rows = 2ll * c->H + a.hq;
-  a.tokens = n_new < kRotTokens ? n_new : kRotTokens;
   int sms = 0;
   if ((s = sm_count(&sms)) != QS_OK) return s;
-  const long long tiles = (long long)((n_new + a.tokens - 1) / a.tokens) * c->B;
-  // few token tiles: their rows split over CTAs, 32 items of 8 lanes each at least
-  long long split = (2ll * sms + tiles - 1) / tiles, most = (n_rows * a.tokens + 31) / 32;
+  // four tokens to a CTA, fewer where that leaves SMs without one; then their rows over
+  // several CTAs, 32 items (of 8 lanes) each at least
+  a.log_tokens = 2;
+  const auto tiles = [&] { return (long long)((n_new + (1 << a.log_tokens) - 1) >> a.log_tokens) * c->B; };
+  while (a.log_tokens > 0 && tiles() < sms) --a.log_tokens;
+  long long split = (2ll * sms + tiles() - 1) / tiles(), most = ((n_rows << a.log_tokens) + 31) / 32;
   if (split > most) split = most;
   a.splits = (int)(split < 1 ? 1 : split > 65535 ? 65535 : split);
-  return launch_pdl(append_rotary_kernel, dim3((n_new + a.tokens - 1) / a.tokens, a.splits, c->B),
+  const dim3 grid((n_new + (1 << a.log_tokens) - 1) >> a.log_tokens, a.splits, c->B);
+  return launch_pdl(a.inter ? append_rotary_kernel<true> : append_rotary_kernel<false>, grid,
                     dim3(kRotThreads), 0, (cudaStream_t)stream, a);
 }
 

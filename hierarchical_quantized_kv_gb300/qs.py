@@ -103,9 +103,8 @@ _SIGS = {
                                  ctypes.c_float, _P, _P, _P],
     "qs_attn_decode_append": [ctypes.POINTER(QsCacheStruct), ctypes.c_int, _P, _P, _I32, _P, _I32,
                               _I32, ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P],
-    "qs_buffer_append_rotary": [ctypes.POINTER(QsCacheStruct), ctypes.POINTER(QsRowsStruct),
-                                ctypes.POINTER(QsRowsStruct), ctypes.POINTER(QsRowsStruct), _P, _I32,
-                                _I32, _P, _P, _I32, _I32, _P],
+    "qs_buffer_append_rotary": [ctypes.POINTER(QsCacheStruct), _P, _P, _P, _P, _I32, _I32, _P, _P, _I32,
+                                _I32, _P],
     "qs_attn_tree_workspace_size": [ctypes.POINTER(QsCacheStruct), _I32, _I32,
                                     ctypes.POINTER(ctypes.c_size_t)],
     "qs_attn_decode_tree": [ctypes.POINTER(QsCacheStruct), ctypes.POINTER(QsPagesStruct), ctypes.c_int,
@@ -524,9 +523,17 @@ def qs_attn_decode_sparse(cache, mode, sel, q, softmax_scale, out, lse=None, wor
 
 # ------------------------------------- a round over a tree of drafted tokens
 
+_get_device = None
+
+
 def _current_device():
-    import torch
-    return torch.cuda.current_device()
+    global _get_device
+    if _get_device is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getDevice", None)
+        torch.cuda.init()
+        _get_device = raw or torch.cuda.current_device
+    return _get_device()
 
 
 def _check_device(dev):
@@ -535,18 +542,21 @@ def _check_device(dev):
         raise QsArgumentError("the tensors lie on cuda:%d, which is not the current device" % dev)
 
 
-def _rows_struct(cache, t, name, heads, n):
-    """fp16 [B, heads, n, D] with any strides, the last one 1."""
+def _rows(cache, t, name, heads, n):
+    """The numbers of a qs_rows: fp16 [B, heads, n, D] with any strides, the last
+    one 1."""
     shape = t.shape
-    if not (len(shape) == 4 and shape[0] == cache.B and shape[1] == heads and shape[2] == n and
-            shape[3] == cache.D and t.dtype is cache._f16 and t.get_device() == cache._dev):
+    if shape != (cache.B, heads, n, cache.D) or t.dtype is not cache._f16 or t.get_device() != cache._dev:
         raise QsArgumentError("%s: float16 [%d, %d, %d, %d] on the cache's device"
                               % (name, cache.B, heads, n, cache.D))
-    s = t.stride()
-    if s[3] != 1:
+    b, h, t_, d = t.stride()
+    if d != 1:
         raise QsArgumentError("%s: the elements of a row lie side by side" % name)
     # (the stride of a dimension of one is of no account)
-    return QsRowsStruct(t.data_ptr(), *(s[i] if shape[i] > 1 else 0 for i in range(3)))
+    return t.data_ptr(), b if cache.B > 1 else 0, h if heads > 1 else 0, t_ if n > 1 else 0
+
+
+_THREE_ROWS = ctypes.c_int64 * 12
 
 
 def qs_buffer_append_rotary(cache, k, v, inv_freq, q=None, q_out=None, offset=None, interleaved=False,
@@ -557,29 +567,29 @@ def qs_buffer_append_rotary(cache, k, v, inv_freq, q=None, q_out=None, offset=No
     float32 [rot / 2]; offset: int32 [B, n] or None."""
     _check_device(cache._dev)
     n = k.shape[2] if k.dim() == 4 else 0
-    ks, vs = _rows_struct(cache, k, "k", cache.H, n), _rows_struct(cache, v, "v", cache.H, n)
-    if (q is None) != (q_out is None):
-        raise QsArgumentError("q and q_out go together")
-    group, q_ref = 1, None
-    if q is not None:
+    group, q_rows = 1, (0, 0, 0, 0)
+    if q is not None and q_out is not None:
         group = q.shape[1] // cache.H if q.dim() == 4 else 0
-        qrows = _rows_struct(cache, q, "q", cache.H * group, n)
-        q_ref = ctypes.byref(qrows)
+        q_rows = _rows(cache, q, "q", cache.H * group, n)
         if q_out.shape != q.shape:
             raise QsArgumentError("q_out: the shape of q")
         _check_f16(cache, q_out, "q_out")
+    elif q is not None or q_out is not None:
+        raise QsArgumentError("q and q_out go together")
+    rows = _THREE_ROWS(*_rows(cache, k, "k", cache.H, n), *_rows(cache, v, "v", cache.H, n), *q_rows)
     if not (inv_freq.dim() == 1 and inv_freq.dtype is cache._f32 and inv_freq.is_contiguous() and
             inv_freq.get_device() == cache._dev):
         raise QsArgumentError("inv_freq: contiguous float32 [rot / 2] on the cache's device")
     if offset is not None:
         _check_i32(cache, offset, "offset", (cache.B, n))
+    at = ctypes.addressof(rows)
     _check("qs_buffer_append_rotary", lib().qs_buffer_append_rotary(
-        cache._ref, ctypes.byref(ks), ctypes.byref(vs), q_ref, _ptr(q_out), group, n, _ptr(offset),
-        _ptr(inv_freq), 2 * inv_freq.shape[0], int(bool(interleaved)), _stream(stream)))
+        cache._ref, at, at + 32, None if q is None else at + 64, _ptr(q_out), group, n, _ptr(offset),
+        _ptr(inv_freq), 2 * inv_freq.shape[0], 1 if interleaved else 0, _stream(stream)))
 
 
 def _check_i32(cache, t, name, shape):
-    if not (tuple(t.shape) == tuple(shape) and t.dtype is cache._i32 and t.is_contiguous() and
+    if not (t.shape == shape and t.dtype is cache._i32 and t.is_contiguous() and
             t.get_device() == cache._dev):
         raise QsArgumentError("%s: contiguous int32 %s on the cache's device" % (name, list(shape)))
 
@@ -619,35 +629,53 @@ def qs_tree_accept(cache, parent, draft, target, n_keep, path, emitted, stream=N
         _ptr(emitted), _stream(stream)))
 
 
+_logit_types = {}
+
+
+def _sample_types():
+    import torch
+    if not _logit_types:
+        _logit_types.update({torch.float16: QS_FP16, torch.bfloat16: QS_BF16, torch.float32: QS_FP32})
+    return torch.float32, torch.int32
+
+
+def _check_row(t, name, dtype, shape, dev):
+    if not (t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev):
+        raise QsArgumentError("%s: contiguous %s %s on the logits' device" % (name, dtype, list(shape)))
+
+
 def qs_sample(logits, u, token, probs=None, temperature=None, top_k=None, top_p=None, min_p=None,
               stream=None):
     """A token (int32 [rows]) for each row of logits, fp16, bf16 or fp32
     [rows, V] with any row stride, by u, float32 [rows]; probs: float32 [rows, V]
     or None; temperature, top_p, min_p: float32 [rows], top_k: int32 [rows], or
     None."""
-    import torch
-    types = {torch.float16: QS_FP16, torch.bfloat16: QS_BF16, torch.float32: QS_FP32}
-    if logits.dim() != 2 or logits.dtype not in types:
+    f32, i32 = _sample_types()
+    kind = _logit_types.get(logits.dtype)
+    if logits.dim() != 2 or kind is None:
         raise QsArgumentError("logits: fp16, bf16 or fp32 [rows, V]")
     rows, V = logits.shape
     dev = logits.get_device()
     if dev < 0:
         raise QsArgumentError("logits: on a CUDA device")
     _check_device(dev)
-    if logits.stride(1) != 1 and V > 1:
+    row, step = logits.stride()
+    if step != 1 and V > 1:
         raise QsArgumentError("logits: the elements of a row lie side by side")
-    for name, t, dtype, shape in (("u", u, torch.float32, (rows,)), ("token", token, torch.int32, (rows,)),
-                                  ("probs", probs, torch.float32, (rows, V)),
-                                  ("temperature", temperature, torch.float32, (rows,)),
-                                  ("top_k", top_k, torch.int32, (rows,)),
-                                  ("top_p", top_p, torch.float32, (rows,)),
-                                  ("min_p", min_p, torch.float32, (rows,))):
-        if t is None and name not in ("u", "token"):
-            continue
-        if not (t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev):
-            raise QsArgumentError("%s: contiguous %s %s on the logits' device" % (name, dtype, list(shape)))
+    _check_row(u, "u", f32, (rows,), dev)
+    _check_row(token, "token", i32, (rows,), dev)
+    if probs is not None:
+        _check_row(probs, "probs", f32, (rows, V), dev)
+    if temperature is not None:
+        _check_row(temperature, "temperature", f32, (rows,), dev)
+    if top_k is not None:
+        _check_row(top_k, "top_k", i32, (rows,), dev)
+    if top_p is not None:
+        _check_row(top_p, "top_p", f32, (rows,), dev)
+    if min_p is not None:
+        _check_row(min_p, "min_p", f32, (rows,), dev)
     _check("qs_sample", lib().qs_sample(
-        _ptr(logits), types[logits.dtype], rows, V, logits.stride(0) if rows > 1 else V,
+        _ptr(logits), kind, rows, V, row if rows > 1 else V,
         _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(token), _ptr(probs),
         _stream(stream)))
 

@@ -199,13 +199,9 @@ def test_rows_of_any_strides_reach_the_library():
     the strides that the library is told."""
     c = qs.PagedCache(B, H, 4, 5, device="cpu")
     x = half(B, N, 4 * H, 128).transpose(1, 2)
-    r = qs._rows_struct(c, x[:, H:2 * H], "k", H, N)
-    assert (r.data, r.stride_b, r.stride_h, r.stride_t) == (x.data_ptr() + H * 256, N * 4 * H * 128, 128,
-                                                            4 * H * 128)
-    r = qs._rows_struct(c, half(B, 1, N, 128).expand(B, H, N, 128), "k", H, N)
-    assert (r.stride_h, r.stride_t) == (0, 128)
-    r = qs._rows_struct(c, half(B, H, 1, 128), "k", H, 1)
-    assert (r.stride_b, r.stride_h, r.stride_t) == (H * 128, 128, 0)
+    assert qs._rows(c, x[:, H:2 * H], "k", H, N) == (x.data_ptr() + H * 256, N * 4 * H * 128, 128, 4 * H * 128)
+    assert qs._rows(c, half(B, 1, N, 128).expand(B, H, N, 128), "k", H, N)[2:] == (0, 128)
+    assert qs._rows(c, half(B, H, 1, 128), "k", H, 1)[1:] == (H * 128, 128, 0)
 
 
 # -------------------------------------------------- the model these tests use
