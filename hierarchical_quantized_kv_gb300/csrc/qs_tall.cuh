@@ -444,6 +444,15 @@ __device__ __noinline__ uint64_t buffer_values_tile(const uint4 *src, int base, 
   return bad;
 }
 
+// The row (of up to 128) that tile row t of stream s stands for with one row tile, or
+// -1: few rows lie there twice, so that the streams' softmax warps (a quarter of the
+// tile's rows each, and with it one of the SM's four schedulers) are not the same.
+__device__ __forceinline__ int one_tile_row(int t, int s, int R) {
+  if (R <= 32) return (t >> 5) == 1 + s ? t & 31 : -1;
+  if (R <= 64) return (t >> 6) == s ? t & 63 : -1;
+  return t;
+}
+
 // A piece's queries into their operand tiles (rows past the last: zeros).
 template <int MT>
 __device__ __noinline__ void query_tiles(const uint4 *src, int row0, int R, uint32_t tiles, int dt) {
@@ -452,8 +461,10 @@ __device__ __noinline__ void query_tiles(const uint4 *src, int row0, int R, uint
     uint4 x[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int i = i0 + k * 32 * kDeqWarps, row = row0 + (i >> 4);
-      x[k] = row < R ? src[(size_t)row * 16 + (i & 15)] : make_uint4(0, 0, 0, 0);
+      const int i = i0 + k * 32 * kDeqWarps;
+      int row = row0 + (i >> 4);
+      if (MT == 1) row = max(one_tile_row(row, 0, R), one_tile_row(row, 1, R));
+      x[k] = row >= 0 && row < R ? src[(size_t)row * 16 + (i & 15)] : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -790,8 +801,10 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
     for (int x = x0, piece = 0; ok && x < x1; x += pc.n, ++piece) {
       piece_at(c.B, prm.n_mp, T, x, x1, pc);
       const int n = pc.n;
-      const int row = 2 * kTile * pc.mp + (MT == 2 ? s * kTile : 0) + row_t;
-      const bool live_warp = row - lane < prm.R;
+      // (row: of the KV head; row_p: in the partial)
+      const int row_p = MT == 2 ? row_t : one_tile_row(row_t, s, prm.R);
+      const int row = MT == 2 ? 2 * kTile * pc.mp + s * kTile + row_t : row_p;
+      const bool live_warp = row >= 0 && row - lane < prm.R;
       uint64_t sees = 0;
       if (pc.u0 + n > pc.ng && live_warp) {  // the buffer: the nodes that this row sees
         uint64_t mm[2];
@@ -887,7 +900,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
             if (mine)
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                reinterpret_cast<float4 *>(part)[(8 * k + i) * prm.rows + row_t] =
+                reinterpret_cast<float4 *>(part)[(8 * k + i) * prm.rows + row_p] =
                     make_float4(__uint_as_float(v[4 * i]) + poison, __uint_as_float(v[4 * i + 1]) + poison,
                                 __uint_as_float(v[4 * i + 2]) + poison, __uint_as_float(v[4 * i + 3]) + poison);
           }
@@ -897,8 +910,8 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
         if (lane == 0) mbar_arrive(bar(sh.o_empty[s]));
       }
       if (mine) {
-        part[prm.rows * kD + row_t] = m;
-        part[prm.rows * (kD + 1) + row_t] = l;
+        part[prm.rows * kD + row_p] = m;
+        part[prm.rows * (kD + 1) + row_p] = l;
       }
       unit0 += n;
     }
