@@ -25,6 +25,13 @@
 //    and values; else they take every other unit.
 //  * S (fp32) and O lie in tensor memory; P replaces S there as fp16 and is the second
 //    product's A operand, so scores never touch shared memory.
+//  * Keys enter the product in two fp16 tiles that add up to them, K = T1 + T2.  Rounded
+//    to fp16 once, a key with a large channel moves its scores by 1e-3 and more, and
+//    the output by as much as six of its own roundings.  With s = s_h + s_l, s_h the top
+//    three bits of the scale, and codes centred on 128, T1 = s_h c' + z_h is exact (a
+//    multiple of the last bit of s_h below 2048 of them) and T2 = s_l c' + z_l, an eighth
+//    of the range at most, is rounded: two fused multiply-adds for a pair instead of
+//    one.  A warp of its own splits the scales and zeros of a group, once.
 //  * The planes' layouts fit: keys are stored by token, channels side by side, and
 //    values by channel, tokens side by side, both K-major as they are.  Within
 //    eight channels the keys' nibbles come out as 0 4 1 5 2 6 3 7; the queries are
@@ -38,10 +45,12 @@ namespace {
 
 constexpr int kTile = 128;                 // rows, tokens and channels of a tile
 constexpr int kTileBytes = kTile * kTile * 2;
-constexpr int kOpTiles = 3;                // operand tiles (keys or values) in the ring
+// Operand tiles in the ring: a unit has three (T1 and T2 of the keys, the values).
+template <int MT>
+constexpr int op_tiles() { return MT == 2 ? 3 : 4; }
 constexpr int kSoftWarps = 8, kDeqWarps = 8;  // (of the latter for keys, and for values)
-constexpr int kMmaWarp = kSoftWarps + 2 * kDeqWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kTallThreads = 32 * (kLoadWarp + 1);
+constexpr int kMmaWarp = kSoftWarps + 2 * kDeqWarps, kLoadWarp = kMmaWarp + 1, kPrepWarp = kMmaWarp + 2;
+constexpr int kTallThreads = 32 * (kPrepWarp + 1);
 constexpr float kRaise = 8.f;              // log2 by which a maximum may be behind
 constexpr int kFlags = 8;                  // units whose flags are kept
 constexpr int kMaxTreeRows = 512;
@@ -51,13 +60,16 @@ template <int MODE>
 struct TallCfg {
   static constexpr bool kDraft = MODE == QS_DRAFT_UPPER4;
   static constexpr int kUpOff = 0, kLowOff = 8192, kMetaOff = kDraft ? 8192 : 16384;
-  static constexpr int kRawBytes = kMetaOff + 512;
+  // scales and zeros as the tiles' makers take them: of keys s_h, s_l, z_h, z_l in the
+  // order of the key codes, of values s and z in the order of the tokens
+  static constexpr int kPrepOff = kMetaOff + 512;
+  static constexpr int kRawBytes = kPrepOff + 1024;
 };
 template <int MODE, int MT>
 struct TallLayout {
   static constexpr int kQOff = 0;
   static constexpr int kOpOff = MT * kTileBytes;
-  static constexpr int kRawOff = kOpOff + kOpTiles * kTileBytes;
+  static constexpr int kRawOff = kOpOff + op_tiles<MT>() * kTileBytes;
   static constexpr int kRest = 227 * 1024 - 1024 - kRawOff - 7 * kMaxB * 4 - 512;
   static constexpr int kRawFit = kRest / TallCfg<MODE>::kRawBytes;
   static constexpr int kRaw = kRawFit < 10 ? kRawFit : 10;
@@ -157,8 +169,8 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&v)[16]) 
 // ------------------------------------------------------- operand conversion
 
 // Eight codes of a word pair as four fp16 pairs (elements j and j + 4), exact: the
-// code goes into the mantissa of 1024 (or 1024 and the draft's midpoint), which is
-// taken off again; then scale and zero in one rounding.
+// code goes into the mantissa of 1024 (with the draft's midpoint), and 1024 and 128 are
+// taken off again.
 template <int MODE>
 __device__ __forceinline__ void code_pairs(uint32_t wu, uint32_t wl, uint32_t (&e)[4]) {
   if (MODE == QS_VERIFY_INT8) {
@@ -185,9 +197,15 @@ __device__ __forceinline__ void code_pairs2(uint32_t x, uint32_t (&e)[4]) {
   e[2] = ((x >> (2 + SH)) & m) | k;
   e[3] = ((x >> (6 + SH)) & m) | k;
 }
-__device__ __forceinline__ uint32_t dequant2(uint32_t e, uint32_t s, uint32_t z) {
-  const __half2 k1024 = __half2half2(__ushort_as_half(0x6400));
-  return h2_as_u32(__hfma2(__hsub2(u32_as_h2(e), k1024), u32_as_h2(s), u32_as_h2(z)));
+// The code less 128, and less nothing.
+__device__ __forceinline__ uint32_t centred(uint32_t e) {
+  return h2_as_u32(__hsub2(u32_as_h2(e), __half2half2(__ushort_as_half(0x6480))));
+}
+__device__ __forceinline__ uint32_t uncentred(uint32_t e) {
+  return h2_as_u32(__hsub2(u32_as_h2(e), __half2half2(__ushort_as_half(0x6400))));
+}
+__device__ __forceinline__ uint32_t fma2(uint32_t e, uint32_t s, uint32_t z) {
+  return h2_as_u32(__hfma2(u32_as_h2(e), u32_as_h2(s), u32_as_h2(z)));
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   if (!chk(smem_in(a, 16), 60)) return;
@@ -202,10 +220,10 @@ __device__ __forceinline__ void sts_permuted(uint32_t a, uint4 x) {
   sts128(a, prmt(x.x, x.z, 0x5410), prmt(x.x, x.z, 0x7632), prmt(x.y, x.w, 0x5410), prmt(x.y, x.w, 0x7632));
 }
 
-// The four words of upper codes (and of lower ones) of 16-byte piece i of a plane; a
-// two-bit draft gets its two C_U2 words doubled.
+// Four (N = 4) or two words of upper codes, and of lower ones, from word 4 i (2 i) of a
+// plane on; a two-bit draft gets its C_U2 words doubled.
 template <int MODE, int UB>
-__device__ __forceinline__ void raw_words(uint32_t raw, int i, uint32_t (&u)[4], uint32_t (&l)[4]) {
+__device__ __forceinline__ void raw_words4(uint32_t raw, int i, uint32_t (&u)[4], uint32_t (&l)[4]) {
   using C = TallCfg<MODE>;
   if (UB == 4) {
     const uint4 x = lds128(raw + C::kUpOff + 16 * i);
@@ -221,11 +239,31 @@ __device__ __forceinline__ void raw_words(uint32_t raw, int i, uint32_t (&u)[4],
       u[2] = upper_from2(a.y, m.y, 0); u[3] = upper_from2(a.y, m.y, 2);
     }
   }
+  l[0] = l[1] = l[2] = l[3] = 0;
   if (!C::kDraft) {
     const uint4 x = lds128(raw + C::kLowOff + 16 * i);
     l[0] = x.x; l[1] = x.y; l[2] = x.z; l[3] = x.w;
+  }
+}
+template <int MODE, int UB>
+__device__ __forceinline__ void raw_words2(uint32_t raw, int i, uint32_t (&u)[2], uint32_t (&l)[2]) {
+  using C = TallCfg<MODE>;
+  if (UB == 4) {
+    const uint2 x = lds64(raw + C::kUpOff + 8 * i);
+    u[0] = x.x; u[1] = x.y;
   } else {
-    l[0] = l[1] = l[2] = l[3] = 0;
+    const uint32_t a = lds32(raw + C::kUpOff + 4 * i);
+    if (C::kDraft) {
+      u[0] = u[1] = a;
+    } else {
+      const uint32_t m = lds32(raw + C::kUpOff + 4096 + 4 * i);
+      u[0] = upper_from2(a, m, 0); u[1] = upper_from2(a, m, 2);
+    }
+  }
+  l[0] = l[1] = 0;
+  if (!C::kDraft) {
+    const uint2 x = lds64(raw + C::kLowOff + 8 * i);
+    l[0] = x.x; l[1] = x.y;
   }
 }
 template <int MODE, int UB, int W>
@@ -234,37 +272,102 @@ __device__ __forceinline__ void word_pairs(uint32_t u, uint32_t l, uint32_t (&e)
   else code_pairs<MODE>(u, l, e);
 }
 
-// A group's keys into an operand tile, by the dequantizing warps (dw of 0 .. 7): a
-// lane takes 32 channels of a token; its scales and zeros stay in registers.  The
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
+  if (!chk(smem_in(a, 8), 60)) return;
+  asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+
+// A group's scales and zeros, by one warp, four channels (tokens) a lane.  Keys: s_h
+// the top three bits of s, s_l the rest; g a unit of the last one of them; z + 128 s
+// (the zero of centred codes) in z_h, its nearest multiple of g as far as 1152 g, and
+// z_l.  |s_h c' + z_h| <= 7 * 128 g + 1152 g = 2048 g: exact.
+template <int MODE>
+__device__ __forceinline__ void prep_keys(uint32_t raw, int lane) {
+  using C = TallCfg<MODE>;
+  const uint2 sw = lds64(raw + C::kMetaOff + 8 * lane), zw = lds64(raw + C::kMetaOff + 256 + 8 * lane);
+  uint32_t sh[2], sl[2], zh[2], zl[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t s2 = k ? sw.y : sw.x, z2 = k ? zw.y : zw.x;
+    sh[k] = s2 & 0xFF00FF00u;
+    sl[k] = h2_as_u32(__hsub2(u32_as_h2(s2), u32_as_h2(sh[k])));
+    const float2 s = __half22float2(u32_as_h2(s2)), z = __half22float2(u32_as_h2(z2));
+    float h[2], l[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float sf = i ? s.y : s.x, zc = fmaf(128.f, sf, i ? z.y : z.x);
+      // g and 1 / g from the exponent (a scale of 0: the zero alone)
+      const uint32_t ex = __float_as_uint(sf) & 0x7F800000u;
+      const float g = __uint_as_float(ex) * 0.25f, inv = __uint_as_float((254u << 23) - ex) * 4.f;
+      h[i] = ex ? fminf(fmaxf(rintf(zc * inv), -1152.f), 1152.f) * g : __half2float(__float2half_rn(zc));
+      l[i] = zc - h[i];
+    }
+    zh[k] = pack_half2(h[0], h[1]);
+    zl[k] = pack_half2(l[0], l[1]);
+  }
+  const uint32_t at = raw + C::kPrepOff + 8 * lane;
+  sts64(at, sh[0], sh[1]);
+  sts64(at + 256, sl[0], sl[1]);
+  sts64(at + 512, zh[0], zh[1]);
+  sts64(at + 768, zl[0], zl[1]);
+}
+// Values: the four entries of position 4 k of a quarter are tokens k, k + 8, k + 16,
+// k + 24 of it.
+template <int MODE>
+__device__ __forceinline__ void prep_values(uint32_t raw, int lane) {
+  using C = TallCfg<MODE>;
+  // lane: quarter lane / 8, its tokens k = lane % 8 (+ 8 j)
+  const uint32_t at = raw + C::kPrepOff + 64 * (lane >> 3) + 2 * (lane & 7);
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const uint2 x = lds64(raw + C::kMetaOff + 256 * r + 8 * lane);
+    const uint32_t v[4] = {x.x & 0xFFFFu, x.x >> 16, x.y & 0xFFFFu, x.y >> 16};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t a = at + 256 * r + 16 * j;
+      if (chk(smem_in(a, 2), 60))
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"((unsigned short)v[j]) : "memory");
+    }
+  }
+}
+
+// A group's keys into the tiles T1 and T2, by the eight key warps (dw): a lane takes 16
+// channels of a token, a pass 4 tokens of the warp; the scales stay in registers.  The
 // lanes of a quarter-warp write all eight 16-byte columns of the swizzle.
 template <int MODE, int UB>
-__device__ __forceinline__ void keys_tile(uint32_t raw, uint32_t tile, int dw, int lane) {
-  const int p = (lane & 1) | ((lane >> 2) & 2), tl = ((lane >> 1) & 3) | ((lane >> 4) << 2);
-  uint32_t s[4][4], z[4][4];
+__device__ __forceinline__ void keys_tile(uint32_t raw, uint32_t t1, uint32_t t2, int dw, int lane) {
+  const int p = (lane & 3) | ((lane >> 1) & 4), tl = ((lane >> 2) & 1) | ((lane >> 3) & 2);
+  // the 16-byte piece of a scale row that holds word w of the lane's channels (words
+  // 2 p + w of a token's 16)
+  uint32_t sh[2][4], sl[2][4], zh[2][4], zl[2][4];
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const uint4 a = lds128(raw + TallCfg<MODE>::kMetaOff + 16 * (p + 4 * w));
-    const uint4 b = lds128(raw + TallCfg<MODE>::kMetaOff + 256 + 16 * (p + 4 * w));
-    s[w][0] = a.x; s[w][1] = a.y; s[w][2] = a.z; s[w][3] = a.w;
-    z[w][0] = b.x; z[w][1] = b.y; z[w][2] = b.z; z[w][3] = b.w;
+  for (int w = 0; w < 2; ++w) {
+    const int word = 2 * p + w, at = 16 * ((word >> 2) + 4 * (word & 3));
+    const uint32_t prep = raw + TallCfg<MODE>::kPrepOff + at;
+    const uint4 a = lds128(prep), b = lds128(prep + 256), d = lds128(prep + 512), f = lds128(prep + 768);
+    sh[w][0] = a.x; sh[w][1] = a.y; sh[w][2] = a.z; sh[w][3] = a.w;
+    sl[w][0] = b.x; sl[w][1] = b.y; sl[w][2] = b.z; sl[w][3] = b.w;
+    zh[w][0] = d.x; zh[w][1] = d.y; zh[w][2] = d.z; zh[w][3] = d.w;
+    zl[w][0] = f.x; zl[w][1] = f.y; zl[w][2] = f.z; zl[w][3] = f.w;
   }
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    const int t = 16 * dw + 8 * pass + tl;
-    uint32_t u[4], l[4], e[4] = {};
-    raw_words<MODE, UB>(raw, 4 * t + p, u, l);
+  for (int pass = 0; pass < 4; ++pass) {
+    const int t = 16 * dw + 4 * pass + tl;
+    uint32_t u[2], l[2], e[4] = {};
+    raw_words2<MODE, UB>(raw, 8 * t + p, u, l);
     auto put = [&](int w) {
-      sts128(tile_at(tile, t, 4 * p + w), dequant2(e[0], s[w][0], z[w][0]), dequant2(e[1], s[w][1], z[w][1]),
-             dequant2(e[2], s[w][2], z[w][2]), dequant2(e[3], s[w][3], z[w][3]));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[j] = centred(e[j]);
+      const uint32_t at = tile_at(0, t, 2 * p + w);
+      sts128(t1 + at, fma2(e[0], sh[w][0], zh[w][0]), fma2(e[1], sh[w][1], zh[w][1]),
+             fma2(e[2], sh[w][2], zh[w][2]), fma2(e[3], sh[w][3], zh[w][3]));
+      sts128(t2 + at, fma2(e[0], sl[w][0], zl[w][0]), fma2(e[1], sl[w][1], zl[w][1]),
+             fma2(e[2], sl[w][2], zl[w][2]), fma2(e[3], sl[w][3], zl[w][3]));
     };
     word_pairs<MODE, UB, 0>(u[0], l[0], e);
     put(0);
     word_pairs<MODE, UB, 1>(u[1], l[1], e);
     put(1);
-    word_pairs<MODE, UB, 2>(u[2], l[2], e);
-    put(2);
-    word_pairs<MODE, UB, 3>(u[3], l[3], e);
-    put(3);
   }
 }
 
@@ -274,37 +377,49 @@ __device__ __forceinline__ void keys_tile(uint32_t raw, uint32_t tile, int dw, i
 template <int MODE, int UB>
 __device__ __forceinline__ void values_tile(uint32_t raw, uint32_t tile, int dw, int lane) {
   const int q = dw >> 1;
-  uint32_t s[4][4], z[4][4];  // [word][pair]
+  uint32_t s[4][4], z[4][4];  // [pair][word]
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const uint4 a = lds128(raw + TallCfg<MODE>::kMetaOff + 64 * q + 16 * w);
-    const uint4 b = lds128(raw + TallCfg<MODE>::kMetaOff + 256 + 64 * q + 16 * w);
-    // (a token's four entries: tokens t, t + 8, t + 16, t + 24)
-    s[w][0] = prmt(a.x, a.z, 0x5410); s[w][1] = prmt(a.x, a.z, 0x7632);
-    s[w][2] = prmt(a.y, a.w, 0x5410); s[w][3] = prmt(a.y, a.w, 0x7632);
-    z[w][0] = prmt(b.x, b.z, 0x5410); z[w][1] = prmt(b.x, b.z, 0x7632);
-    z[w][2] = prmt(b.y, b.w, 0x5410); z[w][3] = prmt(b.y, b.w, 0x7632);
+  for (int j = 0; j < 4; ++j) {
+    const uint4 a = lds128(raw + TallCfg<MODE>::kPrepOff + 64 * q + 16 * j);
+    const uint4 b = lds128(raw + TallCfg<MODE>::kPrepOff + 256 + 64 * q + 16 * j);
+    s[j][0] = a.x; s[j][1] = a.y; s[j][2] = a.z; s[j][3] = a.w;
+    z[j][0] = b.x; z[j][1] = b.y; z[j][2] = b.z; z[j][3] = b.w;
   }
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     const int d = 64 * (dw & 1) + 32 * pass + lane;
     uint32_t u[4], l[4], e[4][4];
-    raw_words<MODE, UB>(raw, kTile * q + d, u, l);
+    raw_words4<MODE, UB>(raw, kTile * q + d, u, l);
     word_pairs<MODE, UB, 0>(u[0], l[0], e[0]);
     word_pairs<MODE, UB, 1>(u[1], l[1], e[1]);
     word_pairs<MODE, UB, 2>(u[2], l[2], e[2]);
     word_pairs<MODE, UB, 3>(u[3], l[3], e[3]);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      sts128(tile_at(tile, d, 4 * q + j), dequant2(e[0][j], s[0][j], z[0][j]), dequant2(e[1][j], s[1][j], z[1][j]),
-             dequant2(e[2][j], s[2][j], z[2][j]), dequant2(e[3][j], s[3][j], z[3][j]));
+      sts128(tile_at(tile, d, 4 * q + j), fma2(uncentred(e[0][j]), s[j][0], z[j][0]),
+             fma2(uncentred(e[1][j]), s[j][1], z[j][1]), fma2(uncentred(e[2][j]), s[j][2], z[j][2]),
+             fma2(uncentred(e[3][j]), s[j][3], z[j][3]));
   }
 }
 
 // ------------------------------------------------------------------- kernel
 
-// Item i of a piece's 2 n operand tiles, in the order the MMAs take them: unit and
-// whether it is the values.  MT = 2: K0 V0 K1 V1 ..; MT = 1: K0 K1 V0 K2 V1 .. .
+// The order in which the MMAs take a piece's n units of keys (K, two tiles) and values
+// (V): MT = 2: K0 V0 K1 V1 ..; MT = 1: K0 K1 V0 K2 V1 .. V(n-1).  Places with k tiles for
+// the keys (k = 1: the raw copies), and the steps from one unit's to the next one's.
+template <int MT>
+__device__ __forceinline__ int first_values(int n, int k) {
+  return MT == 2 || n <= 1 ? k : 2 * k;
+}
+template <int MT>
+__device__ __forceinline__ int keys_step(int g, int k) {
+  return MT == 1 && g == 0 ? k : k + 1;
+}
+template <int MT>
+__device__ __forceinline__ int values_step(int g, int n, int k) {
+  return MT == 1 && g == n - 2 ? 1 : k + 1;
+}
+// Item i of the 2 n in that order: its unit, and whether it is the values.
 template <int MT>
 __device__ __forceinline__ int item_of(int i, int n, bool &values) {
   if (MT == 2) {
@@ -313,14 +428,6 @@ __device__ __forceinline__ int item_of(int i, int n, bool &values) {
   }
   values = i > 0 && (!(i & 1) || i == 2 * n - 1);
   return i == 2 * n - 1 ? n - 1 : values ? (i - 2) >> 1 : (i + 1) >> 1;
-}
-template <int MT>
-__device__ __forceinline__ int key_item(int g) {
-  return MT == 2 ? 2 * g : g == 0 ? 0 : 2 * g - 1;
-}
-template <int MT>
-__device__ __forceinline__ int value_item(int g, int n) {
-  return MT == 2 ? 2 * g + 1 : g == n - 1 ? 2 * n - 1 : 2 * g + 2;
 }
 
 // A place in a ring of N and the parity of its turn.
@@ -342,7 +449,7 @@ struct Ring {
 };
 
 struct TallShared {
-  uint64_t raw_full[10], raw_empty[10], op_full[kOpTiles], op_empty[kOpTiles];
+  uint64_t raw_full[10], raw_empty[10], prep_full[10], op_full[4], op_empty[4];
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], q_full, q_empty, drain;
   uint64_t bad[8];        // nodes with values that are not finite, per piece
   long long total;
@@ -503,7 +610,7 @@ template <int MODE, int UB, int MT>
 __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_constant__ TallParams prm) {
   using L = TallLayout<MODE, MT>;
   using C = TallCfg<MODE>;
-  constexpr int NR = L::kRaw;
+  constexpr int NR = L::kRaw, NOP = op_tiles<MT>();
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ TallShared sh;
   // tiles start at multiples of 1024 bytes
@@ -517,9 +624,10 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
     for (int i = 0; i < NR; ++i) {
       mbar_init(smem_addr(&sh.raw_full[i]), 1);
       mbar_init(smem_addr(&sh.raw_empty[i]), kDeqWarps);
+      mbar_init(smem_addr(&sh.prep_full[i]), 1);
     }
 #pragma unroll 1
-    for (int i = 0; i < kOpTiles; ++i) {
+    for (int i = 0; i < NOP; ++i) {
       mbar_init(smem_addr(&sh.op_full[i]), kDeqWarps);
       mbar_init(smem_addr(&sh.op_empty[i]), 1);
     }
@@ -636,7 +744,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
     {
       int n_s = 0, n_e = 0, piece = 0;  // bits 0, 1: parities of the streams' S, and of their sums
       int begun = 0;                    // bits: the stream has handed over sums before
-      Ring<kOpTiles> start;             // the piece's first operand tile
+      Ring<NOP> start;             // the piece's first operand tile
       bool ok = true;
       const uint64_t q_desc = operand_desc(sbase + L::kQOff), op_desc = operand_desc(sbase + L::kOpOff);
 #pragma unroll 1
@@ -644,8 +752,8 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
         piece_at(c.B, prm.n_mp, T, x, x1, pc);
         const int n = pc.n, steps = MT == 2 ? 2 * n + 2 : n + 2;
         x += n;
-        Ring<kOpTiles> rk = start, rv = start;  // the next keys' tile, the next values'
-        rv.add(value_item<MT>(0, n));
+        Ring<NOP> rk = start, rv = start;  // the next keys' tile, the next values'
+        rv.add(first_values<MT>(n, 2));
 #pragma unroll 1
         for (int t = 0; t < steps; ++t) {
           const int s = t & 1, g = MT == 2 ? t >> 1 : t;  // stream; unit whose scores are next
@@ -668,37 +776,45 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
               if (last) mma_commit(bar(sh.o_full[s]));
             }
             __syncwarp();
-            if (MT == 1 || s == 1) rv.add(MT == 1 && gv == n - 2 ? 1 : 2);
+            if (MT == 1 || s == 1) rv.add(values_step<MT>(gv, n, 2));
             if (last) {
               n_e ^= 1 << s;
               begun |= 1 << s;
             }
           }
           if (g < n) {
-            ok = warp_wait(sh, sh.op_full[rk.slot], rk.par, ns);
+            Ring<NOP> r2 = rk;
+            r2.add(1);
+            ok = warp_wait(sh, sh.op_full[rk.slot], rk.par, ns) && warp_wait(sh, sh.op_full[r2.slot], r2.par, ns);
             if (ok && g == 0) ok = warp_wait(sh, sh.q_full, piece & 1, ns);
             if (!ok) break;
             tc_after_sync();
             const uint64_t a = q_desc + (MT == 2 ? s * (kTileBytes >> 4) : 0);
-            const uint64_t b = op_desc + rk.slot * (kTileBytes >> 4);
+            const uint64_t b1 = op_desc + rk.slot * (kTileBytes >> 4), b2 = op_desc + r2.slot * (kTileBytes >> 4);
             if (elect_one()) {
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 const uint32_t off = (k >> 2) * (kTile * 8) + (k & 3) * 2;  // (in units of 16 bytes)
-                mma_ss(tmem + 128 * s, a + off, b + off, k > 0);
+                mma_ss(tmem + 128 * s, a + off, b1 + off, k > 0);
+              }
+              if (MT == 1 || s == 1) mma_commit(bar(sh.op_empty[rk.slot]));
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const uint32_t off = (k >> 2) * (kTile * 8) + (k & 3) * 2;
+                mma_ss(tmem + 128 * s, a + off, b2 + off, 1);
               }
               mma_commit(bar(sh.s_full[s]));
               if (MT == 1 || s == 1) {
-                mma_commit(bar(sh.op_empty[rk.slot]));
+                mma_commit(bar(sh.op_empty[r2.slot]));
                 if (g == n - 1) mma_commit(bar(sh.q_empty));
               }
             }
             __syncwarp();
             n_s ^= 1 << s;
-            if (MT == 1 || s == 1) rk.add(MT == 1 && g == 0 ? 1 : 2);
+            if (MT == 1 || s == 1) rk.add(keys_step<MT>(g, 2));
           }
         }
-        start.add_any(2 * n);
+        start.add_any(3 * n);
       }
       // no MMA may be in flight when the CTA gives its tensor memory back
       if (elect_one()) mma_commit(bar(sh.drain));
@@ -708,11 +824,34 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
         if (globaltimer_ns() - t0 > ns) break;
     }
     __syncwarp();
+  } else if (w == kPrepWarp) {
+    // --------------------------------------------------- scales and zeros
+    Ring<NR> raw;
+    bool ok = true;
+#pragma unroll 1
+    for (int x = x0; ok && x < x1; x += pc.n) {
+      piece_at(c.B, prm.n_mp, T, x, x1, pc);
+      const int n_grp = min(pc.n, max(0, pc.ng - pc.u0));
+#pragma unroll 1
+      for (int i = 0; i < 2 * n_grp; ++i) {
+        bool values;
+        item_of<MT>(i, n_grp, values);
+        ok = warp_wait(sh, sh.raw_full[raw.slot], raw.par, ns);
+        if (!ok) break;
+        if (!*reinterpret_cast<volatile int *>(&sh.raw_dead[raw.slot])) {
+          if (values) prep_values<MODE>(raw_at(raw.slot), lane);
+          else prep_keys<MODE>(raw_at(raw.slot), lane);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh.prep_full[raw.slot]));
+        raw.add(1);
+      }
+    }
   } else if (w >= kSoftWarps) {
     // ----------------------------------------------------- operand tiles
     const bool values = w >= kSoftWarps + kDeqWarps;
     const int dw = (w - kSoftWarps) & (kDeqWarps - 1), dt = dw * 32 + lane;
-    Ring<kOpTiles> start;
+    Ring<NOP> start;
     Ring<NR> raw_start;
     int piece = 0, unit0 = 0, o0 = 0;
     bool ok = true;
@@ -735,43 +874,58 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
         // reads: each is within three pieces of this one)
         sh.bad[(piece + 4) & 7] = 0;
       }
-      Ring<kOpTiles> op = start;
+      Ring<NOP> op = start;
       Ring<NR> raw = raw_start;
+      int o = o0;  // operand tiles before this one
       if (values) {
-        op.add(value_item<MT>(0, n));
-        raw.add(value_item<MT>(0, n_grp));
+        op.add(first_values<MT>(n, 2));
+        raw.add(first_values<MT>(n_grp, 1));
+        o += first_values<MT>(n, 2);
       }
-      int o = o0 + (values ? value_item<MT>(0, n) : 0);  // operand tiles before this one
 #pragma unroll 1
       for (int g = 0; g < n; ++g) {
-        if (o >= kOpTiles && !warp_wait(sh, sh.op_empty[op.slot], op.par ^ 1, ns)) {
+        Ring<NOP> op2 = op;  // (the keys' second tile)
+        op2.add(1);
+        if (o >= NOP && !warp_wait(sh, sh.op_empty[op.slot], op.par ^ 1, ns)) {
           ok = false;
           break;
         }
-        const uint32_t dst = tile(op.slot);
+        if (!values && o + 1 >= NOP && !warp_wait(sh, sh.op_empty[op2.slot], op2.par ^ 1, ns)) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = tile(op.slot), dst2 = tile(op2.slot);
         if (g < n_grp) {
-          if (!warp_wait(sh, sh.raw_full[raw.slot], raw.par, ns)) {
+          // (the copy itself, and what the scales were made into)
+          if (!warp_wait(sh, sh.raw_full[raw.slot], raw.par, ns) ||
+              !warp_wait(sh, sh.prep_full[raw.slot], raw.par, ns)) {
             ok = false;
             break;
           }
           const bool dead = *reinterpret_cast<volatile int *>(&sh.raw_dead[raw.slot]) != 0;
           if (dead) {  // a group that is left out: nothing that could disturb the sums
 #pragma unroll 1
-            for (int k = dt; k < kTileBytes / 16; k += 32 * kDeqWarps) sts128(dst + 16 * k, 0, 0, 0, 0);
+            for (int k = dt; k < kTileBytes / 16; k += 32 * kDeqWarps) {
+              sts128(dst + 16 * k, 0, 0, 0, 0);
+              if (!values) sts128(dst2 + 16 * k, 0, 0, 0, 0);
+            }
           } else if (values) {
             values_tile<MODE, UB>(raw_at(raw.slot), dst, dw, lane);
           } else {
-            keys_tile<MODE, UB>(raw_at(raw.slot), dst, dw, lane);
+            keys_tile<MODE, UB>(raw_at(raw.slot), dst, dst2, dw, lane);
           }
           if (!values && dt == 0) *reinterpret_cast<volatile int *>(&sh.dead[(unit0 + g) % kFlags]) = dead;
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(sh.raw_empty[raw.slot]));
-          raw.add(values ? (MT == 1 && g == n_grp - 2 ? 1 : 2) : (MT == 1 && g == 0 ? 1 : 2));
+          raw.add(values ? values_step<MT>(g, n_grp, 1) : keys_step<MT>(g, 1));
         } else {
           const int i0 = (pc.u0 + g - pc.ng) * kTile, base = pc.hb * kG + i0;
           const size_t row0 = bh * kRing * 16;
           if (!values) {
+            // (fp16 already: T2 is zero)
             buffer_keys_tile(reinterpret_cast<const uint4 *>(c.buf_k) + row0, base, i0, pc.fill, dst, dt);
+#pragma unroll 1
+            for (int k = dt; k < kTileBytes / 16; k += 32 * kDeqWarps) sts128(dst2 + 16 * k, 0, 0, 0, 0);
           } else {
             const uint64_t bad = buffer_values_tile(reinterpret_cast<const uint4 *>(c.buf_v) + row0, base, i0,
                                                     pc.fill, pc.fill - prm.n_tree, dst, dt);
@@ -780,14 +934,17 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(sh.op_full[op.slot]));
-        const int by = values ? (MT == 1 && g == n - 2 ? 1 : 2) : (MT == 1 && g == 0 ? 1 : 2);
+        if (lane == 0) {
+          mbar_arrive(bar(sh.op_full[op.slot]));
+          if (!values) mbar_arrive(bar(sh.op_full[op2.slot]));
+        }
+        const int by = values ? values_step<MT>(g, n, 2) : keys_step<MT>(g, 2);
         op.add(by);
         o += by;
       }
-      start.add_any(2 * n);
+      start.add_any(3 * n);
       raw_start.add_any(2 * n_grp);
-      o0 += 2 * n;
+      o0 += 3 * n;
       unit0 += n;
     }
   } else {
@@ -926,13 +1083,16 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
 }
 
 // Joins the partials: a thread takes four channels of a row (eight rows side by
-// side), its loads in flight four at a time.  The CTAs that hold a segment, and where
-// their partials lie, follow from the counters as in the kernel above.
-constexpr int kJoinThreads = 256;
+// side) and every other partial, six of them in flight; two threads meet at the end.
+// The CTAs that hold a segment, and where their partials lie, follow from the
+// counters as in the kernel above.
+constexpr int kJoinThreads = 512, kJoinBatch = 6;
 
-__global__ void __launch_bounds__(kJoinThreads) tall_join_kernel(const TallParams prm, int MT) {
+__global__ void __launch_bounds__(kJoinThreads) tall_join_kernel(const __grid_constant__ TallParams prm, int MT) {
   __shared__ int tab[7 * kMaxB];
   __shared__ long long s_total;
+  __shared__ float4 s_o[kJoinThreads / 2];
+  __shared__ float2 s_ml[kJoinThreads / 2];
   const qs_cache &c = prm.c;
   Tables T = tables_at(reinterpret_cast<uint8_t *>(tab), 0);
   pdl_trigger();
@@ -944,12 +1104,69 @@ __global__ void __launch_bounds__(kJoinThreads) tall_join_kernel(const TallParam
     if (threadIdx.x == 0) s_total = tot;
   }
   __syncthreads();
-  const long long at = (long long)blockIdx.x * 8 + (threadIdx.x & 7);
-  const int c4 = threadIdx.x >> 3;
-  if (at >= (long long)c.B * c.H * prm.R) return;
-  const int row = (int)(at % prm.R), bh = (int)(at / prm.R), b = bh / c.H, h = bh % c.H;
+  const int half = threadIdx.x / (kJoinThreads / 2), ti = threadIdx.x % (kJoinThreads / 2);
+  const long long at = (long long)blockIdx.x * 8 + (ti & 7);
+  const int c4 = ti >> 3;
+  const bool here = at < (long long)c.B * c.H * prm.R;
+  float M = -INFINITY, Ls = 0.f;
+  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto fold = [&](float mn, float m, float l, float4 o) {
+    if (l == 0.f) return;  // nothing seen there (its sums were not written)
+    const float f = m == -INFINITY ? 1.f : fast_exp2(m - mn);  // (no maximum: all NaN)
+    A.x = fmaf(f, o.x, A.x); A.y = fmaf(f, o.y, A.y);
+    A.z = fmaf(f, o.z, A.z); A.w = fmaf(f, o.w, A.w);
+    Ls = fmaf(f, l, Ls);
+  };
+  auto rescale = [&](float mn) {
+    const float a = M == -INFINITY ? 0.f : fast_exp2(M - mn);
+    A.x *= a; A.y *= a; A.z *= a; A.w *= a;
+    Ls *= a;
+    M = mn;
+  };
+  int len = 0, b = 0;
+  if (here) {
+    const int row = (int)(at % prm.R), bh = (int)(at / prm.R), h = bh % c.H;
+    b = bh / c.H;
+    len = T.len[b];
+    if (len > 0) {
+      const int seg = h * prm.n_mp + row / (2 * kTile), s0 = T.base[b] + seg * len, ord = T.ord0[b] + seg;
+      const int plo = cta_of(s0, s_total, prm.P), phi = cta_of(s0 + len - 1, s_total, prm.P);
+      const int row_t = row % kTile, s_at = MT == 2 ? (row / kTile) & 1 : 0, sh = MT == 2 ? 0 : 1;
+      const size_t size = (size_t)prm.rows * (kD + 2);
+      const int np = (phi - plo + 1) << sh;
+#pragma unroll 1
+      for (int k0 = half; k0 < np; k0 += 2 * kJoinBatch) {
+        float m[kJoinBatch], l[kJoinBatch];
+        float4 o[kJoinBatch];
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i) {
+          const int k = k0 + 2 * i;
+          m[i] = -INFINITY;
+          l[i] = 0.f;
+          if (k >= np) continue;
+          const size_t off = ((size_t)(ord + plo + (k >> sh)) * 2 + s_at + (k & sh)) * size;
+          if (!chk(in_range(off, size, prm.ws_floats), 63)) continue;
+          const float *part = prm.ws + off;
+          m[i] = part[prm.rows * kD + row_t];
+          l[i] = part[prm.rows * (kD + 1) + row_t];
+          o[i] = reinterpret_cast<const float4 *>(part)[c4 * prm.rows + row_t];
+        }
+        float mn = M;
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i) mn = fmaxf(mn, m[i]);
+        rescale(mn);
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i) fold(mn, m[i], l[i], o[i]);
+      }
+    }
+  }
+  if (half) {
+    s_o[ti] = A;
+    s_ml[ti] = make_float2(M, Ls);
+  }
+  __syncthreads();
+  if (half || !here) return;
   uint2 *out = reinterpret_cast<uint2 *>(prm.out + (size_t)at * kD + 4 * c4);
-  const int len = T.len[b];
   if (len == 0) {  // n_tree > fill
     *out = make_uint2(0, 0);
     if (c4 == 0) {
@@ -958,46 +1175,10 @@ __global__ void __launch_bounds__(kJoinThreads) tall_join_kernel(const TallParam
     }
     return;
   }
-  const long long U = s_total;
-  const int seg = h * prm.n_mp + row / (2 * kTile), s0 = T.base[b] + seg * len, ord = T.ord0[b] + seg;
-  const int plo = cta_of(s0, U, prm.P), phi = cta_of(s0 + len - 1, U, prm.P);
-  const int row_t = row % kTile, s_at = MT == 2 ? (row / kTile) & 1 : 0, per = MT == 2 ? 1 : 2;
-  const size_t size = (size_t)prm.rows * (kD + 2);
-  float M = -INFINITY, Ls = 0.f;
-  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int np = (phi - plo + 1) * per;
-  for (int k0 = 0; k0 < np; k0 += 4) {
-    float m[4], l[4];
-    float4 o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = k0 + i;
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-      if (k >= np) continue;
-      const size_t off = ((size_t)(ord + plo + k / per) * 2 + s_at + k % per) * size;
-      if (!chk(in_range(off, size, prm.ws_floats), 63)) continue;
-      const float *part = prm.ws + off;
-      m[i] = part[prm.rows * kD + row_t];
-      l[i] = part[prm.rows * (kD + 1) + row_t];
-      o[i] = reinterpret_cast<const float4 *>(part)[c4 * prm.rows + row_t];
-    }
-    float mn = M;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) mn = fmaxf(mn, m[i]);
-    const float a = M == -INFINITY ? 0.f : fast_exp2(M - mn);
-    A.x *= a; A.y *= a; A.z *= a; A.w *= a;
-    Ls *= a;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (l[i] == 0.f) continue;  // nothing seen there (its sums were not written)
-      const float f = m[i] == -INFINITY ? 1.f : fast_exp2(m[i] - mn);  // (no maximum: all NaN)
-      A.x = fmaf(f, o[i].x, A.x); A.y = fmaf(f, o[i].y, A.y);
-      A.z = fmaf(f, o[i].z, A.z); A.w = fmaf(f, o[i].w, A.w);
-      Ls = fmaf(f, l[i], Ls);
-    }
-    M = mn;
-  }
+  const float2 ml = s_ml[ti];
+  const float mn = fmaxf(M, ml.x);
+  rescale(mn);
+  fold(mn, ml.x, ml.y, s_o[ti]);
   const float inv = 1.f / Ls;
   *out = make_uint2(pack_half2(A.x * inv, A.y * inv), pack_half2(A.z * inv, A.w * inv));
   if (prm.lse && c4 == 0) prm.lse[at] = (M - kExpShift + log2f(Ls)) * 0.69314718055994531f;
