@@ -48,11 +48,15 @@ constexpr int kTileBytes = kTile * kTile * 2;
 // Operand tiles in the ring: a unit has three (T1 and T2 of the keys, the values).
 template <int MT>
 constexpr int op_tiles() { return MT == 2 ? 3 : 4; }
-constexpr int kSoftWarps = 8, kDeqWarps = 8;  // (of the latter for keys, and for values)
-constexpr int kMmaWarp = kSoftWarps + 2 * kDeqWarps, kLoadWarp = kMmaWarp + 1, kPrepWarp = kMmaWarp + 2;
+// Warps of the softmax, and those that make operand tiles of keys and of values (whose
+// tiles take a third of the work).  Each of the former arrives once on a tile's barrier,
+// each of the latter kValArrive times.
+constexpr int kSoftWarps = 8, kKeyWarps = 8, kValWarps = 4, kValArrive = kKeyWarps / kValWarps;
+constexpr int kMmaWarp = kSoftWarps + kKeyWarps + kValWarps, kLoadWarp = kMmaWarp + 1, kPrepWarp = kMmaWarp + 2;
 constexpr int kTallThreads = 32 * (kPrepWarp + 1);
 constexpr float kRaise = 8.f;              // log2 by which a maximum may be behind
 constexpr int kFlags = 8;                  // units whose flags are kept
+constexpr int kScales = 4;                 // units whose value scales are kept
 constexpr int kMaxTreeRows = 512;
 
 // A piece of a unit in the ring of raw copies: keys or values.
@@ -60,8 +64,8 @@ template <int MODE>
 struct TallCfg {
   static constexpr bool kDraft = MODE == QS_DRAFT_UPPER4;
   static constexpr int kUpOff = 0, kLowOff = 8192, kMetaOff = kDraft ? 8192 : 16384;
-  // scales and zeros as the tiles' makers take them: of keys s_h, s_l, z_h, z_l in the
-  // order of the key codes, of values s and z in the order of the tokens
+  // the keys' scales and zeros as their tiles' makers take them: s_h, s_l, z_h, z_l, in
+  // the order of the key codes
   static constexpr int kPrepOff = kMetaOff + 512;
   static constexpr int kRawBytes = kPrepOff + 1024;
 };
@@ -70,10 +74,12 @@ struct TallLayout {
   static constexpr int kQOff = 0;
   static constexpr int kOpOff = MT * kTileBytes;
   static constexpr int kRawOff = kOpOff + op_tiles<MT>() * kTileBytes;
-  static constexpr int kRest = 227 * 1024 - 1024 - kRawOff - 7 * kMaxB * 4 - 512;
+  static constexpr int kScaleBytes = 1024;  // 128 tokens' s, and z + 128 s, in fp32
+  static constexpr int kRest = 227 * 1024 - 1024 - kRawOff - 7 * kMaxB * 4 - kScales * kScaleBytes - 768;
   static constexpr int kRawFit = kRest / TallCfg<MODE>::kRawBytes;
   static constexpr int kRaw = kRawFit < 10 ? kRawFit : 10;
-  static constexpr int kTabOff = kRawOff + kRaw * TallCfg<MODE>::kRawBytes;
+  static constexpr int kScaleOff = kRawOff + kRaw * TallCfg<MODE>::kRawBytes;
+  static constexpr int kTabOff = kScaleOff + kScales * kScaleBytes;
   static constexpr int kSmem = kTabOff + 7 * kMaxB * 4;  // (+ up to 1 KB of alignment)
   static_assert(kRaw >= 3, "");
 };
@@ -151,19 +157,23 @@ __device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&v)[32]) {
       : QS_R8(v, 0), QS_R8(v, 8), QS_R8(v, 16), QS_R8(v, 24)
       : "r"(addr));
 }
-__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::QS_S8(v, 0),
-      QS_S8(v, 8), QS_S8(v, 16), QS_S8(v, 24), "r"(addr)
-      : "memory");
-}
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::
           QS_S8(v, 0),
       QS_S8(v, 8), "r"(addr)
       : "memory");
+}
+__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : QS_R8(v, 0), QS_R8(v, 8)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_st8(uint32_t addr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::QS_S8(v, 0), "r"(addr)
+               : "memory");
 }
 
 // ------------------------------------------------------- operand conversion
@@ -197,15 +207,42 @@ __device__ __forceinline__ void code_pairs2(uint32_t x, uint32_t (&e)[4]) {
   e[2] = ((x >> (2 + SH)) & m) | k;
   e[3] = ((x >> (6 + SH)) & m) | k;
 }
-// The code less 128, and less nothing.
+// The code less 128.
 __device__ __forceinline__ uint32_t centred(uint32_t e) {
   return h2_as_u32(__hsub2(u32_as_h2(e), __half2half2(__ushort_as_half(0x6480))));
 }
-__device__ __forceinline__ uint32_t uncentred(uint32_t e) {
-  return h2_as_u32(__hsub2(u32_as_h2(e), __half2half2(__ushort_as_half(0x6400))));
-}
 __device__ __forceinline__ uint32_t fma2(uint32_t e, uint32_t s, uint32_t z) {
   return h2_as_u32(__hfma2(u32_as_h2(e), u32_as_h2(s), u32_as_h2(z)));
+}
+// Pairs of fp32: one instruction for two.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1,%2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float lo_of(f32x2 x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float hi_of(f32x2 x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ f32x2 fma_f32x2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f32x2 mul_f32x2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 add_f32x2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ ulonglong2 lds2x64(uint32_t a) {
+  if (!chk(smem_in(a, 16), 1)) return make_ulonglong2(0, 0);
+  ulonglong2 v;
+  asm volatile("ld.shared.v2.b64 {%0,%1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(a));
+  return v;
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   if (!chk(smem_in(a, 16), 60)) return;
@@ -311,28 +348,39 @@ __device__ __forceinline__ void prep_keys(uint32_t raw, int lane) {
   sts64(at + 512, zh[0], zh[1]);
   sts64(at + 768, zl[0], zl[1]);
 }
-// Values: the four entries of position 4 k of a quarter are tokens k, k + 8, k + 16,
-// k + 24 of it.
+// Values: s, and the zero of centred codes, of each token in order, in fp32 (raw 0: a
+// unit of buffer tokens, whose values are no codes; dead: nothing).  The four entries
+// from position 4 k of a quarter on are tokens k, k + 8, k + 16, k + 24 of it.
 template <int MODE>
-__device__ __forceinline__ void prep_values(uint32_t raw, int lane) {
+__device__ __forceinline__ void prep_values(uint32_t raw, bool dead, uint32_t to, int lane) {
   using C = TallCfg<MODE>;
-  // lane: quarter lane / 8, its tokens k = lane % 8 (+ 8 j)
-  const uint32_t at = raw + C::kPrepOff + 64 * (lane >> 3) + 2 * (lane & 7);
+  const uint32_t at = to + 128 * (lane >> 3) + 4 * (lane & 7);  // (token 32 (lane / 8) + lane % 8)
+  float s[4], z[4];
+  if (raw && !dead) {
+    const uint2 sw = lds64(raw + C::kMetaOff + 8 * lane), zw = lds64(raw + C::kMetaOff + 256 + 8 * lane);
+    const float2 s0 = __half22float2(u32_as_h2(sw.x)), s1 = __half22float2(u32_as_h2(sw.y));
+    const float2 z0 = __half22float2(u32_as_h2(zw.x)), z1 = __half22float2(u32_as_h2(zw.y));
+    s[0] = s0.x; s[1] = s0.y; s[2] = s1.x; s[3] = s1.y;
+    z[0] = z0.x; z[1] = z0.y; z[2] = z1.x; z[3] = z1.y;
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const uint2 x = lds64(raw + C::kMetaOff + 256 * r + 8 * lane);
-    const uint32_t v[4] = {x.x & 0xFFFFu, x.x >> 16, x.y & 0xFFFFu, x.y >> 16};
+    for (int j = 0; j < 4; ++j) z[j] = fmaf(128.f, s[j], z[j]);
+  } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t a = at + 256 * r + 16 * j;
-      if (chk(smem_in(a, 2), 60))
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"((unsigned short)v[j]) : "memory");
+      s[j] = dead ? 0.f : 1.f;
+      z[j] = 0.f;
     }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (!chk(smem_in(at + 32 * j, 4) && smem_in(at + 512 + 32 * j, 4), 60)) continue;
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 32 * j), "f"(s[j]) : "memory");
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 512 + 32 * j), "f"(z[j]) : "memory");
   }
 }
 
-// A group's keys into the tiles T1 and T2, by the eight key warps (dw): a lane takes 16
-// channels of a token, a pass 4 tokens of the warp; the scales stay in registers.  The
+// A group's keys into the tiles T1 and T2, by the key warps (dw): a lane takes 16
+// channels of a token, a warp 4 tokens at a time; the scales stay in registers.  The
 // lanes of a quarter-warp write all eight 16-byte columns of the swizzle.
 template <int MODE, int UB>
 __device__ __forceinline__ void keys_tile(uint32_t raw, uint32_t t1, uint32_t t2, int dw, int lane) {
@@ -351,8 +399,7 @@ __device__ __forceinline__ void keys_tile(uint32_t raw, uint32_t t1, uint32_t t2
     zl[w][0] = f.x; zl[w][1] = f.y; zl[w][2] = f.z; zl[w][3] = f.w;
   }
 #pragma unroll 1
-  for (int pass = 0; pass < 4; ++pass) {
-    const int t = 16 * dw + 4 * pass + tl;
+  for (int t = 4 * dw + tl; t < kTile; t += 4 * kKeyWarps) {
     uint32_t u[2], l[2], e[4] = {};
     raw_words2<MODE, UB>(raw, 8 * t + p, u, l);
     auto put = [&](int w) {
@@ -371,23 +418,13 @@ __device__ __forceinline__ void keys_tile(uint32_t raw, uint32_t t1, uint32_t t2
   }
 }
 
-// A group's values: a lane takes a quarter's 32 tokens of a channel.  Word w's pair j
-// is tokens 8 j + 2 w and the next, so pair j of the four words is eight tokens in
-// order.
+// A group's value codes, less 128, by the value warps (one to a quarter): a lane takes a
+// quarter's 32 tokens of a channel.  Word w's pair j is tokens 8 j + 2 w and the next,
+// so pair j of the four words is eight tokens in order.
 template <int MODE, int UB>
-__device__ __forceinline__ void values_tile(uint32_t raw, uint32_t tile, int dw, int lane) {
-  const int q = dw >> 1;
-  uint32_t s[4][4], z[4][4];  // [pair][word]
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint4 a = lds128(raw + TallCfg<MODE>::kPrepOff + 64 * q + 16 * j);
-    const uint4 b = lds128(raw + TallCfg<MODE>::kPrepOff + 256 + 64 * q + 16 * j);
-    s[j][0] = a.x; s[j][1] = a.y; s[j][2] = a.z; s[j][3] = a.w;
-    z[j][0] = b.x; z[j][1] = b.y; z[j][2] = b.z; z[j][3] = b.w;
-  }
-#pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    const int d = 64 * (dw & 1) + 32 * pass + lane;
+__device__ __forceinline__ void values_tile(uint32_t raw, uint32_t tile, int q, int lane) {
+#pragma unroll 2
+  for (int d = lane; d < kTile; d += 32) {
     uint32_t u[4], l[4], e[4][4];
     raw_words4<MODE, UB>(raw, kTile * q + d, u, l);
     word_pairs<MODE, UB, 0>(u[0], l[0], e[0]);
@@ -396,9 +433,7 @@ __device__ __forceinline__ void values_tile(uint32_t raw, uint32_t tile, int dw,
     word_pairs<MODE, UB, 3>(u[3], l[3], e[3]);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      sts128(tile_at(tile, d, 4 * q + j), fma2(uncentred(e[0][j]), s[j][0], z[j][0]),
-             fma2(uncentred(e[1][j]), s[j][1], z[j][1]), fma2(uncentred(e[2][j]), s[j][2], z[j][2]),
-             fma2(uncentred(e[3][j]), s[j][3], z[j][3]));
+      sts128(tile_at(tile, d, 4 * q + j), centred(e[0][j]), centred(e[1][j]), centred(e[2][j]), centred(e[3][j]));
   }
 }
 
@@ -448,58 +483,72 @@ struct Ring {
   }
 };
 
-struct TallShared {
-  uint64_t raw_full[10], raw_empty[10], prep_full[10], op_full[4], op_empty[4];
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], q_full, q_empty, drain;
-  uint64_t bad[8];        // nodes with values that are not finite, per piece
-  long long total;
-  uint32_t tmem;
-  int abort;
-  int raw_dead[10], dead[kFlags];
-};
-
 // A CTA's part of one segment.
 struct Piece {
   int b, h, mp, ord;     // sequence, KV head, pair of row tiles, ordinal of the segment
   int u0, n;             // first unit in the segment, units
   int ng, fill, hb;      // of the sequence
 };
-// (Not inlined, as it runs once a piece in four places: the loops of this kernel
-// have to share the instruction caches.)
-__device__ __noinline__ void piece_at(int B, int n_mp, const Tables &T, int x, int x1, Piece &pc) {
-  Seg cur;
-  cur.seek(x, T, B);
-  pc.b = cur.b;
-  pc.h = n_mp == 1 ? cur.h : cur.h >> 1;
-  pc.mp = n_mp == 1 ? 0 : cur.h & 1;
-  pc.ord = cur.ord;
-  pc.u0 = cur.u;
-  pc.n = min(x1, cur.s0 + cur.len) - x;
-  pc.ng = T.ng[cur.b];
-  pc.fill = T.fill[cur.b];
-  pc.hb = T.hb[cur.b];
+
+__device__ __forceinline__ Tables tables_of(const int *tab) {
+  int *t = const_cast<int *>(tab);
+  return Tables{t, t + kMaxB, t + 2 * kMaxB, t + 3 * kMaxB, t + 4 * kMaxB, t + 5 * kMaxB, t + 6 * kMaxB};
+}
+
+struct TallShared {
+  uint64_t raw_full[10], raw_empty[10], prep_full[10], op_full[4], op_empty[4];
+  uint64_t scale_full[kScales], scale_empty[kScales];
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], q_full, q_empty, drain;
+  uint64_t bad[8];        // nodes with values that are not finite, per piece
+  long long total;
+  uint32_t tmem;
+  int abort;
+  int raw_dead[10], dead[kFlags];
+  Piece piece[kPrepWarp + 1];  // each warp's current one
+};
+
+// (Through shared memory, and not inlined: it runs once a piece in five places, whose
+// loops share the instruction caches; and no thread may have a stack.  With nearly all
+// of the SM's memory taken as shared memory, 27 warps' stacks of 200 bytes do not stay in
+// what is left, and every access of theirs went to L2: 1290 us instead of 725.)
+__device__ __noinline__ void piece_at(int B, int n_mp, const int *tab, int x, int x1, Piece *out) {
+  const Tables T = tables_of(tab);
+  int lo = 0, hi = B - 1;  // the last sequence whose units start at x or before (it has units)
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (T.base[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  const int len = T.len[lo], off = x - T.base[lo], seg = off / len, u0 = off - seg * len;
+  __syncwarp();
+  out->b = lo;
+  out->h = n_mp == 1 ? seg : seg >> 1;
+  out->mp = n_mp == 1 ? 0 : seg & 1;
+  out->ord = T.ord0[lo] + seg;
+  out->u0 = u0;
+  out->n = min(x1 - x, len - u0);
+  out->ng = T.ng[lo];
+  out->fill = T.fill[lo];
+  out->hb = T.hb[lo];
+  __syncwarp();
 }
 
 // bar's phase with the given parity, or false when the time is up or another role
 // gave up.  (The clock is asked late: reading it takes longer than most waits.)
-__device__ __noinline__ bool tall_wait_long(TallShared &s, uint32_t a, uint32_t parity, uint64_t ns) {
-  const uint64_t t0 = globaltimer_ns();
-  for (;;) {
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(a, parity)) return true;
+__device__ __forceinline__ bool tall_wait(TallShared &s, const uint64_t &bar, uint32_t parity, uint64_t ns) {
+  const uint32_t a = smem_addr(&bar);
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(a, parity)) return true;
+    if (i & 63) continue;
     if (*reinterpret_cast<volatile int *>(&s.abort)) return false;
-    if (globaltimer_ns() - t0 > ns) {
+    const uint64_t t = globaltimer_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > ns) {
       *reinterpret_cast<volatile int *>(&s.abort) = 1;
       return false;
     }
   }
-}
-__device__ __forceinline__ bool tall_wait(TallShared &s, const uint64_t &bar, uint32_t parity, uint64_t ns) {
-  const uint32_t a = smem_addr(&bar);
-#pragma unroll 1
-  for (int i = 0; i < 64; ++i)
-    if (mbar_try_wait(a, parity)) return true;
-  return tall_wait_long(s, a, parity, ns);
 }
 // The same for a whole warp: all lanes agree.
 __device__ __forceinline__ bool warp_wait(TallShared &s, const uint64_t &bar, uint32_t parity, uint64_t ns) {
@@ -507,46 +556,52 @@ __device__ __forceinline__ bool warp_wait(TallShared &s, const uint64_t &bar, ui
 }
 
 // 128 buffer tokens from i0 on into an operand tile, straight from memory: keys...
-__device__ __noinline__ void buffer_keys_tile(const uint4 *src, int base, int i0, int fill, uint32_t tile, int dt) {
-  uint4 x[8];
+__device__ __forceinline__ void buffer_keys_tile(const uint4 *src, int base, int i0, int fill, uint32_t tile, int dt) {
+  constexpr int kStep = 2 * kKeyWarps;  // tokens at a time
+#pragma unroll 1
+  for (int t0 = dt >> 4; t0 < kTile; t0 += 2 * kStep) {
+    uint4 x[2];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int t = (dt >> 4) + 16 * k;
-    x[k] = i0 + t < fill ? src[((base + t) & (kRing - 1)) * 16 + (dt & 15)] : make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < 2; ++k) {
+      const int t = t0 + kStep * k;
+      x[k] = t < kTile && i0 + t < fill ? src[((base + t) & (kRing - 1)) * 16 + (dt & 15)] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (t0 + kStep * k < kTile) sts_permuted(tile_at(tile, t0 + kStep * k, dt & 15), x[k]);
   }
-#pragma unroll
-  for (int k = 0; k < 8; ++k) sts_permuted(tile_at(tile, (dt >> 4) + 16 * k, dt & 15), x[k]);
 }
-// ... and values, eight tokens of eight channels per thread, turned in registers.
+// ... and values, four tokens of eight channels per thread, turned in registers.
 // Values of nodes (from token tree0 on) that are not finite become 0 (they meet the
 // zero weights of rows that do not see the node); returns those nodes' bits.
-__device__ __noinline__ uint64_t buffer_values_tile(const uint4 *src, int base, int i0, int fill, int tree0,
+__device__ __forceinline__ uint64_t buffer_values_tile(const uint4 *src, int base, int i0, int fill, int tree0,
                                                     uint32_t tile, int dt) {
-  const int tc = (dt & 7) | ((dt >> 4) & 8), dc = (dt >> 3) & 15;
-  uint4 x[8];
   uint64_t bad = 0;
+#pragma unroll 1
+  for (int i = dt; i < 512; i += 32 * kValWarps) {
+    const int tc = (i & 7) | ((i >> 4) & 8), dc = (i >> 3) & 15, t0 = 8 * tc + 4 * (i >> 8);
+    uint4 x[4];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int t = 8 * tc + k;
-    x[k] = i0 + t < fill ? src[((base + t) & (kRing - 1)) * 16 + dc] : make_uint4(0, 0, 0, 0);
-  }
+    for (int k = 0; k < 4; ++k)
+      x[k] = i0 + t0 + k < fill ? src[((base + t0 + k) & (kRing - 1)) * 16 + dc] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int j = i0 + 8 * tc + k - tree0;
-    if (j < 0) continue;
-    unsigned f = drop_nonfinite(x[k].x);
-    f |= drop_nonfinite(x[k].y);
-    f |= drop_nonfinite(x[k].z);
-    f |= drop_nonfinite(x[k].w);
-    if (f) bad |= 1ull << (j & 63);
-  }
-  const uint32_t *xs = reinterpret_cast<const uint32_t *>(x);
+    for (int k = 0; k < 4; ++k) {
+      const int j = i0 + t0 + k - tree0;
+      if (j < 0) continue;
+      unsigned f = drop_nonfinite(x[k].x);
+      f |= drop_nonfinite(x[k].y);
+      f |= drop_nonfinite(x[k].z);
+      f |= drop_nonfinite(x[k].w);
+      if (f) bad |= 1ull << (j & 63);
+    }
+    const uint32_t *xs = reinterpret_cast<const uint32_t *>(x);
 #pragma unroll
-  for (int d = 0; d < 8; ++d) {
-    const uint32_t sel = d & 1 ? 0x7632 : 0x5410;
-    const int k = d >> 1;
-    sts128(tile_at(tile, 8 * dc + d, tc), prmt(xs[k], xs[4 + k], sel), prmt(xs[8 + k], xs[12 + k], sel),
-           prmt(xs[16 + k], xs[20 + k], sel), prmt(xs[24 + k], xs[28 + k], sel));
+    for (int d = 0; d < 8; ++d) {
+      const uint32_t sel = d & 1 ? 0x7632 : 0x5410;
+      const int k = d >> 1;
+      sts64(tile_at(tile, 8 * dc + d, tc) + 8 * (i >> 8), prmt(xs[k], xs[4 + k], sel),
+            prmt(xs[8 + k], xs[12 + k], sel));
+    }
   }
   return bad;
 }
@@ -562,21 +617,22 @@ __device__ __forceinline__ int one_tile_row(int t, int s, int R) {
 
 // A piece's queries into their operand tiles (rows past the last: zeros).
 template <int MT>
-__device__ __noinline__ void query_tiles(const uint4 *src, int row0, int R, uint32_t tiles, int dt) {
+__device__ __forceinline__ void query_tiles(const uint4 *src, int row0, int R, uint32_t tiles, int dt) {
 #pragma unroll 1
-  for (int i0 = dt; i0 < MT * kTile * 16; i0 += 4 * 32 * kDeqWarps) {
-    uint4 x[4];
+  for (int i0 = dt; i0 < MT * kTile * 16; i0 += 2 * 32 * kKeyWarps) {
+    uint4 x[2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = i0 + k * 32 * kDeqWarps;
+    for (int k = 0; k < 2; ++k) {
+      const int i = i0 + k * 32 * kKeyWarps;
       int row = row0 + (i >> 4);
       if (MT == 1) row = max(one_tile_row(row, 0, R), one_tile_row(row, 1, R));
-      x[k] = row >= 0 && row < R ? src[(size_t)row * 16 + (i & 15)] : make_uint4(0, 0, 0, 0);
+      x[k] = i < MT * kTile * 16 && row >= 0 && row < R ? src[(size_t)row * 16 + (i & 15)] : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = i0 + k * 32 * kDeqWarps, row = i >> 4;
-      sts_permuted(tile_at(tiles + (row / kTile) * kTileBytes, row % kTile, i & 15), x[k]);
+    for (int k = 0; k < 2; ++k) {
+      const int i = i0 + k * 32 * kKeyWarps, row = i >> 4;
+      if (i < MT * kTile * 16)
+        sts_permuted(tile_at(tiles + (row / kTile) * kTileBytes, row % kTile, i & 15), x[k]);
     }
   }
 }
@@ -584,7 +640,7 @@ __device__ __noinline__ void query_tiles(const uint4 *src, int row0, int R, uint
 // The tokens i0 .. i0 + 127 of the buffer that a row sees, a bit each: those in front
 // of the tree, and of the tree the bits of sees.  The scores of the others become
 // -inf.
-__device__ __noinline__ void mask_scores(uint32_t t_s, int i0, int fill, int tree0, uint64_t sees, bool dead) {
+__device__ __forceinline__ void mask_scores(uint32_t t_s, int i0, int fill, int tree0, uint64_t sees, bool dead) {
 #pragma unroll 1
   for (int k = 0; k < 4; ++k) {
     const int i = i0 + 32 * k, before = tree0 - i;  // tokens of the word in front of the tree
@@ -596,12 +652,16 @@ __device__ __noinline__ void mask_scores(uint32_t t_s, int i0, int fill, int tre
     const int have = fill - i;
     if (have < 32) vis &= have <= 0 ? 0u : (1u << have) - 1;
     if (dead) vis = 0;
-    uint32_t v[32];
-    tc_ld32(t_s + 32 * k, v);
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      uint32_t v[16];
+      tc_ld16(t_s + 32 * k + 16 * h, v);
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (!(vis >> j & 1)) v[j] = 0xFF800000u;
-    tc_st32(t_s + 32 * k, v);
+      for (int j = 0; j < 16; ++j)
+        if (!(vis >> j & 1)) v[j] = 0xFF800000u;
+      tc_st16(t_s + 32 * k + 16 * h, v);
+      vis >>= 16;
+    }
   }
   tc_wait_st();
 }
@@ -623,12 +683,12 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
 #pragma unroll 1
     for (int i = 0; i < NR; ++i) {
       mbar_init(smem_addr(&sh.raw_full[i]), 1);
-      mbar_init(smem_addr(&sh.raw_empty[i]), kDeqWarps);
+      mbar_init(smem_addr(&sh.raw_empty[i]), kKeyWarps + 1);
       mbar_init(smem_addr(&sh.prep_full[i]), 1);
     }
 #pragma unroll 1
     for (int i = 0; i < NOP; ++i) {
-      mbar_init(smem_addr(&sh.op_full[i]), kDeqWarps);
+      mbar_init(smem_addr(&sh.op_full[i]), kKeyWarps);
       mbar_init(smem_addr(&sh.op_empty[i]), 1);
     }
 #pragma unroll 1
@@ -638,8 +698,13 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
       mbar_init(smem_addr(&sh.o_full[i]), 1);
       mbar_init(smem_addr(&sh.o_empty[i]), 4);
     }
-    mbar_init(smem_addr(&sh.q_full), kDeqWarps);
+    mbar_init(smem_addr(&sh.q_full), kKeyWarps);
     mbar_init(smem_addr(&sh.q_empty), 1);
+#pragma unroll 1
+    for (int i = 0; i < kScales; ++i) {
+      mbar_init(smem_addr(&sh.scale_full[i]), 1);
+      mbar_init(smem_addr(&sh.scale_empty[i]), MT == 2 ? 8 : 4);
+    }
     mbar_init(smem_addr(&sh.drain), 1);
     fence_mbar_init();
     sh.abort = 0;
@@ -668,8 +733,8 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
   const uint64_t ns = prm.wait_ns;
   auto bar = [&](const uint64_t &b) { return smem_addr(&b); };
   auto tile = [&](int slot) { return sbase + L::kOpOff + slot * kTileBytes; };
+  auto scale_at = [&](int slot) { return sbase + L::kScaleOff + slot * L::kScaleBytes; };
   auto raw_at = [&](int slot) { return sbase + L::kRawOff + slot * C::kRawBytes; };
-  Piece pc;
 
   if (w == kLoadWarp) {
     // ------------------------------------------------------------- copies
@@ -677,9 +742,11 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
     const uint64_t pol = l2_evict_first_policy();
     bool ok = true;
 #pragma unroll 1
-    for (int x = x0; ok && x < x1; x += pc.n) {
-      piece_at(c.B, prm.n_mp, T, x, x1, pc);
+    for (int x = x0; ok && x < x1;) {
+      piece_at(c.B, prm.n_mp, T.ng, x, x1, &sh.piece[w]);
+      const volatile Piece &pc = sh.piece[w];  // (read where needed)
       const int n = pc.n;
+      x += n;
       int at0 = -64, places = 0;  // lane k: the place of unit at0 + k
 #pragma unroll 1
       for (int i = 0; i < 2 * n; ++i) {
@@ -749,7 +816,8 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
       const uint64_t q_desc = operand_desc(sbase + L::kQOff), op_desc = operand_desc(sbase + L::kOpOff);
 #pragma unroll 1
       for (int x = x0; ok && x < x1; ++piece) {
-        piece_at(c.B, prm.n_mp, T, x, x1, pc);
+        piece_at(c.B, prm.n_mp, T.ng, x, x1, &sh.piece[w]);
+        const volatile Piece &pc = sh.piece[w];  // (read where needed)
         const int n = pc.n, steps = MT == 2 ? 2 * n + 2 : n + 2;
         x += n;
         Ring<NOP> rk = start, rv = start;  // the next keys' tile, the next values'
@@ -827,37 +895,61 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
   } else if (w == kPrepWarp) {
     // --------------------------------------------------- scales and zeros
     Ring<NR> raw;
+    Ring<kScales> sc;
+    int unit = 0;  // units so far
     bool ok = true;
 #pragma unroll 1
-    for (int x = x0; ok && x < x1; x += pc.n) {
-      piece_at(c.B, prm.n_mp, T, x, x1, pc);
-      const int n_grp = min(pc.n, max(0, pc.ng - pc.u0));
+    for (int x = x0; ok && x < x1;) {
+      piece_at(c.B, prm.n_mp, T.ng, x, x1, &sh.piece[w]);
+      const volatile Piece &pc = sh.piece[w];  // (read where needed)
+      const int n = pc.n;
+      x += n;
 #pragma unroll 1
-      for (int i = 0; i < 2 * n_grp; ++i) {
-        bool values;
-        item_of<MT>(i, n_grp, values);
-        ok = warp_wait(sh, sh.raw_full[raw.slot], raw.par, ns);
-        if (!ok) break;
-        if (!*reinterpret_cast<volatile int *>(&sh.raw_dead[raw.slot])) {
-          if (values) prep_values<MODE>(raw_at(raw.slot), lane);
-          else prep_keys<MODE>(raw_at(raw.slot), lane);
+      for (int i = 0; i < 2 * n; ++i) {
+        bool values, dead = false;
+        const int g = item_of<MT>(i, n, values);
+        const bool group = pc.u0 + g < pc.ng;
+        if (group) {
+          ok = warp_wait(sh, sh.raw_full[raw.slot], raw.par, ns);
+          if (!ok) break;
+          dead = *reinterpret_cast<volatile int *>(&sh.raw_dead[raw.slot]) != 0;
+        }
+        if (!values) {
+          if (!group) continue;
+          if (!dead) prep_keys<MODE>(raw_at(raw.slot), lane);
+        } else {
+          if (unit >= kScales) ok = warp_wait(sh, sh.scale_empty[sc.slot], sc.par ^ 1, ns);
+          if (!ok) break;
+          prep_values<MODE>(group ? raw_at(raw.slot) : 0, dead, scale_at(sc.slot), lane);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(sh.prep_full[raw.slot]));
-        raw.add(1);
+        if (lane == 0) {
+          if (group) {  // (of values too, so that the barrier's turns are the slot's)
+            mbar_arrive(bar(sh.prep_full[raw.slot]));
+            mbar_arrive(bar(sh.raw_empty[raw.slot]));
+          }
+          if (values) mbar_arrive(bar(sh.scale_full[sc.slot]));
+        }
+        if (group) raw.add(1);
+        if (values) {
+          sc.add(1);
+          ++unit;
+        }
       }
     }
   } else if (w >= kSoftWarps) {
     // ----------------------------------------------------- operand tiles
-    const bool values = w >= kSoftWarps + kDeqWarps;
-    const int dw = (w - kSoftWarps) & (kDeqWarps - 1), dt = dw * 32 + lane;
+    const bool values = w >= kSoftWarps + kKeyWarps;
+    const int dw = w - kSoftWarps - (values ? kKeyWarps : 0), dt = dw * 32 + lane;
+    const int threads = 32 * (values ? kValWarps : kKeyWarps), arrivals = values ? kValArrive : 1;
     Ring<NOP> start;
     Ring<NR> raw_start;
     int piece = 0, unit0 = 0, o0 = 0;
     bool ok = true;
 #pragma unroll 1
     for (int x = x0; ok && x < x1; ++piece) {
-      piece_at(c.B, prm.n_mp, T, x, x1, pc);
+      piece_at(c.B, prm.n_mp, T.ng, x, x1, &sh.piece[w]);
+      const volatile Piece &pc = sh.piece[w];  // (read where needed)
       const int n = pc.n, n_grp = min(n, max(0, pc.ng - pc.u0));  // units; groups among them
       const size_t bh = (size_t)pc.b * c.H + pc.h;
       x += n;
@@ -896,16 +988,16 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
         }
         const uint32_t dst = tile(op.slot), dst2 = tile(op2.slot);
         if (g < n_grp) {
-          // (the copy itself, and what the scales were made into)
+          // (the copy itself, and what the keys' scales were made into)
           if (!warp_wait(sh, sh.raw_full[raw.slot], raw.par, ns) ||
-              !warp_wait(sh, sh.prep_full[raw.slot], raw.par, ns)) {
+              (!values && !warp_wait(sh, sh.prep_full[raw.slot], raw.par, ns))) {
             ok = false;
             break;
           }
           const bool dead = *reinterpret_cast<volatile int *>(&sh.raw_dead[raw.slot]) != 0;
           if (dead) {  // a group that is left out: nothing that could disturb the sums
 #pragma unroll 1
-            for (int k = dt; k < kTileBytes / 16; k += 32 * kDeqWarps) {
+            for (int k = dt; k < kTileBytes / 16; k += threads) {
               sts128(dst + 16 * k, 0, 0, 0, 0);
               if (!values) sts128(dst2 + 16 * k, 0, 0, 0, 0);
             }
@@ -916,7 +1008,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
           }
           if (!values && dt == 0) *reinterpret_cast<volatile int *>(&sh.dead[(unit0 + g) % kFlags]) = dead;
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(sh.raw_empty[raw.slot]));
+          if (lane < arrivals) mbar_arrive(bar(sh.raw_empty[raw.slot]));
           raw.add(values ? values_step<MT>(g, n_grp, 1) : keys_step<MT>(g, 1));
         } else {
           const int i0 = (pc.u0 + g - pc.ng) * kTile, base = pc.hb * kG + i0;
@@ -925,7 +1017,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
             // (fp16 already: T2 is zero)
             buffer_keys_tile(reinterpret_cast<const uint4 *>(c.buf_k) + row0, base, i0, pc.fill, dst, dt);
 #pragma unroll 1
-            for (int k = dt; k < kTileBytes / 16; k += 32 * kDeqWarps) sts128(dst2 + 16 * k, 0, 0, 0, 0);
+            for (int k = dt; k < kTileBytes / 16; k += threads) sts128(dst2 + 16 * k, 0, 0, 0, 0);
           } else {
             const uint64_t bad = buffer_values_tile(reinterpret_cast<const uint4 *>(c.buf_v) + row0, base, i0,
                                                     pc.fill, pc.fill - prm.n_tree, dst, dt);
@@ -934,7 +1026,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
+        if (lane < arrivals) {
           mbar_arrive(bar(sh.op_full[op.slot]));
           if (!values) mbar_arrive(bar(sh.op_full[op2.slot]));
         }
@@ -953,11 +1045,14 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
     const uint32_t t_s = tmem + 128 * s + ((uint32_t)lanes << 16);
     const uint32_t t_o = tmem + 256 + 128 * s + ((uint32_t)lanes << 16);
     int n_s = 0, n_e = 0, unit0 = 0;
+    Ring<kScales> scale_start;
     bool ok = true;
 #pragma unroll 1
-    for (int x = x0, piece = 0; ok && x < x1; x += pc.n, ++piece) {
-      piece_at(c.B, prm.n_mp, T, x, x1, pc);
+    for (int x = x0, piece = 0; ok && x < x1; ++piece) {
+      piece_at(c.B, prm.n_mp, T.ng, x, x1, &sh.piece[w]);
+      const volatile Piece &pc = sh.piece[w];  // (read where needed)
       const int n = pc.n;
+      x += n;
       // (row: of the KV head; row_p: in the partial)
       const int row_p = MT == 2 ? row_t : one_tile_row(row_t, s, prm.R);
       const int row = MT == 2 ? 2 * kTile * pc.mp + s * kTile + row_t : row_p;
@@ -970,13 +1065,16 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
         if (bad) atomicOr(&c.state[(size_t)pc.b * QS_STATE_WORDS + QS_ST_ERR], QS_DEV_TREE);
         sees = ancestors_of(mm, prm.n_tree - prm.n_q + row % prm.n_q);
       }
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f, bv = 0.f;  // (bv: what the zeros of the values add)
       int done = 0;
       // the stream's units of the piece
 #pragma unroll 1
       for (int g = MT == 2 ? 0 : s; g < n; g += MT == 2 ? 1 : 2) {
         const int u = pc.u0 + g;
         ok = warp_wait(sh, sh.s_full[s], n_s & 1, ns);
+        Ring<kScales> sc = scale_start;  // unit g's value scales
+        sc.add_any(g);
+        ok = ok && warp_wait(sh, sh.scale_full[sc.slot], sc.par, ns);
         if (!ok) break;
         ++n_s;
         tc_after_sync();
@@ -984,10 +1082,10 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
           const bool dead = u < pc.ng && *reinterpret_cast<volatile int *>(&sh.dead[(unit0 + g) % kFlags]);
           if (dead || u >= pc.ng)
             mask_scores(t_s, (u - pc.ng) * kTile, pc.fill, pc.fill - prm.n_tree, sees, dead);
-          uint32_t v[32];
           float mx = -INFINITY;
 #pragma unroll 1
           for (int k = 0; k < 4; ++k) {
+            uint32_t v[32];
             tc_ld32(t_s + 32 * k, v);
             float a = __uint_as_float(v[0]), e = __uint_as_float(v[1]);
 #pragma unroll
@@ -1003,39 +1101,55 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
             const float a = raise ? (m == -INFINITY ? 0.f : fast_exp2(m - mn)) : 1.f;
             if (done > 0) {
 #pragma unroll 1
-              for (int k = 0; k < 4; ++k) {
-                tc_ld32(t_o + 32 * k, v);
+              for (int k = 0; k < 8; ++k) {
+                uint32_t v[16];
+                tc_ld16(t_o + 16 * k, v);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a);
-                tc_st32(t_o + 32 * k, v);
+                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a);
+                tc_st16(t_o + 16 * k, v);
               }
             }
             l *= a;
+            bv *= a;
             if (raise) m = mn;
           }
           const float off = m == -INFINITY ? 0.f : kExpShift - m;
+          // The values are codes: P' = p s, and their zeros go with p alone, in fp32.  (The
+          // largest p is a power of two, so P' of the token that counts most is exact.)
+          const f32x2 sl2 = pack2(prm.sl2, prm.sl2), off2 = pack2(off, off);
+          f32x2 l2 = pack2(0.f, 0.f), bv2 = l2;
+          const uint32_t scales = scale_at(sc.slot);
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            tc_ld32(t_s + 32 * k, v);
-            uint32_t ph[16];
-            float sum0 = 0.f, sum1 = 0.f;
+          for (int k = 0; k < 8; ++k) {
+            uint32_t y16[16], ph[8];
+            tc_ld16(t_s + 16 * k, y16);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float a = fast_exp2(fmaf(__uint_as_float(v[2 * i]), prm.sl2, off));
-              const float e = fast_exp2(fmaf(__uint_as_float(v[2 * i + 1]), prm.sl2, off));
-              sum0 += a;
-              sum1 += e;
-              ph[i] = pack_half2(a, e);
+            for (int i = 0; i < 4; ++i) {
+              const ulonglong2 s4 = lds2x64(scales + 64 * k + 16 * i), z4 = lds2x64(scales + 512 + 64 * k + 16 * i);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const f32x2 y = fma_f32x2(
+                    pack2(__uint_as_float(y16[4 * i + 2 * h]), __uint_as_float(y16[4 * i + 2 * h + 1])), sl2, off2);
+                const f32x2 p = pack2(fast_exp2(lo_of(y)), fast_exp2(hi_of(y)));
+                l2 = add_f32x2(l2, p);
+                bv2 = fma_f32x2(p, h ? z4.y : z4.x, bv2);
+                const f32x2 ps = mul_f32x2(p, h ? s4.y : s4.x);
+                ph[2 * i + h] = pack_half2(lo_of(ps), hi_of(ps));
+              }
             }
-            l += sum0 + sum1;
-            tc_st16(t_s + 16 * k, ph);
+            tc_st8(t_s + 8 * k, ph);
           }
+          l += lo_of(l2) + hi_of(l2);
+          bv += lo_of(bv2) + hi_of(bv2);
           tc_wait_st();
         }
         ++done;
         tc_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(sh.p_full[s]));
+        if (lane == 0) {
+          mbar_arrive(bar(sh.p_full[s]));
+          mbar_arrive(bar(sh.scale_empty[sc.slot]));
+        }
       }
       if (!ok) break;
       // the piece's partial: rows side by side, four channels each
@@ -1049,17 +1163,17 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
         tc_after_sync();
         if (live_warp) {
           if (sees & *reinterpret_cast<volatile uint64_t *>(&sh.bad[piece & 7])) l = NAN;
-          const float poison = l == l ? 0.f : NAN;
+          const float add = l == l ? bv : NAN;
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            uint32_t v[32];
-            tc_ld32(t_o + 32 * k, v);
+          for (int k = 0; k < 8; ++k) {
+            uint32_t v[16];
+            tc_ld16(t_o + 16 * k, v);
             if (mine)
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                reinterpret_cast<float4 *>(part)[(8 * k + i) * prm.rows + row_p] =
-                    make_float4(__uint_as_float(v[4 * i]) + poison, __uint_as_float(v[4 * i + 1]) + poison,
-                                __uint_as_float(v[4 * i + 2]) + poison, __uint_as_float(v[4 * i + 3]) + poison);
+              for (int i = 0; i < 4; ++i)
+                reinterpret_cast<float4 *>(part)[(4 * k + i) * prm.rows + row_p] =
+                    make_float4(__uint_as_float(v[4 * i]) + add, __uint_as_float(v[4 * i + 1]) + add,
+                                __uint_as_float(v[4 * i + 2]) + add, __uint_as_float(v[4 * i + 3]) + add);
           }
         }
         tc_before_sync();
@@ -1071,6 +1185,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
         part[prm.rows * (kD + 1) + row_p] = l;
       }
       unit0 += n;
+      scale_start.add_any(n);
     }
   }
   __syncthreads();
