@@ -257,8 +257,7 @@ __device__ __forceinline__ void sts_permuted(uint32_t a, uint4 x) {
   sts128(a, prmt(x.x, x.z, 0x5410), prmt(x.x, x.z, 0x7632), prmt(x.y, x.w, 0x5410), prmt(x.y, x.w, 0x7632));
 }
 
-// Four (N = 4) or two words of upper codes, and of lower ones, from word 4 i (2 i) of a
-// plane on; a two-bit draft gets its C_U2 words doubled.
+// Four words of upper codes, and of lower ones, from word 4 i of a plane on; a two-bit draft gets its C_U2 words doubled.
 template <int MODE, int UB>
 __device__ __forceinline__ void raw_words4(uint32_t raw, int i, uint32_t (&u)[4], uint32_t (&l)[4]) {
   using C = TallCfg<MODE>;
@@ -280,27 +279,6 @@ __device__ __forceinline__ void raw_words4(uint32_t raw, int i, uint32_t (&u)[4]
   if (!C::kDraft) {
     const uint4 x = lds128(raw + C::kLowOff + 16 * i);
     l[0] = x.x; l[1] = x.y; l[2] = x.z; l[3] = x.w;
-  }
-}
-template <int MODE, int UB>
-__device__ __forceinline__ void raw_words2(uint32_t raw, int i, uint32_t (&u)[2], uint32_t (&l)[2]) {
-  using C = TallCfg<MODE>;
-  if (UB == 4) {
-    const uint2 x = lds64(raw + C::kUpOff + 8 * i);
-    u[0] = x.x; u[1] = x.y;
-  } else {
-    const uint32_t a = lds32(raw + C::kUpOff + 4 * i);
-    if (C::kDraft) {
-      u[0] = u[1] = a;
-    } else {
-      const uint32_t m = lds32(raw + C::kUpOff + 4096 + 4 * i);
-      u[0] = upper_from2(a, m, 0); u[1] = upper_from2(a, m, 2);
-    }
-  }
-  l[0] = l[1] = 0;
-  if (!C::kDraft) {
-    const uint2 x = lds64(raw + C::kLowOff + 8 * i);
-    l[0] = x.x; l[1] = x.y;
   }
 }
 template <int MODE, int UB, int W>
@@ -379,42 +357,44 @@ __device__ __forceinline__ void prep_values(uint32_t raw, bool dead, uint32_t to
   }
 }
 
-// A group's keys into the tiles T1 and T2, by the key warps (dw): a lane takes 16
-// channels of a token, a warp 4 tokens at a time; the scales stay in registers.  The
-// lanes of a quarter-warp write all eight 16-byte columns of the swizzle.
+// A group's keys into the tiles T1 and T2, by the key warps (dw): a lane takes a word
+// (eight channels) of a token, a warp two tokens at a time, kAhead of them loaded
+// before the first is used; the scales stay in registers.  The lanes of a
+// quarter-warp write all eight 16-byte columns of the swizzle.
 template <int MODE, int UB>
 __device__ __forceinline__ void keys_tile(uint32_t raw, uint32_t t1, uint32_t t2, int dw, int lane) {
-  const int p = (lane & 3) | ((lane >> 1) & 4), tl = ((lane >> 2) & 1) | ((lane >> 3) & 2);
-  // the 16-byte piece of a scale row that holds word w of the lane's channels (words
-  // 2 p + w of a token's 16)
-  uint32_t sh[2][4], sl[2][4], zh[2][4], zl[2][4];
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const int word = 2 * p + w, at = 16 * ((word >> 2) + 4 * (word & 3));
-    const uint32_t prep = raw + TallCfg<MODE>::kPrepOff + at;
-    const uint4 a = lds128(prep), b = lds128(prep + 256), d = lds128(prep + 512), f = lds128(prep + 768);
-    sh[w][0] = a.x; sh[w][1] = a.y; sh[w][2] = a.z; sh[w][3] = a.w;
-    sl[w][0] = b.x; sl[w][1] = b.y; sl[w][2] = b.z; sl[w][3] = b.w;
-    zh[w][0] = d.x; zh[w][1] = d.y; zh[w][2] = d.z; zh[w][3] = d.w;
-    zl[w][0] = f.x; zl[w][1] = f.y; zl[w][2] = f.z; zl[w][3] = f.w;
-  }
+  using C = TallCfg<MODE>;
+  constexpr int kAhead = 4;
+  static_assert(kTile % (2 * kKeyWarps * kAhead) == 0, "");
+  const int w = lane & 15, f = 2 * (w & 1);
+  // the 16-byte piece of a scale row that belongs to word w
+  const uint32_t prep = raw + C::kPrepOff + 16 * ((w >> 2) + 4 * (w & 3));
+  const uint4 sh = lds128(prep), sl = lds128(prep + 256), zh = lds128(prep + 512), zl = lds128(prep + 768);
 #pragma unroll 1
-  for (int t = 4 * dw + tl; t < kTile; t += 4 * kKeyWarps) {
-    uint32_t u[2], l[2], e[4] = {};
-    raw_words2<MODE, UB>(raw, 8 * t + p, u, l);
-    auto put = [&](int w) {
+  for (int t0 = 2 * dw + (lane >> 4); t0 < kTile; t0 += 2 * kKeyWarps * kAhead) {
+    uint32_t u[kAhead], l[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int t = t0 + 2 * kKeyWarps * k;
+      if (UB == 4) {
+        u[k] = lds32(raw + C::kUpOff + 64 * t + 4 * w);
+      } else {
+        u[k] = lds32(raw + C::kUpOff + 32 * t + 4 * (w >> 1));
+        if (C::kDraft) u[k] >>= f;
+        else u[k] = upper_from2(u[k], lds32(raw + C::kUpOff + 4096 + 32 * t + 4 * (w >> 1)), f);
+      }
+      l[k] = C::kDraft ? 0 : lds32(raw + C::kLowOff + 64 * t + 4 * w);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      uint32_t e[4];
+      word_pairs<MODE, UB, 0>(u[k], l[k], e);
 #pragma unroll
       for (int j = 0; j < 4; ++j) e[j] = centred(e[j]);
-      const uint32_t at = tile_at(0, t, 2 * p + w);
-      sts128(t1 + at, fma2(e[0], sh[w][0], zh[w][0]), fma2(e[1], sh[w][1], zh[w][1]),
-             fma2(e[2], sh[w][2], zh[w][2]), fma2(e[3], sh[w][3], zh[w][3]));
-      sts128(t2 + at, fma2(e[0], sl[w][0], zl[w][0]), fma2(e[1], sl[w][1], zl[w][1]),
-             fma2(e[2], sl[w][2], zl[w][2]), fma2(e[3], sl[w][3], zl[w][3]));
-    };
-    word_pairs<MODE, UB, 0>(u[0], l[0], e);
-    put(0);
-    word_pairs<MODE, UB, 1>(u[1], l[1], e);
-    put(1);
+      const uint32_t at = tile_at(0, t0 + 2 * kKeyWarps * k, w);
+      sts128(t1 + at, fma2(e[0], sh.x, zh.x), fma2(e[1], sh.y, zh.y), fma2(e[2], sh.z, zh.z), fma2(e[3], sh.w, zh.w));
+      sts128(t2 + at, fma2(e[0], sl.x, zl.x), fma2(e[1], sl.y, zl.y), fma2(e[2], sl.z, zl.z), fma2(e[3], sl.w, zl.w));
+    }
   }
 }
 
