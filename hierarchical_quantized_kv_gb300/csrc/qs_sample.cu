@@ -51,6 +51,7 @@ constexpr int kQueue = 32 + 32 * 8;  // places that a warp collects
 constexpr int kMaxC = 8;          // CTAs to a row at most
 constexpr int kSmallK = 512;      // top-k at most for the short way
 constexpr int kFew = 128;         // candidates that are put in order by counting
+constexpr int kFewInBin = 256;    // ... of a bin
 constexpr int kUnit = 44;         // a weight of 1 is 2^44
 constexpr int kOutline = 14;      // an outline of the weights is in multiples of 2^14
 constexpr float kNone = -INFINITY;
@@ -158,7 +159,7 @@ __device__ __noinline__ u64 part_of(u64 x, float y) {
 struct Shared {
   float mx, mn, mt;       // of the slice: largest, smallest; the smallest of the threads' largest
   float rmx, rmn;         // of the bin that is spread again
-  u64 total[2];           // sum of a pass over the slice (one pass, and the next)
+  u64 total[2][2];        // sums of a pass over the slice (one pass, and the next)
   u64 front, in_bin;      // in front of a bin, and in it
   float top_p, min_p, u;  // of the row, read by the first CTA for all
   int top_k;
@@ -272,17 +273,25 @@ struct Row {
     for (int k = 0; k < kWarpsS; ++k) a += s.scan[k];
     return a;
   }
-  // The cluster's sum of each CTA's own; what the lower ranks have.
-  __device__ __noinline__ u64 exchange(u64 own, u64 &before) {
+  // The cluster's sum of each CTA's own; what the lower ranks have; and the sum of
+  // a second number.
+  __device__ __noinline__ u64 exchange(u64 own, u64 &before, u64 own2, u64 &total2) {
     // (a CTA may be a pass ahead of one that still reads this sum, never two)
     const int k = pass++ & 1;
-    if (tid == 0) s.total[k] = own;
+    if (tid == 0) {
+      s.total[k][0] = own;
+      s.total[k][1] = own2;
+    }
     cluster_sync();
     // (the sums of all CTAs at once, a lane each)
-    const u64 t = lane < C ? of(lane).total[k] : 0;
+    const u64 t = lane < C ? of(lane).total[k][0] : 0, t2 = lane < C ? of(lane).total[k][1] : 0;
     before = warp_sum(lane < rank ? t : 0);
-    const u64 total = warp_sum(t);
-    return total;
+    total2 = warp_sum(t2);
+    return warp_sum(t);
+  }
+  __device__ __forceinline__ u64 exchange(u64 own, u64 &before) {
+    u64 none;
+    return exchange(own, before, 0, none);
   }
 
   // Sums of weight(x, index) in the order of the indices: the cluster's total, what
@@ -709,6 +718,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
     }
   }
+  float *probs = a.probs ? a.probs + (size_t)row * a.V : nullptr;
+  if (probs) {
+    // zeros, while the rest is found out; what is kept is written over them at the end
+    // (by other threads, many barriers later)
+    float *z = probs + lo_i;
+    const int head = min(n, (int)(-(reinterpret_cast<uintptr_t>(z) >> 2) & 3)), quads = (n - head) >> 2;
+    if (tid < head) z[tid] = 0.f;
+    float4 *z4 = reinterpret_cast<float4 *>(z + head);
+    for (int i = tid; i < quads; i += kThreads) z4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int i = head + 4 * quads + tid;
+    if (i < n) z[i] = 0.f;
+  }
   const float mine = hi;  // the largest of this thread's logits
   float mn, mt = hi > kNone ? hi : INFINITY;
   {
@@ -753,11 +774,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     mt = __shfl_sync(0xffffffffu, mt, 0);
   }
   const float m = R.m = hi;
-  float *probs = a.probs ? a.probs + (size_t)row * a.V : nullptr;
   if (!(m > kNone)) {  // nothing to keep (the whole cluster alike)
     if (rank == 0 && tid == 0) a.token[row] = -1;
-    if (probs)
-      for (int i = lo_i + tid; i < hi_i; i += kThreads) probs[i] = 0.f;
     cluster_sync();  // (the others have read this CTA's maximum)
     return;
   }
@@ -904,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     if (k < a.V)
       R.template element<true>(k == 1 ? m : floor_x, m, [](float) -> u64 { return 1; }, (u64)k, t, tie);
     if (tie < 0) t = kNone;
-    u64 front, own;
+    u64 front, own, total = 0;  // of what is kept (0: not known yet)
     if (top_p < 1.f && k > 1) {
       // ---- top-p: the total and an outline of the weights, then the bin it points to
       const float lo_p = fmaxf(floor_x, t);
@@ -925,8 +943,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           if (r & 0x7FFF) atomicAdd(&hist[b], r & 0x7FFF);
           if (r >> 15) atomicAdd(&hist[kBins + b], r >> 15);
         });
-        const u64 total = R.exchange(R.block_sum(sum), front);
-        target = ceil_part_of(total, top_p);
+        target = ceil_part_of(R.exchange(R.block_sum(sum), front), top_p);
         if (target < 1) target = 1;
         if (rank == 0) {
           u64 bw[Row<T>::P];
@@ -962,46 +979,87 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                       R.collect(s0, list0, x, i);
                     }
                   });
-        u64 none;
-        const u64 sum_a = R.exchange(R.block_sum(above), none);
-        const u64 sum_i = R.exchange(R.block_sum(inside), none);
+        // (a warp's share is that of its run of the slice, as the draw wants it)
+        above = R.warp_sum(above);
+        if (lane == 0) s.part[warp] = above;
+        u64 sum_i;
+        const u64 own_a = R.block_sum(lane == 0 ? above : 0);
+        __syncthreads();
+        const u64 sum_a = R.exchange(own_a, front, R.block_sum(inside), sum_i);
         const int n_list = s0.n_list;
         found = bin >= 0 && n_list <= kCap && sum_a < target && target <= sum_a + sum_i;
         if (found && rank == 0) {
-          R.sort(n_list);
-          const int i = R.reach(n_list, w, sum_a, target);
-          if (tid == 0) {
-            s.t = Row<T>::value(R.list[i]);
-            s.tie = (int)(uint32_t)R.list[i];
+          if (n_list <= kFewInBin) {
+            // a thread each: the one whose turn it is knows it from those in front of it
+            u64 *weight_of = reinterpret_cast<u64 *>(smem + a.part_off);
+            u64 e = 0, wx = 0, before = sum_a;
+            if (tid < n_list) {
+              e = R.list[tid];
+              weight_of[tid] = wx = w(Row<T>::value(e));
+            }
+            __syncthreads();
+            if (tid < n_list) {
+#pragma unroll 4
+              for (int i = 0; i < n_list; ++i)
+                if (R.list[i] < e) before += weight_of[i];
+              if (before < target && target <= before + wx) {
+                s.t = Row<T>::value(e);
+                s.tie = (int)(uint32_t)e;
+                s.front = before + wx;
+              }
+            }
+          } else {
+            R.sort(n_list);
+            const int at = R.reach(n_list, w, sum_a, target);
+            if (tid == 0) {
+              s.t = Row<T>::value(R.list[at]);
+              s.tie = (int)(uint32_t)R.list[at];
+              s.front = 0;
+            }
           }
         }
         cluster_sync();
         if (found) {
           t = s0.t;
           tie = s0.tie;
+          // Where min-p takes nothing more, the draw's sums are known but for the bin's
+          // share in them: of the slices in front, and of this one's warps.
+          const u64 all = s0.front;
+          if (all && !(x_min > t)) {
+            const int per_warp = max(1, (n_vec + kWarpsS - 1) / kWarpsS);
+            u64 f = 0;
+            if (tid < n_list) {
+              const u64 e = list0[tid];
+              const float x = Row<T>::value(e);
+              const int i = (int)(uint32_t)e;
+              if (i < hi_i && in_front(x, i)) {
+                const u64 wx = w(x);
+                if (i < lo_i) f = wx;
+                else atomicAdd(&s.part[(i - R.x0) / E / per_warp], wx);
+              }
+            }
+            front += R.block_sum(f);
+            total = all;
+          }
         }
       } else {
         // all equal: so many of them
-        const u64 total = R.sums([&](float x, int i) -> u64 { return in_front(x, i) ? w(x) : 0; }, front, own);
-        target = ceil_part_of(total, top_p);
+        target = ceil_part_of(
+            R.sums([&](float x, int i) -> u64 { return in_front(x, i) ? w(x) : 0; }, front, own), top_p);
         if (target < 1) target = 1;
       }
       if (!found) R.template element<false>(lo_p, m, w, target, t, tie);
     }
     auto kept = [&](float x, int i) -> u64 { return x >= x_min && in_front(x, i) ? w(x) : 0; };
-    const u64 total = R.sums_named([&](float x, int i) { return x >= x_min && x >= floor_x && in_front(x, i); },
-                                   w, front, own);
+    if (!total)
+      total = R.sums_named([&](float x, int i) { return x >= x_min && x >= floor_x && in_front(x, i); }, w, front, own);
     const int index = R.locate(kept, front, draw_target(total, u));
     if (index >= 0) a.token[row] = index;
     scale = 17592186044416.f / (float)total;
   }
-  if (probs) {
-    // zeros side by side, then the kept ones
-    for (int i = lo_i + tid; i < hi_i; i += kThreads) probs[i] = 0.f;
-    __syncthreads();
+  if (probs)
     R.named([&](float x, int i) { return x >= x_min && in_front(x, i); },
             [&](float x, int i) { probs[i] = w.scaled(x, scale); });
-  }
   cluster_sync();  // the others have read this CTA's sums
 }
 
@@ -1034,12 +1092,12 @@ extern "C" qs_status qs_sample(const void *logits, qs_dtype dtype, int32_t rows,
   SampleArgs a = {logits, V, 1, rows > 1 ? row_stride : 0, temperature, top_p, min_p, u, top_k, token,
                   probs, 0, 0, 0, 0};
   // CTAs to a row: so many that two fit an SM (slices of 64 KB), and more while all
-  // rows' CTAs still run at once and have 4096 logits each.  (Measured: RULE)
+  // rows' CTAs still run at once and have 8192 logits each.  (RULE)
   int sms = 0;
   const qs_status st0 = sm_count(&sms);
   if (st0 != QS_OK) return st0;
   while (a.C < kMaxC && (long long)V * size > 66 * 1024 * a.C) a.C *= 2;
-  while (a.C < kMaxC && (long long)rows * a.C <= sms && V > 4096 * a.C) a.C *= 2;
+  while (a.C < kMaxC && (long long)rows * a.C <= sms && V > 8192 * a.C) a.C *= 2;
   const int per = (V + a.C - 1) / a.C;
   a.hist_off = (per * size + 32 + 127) / 128 * 128;
   // (the candidates' weights take room of a histogram: no step has both)
