@@ -56,8 +56,9 @@ constexpr int kMmaWarp = kSoftWarps + kKeyWarps + kValWarps, kLoadWarp = kMmaWar
 constexpr int kTallThreads = 32 * (kPrepWarp + 1);
 constexpr float kRaise = 8.f;              // log2 by which a maximum may be behind
 constexpr int kFlags = 8;                  // units whose flags are kept
-constexpr int kScales = 4;                 // units whose value scales are kept
+constexpr int kScales = 3;                 // units whose value scales are kept
 constexpr int kMaxTreeRows = 512;
+constexpr int kStaticBytes = 3584;         // room for TallShared
 
 // A piece of a unit in the ring of raw copies: keys or values.
 template <int MODE>
@@ -75,7 +76,7 @@ struct TallLayout {
   static constexpr int kOpOff = MT * kTileBytes;
   static constexpr int kRawOff = kOpOff + op_tiles<MT>() * kTileBytes;
   static constexpr int kScaleBytes = 1024;  // 128 tokens' s, and z + 128 s, in fp32
-  static constexpr int kRest = 227 * 1024 - 1024 - kRawOff - 7 * kMaxB * 4 - kScales * kScaleBytes - 768;
+  static constexpr int kRest = 227 * 1024 - 1024 - kRawOff - 7 * kMaxB * 4 - kScales * kScaleBytes - kStaticBytes;
   static constexpr int kRawFit = kRest / TallCfg<MODE>::kRawBytes;
   static constexpr int kRaw = kRawFit < 10 ? kRawFit : 10;
   static constexpr int kScaleOff = kRawOff + kRaw * TallCfg<MODE>::kRawBytes;
@@ -478,14 +479,16 @@ __device__ __forceinline__ Tables tables_of(const int *tab) {
 struct TallShared {
   uint64_t raw_full[10], raw_empty[10], prep_full[10], op_full[4], op_empty[4];
   uint64_t scale_full[kScales], scale_empty[kScales];
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], q_full, q_empty, drain;
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], q_full, q_empty, drain, pair[4];
   uint64_t bad[8];        // nodes with values that are not finite, per piece
   long long total;
   uint32_t tmem;
   int abort;
   int raw_dead[10], dead[kFlags];
   Piece piece[kPrepWarp + 1];  // each warp's current one
+  float swap[2][kSoftWarps][32];  // between two threads of a row
 };
+static_assert(sizeof(TallShared) <= kStaticBytes, "");
 
 // (Through shared memory, and not inlined: it runs once a piece in five places, whose
 // loops share the instruction caches; and no thread may have a stack.  With nearly all
@@ -617,12 +620,21 @@ __device__ __forceinline__ void query_tiles(const uint4 *src, int row0, int R, u
   }
 }
 
+// Up to this many rows a row has two threads in the softmax, of warps that read the
+// same lanes of tensor memory, for 64 tokens each.
+constexpr int kPairedRows = 64;
+
+// Column of the first of tokens 16 k .. of P, in the place of S: with each half of the
+// tokens inside its half of S, so that two warps do not write what the other reads.
+__device__ __forceinline__ constexpr int p_column(int k) { return 8 * k + (k >= 4 ? 32 : 0); }
+
 // The tokens i0 .. i0 + 127 of the buffer that a row sees, a bit each: those in front
-// of the tree, and of the tree the bits of sees.  The scores of the others become
-// -inf.
-__device__ __forceinline__ void mask_scores(uint32_t t_s, int i0, int fill, int tree0, uint64_t sees, bool dead) {
+// of the tree, and of the tree the bits of sees.  The scores of the others (of tokens
+// 16 k0 .. 16 k1 - 1) become -inf.
+__device__ __forceinline__ void mask_scores(uint32_t t_s, int k0, int k1, int i0, int fill, int tree0, uint64_t sees,
+                                            bool dead) {
 #pragma unroll 1
-  for (int k = 0; k < 4; ++k) {
+  for (int k = k0 >> 1; k < k1 >> 1; ++k) {
     const int i = i0 + 32 * k, before = tree0 - i;  // tokens of the word in front of the tree
     uint32_t vis = before >= 32 ? ~0u : before <= 0 ? 0u : (1u << before) - 1;
     if (before < 32) {
@@ -686,6 +698,8 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
       mbar_init(smem_addr(&sh.scale_empty[i]), MT == 2 ? 8 : 4);
     }
     mbar_init(smem_addr(&sh.drain), 1);
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) mbar_init(smem_addr(&sh.pair[i]), 2);
     fence_mbar_init();
     sh.abort = 0;
 #pragma unroll 1
@@ -818,7 +832,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
             if (elect_one()) {
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                mma_ts(tmem + 256 + 128 * s, tmem + 128 * s + 8 * k, b + ((k >> 2) * (kTile * 8) + (k & 3) * 2),
+                mma_ts(tmem + 256 + 128 * s, tmem + 128 * s + p_column(k), b + ((k >> 2) * (kTile * 8) + (k & 3) * 2),
                        !first || k > 0);
               if (MT == 1 || s == 1) mma_commit(bar(sh.op_empty[rv.slot]));
               if (last) mma_commit(bar(sh.o_full[s]));
@@ -833,7 +847,8 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
           if (g < n) {
             Ring<NOP> r2 = rk;
             r2.add(1);
-            ok = warp_wait(sh, sh.op_full[rk.slot], rk.par, ns) && warp_wait(sh, sh.op_full[r2.slot], r2.par, ns);
+            // (the first tile's arrivals come before the second one's)
+            ok = warp_wait(sh, sh.op_full[r2.slot], r2.par, ns);
             if (ok && g == 0) ok = warp_wait(sh, sh.q_full, piece & 1, ns);
             if (!ok) break;
             tc_after_sync();
@@ -958,19 +973,17 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
       for (int g = 0; g < n; ++g) {
         Ring<NOP> op2 = op;  // (the keys' second tile)
         op2.add(1);
-        if (o >= NOP && !warp_wait(sh, sh.op_empty[op.slot], op.par ^ 1, ns)) {
-          ok = false;
-          break;
-        }
-        if (!values && o + 1 >= NOP && !warp_wait(sh, sh.op_empty[op2.slot], op2.par ^ 1, ns)) {
+        // (tiles are consumed in the ring's order: with the second one free the first is)
+        const Ring<NOP> &last = values ? op : op2;
+        if (o + (values ? 0 : 1) >= NOP && !warp_wait(sh, sh.op_empty[last.slot], last.par ^ 1, ns)) {
           ok = false;
           break;
         }
         const uint32_t dst = tile(op.slot), dst2 = tile(op2.slot);
         if (g < n_grp) {
-          // (the copy itself, and what the keys' scales were made into)
-          if (!warp_wait(sh, sh.raw_full[raw.slot], raw.par, ns) ||
-              (!values && !warp_wait(sh, sh.prep_full[raw.slot], raw.par, ns))) {
+          // the copy; and, by a warp that has waited for it, what the keys' scales were
+          // made into
+          if (!warp_wait(sh, values ? sh.raw_full[raw.slot] : sh.prep_full[raw.slot], raw.par, ns)) {
             ok = false;
             break;
           }
@@ -1021,12 +1034,25 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const int s = w >> 2, lanes = 32 * (w & 3), row_t = lanes + lane;  // stream; row in the tile
+    const bool paired = MT == 1 && prm.R <= kPairedRows;
+    const int s = paired ? (w >> 1) & 1 : w >> 2, lanes = 32 * (w & 3), row_t = lanes + lane;  // stream; row in the tile
+    // this warp's share of the tokens, and of the channels of O, in sixteens
+    const int k0 = paired ? w & 4 : 0, k1 = paired ? k0 + 4 : 8;
     const uint32_t t_s = tmem + 128 * s + ((uint32_t)lanes << 16);
     const uint32_t t_o = tmem + 256 + 128 * s + ((uint32_t)lanes << 16);
-    int n_s = 0, n_e = 0, unit0 = 0;
+    int n_s = 0, n_e = 0, n_x = 0, unit0 = 0;
     Ring<kScales> scale_start;
     bool ok = true;
+    // what the row's other thread has
+    auto swap = [&](float mine, float &other) {
+      sh.swap[n_x & 1][w][lane] = mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sh.pair[w & 3]));
+      if (!warp_wait(sh, sh.pair[w & 3], n_x & 1, ns)) return false;
+      other = sh.swap[n_x & 1][w ^ 4][lane];
+      ++n_x;
+      return true;
+    };
 #pragma unroll 1
     for (int x = x0, piece = 0; ok && x < x1; ++piece) {
       piece_at(c.B, prm.n_mp, T.ng, x, x1, &sh.piece[w]);
@@ -1061,12 +1087,12 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
         if (live_warp) {
           const bool dead = u < pc.ng && *reinterpret_cast<volatile int *>(&sh.dead[(unit0 + g) % kFlags]);
           if (dead || u >= pc.ng)
-            mask_scores(t_s, (u - pc.ng) * kTile, pc.fill, pc.fill - prm.n_tree, sees, dead);
+            mask_scores(t_s, k0, k1, (u - pc.ng) * kTile, pc.fill, pc.fill - prm.n_tree, sees, dead);
           float mx = -INFINITY;
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
+          for (int k = k0; k < k1; k += 2) {
             uint32_t v[32];
-            tc_ld32(t_s + 32 * k, v);
+            tc_ld32(t_s + 16 * k, v);
             float a = __uint_as_float(v[0]), e = __uint_as_float(v[1]);
 #pragma unroll
             for (int i = 2; i < 32; i += 2) {
@@ -1075,13 +1101,19 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
             }
             mx = fmaxf(mx, fmaxf(a, e));
           }
+          if (paired) {
+            float other;
+            ok = swap(mx, other);
+            if (!ok) break;
+            mx = fmaxf(mx, other);
+          }
           const float mn = mx * prm.sl2;
           const bool raise = mn > m + kRaise || (m == -INFINITY && mn > -INFINITY);
           if (__any_sync(0xffffffffu, raise)) {
             const float a = raise ? (m == -INFINITY ? 0.f : fast_exp2(m - mn)) : 1.f;
             if (done > 0) {
 #pragma unroll 1
-              for (int k = 0; k < 8; ++k) {
+              for (int k = k0; k < k1; ++k) {
                 uint32_t v[16];
                 tc_ld16(t_o + 16 * k, v);
 #pragma unroll
@@ -1100,7 +1132,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
           f32x2 l2 = pack2(0.f, 0.f), bv2 = l2;
           const uint32_t scales = scale_at(sc.slot);
 #pragma unroll 1
-          for (int k = 0; k < 8; ++k) {
+          for (int k = k0; k < k1; ++k) {
             uint32_t y16[16], ph[8];
             tc_ld16(t_s + 16 * k, y16);
 #pragma unroll
@@ -1117,7 +1149,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
                 ph[2 * i + h] = pack_half2(lo_of(ps), hi_of(ps));
               }
             }
-            tc_st8(t_s + 8 * k, ph);
+            tc_st8(t_s + p_column(k), ph);
           }
           l += lo_of(l2) + hi_of(l2);
           bv += lo_of(bv2) + hi_of(bv2);
@@ -1132,6 +1164,13 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
         }
       }
       if (!ok) break;
+      if (paired && live_warp) {
+        float l2, bv2;
+        ok = swap(l, l2) && swap(bv, bv2);
+        if (!ok) break;
+        l += l2;
+        bv += bv2;
+      }
       // the piece's partial: rows side by side, four channels each
       float *part = prm.ws + ((size_t)(pc.ord + p) * 2 + s) * prm.rows * (kD + 2);
       const bool mine = live_warp && row < prm.R &&
@@ -1145,7 +1184,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
           if (sees & *reinterpret_cast<volatile uint64_t *>(&sh.bad[piece & 7])) l = NAN;
           const float add = l == l ? bv : NAN;
 #pragma unroll 1
-          for (int k = 0; k < 8; ++k) {
+          for (int k = k0; k < k1; ++k) {
             uint32_t v[16];
             tc_ld16(t_o + 16 * k, v);
             if (mine)
@@ -1160,7 +1199,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sh.o_empty[s]));
       }
-      if (mine) {
+      if (mine && k0 == 0) {
         part[prm.rows * kD + row_p] = m;
         part[prm.rows * (kD + 1) + row_p] = l;
       }
