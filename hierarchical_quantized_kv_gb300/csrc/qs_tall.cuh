@@ -7,7 +7,10 @@
 //   P = 2^(S c - m),  O <- O a + P V,  l <- l a + sum P,  a = 2^(m_old - m),
 // where m only moves when a row's maximum rises by more than 2^kRaise, so that O,
 // which lives in tensor memory, is rescaled a few times in a call and not in every
-// tile.  A token's mask (what a node of the tree sees) concerns the buffer alone.
+// tile.  The values enter as their codes less 128, exact in fp16, and their scales go
+// with the weights, P' = P s, rounded to fp16 (of a P and an s in fp32); the zeros are
+// summed in fp32.  m is a maximum of S c + e, 2^e the least power of two above a unit's
+// scales, so that P' uses fp16's range for values of any size and never passes it.  A token's mask (what a node of the tree sees) concerns the buffer alone.
 //
 // Design (GB300).
 //  * One CTA per SM takes an equal range of (sequence, KV head, unit)s, as the split
@@ -55,6 +58,7 @@ constexpr int kSoftWarps = 8, kKeyWarps = 8, kValWarps = 4, kValArrive = kKeyWar
 constexpr int kMmaWarp = kSoftWarps + kKeyWarps + kValWarps, kLoadWarp = kMmaWarp + 1, kPrepWarp = kMmaWarp + 2;
 constexpr int kTallThreads = 32 * (kPrepWarp + 1);
 constexpr float kRaise = 8.f;              // log2 by which a maximum may be behind
+constexpr float kTallShift = 7.f;          // weights are taken as 2^(y - m + 7): P' up to 2^15
 constexpr int kFlags = 8;                  // units whose flags are kept
 constexpr int kScales = 3;                 // units whose value scales are kept
 constexpr int kMaxTreeRows = 512;
@@ -296,7 +300,11 @@ __device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
 // A group's scales and zeros, by one warp, four channels (tokens) a lane.  Keys: s_h
 // the top three bits of s, s_l the rest; g a unit of the last one of them; z + 128 s
 // (the zero of centred codes) in z_h, its nearest multiple of g as far as 1152 g, and
-// z_l.  |s_h c' + z_h| <= 7 * 128 g + 1152 g = 2048 g: exact.
+// z_l.  |s_h c' + z_h| <= 7 * 128 g + 1152 g = 2048 g: exact.  (And z_h keeps it within
+// fp16, -128 s_h + z_h >= -65504 and 127 s_h + z_h <= 65504, so that keys near the type's
+// ends leave no infinity in a tile.)  A zero far outside the range, |z + 128 s| above about
+// a half of 255 s, stays in T2 in part, which is then rounded at that size: at worst as
+// one rounding of the key would.
 template <int MODE>
 __device__ __forceinline__ void prep_keys(uint32_t raw, int lane) {
   using C = TallCfg<MODE>;
@@ -315,7 +323,10 @@ __device__ __forceinline__ void prep_keys(uint32_t raw, int lane) {
       // g and 1 / g from the exponent (a scale of 0: the zero alone)
       const uint32_t ex = __float_as_uint(sf) & 0x7F800000u;
       const float g = __uint_as_float(ex) * 0.25f, inv = __uint_as_float((254u << 23) - ex) * 4.f;
-      h[i] = ex ? fminf(fmaxf(rintf(zc * inv), -1152.f), 1152.f) * g : __half2float(__float2half_rn(zc));
+      const float s_h = i ? __high2float(u32_as_h2(sh[k])) : __low2float(u32_as_h2(sh[k]));
+      const float least = fmaxf(-1152.f, ceilf(fmaf(128.f, s_h, -65504.f) * inv));
+      const float most = fminf(1152.f, floorf(fmaf(-127.f, s_h, 65504.f) * inv));
+      h[i] = ex ? fminf(fmaxf(rintf(zc * inv), least), most) * g : __half2float(__float2half_rn(zc));
       l[i] = zc - h[i];
     }
     zh[k] = pack_half2(h[0], h[1]);
@@ -330,16 +341,19 @@ __device__ __forceinline__ void prep_keys(uint32_t raw, int lane) {
 // Values: s, and the zero of centred codes, of each token in order, in fp32 (raw 0: a
 // unit of buffer tokens, whose values are no codes; dead: nothing).  The four entries
 // from position 4 k of a quarter on are tokens k, k + 8, k + 16, k + 24 of it.
+// Returns e with s <= 2^e for all of them (for normal ones the least).
 template <int MODE>
-__device__ __forceinline__ void prep_values(uint32_t raw, bool dead, uint32_t to, int lane) {
+__device__ __forceinline__ int prep_values(uint32_t raw, bool dead, uint32_t to, int lane) {
   using C = TallCfg<MODE>;
   const uint32_t at = to + 128 * (lane >> 3) + 4 * (lane & 7);  // (token 32 (lane / 8) + lane % 8)
   float s[4], z[4];
+  uint32_t most2 = dead ? 0 : 0x3C00u;
   if (raw && !dead) {
     const uint2 sw = lds64(raw + C::kMetaOff + 8 * lane), zw = lds64(raw + C::kMetaOff + 256 + 8 * lane);
     const float2 s0 = __half22float2(u32_as_h2(sw.x)), s1 = __half22float2(u32_as_h2(sw.y));
     const float2 z0 = __half22float2(u32_as_h2(zw.x)), z1 = __half22float2(u32_as_h2(zw.y));
     s[0] = s0.x; s[1] = s0.y; s[2] = s1.x; s[3] = s1.y;
+    most2 = __vmaxu2(sw.x, sw.y);
     z[0] = z0.x; z[1] = z0.y; z[2] = z1.x; z[3] = z1.y;
 #pragma unroll
     for (int j = 0; j < 4; ++j) z[j] = fmaf(128.f, s[j], z[j]);
@@ -356,6 +370,9 @@ __device__ __forceinline__ void prep_values(uint32_t raw, bool dead, uint32_t to
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 32 * j), "f"(s[j]) : "memory");
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 512 + 32 * j), "f"(z[j]) : "memory");
   }
+  // (not negative, so their bits keep the order)
+  const uint32_t most = __reduce_max_sync(0xffffffffu, max(most2 & 0xFFFFu, most2 >> 16));
+  return (int)((most + 0x3FFu) >> 10) - 15;
 }
 
 // A group's keys into the tiles T1 and T2, by the key warps (dw): a lane takes a word
@@ -484,7 +501,7 @@ struct TallShared {
   long long total;
   uint32_t tmem;
   int abort;
-  int raw_dead[10], dead[kFlags];
+  int raw_dead[10], dead[kFlags], scale_exp[kScales];
   Piece piece[kPrepWarp + 1];  // each warp's current one
   float swap[2][kSoftWarps][32];  // between two threads of a row
 };
@@ -915,7 +932,8 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
         } else {
           if (unit >= kScales) ok = warp_wait(sh, sh.scale_empty[sc.slot], sc.par ^ 1, ns);
           if (!ok) break;
-          prep_values<MODE>(group ? raw_at(raw.slot) : 0, dead, scale_at(sc.slot), lane);
+          const int e = prep_values<MODE>(group ? raw_at(raw.slot) : 0, dead, scale_at(sc.slot), lane);
+          if (lane == 0) *reinterpret_cast<volatile int *>(&sh.scale_exp[sc.slot]) = e;
         }
         __syncwarp();
         if (lane == 0) {
@@ -1107,7 +1125,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
             if (!ok) break;
             mx = fmaxf(mx, other);
           }
-          const float mn = mx * prm.sl2;
+          const float mn = mx * prm.sl2 + (float)*reinterpret_cast<volatile int *>(&sh.scale_exp[sc.slot]);
           const bool raise = mn > m + kRaise || (m == -INFINITY && mn > -INFINITY);
           if (__any_sync(0xffffffffu, raise)) {
             const float a = raise ? (m == -INFINITY ? 0.f : fast_exp2(m - mn)) : 1.f;
@@ -1125,7 +1143,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
             bv *= a;
             if (raise) m = mn;
           }
-          const float off = m == -INFINITY ? 0.f : kExpShift - m;
+          const float off = m == -INFINITY ? 0.f : kTallShift - m;
           // The values are codes: P' = p s, and their zeros go with p alone, in fp32.  (The
           // largest p is a power of two, so P' of the token that counts most is exact.)
           const f32x2 sl2 = pack2(prm.sl2, prm.sl2), off2 = pack2(off, off);
@@ -1315,7 +1333,7 @@ __global__ void __launch_bounds__(kJoinThreads) tall_join_kernel(const __grid_co
   fold(mn, ml.x, ml.y, s_o[ti]);
   const float inv = 1.f / Ls;
   *out = make_uint2(pack_half2(A.x * inv, A.y * inv), pack_half2(A.z * inv, A.w * inv));
-  if (prm.lse && c4 == 0) prm.lse[at] = (M - kExpShift + log2f(Ls)) * 0.69314718055994531f;
+  if (prm.lse && c4 == 0) prm.lse[at] = (M - kTallShift + log2f(Ls)) * 0.69314718055994531f;
 }
 
 // --------------------------------------------------------------- host side

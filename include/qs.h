@@ -560,7 +560,9 @@ qs_status qs_attn_tree_workspace_size(const qs_cache *c, int32_t n_q, int32_t gr
  * other row (in front of the tree such values reach every row, as in the other
  * attention calls).  Up to 24 rows per KV head (group * n_q) run as
  * qs_attn_decode_paged does; more of them go through the tensor cores 128 at a
- * time, their keys and values rounded to fp16 once.  Errors as qs_attn_decode_gqa,
+ * time: there a key is the sum of an exact fp16 tile and of a rounded one of an eighth
+ * of its range, value codes are exact, and a weight times its value's scale is rounded
+ * to fp16 once.  Errors as qs_attn_decode_gqa,
  * QS_ERR_ARG also for a null parent and sizes out of range. */
 qs_status qs_attn_decode_tree(const qs_cache *c, const qs_pages *pg, qs_mode mode,
                               const int32_t *parent, int32_t n_tree, const uint16_t *q, int32_t n_q,
@@ -604,7 +606,8 @@ typedef enum { QS_FP16 = 0, QS_BF16 = 1, QS_FP32 = 2 } qs_dtype;
  *           each may be NULL: 1, off, off, off;
  *   u       float [rows]: uniform numbers in [0, 1);
  *   token   int32 [rows] (out);
- *   probs   float [rows][V] (out) or NULL.
+ *   probs   float [rows][V] (out) or NULL; may be the logits themselves where those
+ *           are fp32 with row_stride V.
  * With x the row's logits and m the largest, token i weighs w_i = exp((x_i - m) /
  * temperature).  The tokens in order of falling logits, equal ones by rising index:
  *   top_k   keeps the first top_k (0 or less, or V and more: all);
@@ -615,7 +618,7 @@ typedef enum { QS_FP16 = 0, QS_BF16 = 1, QS_FP32 = 2 } qs_dtype;
  * probs_i is w_i over the sum of the kept weights, 0 for the others.  The token is
  * the first one, by index, at which the running sum of the kept weights exceeds u
  * times their sum (u below 0 or NaN counts as 0, 1 and more takes the last kept
- * token).  Weights are formed to about 2^-37 of themselves and added as 64-bit
+ * token).  Weights are formed to about 2^-36 of themselves and added as 64-bit
  * integers, so a result does not depend on an order of summation.  A temperature
  * of 0 (of less than 2^-60, or NaN) takes the largest logit, the lowest index among
  * equal ones.  Logits of -inf or NaN are never kept; where one is +inf, those with

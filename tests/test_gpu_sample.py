@@ -1,6 +1,6 @@
 """qs_sample against its definition in 64 bits: the same tokens, the same tokens
-kept, and probabilities to fp32 (weights of 2^-36, one rounding to fp32 each of the
-weight, the scale and their product: 3 halves of 2^-23, and 2^-22 is allowed; what
+kept, and probabilities to fp32: weights of 2^-36, and half a step, 2^-24, each for the
+weight, the total, their quotient's scale and the product, 2^-22 together; what
 weighs less than 2^-45 of the largest may be 0)."""
 import numpy as np
 import pytest
@@ -227,3 +227,17 @@ def test_streams_and_graphs(torch):
     torch.cuda.synchronize()
     want = [trees.sample(d["x"][r].double().cpu().numpy(), float(d["u"][r]), top_k=int(k[r]))[0] for r in range(3)]
     assert d["token"][0].tolist() == want
+
+
+@pytest.mark.parametrize("V", [1000, 32000, 65537])
+def test_probabilities_in_the_place_of_the_logits(torch, V):
+    rng = np.random.default_rng(V)
+    rows = 5
+    x, u = logits(torch, rng, rows, V, "float32"), rng.random(rows)
+    s = settings(rng, rows, top_p=0.9)
+    token, pr = run(torch, x, u, **s)
+    dev = {k: torch.from_numpy(v).cuda() for k, v in s.items()}
+    t2 = torch.full((rows,), -77, dtype=torch.int32, device="cuda")
+    qs.qs_sample(x, torch.from_numpy(u.astype(np.float32)).cuda(), t2, probs=x, **dev)
+    torch.cuda.synchronize()
+    assert np.array_equal(t2.cpu().numpy(), token) and np.array_equal(x.double().cpu().numpy(), pr)

@@ -8,6 +8,7 @@ out over its tokens, but a single token may carry it: twice more); the keys, whi
 move a score by up to 4e-4 with the eightfold channels of these inputs.  In squares
 7e-4."""
 import numpy as np
+import oracle
 import pytest
 
 from hierarchical_quantized_kv_gb300 import qs
@@ -222,3 +223,31 @@ def test_streams_graphs_and_no_lse(torch):
     x["oc"].state[:, 1] -= 3  # (its fill)
     want = trees.attention(x["oc"], x["q"][4], parent, False, group)[0]
     check(x["out"][1].double().cpu().numpy(), None, want, None)
+
+
+@pytest.mark.parametrize("size", [-10, 0, 12])
+@pytest.mark.parametrize("n,group", [(8, 1), (40, 1), (50, 2), (64, 4)])
+def test_keys_with_offsets_and_values_of_any_size(torch, n, group, size):
+    """Values of 2^size, three channels of the keys far from zero, and one that reaches
+    both ends of fp16 (against small queries).  The offset channels stand at 15 +- 2
+    or more: what lies outside a tile's range there, up to 16, is rounded by 2^-8 /
+    sqrt(3) in rms, three of them move a score by 3.4e-4, so 8e-4 with the rest."""
+    rng = np.random.default_rng([n, group, size + 20])
+    B, H, ng, fill = 1, 2, 4, 200
+    k = rng.standard_normal((B, H, ng * 128 + fill, 128)) * 2
+    k[..., :3] += 15
+    k[..., 9] = np.where(rng.random(k.shape[:3]) < 0.1, 65504 * np.sign(k[..., 8]), 100 * k[..., 9])
+    v = rng.standard_normal(k.shape) * 2.0 ** size + 2.0 ** size
+    k, v = k.astype(np.float16), v.astype(np.float16)
+    oc = oracle.OracleCache(B, H, 128, 128, ng)
+    oracle.prefill(oc, lambda b, t0, m: (k[b, :, t0:t0 + m], v[b, :, t0:t0 + m]), [ng], [fill])
+    parent = trees.random_parents(rng, B, n)
+    q = h16(rng, (B, H * group, n, 128))
+    q[..., 9] *= np.float16(2.0 ** -13)
+    for ub in (4, 2):
+        cache = load(torch, oc, rng, ub)
+        for mode in (DRAFT, VERIFY):
+            got, gl = run(torch, cache, mode, q, parent, group)
+            ref, rl = trees.attention(oc, q, parent, mode == DRAFT, group, ub)
+            rel = np.linalg.norm(got - ref) / np.linalg.norm(ref)
+            assert rel <= RRMS and np.abs(gl - rl).max() <= 5e-3, (mode, ub, rel, np.abs(gl - rl).max())
