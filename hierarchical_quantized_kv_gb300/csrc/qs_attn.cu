@@ -113,7 +113,8 @@ extern "C" int qs_checked_failures_tree(unsigned long long *out2, int reset);
 // the selection, 32 place of a unit, 33 a cluster's sums in shared memory, 34 its
 // sums in the workspace; selection: 40 score, 41 list of close groups, 42 output,
 // 43 scales and zeros, 44 query row; read back: 50 group, 51 buffer row, 52 output
-// row, 53 tile row).  reset != 0 zeroes the counts.  Returns 0, or 1 if a CUDA call
+// row, 53 tile row; attention of many rows: 60 store to shared memory, 61 copy,
+// 62 partial written, 63 partial read).  reset != 0 zeroes the counts.  Returns 0, or 1 if a CUDA call
 // failed.
 extern "C" int qs_checked_failures(unsigned long long *count, unsigned int *first_tag, int reset) {
   unsigned long long f[6][2];
