@@ -10,19 +10,21 @@
 // tile.  The values enter as their codes less 128, exact in fp16, and their scales go
 // with the weights, P' = P s, rounded to fp16 (of a P and an s in fp32); the zeros are
 // summed in fp32.  m is a maximum of S c + e, 2^e the least power of two above a unit's
-// scales, so that P' uses fp16's range for values of any size and never passes it.  A token's mask (what a node of the tree sees) concerns the buffer alone.
+// scales, so that P' uses fp16's range for values of any size and never passes it.  A
+// token's mask (what a node of the tree sees) concerns the buffer alone.
 //
 // Design (GB300).
 //  * One CTA per SM takes an equal range of (sequence, KV head, unit)s, as the split
 //    kernel does, and writes a partial (O, m, l) for each segment it touches; a second
 //    kernel joins them.
-//  * Roles: one warp starts the bulk copies of planes and scales into a ring; eight
-//    warps make fp16 operand tiles of the keys (128 rows of 128 fp16, the 128-byte
-//    swizzle of K-major operands), eight of the values, in a ring of three; one thread
-//    issues the MMAs; two groups of four warps do the softmax, a row per thread.
-//  * 26 warps in five roles share the instruction caches: the loops are kept short
-//    (unrolled over whole tiles, with the segments' bookkeeping inside, the same
-//    kernel had 188 KB of code and took 102 us instead of 62 for 240 rows of 32k).
+//  * Roles (23 warps): one starts the bulk copies of planes and scales into a ring; one
+//    makes scales and zeros ready; eight make the operand tiles of the keys (128 rows of
+//    128 fp16, the 128-byte swizzle of K-major operands), four those of the values, in a
+//    ring of three or four; one issues the MMAs (an elected lane, from uniform code); eight
+//    do the softmax, a row per thread or, up to 64 rows, two threads.
+//  * The roles share the instruction caches: the loops are kept short (unrolled over
+//    whole tiles, with the segments' bookkeeping inside, an early form had 188 KB of code
+//    and took 102 us instead of 62 for 240 rows of 32k).
 //  * Two streams alternate on the tensor core, so that one multiplies while the other's
 //    softmax runs.  With more than 128 rows they are two row tiles over the same keys
 //    and values; else they take every other unit.
@@ -30,11 +32,11 @@
 //    product's A operand, so scores never touch shared memory.
 //  * Keys enter the product in two fp16 tiles that add up to them, K = T1 + T2.  Rounded
 //    to fp16 once, a key with a large channel moves its scores by 1e-3 and more, and
-//    the output by as much as six of its own roundings.  With s = s_h + s_l, s_h the top
-//    three bits of the scale, and codes centred on 128, T1 = s_h c' + z_h is exact (a
-//    multiple of the last bit of s_h below 2048 of them) and T2 = s_l c' + z_l, an eighth
-//    of the range at most, is rounded: two fused multiply-adds for a pair instead of
-//    one.  A warp of its own splits the scales and zeros of a group, once.
+//    the output by as much as six of its own roundings.  With s = s_h + s_l, s_h the
+//    scale to three bits, and codes centred on 128, T1 = s_h c' + z_h is exact (a multiple
+//    of a unit below 2048 of them) and T2 = s_l c' + z_l, a sixteenth of the range at
+//    most, is rounded: two fused multiply-adds for a pair instead of one, and a third
+//    product.  A warp of its own splits the scales and zeros of a group, once.
 //  * The planes' layouts fit: keys are stored by token, channels side by side, and
 //    values by channel, tokens side by side, both K-major as they are.  Within
 //    eight channels the keys' nibbles come out as 0 4 1 5 2 6 3 7; the queries are
@@ -298,9 +300,9 @@ __device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
 }
 
 // A group's scales and zeros, by one warp, four channels (tokens) a lane.  Keys: s_h
-// the top three bits of s, s_l the rest; g a unit of the last one of them; z + 128 s
-// (the zero of centred codes) in z_h, its nearest multiple of g as far as 1152 g, and
-// z_l.  |s_h c' + z_h| <= 7 * 128 g + 1152 g = 2048 g: exact.  (And z_h keeps it within
+// s to its nearest three bits, 4 g .. 8 g with g a quarter of its power of two, s_l the
+// rest; z + 128 s (the zero of centred codes) in z_h, its nearest multiple of g as far as
+// 1024 g, and z_l.  |s_h c' + z_h| <= 8 * 128 g + 1024 g = 2048 g: exact.  (And z_h keeps it within
 // fp16, -128 s_h + z_h >= -65504 and 127 s_h + z_h <= 65504, so that keys near the type's
 // ends leave no infinity in a tile.)  A zero far outside the range, |z + 128 s| above about
 // a half of 255 s, stays in T2 in part, which is then rounded at that size: at worst as
@@ -313,7 +315,7 @@ __device__ __forceinline__ void prep_keys(uint32_t raw, int lane) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const uint32_t s2 = k ? sw.y : sw.x, z2 = k ? zw.y : zw.x;
-    sh[k] = s2 & 0xFF00FF00u;
+    sh[k] = (s2 + 0x00800080u) & 0xFF00FF00u;  // (a scale is 514 at most)
     sl[k] = h2_as_u32(__hsub2(u32_as_h2(s2), u32_as_h2(sh[k])));
     const float2 s = __half22float2(u32_as_h2(s2)), z = __half22float2(u32_as_h2(z2));
     float h[2], l[2];
@@ -324,8 +326,8 @@ __device__ __forceinline__ void prep_keys(uint32_t raw, int lane) {
       const uint32_t ex = __float_as_uint(sf) & 0x7F800000u;
       const float g = __uint_as_float(ex) * 0.25f, inv = __uint_as_float((254u << 23) - ex) * 4.f;
       const float s_h = i ? __high2float(u32_as_h2(sh[k])) : __low2float(u32_as_h2(sh[k]));
-      const float least = fmaxf(-1152.f, ceilf(fmaf(128.f, s_h, -65504.f) * inv));
-      const float most = fminf(1152.f, floorf(fmaf(-127.f, s_h, 65504.f) * inv));
+      const float least = fmaxf(-1024.f, ceilf(fmaf(128.f, s_h, -65504.f) * inv));
+      const float most = fminf(1024.f, floorf(fmaf(-127.f, s_h, 65504.f) * inv));
       h[i] = ex ? fminf(fmaxf(rintf(zc * inv), least), most) * g : __half2float(__float2half_rn(zc));
       l[i] = zc - h[i];
     }
