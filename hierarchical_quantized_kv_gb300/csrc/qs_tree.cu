@@ -66,8 +66,12 @@ __device__ __forceinline__ void turn_halves(uint4 &a, uint4 &b, const float2 *cs
 // 16-byte vectors of a row, eight items a row, whose lanes' vectors lie side by side:
 // a pair of vectors that turn together, or two on their own.  The CTA's angles go
 // through shared memory, so their sines are formed once for all heads.
+// Bound by memory, for few tokens by a launch and its chain of reads.  Two items a
+// thread in flight and five CTAs an SM, against four items and three: eight trees of 64
+// tokens 7.0 us (9.0), sixteen sequences of 256 35.6 (36.6; 201 MB, 0.83 of the copy
+// bandwidth).  Rows split over two or three CTAs more: 39 and 42.
 template <bool INTER>
-__global__ void __launch_bounds__(kRotThreads) append_rotary_kernel(const RotArgs a) {
+__global__ void __launch_bounds__(kRotThreads, 5) append_rotary_kernel(const RotArgs a) {
   __shared__ float2 s_cs[kRotTokens * kMaxHalf];
   __shared__ unsigned long long s_turns[kMaxHalf];
   const qs_cache &c = a.c;
@@ -96,7 +100,7 @@ __global__ void __launch_bounds__(kRotThreads) append_rotary_kernel(const RotArg
   const int r0 = blockIdx.y * per, r1 = min(rows, r0 + per);
   const int n_items = (r1 - r0) << (a.log_tokens + 3);
   const int turning = INTER ? 0 : a.rot / 16;  // items of a row whose vectors turn together
-  constexpr int U = 4;  // items in flight per thread
+  constexpr int U = 2;  // items in flight per thread
 #pragma unroll 1
   for (int e0 = threadIdx.x; e0 < n_items; e0 += U * kRotThreads) {
     uint4 x[U], y[U];
