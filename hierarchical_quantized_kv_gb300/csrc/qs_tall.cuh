@@ -1091,7 +1091,8 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
         if (bad) atomicOr(&c.state[(size_t)pc.b * QS_STATE_WORDS + QS_ST_ERR], QS_DEV_TREE);
         sees = ancestors_of(mm, prm.n_tree - prm.n_q + row % prm.n_q);
       }
-      float m = -INFINITY, l = 0.f, bv = 0.f;  // (bv: what the zeros of the values add)
+      // the weights' maximum: 2^(m c + em); bv: what the zeros of the values add
+      float m = -INFINITY, em = 0.f, l = 0.f, bv = 0.f;
       int done = 0;
       // the stream's units of the piece
 #pragma unroll 1
@@ -1127,10 +1128,13 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
             if (!ok) break;
             mx = fmaxf(mx, other);
           }
-          const float mn = mx * prm.sl2 + (float)*reinterpret_cast<volatile int *>(&sh.scale_exp[sc.slot]);
-          const bool raise = mn > m + kRaise || (m == -INFINITY && mn > -INFINITY);
+          // (differences of scores, not of products: one may be far beyond what a
+          // product keeps to the last bit)
+          const float es = (float)*reinterpret_cast<volatile int *>(&sh.scale_exp[sc.slot]);
+          const float up = (mx - m) * prm.sl2 + (es - em);
+          const bool raise = mx > -INFINITY && (m == -INFINITY || up > kRaise);
           if (__any_sync(0xffffffffu, raise)) {
-            const float a = raise ? (m == -INFINITY ? 0.f : fast_exp2(m - mn)) : 1.f;
+            const float a = raise ? (m == -INFINITY ? 0.f : fast_exp2(-up)) : 1.f;
             if (done > 0) {
 #pragma unroll 1
               for (int k = k0; k < k1; ++k) {
@@ -1143,12 +1147,15 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
             }
             l *= a;
             bv *= a;
-            if (raise) m = mn;
+            if (raise) {
+              m = mx;
+              em = es;
+            }
           }
-          const float off = m == -INFINITY ? 0.f : kTallShift - m;
+          const float off = kTallShift - em, base = m == -INFINITY ? 0.f : -m;
           // The values are codes: P' = p s, and their zeros go with p alone, in fp32.  (The
           // largest p is a power of two, so P' of the token that counts most is exact.)
-          const f32x2 sl2 = pack2(prm.sl2, prm.sl2), off2 = pack2(off, off);
+          const f32x2 sl2 = pack2(prm.sl2, prm.sl2), off2 = pack2(off, off), base2 = pack2(base, base);
           f32x2 l2 = pack2(0.f, 0.f), bv2 = l2;
           const uint32_t scales = scale_at(sc.slot);
 #pragma unroll 1
@@ -1160,8 +1167,8 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
               const ulonglong2 s4 = lds2x64(scales + 64 * k + 16 * i), z4 = lds2x64(scales + 512 + 64 * k + 16 * i);
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const f32x2 y = fma_f32x2(
-                    pack2(__uint_as_float(y16[4 * i + 2 * h]), __uint_as_float(y16[4 * i + 2 * h + 1])), sl2, off2);
+                const f32x2 x = pack2(__uint_as_float(y16[4 * i + 2 * h]), __uint_as_float(y16[4 * i + 2 * h + 1]));
+                const f32x2 y = fma_f32x2(add_f32x2(x, base2), sl2, off2);
                 const f32x2 p = pack2(fast_exp2(lo_of(y)), fast_exp2(hi_of(y)));
                 l2 = add_f32x2(l2, p);
                 bv2 = fma_f32x2(p, h ? z4.y : z4.x, bv2);
@@ -1220,7 +1227,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
         if (lane == 0) mbar_arrive(bar(sh.o_empty[s]));
       }
       if (mine && k0 == 0) {
-        part[prm.rows * kD + row_p] = m;
+        part[prm.rows * kD + row_p] = fmaf(m, prm.sl2, em);
         part[prm.rows * (kD + 1) + row_p] = l;
       }
       unit0 += n;

@@ -251,3 +251,50 @@ def test_keys_with_offsets_and_values_of_any_size(torch, n, group, size):
             ref, rl = trees.attention(oc, q, parent, mode == DRAFT, group, ub)
             rel = np.linalg.norm(got - ref) / np.linalg.norm(ref)
             assert rel <= RRMS and np.abs(gl - rl).max() <= 5e-3, (mode, ub, rel, np.abs(gl - rl).max())
+
+
+@pytest.mark.parametrize("q_size,k_size", [(1, 3000), (100, 100), (3000, 3000), (8000, 8000)])
+@pytest.mark.parametrize("n,group", [(40, 1), (30, 5)])
+def test_scores_of_any_size(torch, n, group, q_size, k_size):
+    """Above 24 rows finite queries and keys give finite results, however large their
+    products.  A score is then off by the rounding of the keys' second part, a
+    fifteenth of their range, so 2^-12 / sqrt(3) of 2 / 15 of the largest key (4 of its
+    sizes) in each of 128 channels, against a log-sum-exp of some 3.5 of a
+    score's sizes: 2.1e-5 of it in rms, and five of those are allowed."""
+    rng = np.random.default_rng([n, group, q_size, k_size])
+    B, H, ng, fill = 1, 2, 4, 200
+    k = np.clip(rng.standard_normal((B, H, ng * 128 + fill, 128)) * k_size, -65504, 65504).astype(np.float16)
+    v = rng.standard_normal(k.shape).astype(np.float16)
+    oc = oracle.OracleCache(B, H, 128, 128, ng)
+    oracle.prefill(oc, lambda b, t0, m: (k[b, :, t0:t0 + m], v[b, :, t0:t0 + m]), [ng], [fill])
+    parent = trees.random_parents(rng, B, n)
+    q = np.clip(rng.standard_normal((B, H * group, n, 128)) * q_size, -65504, 65504).astype(np.float16)
+    cache = load(torch, oc, rng)
+    for mode in (DRAFT, VERIFY):
+        got, gl = run(torch, cache, mode, q, parent, group)
+        _, rl = trees.attention(oc, q, parent, mode == DRAFT, group)
+        assert np.isfinite(got).all() and np.abs(got).max() <= np.abs(v).max() * 1.01
+        assert np.all(np.abs(gl - rl) <= 1.1e-4 * np.abs(rl))
+
+
+@pytest.mark.parametrize("B,H,n,group", [(256, 1, 30, 1), (256, 2, 3, 2), (1, 1, 1, 512), (2, 1, 2, 256)])
+def test_many_sequences_and_many_heads(torch, B, H, n, group):
+    """As many sequences as a cache holds, some without room for the tree (all of them
+    in the last call); a KV head with as many query heads as a call takes."""
+    rng = np.random.default_rng([B, H, n, group])
+    ng = [int(x) for x in rng.integers(0, 2, B)]
+    fill = [int(x) for x in rng.integers(max(1, n - 2), n + 40, B)]
+    oc = _oracle_state(rng, B, H, ng, fill, cap=1)
+    parent = trees.random_parents(rng, B, n)
+    q = h16(rng, (B, H * group, n, 128))
+    cache = load(torch, oc, rng)
+    got, gl = run(torch, cache, VERIFY, q, parent, group)
+    ref, rl = trees.attention(oc, q, parent, False, group)
+    fits = np.array(fill) >= n
+    check(got, gl, ref, rl)
+    assert np.all(got[~fits] == 0) and np.all(gl[~fits] == -np.inf)
+    assert list(qs.qs_get_errors(cache)) == [0 if f else qs.DEV_NQ_GT_FILL for f in fits]
+    cache.state[:, 1] = 0
+    got, gl = run(torch, cache, VERIFY, q, parent, group)
+    assert np.all(got == 0) and np.all(gl == -np.inf)
+    assert list(qs.qs_get_errors(cache)) == [qs.DEV_NQ_GT_FILL] * B
