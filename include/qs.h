@@ -560,10 +560,11 @@ qs_status qs_attn_tree_workspace_size(const qs_cache *c, int32_t n_q, int32_t gr
  * other row (in front of the tree such values reach every row, as in the other
  * attention calls).  Up to 24 rows per KV head (group * n_q) run as
  * qs_attn_decode_paged does (a query's element times a key scale stays within fp16
- * there); more of them go through the tensor cores 128 at a
- * time: there a key is the sum of an exact fp16 number and of a rounded one of a sixteenth
- * of its group's range (plus what of its zero lies outside), value codes are exact, and a weight times its value's scale is rounded
- * to fp16 once.  Errors as qs_attn_decode_gqa,
+ * there); more of them go through the tensor cores 128 at a time: there a key is
+ * the sum of an exact fp16 number and of one that is rounded, a sixteenth of its
+ * group's range (and what of its zero lies outside that range), value codes are
+ * exact, and a weight times its value's scale is rounded to fp16 once.  Errors as
+ * qs_attn_decode_gqa,
  * QS_ERR_ARG also for a null parent and sizes out of range. */
 qs_status qs_attn_decode_tree(const qs_cache *c, const qs_pages *pg, qs_mode mode,
                               const int32_t *parent, int32_t n_tree, const uint16_t *q, int32_t n_q,
