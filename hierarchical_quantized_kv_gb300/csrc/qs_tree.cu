@@ -168,7 +168,9 @@ constexpr int kAccThreads = 256;
 // a step is a shuffle (the target's token of the current node) and two votes (the
 // nodes that hang from it with that token).  Then the CTA reads the rows of the
 // path that have to move, all before the first is written: they only move
-// forward, so one may lie where an earlier one goes.
+// forward, so one may lie where an earlier one goes.  Bound by its chain of reads
+// (counters, tree, rows): with a copy of the counters and an append in front 5.9 us for
+// a tree of 16 nodes of 8 heads, 10 for sixteen of 64 of 32 heads.
 __global__ void __launch_bounds__(kAccThreads)
     tree_accept_kernel(qs_cache c, const int32_t *parent, const int32_t *draft, const int32_t *target,
                        int n, int32_t *n_keep, int32_t *path, int32_t *emitted) {
