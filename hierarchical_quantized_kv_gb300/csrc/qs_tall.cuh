@@ -1249,17 +1249,18 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
   }
 }
 
-// Joins the partials: a thread takes four channels of a row (eight rows side by
-// side) and every other partial, six of them in flight; two threads meet at the end.
-// The CTAs that hold a segment, and where their partials lie, follow from the
-// counters as in the kernel above.
-constexpr int kJoinThreads = 512, kJoinBatch = 6;
+// Joins the partials: a CTA has eight rows of a KV head, so that its threads walk the
+// same partials (with eight rows across two heads a call of 25 rows took 4 us more); a
+// thread takes four channels of a row and every kJoinParts-th partial, six of them in
+// flight, and they meet at the end.  The CTAs that hold a segment, and where their
+// partials lie, follow from the counters as in the kernel above.
+constexpr int kJoinParts = 4, kJoinLane = 256, kJoinThreads = kJoinParts * kJoinLane, kJoinBatch = 6;
 
 __global__ void __launch_bounds__(kJoinThreads) tall_join_kernel(const __grid_constant__ TallParams prm, int MT) {
   __shared__ int tab[7 * kMaxB];
   __shared__ long long s_total;
-  __shared__ float4 s_o[kJoinThreads / 2];
-  __shared__ float2 s_ml[kJoinThreads / 2];
+  __shared__ float4 s_o[kJoinThreads - kJoinLane];
+  __shared__ float2 s_ml[kJoinThreads - kJoinLane];
   const qs_cache &c = prm.c;
   Tables T = tables_at(reinterpret_cast<uint8_t *>(tab), 0);
   pdl_trigger();
@@ -1271,10 +1272,11 @@ __global__ void __launch_bounds__(kJoinThreads) tall_join_kernel(const __grid_co
     if (threadIdx.x == 0) s_total = tot;
   }
   __syncthreads();
-  const int half = threadIdx.x / (kJoinThreads / 2), ti = threadIdx.x % (kJoinThreads / 2);
-  const long long at = (long long)blockIdx.x * 8 + (ti & 7);
-  const int c4 = ti >> 3;
-  const bool here = at < (long long)c.B * c.H * prm.R;
+  const int part = threadIdx.x / kJoinLane, ti = threadIdx.x % kJoinLane;
+  const int eights = (prm.R + 7) / 8, bh = blockIdx.x / eights, c4 = ti >> 3;
+  const int row = 8 * (blockIdx.x % eights) + (ti & 7);
+  const bool here = row < prm.R;
+  const size_t at = (size_t)bh * prm.R + row;
   float M = -INFINITY, Ls = 0.f;
   float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
   auto fold = [&](float mn, float m, float l, float4 o) {
@@ -1292,7 +1294,7 @@ __global__ void __launch_bounds__(kJoinThreads) tall_join_kernel(const __grid_co
   };
   int len = 0, b = 0;
   if (here) {
-    const int row = (int)(at % prm.R), bh = (int)(at / prm.R), h = bh % c.H;
+    const int h = bh % c.H;
     b = bh / c.H;
     len = T.len[b];
     if (len > 0) {
@@ -1302,21 +1304,21 @@ __global__ void __launch_bounds__(kJoinThreads) tall_join_kernel(const __grid_co
       const size_t size = (size_t)prm.rows * (kD + 2);
       const int np = (phi - plo + 1) << sh;
 #pragma unroll 1
-      for (int k0 = half; k0 < np; k0 += 2 * kJoinBatch) {
+      for (int k0 = part; k0 < np; k0 += kJoinParts * kJoinBatch) {
         float m[kJoinBatch], l[kJoinBatch];
         float4 o[kJoinBatch];
 #pragma unroll
         for (int i = 0; i < kJoinBatch; ++i) {
-          const int k = k0 + 2 * i;
+          const int k = k0 + kJoinParts * i;
           m[i] = -INFINITY;
           l[i] = 0.f;
           if (k >= np) continue;
           const size_t off = ((size_t)(ord + plo + (k >> sh)) * 2 + s_at + (k & sh)) * size;
           if (!chk(in_range(off, size, prm.ws_floats), 63)) continue;
-          const float *part = prm.ws + off;
-          m[i] = part[prm.rows * kD + row_t];
-          l[i] = part[prm.rows * (kD + 1) + row_t];
-          o[i] = reinterpret_cast<const float4 *>(part)[c4 * prm.rows + row_t];
+          const float *from = prm.ws + off;
+          m[i] = from[prm.rows * kD + row_t];
+          l[i] = from[prm.rows * (kD + 1) + row_t];
+          o[i] = reinterpret_cast<const float4 *>(from)[c4 * prm.rows + row_t];
         }
         float mn = M;
 #pragma unroll
@@ -1327,13 +1329,13 @@ __global__ void __launch_bounds__(kJoinThreads) tall_join_kernel(const __grid_co
       }
     }
   }
-  if (half) {
-    s_o[ti] = A;
-    s_ml[ti] = make_float2(M, Ls);
+  if (part) {
+    s_o[threadIdx.x - kJoinLane] = A;
+    s_ml[threadIdx.x - kJoinLane] = make_float2(M, Ls);
   }
   __syncthreads();
-  if (half || !here) return;
-  uint2 *out = reinterpret_cast<uint2 *>(prm.out + (size_t)at * kD + 4 * c4);
+  if (part || !here) return;
+  uint2 *out = reinterpret_cast<uint2 *>(prm.out + at * kD + 4 * c4);
   if (len == 0) {  // n_tree > fill
     *out = make_uint2(0, 0);
     if (c4 == 0) {
@@ -1342,10 +1344,13 @@ __global__ void __launch_bounds__(kJoinThreads) tall_join_kernel(const __grid_co
     }
     return;
   }
-  const float2 ml = s_ml[ti];
-  const float mn = fmaxf(M, ml.x);
+  float mn = M;
+#pragma unroll
+  for (int k = 0; k < kJoinParts - 1; ++k) mn = fmaxf(mn, s_ml[k * kJoinLane + ti].x);
   rescale(mn);
-  fold(mn, ml.x, ml.y, s_o[ti]);
+#pragma unroll
+  for (int k = 0; k < kJoinParts - 1; ++k)
+    fold(mn, s_ml[k * kJoinLane + ti].x, s_ml[k * kJoinLane + ti].y, s_o[k * kJoinLane + ti]);
   const float inv = 1.f / Ls;
   *out = make_uint2(pack_half2(A.x * inv, A.y * inv), pack_half2(A.z * inv, A.w * inv));
   if (prm.lse && c4 == 0) prm.lse[at] = (M - kTallShift + log2f(Ls)) * 0.69314718055994531f;
@@ -1368,8 +1373,7 @@ qs_status launch_tall(const TallParams &prm, cudaStream_t st) {
   if (s != QS_OK) return s;
   s = launch_pdl(tall_kernel<MODE, UB, MT>, dim3(prm.P), dim3(kTallThreads), smem, st, prm);
   if (s != QS_OK) return s;
-  const long long rows = (long long)prm.c.B * prm.c.H * prm.R;
-  return launch_pdl(tall_join_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(kJoinThreads), 0, st, prm, MT);
+  return launch_pdl(tall_join_kernel, dim3((unsigned)(prm.c.B * prm.c.H * ((prm.R + 7) / 8))), dim3(kJoinThreads), 0, st, prm, MT);
 }
 template <int MODE>
 qs_status launch_tall_mode(const TallParams &prm, cudaStream_t st) {
