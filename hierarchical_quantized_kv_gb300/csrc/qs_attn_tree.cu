@@ -1,5 +1,5 @@
 // qs_attn_tree.cu -- decode attention of the nodes of a tree of drafted tokens.
-// Up to 24 rows per KV head run through the split kernel (qs_split.cuh) in its tree
+// Few rows per KV head run through the split kernel (qs_split.cuh) in its tree
 // variants, more of them through the tensor cores 128 at a time (qs_tall.cuh).
 #include "qs_tall.cuh"
 
@@ -11,6 +11,15 @@ namespace {
 bool tree_sizes_ok(int32_t n_q, int32_t group) {
   return n_q >= 1 && n_q <= QS_MAX_TREE && group >= 1 && group <= kMaxTreeRows && group * n_q <= kMaxTreeRows;
 }
+
+// Rows that the split kernel takes: its work grows with each eight of them, the other
+// kernel's does not, and a draft's halves it there only.  Split / tall, us, for 32 heads
+// of 32k tokens, 8 heads of 32k, 8 heads of 4k, 4 x 32 heads of 32k:
+//   verify, 16 rows   87 / 114   34 / 41   15 / 19   280 / 409
+//   verify, 17 rows  131 / 115   45 / 42   20 / 20   454 / 411
+//   draft,  24 rows  100 / 115   35 / 42   18 / 20   334 / 408
+// (24 is also the most that the split kernel's layout holds.)
+int split_rows(qs_mode mode) { return mode == QS_VERIFY_INT8 ? 16 : kMaxR; }
 
 qs_status decode_tall(const Params &a, qs_mode mode, void *workspace, size_t workspace_bytes,
                       cudaStream_t st) {
@@ -53,7 +62,7 @@ qs_status decode_tree(const qs_cache *c, const qs_pages *pg, qs_mode mode, const
   prm.wait_ns = wait_ns;
   prm.no_issue = no_issue;
   cudaStream_t st = (cudaStream_t)stream;
-  if (group * n_q > kMaxR) {
+  if (group * n_q > split_rows(mode)) {
     s = check_queries(mode, q, softmax_scale, out, lse);
     if (s != QS_OK) return s;
     set_queries(prm, q, n_q, group, softmax_scale, out, lse);
@@ -79,19 +88,23 @@ qs_status qs_attn_tree_workspace_size(const qs_cache *c, int32_t n_q, int32_t gr
   if (s != QS_OK) return s;
   if (!bytes || !tree_sizes_ok(n_q, group)) return QS_ERR_ARG;
   const int bits = c->upper_bits & ~QS_PAGED, R = group * n_q;
-  if (R > kMaxR) {
+  // (for either mode)
+  *bytes = 0;
+  if (R > split_rows(QS_VERIFY_INT8)) {
     int sms = 0;
     if ((s = sm_count(&sms)) != QS_OK) return s;
     *bytes = tall_ws_bytes(sms, c->B, c->H, R);
-    return QS_OK;
   }
+  if (R > split_rows(QS_DRAFT_UPPER4)) return QS_OK;
   int P = 0;
   for (const qs_mode mode : {QS_DRAFT_UPPER4, QS_VERIFY_INT8}) {
+    if (R > split_rows(mode)) continue;
     int p = 0;
     if ((s = grid_size<kListed | kTree>(mode, packed_rows(mode, R), bits, (R + 7) / 8, p)) != QS_OK) return s;
     if (p > P) P = p;
   }
-  *bytes = ws_bytes(P, c->B, c->H, R);
+  const size_t split = ws_bytes(P, c->B, c->H, R);
+  if (split > *bytes) *bytes = split;
   return QS_OK;
 }
 

@@ -558,8 +558,8 @@ qs_status qs_attn_tree_workspace_size(const qs_cache *c, int32_t n_q, int32_t gr
  * A parent that is not allowed flags QS_DEV_TREE and counts as -1.  A node whose
  * value row holds an infinity or a NaN makes the rows that see it NaN, and no
  * other row (in front of the tree such values reach every row, as in the other
- * attention calls).  Up to 24 rows per KV head (group * n_q) run as
- * qs_attn_decode_paged does (a query's element times a key scale stays within fp16
+ * attention calls).  Up to 24 rows per KV head (group * n_q), 16 of a
+ * verification, run as qs_attn_decode_paged does (a query's element times a key scale stays within fp16
  * there); more of them go through the tensor cores 128 at a time: there a key is
  * the sum of an exact fp16 number and of one that is rounded, a sixteenth of its
  * group's range (and what of its zero lies outside that range), value codes are
