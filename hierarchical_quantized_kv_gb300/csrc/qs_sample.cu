@@ -127,11 +127,12 @@ struct Weights {
     if (!parts(x, -45.9f, i, q)) return 0;
     return combine(pow2[i], q);
   }
-  // times scale, as a float; 0 for less than 2^-64
+  // times scale, as a float; 0 for less than 2^-107 (a share in up to QS_MAX_VOCAB
+  // weights is a normal number down to there)
   __device__ __forceinline__ float scaled(float x, float scale) const {
     if (flat) return scale;
     int i, q;
-    if (!parts(x, -64.f, i, q)) return 0.f;
+    if (!parts(x, -107.f, i, q)) return 0.f;
     const u64 w = combine(pow2[i & 15], q);
     return (float)w * 5.684341886080802e-14f * scale * __int_as_float((127 - (i >> 4)) << 23);
   }

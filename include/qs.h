@@ -617,7 +617,8 @@ typedef enum { QS_FP16 = 0, QS_BF16 = 1, QS_FP32 = 2 } qs_dtype;
  *           weight stands, so the first always (1 and more, or NaN: all);
  *   min_p   of those, keeps the ones with w_i >= min_p (0 and less, or NaN: all;
  *           above 1 counts as 1).
- * probs_i is w_i over the sum of the kept weights, 0 for the others.  The token is
+ * probs_i is w_i over the sum of the kept weights, 0 for the others (and where w_i
+ * is less than 2^-107).  The token is
  * the first one, by index, at which the running sum of the kept weights exceeds u
  * times their sum (u below 0 or NaN counts as 0, 1 and more takes the last kept
  * token).  Weights are formed to about 2^-36 of themselves and added as 64-bit

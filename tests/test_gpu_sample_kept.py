@@ -42,3 +42,19 @@ def test_a_top_k_beyond_what_weighs(torch, dtype, V, k, T):  # noqa: F811
     check_kept(torch, x, rng.random(rows), -60, **s)
     s["top_p"] = np.array([1, 1, 0.999, 1, 0.5, 1], np.float32)
     check_kept(torch, x, rng.random(rows), -60, **s)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16", "float32"])
+@pytest.mark.parametrize("V,T", [(1000, 0.2), (32000, 0.25), (131073, 0.3), (368640, 0.25)])
+def test_kept_tokens_of_small_weights(torch, dtype, V, T):  # noqa: F811
+    """Whatever is kept has its share, down to 2^-107 of the largest weight: with up to
+    2^18.5 tokens the quotient is a normal number of fp32 there."""
+    rng = np.random.default_rng([V, len(dtype)])
+    rows = 4
+    x = logits(torch, rng, rows, V, dtype)
+    full = lambda v, t: np.full(rows, v, t)  # noqa: E731
+    s = dict(temperature=full(T, np.float32))
+    check_kept(torch, x, rng.random(rows), -106.9, **s)
+    s["top_k"] = np.array([0, 700, V - 1, 0], np.int32)
+    s["min_p"] = np.array([1e-25, 0, 0, 1e-31], np.float32)
+    check_kept(torch, x, rng.random(rows), -106.9, **s)
