@@ -1204,7 +1204,11 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
         l += l2;
         bv += bv2;
       }
-      // the piece's partial: rows side by side, four channels each
+      // the piece's partial: rows side by side, four channels each; its sums without the
+      // values' exponent (a power of two, so nothing is rounded), so that m alone stands
+      // for their size and partials are compared by differences of scores too
+      const float unit = __int_as_float((127 + (int)em) << 23);
+      l *= unit;
       float *part = prm.ws + ((size_t)(pc.ord + p) * 2 + s) * prm.rows * (kD + 2);
       const bool mine = live_warp && row < prm.R &&
                         chk(in_range((size_t)(part - prm.ws), (size_t)prm.rows * (kD + 2), prm.ws_floats), 62);
@@ -1224,8 +1228,8 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 reinterpret_cast<float4 *>(part)[(4 * k + i) * prm.rows + row_p] =
-                    make_float4(__uint_as_float(v[4 * i]) + add, __uint_as_float(v[4 * i + 1]) + add,
-                                __uint_as_float(v[4 * i + 2]) + add, __uint_as_float(v[4 * i + 3]) + add);
+                    make_float4((__uint_as_float(v[4 * i]) + add) * unit, (__uint_as_float(v[4 * i + 1]) + add) * unit,
+                                (__uint_as_float(v[4 * i + 2]) + add) * unit, (__uint_as_float(v[4 * i + 3]) + add) * unit);
           }
         }
         tc_before_sync();
@@ -1233,7 +1237,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
         if (lane == 0) mbar_arrive(bar(sh.o_empty[s]));
       }
       if (mine && k0 == 0) {
-        part[prm.rows * kD + row_p] = fmaf(m, prm.sl2, em);
+        part[prm.rows * kD + row_p] = m;
         part[prm.rows * (kD + 1) + row_p] = l;
       }
       unit0 += n;
@@ -1281,13 +1285,13 @@ __global__ void __launch_bounds__(kJoinThreads) tall_join_kernel(const __grid_co
   float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
   auto fold = [&](float mn, float m, float l, float4 o) {
     if (l == 0.f) return;  // nothing seen there (its sums were not written)
-    const float f = m == -INFINITY ? 1.f : fast_exp2(m - mn);  // (no maximum: all NaN)
+    const float f = m == -INFINITY ? 1.f : fast_exp2((m - mn) * prm.sl2);  // (no maximum: all NaN)
     A.x = fmaf(f, o.x, A.x); A.y = fmaf(f, o.y, A.y);
     A.z = fmaf(f, o.z, A.z); A.w = fmaf(f, o.w, A.w);
     Ls = fmaf(f, l, Ls);
   };
   auto rescale = [&](float mn) {
-    const float a = M == -INFINITY ? 0.f : fast_exp2(M - mn);
+    const float a = M == -INFINITY ? 0.f : fast_exp2((M - mn) * prm.sl2);
     A.x *= a; A.y *= a; A.z *= a; A.w *= a;
     Ls *= a;
     M = mn;
@@ -1353,7 +1357,7 @@ __global__ void __launch_bounds__(kJoinThreads) tall_join_kernel(const __grid_co
     fold(mn, s_ml[k * kJoinLane + ti].x, s_ml[k * kJoinLane + ti].y, s_o[k * kJoinLane + ti]);
   const float inv = 1.f / Ls;
   *out = make_uint2(pack_half2(A.x * inv, A.y * inv), pack_half2(A.z * inv, A.w * inv));
-  if (prm.lse && c4 == 0) prm.lse[at] = (M - kTallShift + log2f(Ls)) * 0.69314718055994531f;
+  if (prm.lse && c4 == 0) prm.lse[at] = fmaf(M, prm.sl2, log2f(Ls) - kTallShift) * 0.69314718055994531f;
 }
 
 // --------------------------------------------------------------- host side
