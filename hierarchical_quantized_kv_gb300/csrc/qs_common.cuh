@@ -23,6 +23,12 @@ constexpr int kMaxQ = 8;        // queries per call (one n8 MMA tile)
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// [p, p + n) and [q, q + m), in bytes, share some.
+inline bool overlap(const void *p, size_t n, const void *q, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + m && b < a + n;
+}
+
 // A cache of either kind (contiguous groups or pages): for the calls that
 // touch only the buffer and the counters.
 inline qs_status check_cache_any(const qs_cache *c) {

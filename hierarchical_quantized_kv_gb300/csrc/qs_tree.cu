@@ -327,6 +327,11 @@ qs_status qs_tree_accept(const qs_cache *c, const int32_t *parent, const int32_t
   const void *ptrs[] = {parent, draft, target, n_keep, path, emitted};
   for (const void *p : ptrs)
     if (reinterpret_cast<uintptr_t>(p) % 4) return QS_ERR_ALIGN;
+  // every head's CTA walks the tree, while one of them already writes the outputs
+  const size_t nodes = sizeof(int32_t) * c->B * n_tree, sizes[] = {nodes, nodes, nodes, sizeof(int32_t) * c->B, nodes, nodes};
+  for (int out = 3; out < 6; ++out)
+    for (int i = 0; i < out; ++i)
+      if (overlap(ptrs[out], sizes[out], ptrs[i], sizes[i])) return QS_ERR_ARG;
   return launch_pdl(tree_accept_kernel, dim3(c->H, c->B), dim3(kAccThreads), 0, (cudaStream_t)stream,
                     *c, parent, draft, target, (int)n_tree, n_keep, path, emitted);
 }

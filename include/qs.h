@@ -589,7 +589,8 @@ qs_status qs_attn_decode_tree(const qs_cache *c, const qs_pages *pg, qs_mode mod
  * tokens are committed with the path).  A sequence with fewer than n_tree pending
  * tokens or a parent that is not allowed gets QS_DEV_TREE: n_keep 0, path and
  * emitted -1, buffer and counters as they were.  All arrays are the caller's,
- * 4-byte aligned.  Errors: QS_ERR_ARG (null pointers, n_tree out of range),
+ * 4-byte aligned; an output lies on no other of them.  Errors: QS_ERR_ARG (null
+ * pointers, n_tree out of range, an output that overlaps another array),
  * QS_ERR_ALIGN.  Source: Pith review page, referee report on Algorithm 1 (verify,
  * keep what the target confirms, roll back the rest), here along a tree. */
 qs_status qs_tree_accept(const qs_cache *c, const int32_t *parent, const int32_t *draft,
