@@ -276,6 +276,21 @@ qs_status check_rows(const qs_rows *r) {
   return aligned16(r->data) ? QS_OK : QS_ERR_ALIGN;
 }
 
+// [p, p + bytes) shares memory with what lies between the first and the last of B x heads
+// x n rows.
+bool over_rows(const void *p, size_t bytes, const qs_rows &r, int B, int heads, int n) {
+  const int64_t ends[] = {(B - 1) * r.stride_b, (heads - 1) * r.stride_h, (n - 1) * r.stride_t};
+  int64_t lo = 0, hi = kD;
+  for (const int64_t e : ends) (e < 0 ? lo : hi) += e;
+  return overlap(p, bytes, r.data + lo, (size_t)(hi - lo) * sizeof(uint16_t));
+}
+
+// The rows lie as a contiguous [B][heads][n][D] does.
+bool contiguous_rows(const qs_rows &r, int B, int heads, int n) {
+  return (n == 1 || r.stride_t == kD) && (heads == 1 || r.stride_h == (int64_t)n * kD) &&
+         (B == 1 || r.stride_b == (int64_t)heads * n * kD);
+}
+
 }  // namespace
 }  // namespace qs
 
@@ -301,6 +316,13 @@ qs_status qs_buffer_append_rotary(const qs_cache *c, const qs_rows *k, const qs_
     return QS_ERR_ALIGN;
   RotArgs a = {*c, *k, *v, q ? *q : none, q_out, offset, inv_freq, q ? c->H * group : 0, n_new, rot,
                interleaved != 0, 0, 1};
+  if (q) {  // (a row is written when others may still be read)
+    const size_t bytes = sizeof(uint16_t) * kD * c->B * a.hq * n_new;
+    const bool in_place = q_out == q->data && contiguous_rows(*q, c->B, a.hq, n_new);
+    if ((!in_place && over_rows(q_out, bytes, *q, c->B, a.hq, n_new)) ||
+        over_rows(q_out, bytes, *k, c->B, c->H, n_new) || over_rows(q_out, bytes, *v, c->B, c->H, n_new))
+      return QS_ERR_ARG;
+  }
   const long long n_rows = 2ll * c->H + a.hq;
   int sms = 0;
   if ((s = sm_count(&sms)) != QS_OK) return s;

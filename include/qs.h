@@ -518,7 +518,8 @@ typedef struct {
  *   k, v    rows of H heads and n_new tokens (v is not rotated);
  *   q       rows of H * group heads and n_new tokens, or NULL (with q_out NULL);
  *   q_out   fp16 [B][H*group][n_new][D]: the rotated queries, as the attention
- *           calls take them (may be q itself where that has this layout);
+ *           calls take them (may be q itself where that has this layout; else
+ *           nowhere between an input's first row and its last);
  *   offset  int32 [B][n_new], 4-byte aligned, or NULL: token j stands at position
  *             n_groups * G + fill - pending + offset[j]
  *           (the committed tokens, and the depth of a node in a tree), with NULL
@@ -534,7 +535,7 @@ typedef struct {
  * A sequence without room for the tokens gets QS_DEV_OVERFLOW: its buffer and
  * counters stay, its queries are written all the same.  Errors: QS_ERR_ARG
  * (null pointers, n_new outside 1..2G, group < 1 with q, q without q_out or the
- * other way round, rot out of range), QS_ERR_SHAPE (a stride that is no multiple
+ * other way round, rot out of range, q_out on the inputs), QS_ERR_SHAPE (a stride that is no multiple
  * of 8), QS_ERR_ALIGN.  The inputs must not overlap the buffers.  Source: as
  * qs_buffer_append; rotary positions are a published method (RoFormer, 2021). */
 qs_status qs_buffer_append_rotary(const qs_cache *c, const qs_rows *k, const qs_rows *v,

@@ -41,3 +41,37 @@ def test_accept(L, out, other):
     mine = 4 * B if out == "n_keep" else BYTES
     for start in (at, at + size - 4, at - mine + 4):
         assert accept(L, **{other: at, out: start}) == qs.QS_ERR_ARG, hex(start)
+
+
+H, GROUP, T = 3, 2, 5  # KV heads, query heads on each, new tokens
+ROW = 256              # bytes
+
+
+def append(L, q_out, **rows):
+    """k, v and q heads of a token side by side from 0x100000 on, as one projection
+    leaves them (rows: (data, stride_b, stride_h, stride_t), strides in rows)."""
+    heads = (2 + GROUP) * H
+    a = {n: (0x100000 + at * ROW, T * heads, 1, heads) for n, at in (("q", 0), ("k", GROUP * H), ("v", GROUP * H + H))}
+    a.update(rows)
+    r = {n: qs.QsRowsStruct(x[0], *(128 * s for s in x[1:])) for n, x in a.items()}
+    c = _fake_cache(B=B, H=H)
+    return L.qs_buffer_append_rotary(ctypes.byref(c), ctypes.byref(r["k"]), ctypes.byref(r["v"]),
+                                     ctypes.byref(r["q"]), ctypes.c_void_p(q_out), GROUP, T, None,
+                                     ctypes.c_void_p(0x20000), 64, 0, None)
+
+
+def test_append(L):
+    end = 0x100000 + B * T * (2 + GROUP) * H * ROW
+    size = B * T * GROUP * H * ROW
+    for q_out in (0x100000, 0x100000 + 16, end - 16, 0x100000 - size + 16):
+        assert append(L, q_out) == qs.QS_ERR_ARG, hex(q_out)
+    own = (0x400000, T * GROUP * H, T, 1)  # q_out's layout
+    for q_out in (0x400000 + ROW, 0x400000 - ROW, 0x400000 + size - 16):
+        assert append(L, q_out, q=own) == qs.QS_ERR_ARG
+    for q in ((own[0], own[1], 1, GROUP * H), (own[0], 0, T, 1), (own[0], own[1], 0, 1)):
+        assert append(L, 0x400000, q=q) == qs.QS_ERR_ARG, q
+    # strides below zero: the rows lie in front of the first
+    last = (0x900000, -T * H, -T, -1)
+    for name in ("k", "v"):
+        assert append(L, 0x900000 - ROW, **{name: last}) == qs.QS_ERR_ARG
+        assert append(L, 0x900000 - (B * T * H - 1) * ROW - size + 16, **{name: last}) == qs.QS_ERR_ARG
