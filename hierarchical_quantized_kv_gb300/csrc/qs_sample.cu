@@ -1103,6 +1103,15 @@ extern "C" qs_status qs_sample(const void *logits, qs_dtype dtype, int32_t rows,
   const void *ptrs[] = {temperature, top_k, top_p, min_p, u, token, probs};
   for (const void *p : ptrs)
     if (reinterpret_cast<uintptr_t>(p) % 4) return QS_ERR_ALIGN;
+  // probabilities are written while other rows' logits may still be read: only row on row
+  if (probs && !(probs == logits && dtype == QS_FP32 && (rows == 1 || row_stride == V))) {
+    // the first row that ends behind the start of probs
+    const intptr_t step = rows > 1 ? row_stride * size : 0, len = (intptr_t)V * size;
+    const intptr_t behind = reinterpret_cast<intptr_t>(probs) - reinterpret_cast<intptr_t>(logits) - len;
+    const intptr_t r = behind < 0 || step == 0 ? 0 : behind / step + 1;
+    if (r < rows && overlap(probs, sizeof(float) * V * rows, static_cast<const char *>(logits) + r * step, len))
+      return QS_ERR_ARG;
+  }
   SampleArgs a = {logits, V, 1, rows > 1 ? row_stride : 0, temperature, top_p, min_p, u, top_k, token,
                   probs, 0, 0, 0, 0};
   // CTAs to a row: so many that two fit an SM (slices of 64 KB), and more while every

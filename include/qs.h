@@ -611,7 +611,7 @@ typedef enum { QS_FP16 = 0, QS_BF16 = 1, QS_FP32 = 2 } qs_dtype;
  *   u       float [rows]: uniform numbers in [0, 1);
  *   token   int32 [rows] (out);
  *   probs   float [rows][V] (out) or NULL; may be the logits themselves where those
- *           are fp32 with row_stride V.
+ *           are fp32 with row_stride V, and lies on none of them otherwise.
  * With x the row's logits and m the largest, token i weighs w_i = exp((x_i - m) /
  * temperature).  The tokens in order of falling logits, equal ones by rising index:
  *   top_k   keeps the first top_k (0 or less, or V and more: all);
@@ -630,7 +630,7 @@ typedef enum { QS_FP16 = 0, QS_BF16 = 1, QS_FP32 = 2 } qs_dtype;
  * equal ones.  Logits of -inf or NaN are never kept; where one is +inf, those with
  * +inf weigh 1 and all others 0.  A row without any token to keep gives token -1 and
  * zero probs.  One launch.  Errors: QS_ERR_ARG (null pointers, bad type, rows or V
- * < 1, a row_stride below V), QS_ERR_UNSUPPORTED (V > QS_MAX_VOCAB), QS_ERR_ALIGN.
+ * < 1, a row_stride below V, probs on the logits in another way), QS_ERR_UNSUPPORTED (V > QS_MAX_VOCAB), QS_ERR_ALIGN.
  * Source: "QuantSpec Guide", "The Self-Speculative Verification Loop" (tokens are
  * drawn from draft and target distributions, which qs_spec_accept takes); the
  * filters are those in common use. */

@@ -75,3 +75,22 @@ def test_append(L):
     for name in ("k", "v"):
         assert append(L, 0x900000 - ROW, **{name: last}) == qs.QS_ERR_ARG
         assert append(L, 0x900000 - (B * T * H - 1) * ROW - size + 16, **{name: last}) == qs.QS_ERR_ARG
+
+
+def sample(L, probs, dtype=qs.QS_FP32, rows=4, vocab=100, stride=100):
+    at = ctypes.c_void_p
+    return L.qs_sample(at(0x100000), dtype, rows, vocab, stride, None, None, None, None, at(0x20000), at(0x30000),
+                       at(probs), None)
+
+
+def test_sample(L):
+    """Probabilities in the logits' memory, but not in their place: of another type, with
+    another stride, or shifted."""
+    x, row = 0x100000, 400
+    for kw in (dict(dtype=qs.QS_FP16), dict(dtype=qs.QS_BF16), dict(stride=104), dict(dtype=qs.QS_FP16, rows=1)):
+        assert sample(L, x, **kw) == qs.QS_ERR_ARG, kw
+    for probs in (x + 4, x - 4, x + row, x - row, x + 4 * row - 4, x - 4 * row + 4):
+        assert sample(L, probs) == qs.QS_ERR_ARG, hex(probs)
+    # in front of the second, or behind the first, of rows far apart
+    for probs in (x + 4000 - 1600 + 4, x + row - 4, x + 3 * 4000 + row - 4):
+        assert sample(L, probs, stride=1000) == qs.QS_ERR_ARG, hex(probs)
