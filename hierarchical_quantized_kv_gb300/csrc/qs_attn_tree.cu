@@ -88,23 +88,21 @@ qs_status qs_attn_tree_workspace_size(const qs_cache *c, int32_t n_q, int32_t gr
   if (s != QS_OK) return s;
   if (!bytes || !tree_sizes_ok(n_q, group)) return QS_ERR_ARG;
   const int bits = c->upper_bits & ~QS_PAGED, R = group * n_q;
-  // (for either mode)
+  // for either mode, and for every call of fewer rows (a level of the tree, say): few rows
+  // may take the split kernel, whose CTAs leave more partials than the other one's
   *bytes = 0;
   if (R > split_rows(QS_VERIFY_INT8)) {
     int sms = 0;
     if ((s = sm_count(&sms)) != QS_OK) return s;
     *bytes = tall_ws_bytes(sms, c->B, c->H, R);
   }
-  if (R > split_rows(QS_DRAFT_UPPER4)) return QS_OK;
-  int P = 0;
-  for (const qs_mode mode : {QS_DRAFT_UPPER4, QS_VERIFY_INT8}) {
-    if (R > split_rows(mode)) continue;
-    int p = 0;
-    if ((s = grid_size<kListed | kTree>(mode, packed_rows(mode, R), bits, (R + 7) / 8, p)) != QS_OK) return s;
-    if (p > P) P = p;
-  }
-  const size_t split = ws_bytes(P, c->B, c->H, R);
-  if (split > *bytes) *bytes = split;
+  for (const qs_mode mode : {QS_DRAFT_UPPER4, QS_VERIFY_INT8})
+    for (int r = 1; r <= R && r <= split_rows(mode); ++r) {
+      int P = 0;
+      if ((s = grid_size<kListed | kTree>(mode, packed_rows(mode, r), bits, (r + 7) / 8, P)) != QS_OK) return s;
+      const size_t split = ws_bytes(P, c->B, c->H, r);
+      if (split > *bytes) *bytes = split;
+    }
   return QS_OK;
 }
 

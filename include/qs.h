@@ -544,7 +544,9 @@ qs_status qs_buffer_append_rotary(const qs_cache *c, const qs_rows *k, const qs_
                                   int32_t interleaved, qs_stream_t stream);
 
 /* Bytes of device workspace qs_attn_decode_tree needs for n_q queries and
- * `group` query heads per KV head.  Errors: as qs_attn_decode_tree. */
+ * `group` query heads per KV head, in either mode, and for any calls of fewer rows
+ * (group * n_q): what the whole tree's verification asks for serves its levels too.
+ * Errors: as qs_attn_decode_tree. */
 qs_status qs_attn_tree_workspace_size(const qs_cache *c, int32_t n_q, int32_t group, size_t *bytes);
 
 /* Decode attention of a tree's nodes: as qs_attn_decode_gqa (pg NULL: a
