@@ -19,7 +19,8 @@ bool tree_sizes_ok(int32_t n_q, int32_t group) {
 //   verify, 17 rows  131 / 115   45 / 42   20 / 20   454 / 411
 //   draft,  24 rows  100 / 115   35 / 42   18 / 20   334 / 408
 // (24 is also the most that the split kernel's layout holds.)
-int split_rows(qs_mode mode) { return mode == QS_VERIFY_INT8 ? 16 : kMaxR; }
+constexpr int split_rows(qs_mode mode) { return mode == QS_VERIFY_INT8 ? 16 : kMaxR; }
+static_assert(split_rows(QS_VERIFY_INT8) <= 16, "wide_verify leaves out the variants for more");
 
 qs_status decode_tall(const Params &a, qs_mode mode, void *workspace, size_t workspace_bytes,
                       cudaStream_t st) {

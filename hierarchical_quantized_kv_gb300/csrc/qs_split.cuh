@@ -2136,13 +2136,18 @@ qs_status grid_for_device(int dev, int &P, const int **clusters) {
   return QS_OK;
 }
 
+// Verify tiles of more than 16 rows have variants of their own, but not over a tree: there
+// so many rows go another way (qs_attn_tree.cu).
+constexpr bool wide_verify(int kind) { return !(kind & kTree); }
+
 template <int UB, int KIND>
 qs_status grid_size_ub(int dev, qs_mode mode, bool packed, int ncg, int &P, const int **cl) {
   if (mode == QS_DRAFT_UPPER4)
     return packed ? grid_for_device<QS_DRAFT_UPPER4, true, UB, kWarps, KIND>(dev, P, cl)
                   : grid_for_device<QS_DRAFT_UPPER4, false, UB, kWarps, KIND>(dev, P, cl);
-  return ncg <= 2 ? grid_for_device<QS_VERIFY_INT8, false, UB, kVerifyWarps, KIND>(dev, P, cl)
-                  : grid_for_device<QS_VERIFY_INT8, false, UB, kWarps, KIND>(dev, P, cl);
+  if constexpr (wide_verify(KIND))
+    if (ncg > 2) return grid_for_device<QS_VERIFY_INT8, false, UB, kWarps, KIND>(dev, P, cl);
+  return grid_for_device<QS_VERIFY_INT8, false, UB, kVerifyWarps, KIND>(dev, P, cl);
 }
 
 template <int KIND>
@@ -2175,9 +2180,11 @@ qs_status launch(const Params &prm, cudaStream_t s) {
 
 template <int UB, int KIND>
 qs_status launch_ub(qs_mode mode, bool packed, const Params &prm, cudaStream_t st) {
-  if (mode == QS_VERIFY_INT8)
-    return prm.ncg <= 2 ? launch<QS_VERIFY_INT8, false, UB, kVerifyWarps, KIND>(prm, st)
-                        : launch<QS_VERIFY_INT8, false, UB, kWarps, KIND>(prm, st);
+  if (mode == QS_VERIFY_INT8) {
+    if constexpr (wide_verify(KIND))
+      if (prm.ncg > 2) return launch<QS_VERIFY_INT8, false, UB, kWarps, KIND>(prm, st);
+    return launch<QS_VERIFY_INT8, false, UB, kVerifyWarps, KIND>(prm, st);
+  }
   return packed ? launch<QS_DRAFT_UPPER4, true, UB, kWarps, KIND>(prm, st)
                 : launch<QS_DRAFT_UPPER4, false, UB, kWarps, KIND>(prm, st);
 }
