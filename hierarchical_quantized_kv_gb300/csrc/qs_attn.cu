@@ -103,6 +103,8 @@ extern "C" int qs_checked_failures_listed(unsigned long long *out2, int reset);
 extern "C" int qs_checked_failures_select(unsigned long long *out2, int reset);
 extern "C" int qs_checked_failures_read(unsigned long long *out2, int reset);
 extern "C" int qs_checked_failures_tree(unsigned long long *out2, int reset);
+extern "C" int qs_checked_failures_buffer_tree(unsigned long long *out2, int reset);
+extern "C" int qs_checked_failures_sample(unsigned long long *out2, int reset);
 
 // Checked build only (-DQS_CHECKED=1): the number of failed bounds checks of
 // the kernels since the last reset, and the tag of the first (attention: 1
@@ -114,13 +116,17 @@ extern "C" int qs_checked_failures_tree(unsigned long long *out2, int reset);
 // sums in the workspace; selection: 40 score, 41 list of close groups, 42 output,
 // 43 scales and zeros, 44 query row; read back: 50 group, 51 buffer row, 52 output
 // row, 53 tile row; attention of many rows: 60 store to shared memory, 61 copy,
-// 62 partial written, 63 partial read).  reset != 0 zeroes the counts.  Returns 0, or 1 if a CUDA call
-// failed.
+// 62 partial written, 63 partial read, 64 sequence and head (of queries, buffer rows and
+// parents), 65 output row; sampling: 70 slice, 71 queue, 72 place in the slice, 73 list,
+// 74 bin, 75 the candidates' weights, 77 a warp's sum, 78 probability; append with
+// rotation: 80 angle, 81 input row, 82 query row, 83 ring row; acceptance: 84 node, 85
+// ring row).  reset != 0 zeroes the counts.  Returns 0, or 1 if a CUDA call failed.
 extern "C" int qs_checked_failures(unsigned long long *count, unsigned int *first_tag, int reset) {
-  unsigned long long f[6][2];
+  unsigned long long f[8][2];
   if (read_check_failures(f[0], reset) || qs_checked_failures_quantize(f[1], reset) ||
       qs_checked_failures_listed(f[2], reset) || qs_checked_failures_select(f[3], reset) ||
-      qs_checked_failures_read(f[4], reset) || qs_checked_failures_tree(f[5], reset))
+      qs_checked_failures_read(f[4], reset) || qs_checked_failures_tree(f[5], reset) ||
+      qs_checked_failures_buffer_tree(f[6], reset) || qs_checked_failures_sample(f[7], reset))
     return 1;
   *count = 0;
   *first_tag = 0;

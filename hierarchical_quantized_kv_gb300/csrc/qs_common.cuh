@@ -176,8 +176,9 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 }
 
 // ---- checked build (-DQS_CHECKED=1): the kernels check the bounds of their
-// shared-memory and global indexing on the device (attention, quantizer,
-// selection, read back; the tags are listed at qs_checked_failures).  A failing
+// shared-memory and global indexing on the device (attention, quantizer, selection,
+// read back, a tree's append and acceptance, sampling; the tags are listed at
+// qs_checked_failures).  A failing
 // access is skipped (a load reads zero) and counted with a tag naming it, never
 // trapped; the checked library exports qs_checked_failures to read the
 // counts.  The ordinary build compiles every check away.

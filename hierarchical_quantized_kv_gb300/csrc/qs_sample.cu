@@ -317,8 +317,9 @@ struct Row {
     int v0, v1, count = 0;
     run_of(v0, v1);
     auto work = [&](int from, bool mine) {
-      if (!mine) return;
+      if (!mine || !chk(from + lane < kQueue, 71)) return;
       const int at = q[from + lane];
+      if (!chk(at < n_vec * E, 72)) return;
       body(__fadd_rn(as_float(reinterpret_cast<const T *>(slice)[at]), 0.f), x0 + at);
     };
 #pragma unroll 1
@@ -344,7 +345,9 @@ struct Row {
       }
       const int all = __shfl_sync(0xffffffffu, before, 31);
       uint16_t *to = q + count + before - n;
-      for (; hits; hits &= hits - 1) *to++ = (uint16_t)(v * E + __ffs(hits) - 1);
+      for (; hits; hits &= hits - 1)
+        if (chk(smem_in(smem_addr(to), 2) && to < q + kQueue && v * E + E <= 65536, 71))
+          *to++ = (uint16_t)(v * E + __ffs(hits) - 1);
       count += all;
       __syncwarp();
       while (count >= 32) {
@@ -425,6 +428,7 @@ struct Row {
   __device__ __noinline__ void sort(int n) {
     int p = 32;
     while (p < n) p <<= 1;
+    if (!chk(p <= kCap && smem_in(smem_addr(list), 8 * p), 73)) return;
     for (int i = n + tid; i < p; i += kThreads) list[i] = ~0ull;
 #pragma unroll 1
     for (int k = 2; k <= p; k <<= 1)
@@ -452,7 +456,7 @@ struct Row {
   // Put a logit into the first CTA's list (which holds kCap; all are counted).
   __device__ __forceinline__ void collect(Shared &s0, u64 *list0, float x, int i) const {
     const int k = atomicAdd(&s0.n_list, 1);
-    if (k < kCap) list0[k] = entry(x, i);
+    if (k < kCap && chk(smem_in(smem_addr(list + k), 8) && i >= 0, 73)) list0[k] = entry(x, i);
   }
 
   // In the first CTA: the position in the sorted list at which a running sum of
@@ -531,6 +535,7 @@ struct Row {
     each([&](float x, int) {
       if (x < lo || x > hi) return;
       const int b = bin_of(x);
+      if (!chk(b >= 0 && b < kBins && smem_in(smem_addr(hist + 3 * kBins + b), 4), 74)) return;
       atomicAdd(&hist[3 * kBins + b], 1u);
       if (!COUNT) {
         const u64 w = weight(x);
@@ -694,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int v = v0 + k * kThreads;
-        if (v >= n_vec) continue;
+        if (v >= n_vec || !chk(16 * (v + 1) <= a.hist_off, 70)) continue;
         if (v * E >= first && (v + 1) * E - first <= n) {
           x[k] = vsrc[v];
         } else {  // an end: element by element, NaN outside
@@ -710,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int v = v0 + k * kThreads;
-        if (v >= n_vec) continue;
+        if (v >= n_vec || !chk(16 * (v + 1) <= a.hist_off, 70)) continue;
         reinterpret_cast<uint4 *>(smem)[v] = x[k];
         const T *p = reinterpret_cast<const T *>(&x[k]);
 #pragma unroll
@@ -747,7 +752,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       const int head = min(n, (int)(-(reinterpret_cast<uintptr_t>(z) >> 2) & 3)), quads = (n - head) >> 2;
       if (tid < head) z[tid] = 0.f;
       float4 *z4 = reinterpret_cast<float4 *>(z + head);
-      for (int i = tid; i < quads; i += kThreads) z4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = tid; i < quads; i += kThreads)
+        if (chk(head + 4 * i + 4 <= n && lo_i + n <= a.V, 78)) z4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       const int i = head + 4 * quads + tid;
       if (i < n) z[i] = 0.f;
     }
@@ -821,7 +827,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (k <= kSmallK && k < a.V && !R.inf && mt < m) {
     // ---- a small top-k: the k-th largest of the threads' largest logits bounds it
     const typename Row<T>::Binning bin_of(mt, m);
-    if (mine > kNone) atomicAdd(&cl.map_shared_rank(hist, 0)[bin_of(mine)], 1u);
+    if (mine > kNone && chk(bin_of(mine) >= 0 && bin_of(mine) < kBins, 74))
+      atomicAdd(&cl.map_shared_rank(hist, 0)[bin_of(mine)], 1u);
     cluster_sync();
     if (rank == 0) {
       u64 cw[Row<T>::P];
@@ -865,12 +872,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         const u64 wx = mine_k ? w(x) : 0;
         if (few) {
           __syncthreads();
-          if (mine_k) {
+          if (mine_k && chk(place < kCap && a.part_off + 8 * (place + 1) <= a.list_off, 75)) {
             R.list[place] = e;
             weight_of[place] = wx;
           }
           __syncthreads();
-        } else if (mine_k) {
+        } else if (mine_k && chk(a.part_off + 8 * (tid + 1) <= a.list_off, 75)) {
           weight_of[tid] = wx;
         }
         // what stands in front of each, and all together
@@ -954,6 +961,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           // (in units of 2^-30, in two parts: most weights have but one)
           const uint32_t r = (uint32_t)((wx + (1ull << (kOutline - 1))) >> kOutline);
           const int b = bin_of(x);
+          if (!chk(b >= 0 && b < kBins, 74)) return;
           if (r & 0x7FFF) atomicAdd(&hist[b], r & 0x7FFF);
           if (r >> 15) atomicAdd(&hist[kBins + b], r >> 15);
         });
@@ -1007,7 +1015,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             // a thread each: the one whose turn it is knows it from those in front of it
             u64 *weight_of = reinterpret_cast<u64 *>(smem + a.part_off);
             u64 e = 0, wx = 0, before = sum_a;
-            if (tid < n_list) {
+            if (tid < n_list && chk(a.part_off + 8 * (tid + 1) <= a.list_off, 75)) {
               e = R.list[tid];
               weight_of[tid] = wx = w(Row<T>::value(e));
             }
@@ -1049,7 +1057,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
               if (i < hi_i && in_front(x, i)) {
                 const u64 wx = w(x);
                 if (i < lo_i) f = wx;
-                else atomicAdd(&s.part[(i - R.x0) / E / per_warp], wx);
+                else if (chk((i - R.x0) / E / per_warp < kWarpsS, 77)) atomicAdd(&s.part[(i - R.x0) / E / per_warp], wx);
               }
             }
             front += R.block_sum(f);
@@ -1073,7 +1081,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
   if (probs)
     R.named([&](float x, int i) { return x >= x_min && in_front(x, i); },
-            [&](float x, int i) { probs[i] = w.scaled(x, scale); });
+            [&](float x, int i) {
+              if (chk(i >= 0 && i < a.V, 78)) probs[i] = w.scaled(x, scale);
+            });
   cluster_sync();  // the others have read this CTA's sums
 }
 
@@ -1137,3 +1147,10 @@ extern "C" qs_status qs_sample(const void *logits, qs_dtype dtype, int32_t rows,
   if (dtype == QS_FP16) return launch_sample<__half>(a, rows, smem, st);
   return launch_sample<__nv_bfloat16>(a, rows, smem, st);
 }
+
+#if QS_CHECKED
+// Checked build only: this file's failure count and first failing tag.
+extern "C" int qs_checked_failures_sample(unsigned long long *out2, int reset) {
+  return read_check_failures(out2, reset);
+}
+#endif

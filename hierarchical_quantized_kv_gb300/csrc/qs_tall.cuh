@@ -972,6 +972,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
       piece_at(c.B, prm.n_mp, T.ng, x, x1, &sh.piece[w]);
       const volatile Piece &pc = sh.piece[w];  // (read where needed)
       const int n = pc.n, n_grp = min(n, max(0, pc.ng - pc.u0));  // units; groups among them
+      if (!chk(pc.b >= 0 && pc.b < c.B && pc.h >= 0 && pc.h < c.H, 64)) break;
       const size_t bh = (size_t)pc.b * c.H + pc.h;
       x += n;
       if (!values) {
@@ -1089,6 +1090,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) tall_kernel(const __grid_cons
       const int row_p = MT == 2 ? row_t : one_tile_row(row_t, s, prm.R);
       const int row = MT == 2 ? 2 * kTile * pc.mp + s * kTile + row_t : row_p;
       const bool live_warp = row >= 0 && row - lane < prm.R;
+      if (!chk(pc.b >= 0 && pc.b < c.B, 64)) break;
       uint64_t sees = 0;
       if (pc.u0 + n > pc.ng && live_warp) {  // the buffer: the nodes that this row sees
         uint64_t mm[2];
@@ -1338,7 +1340,7 @@ __global__ void __launch_bounds__(kJoinThreads) tall_join_kernel(const __grid_co
     s_ml[threadIdx.x - kJoinLane] = make_float2(M, Ls);
   }
   __syncthreads();
-  if (part || !here) return;
+  if (part || !here || !chk(in_range(at, 1, (size_t)c.B * c.H * prm.R), 65)) return;
   uint2 *out = reinterpret_cast<uint2 *>(prm.out + at * kD + 4 * c4);
   if (len == 0) {  // n_tree > fill
     *out = make_uint2(0, 0);

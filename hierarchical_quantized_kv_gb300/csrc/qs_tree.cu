@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kRotThreads, 5) append_rotary_kernel(const Rot
     const long long p = (long long)((unsigned long long)(long long)pos * s_turns[f]);
     float2 cs;
     sincospif((float)(int)(p >> 32) * 4.656612873077393e-10f, &cs.y, &cs.x);
-    s_cs[i] = cs;
+    if (chk(i < kRotTokens * kMaxHalf && f < kMaxHalf, 80)) s_cs[i] = cs;
   }
   __syncthreads();
   const int rows = 2 * c.H + a.hq, per = (rows + a.splits - 1) / a.splits;
@@ -121,12 +121,15 @@ __global__ void __launch_bounds__(kRotThreads, 5) append_rotary_kernel(const Rot
                                                          (j0 + j) * s.stride_t);
       x[u] = src[vx];
       y[u] = src[vy];
+      if (!chk(b < c.B && h >= 0 && h < (is_q ? a.hq : c.H) && j0 + j < a.n_new && vx < kVec && vy < kVec, 81)) continue;
       if (is_q) {
-        dst[u] = reinterpret_cast<uint4 *>(a.q_out) + (((size_t)b * a.hq + h) * a.n_new + j0 + j) * kVec;
+        const size_t at = ((size_t)b * a.hq + h) * a.n_new + j0 + j;
+        if (chk(in_range(at, 1, (size_t)c.B * a.hq * a.n_new), 82)) dst[u] = reinterpret_cast<uint4 *>(a.q_out) + at * kVec;
       } else if (room) {
         const int slot = (base * kG + fill + j0 + j) & (kRing - 1);
-        dst[u] = reinterpret_cast<uint4 *>(is_v ? c.buf_v : c.buf_k) +
-                 (((size_t)b * c.H + h) * kRing + slot) * kVec;
+        const size_t at = ((size_t)b * c.H + h) * kRing + slot;
+        if (chk(in_range(at, 1, (size_t)c.B * c.H * kRing), 83))
+          dst[u] = reinterpret_cast<uint4 *>(is_v ? c.buf_v : c.buf_k) + at * kVec;
       }
     }
 #pragma unroll
@@ -188,7 +191,7 @@ __global__ void __launch_bounds__(kAccThreads)
       const int j = tid + 32 * k;
       const size_t at = (size_t)b * n + j;
       up[k] = tok[k] = tgt[k] = -1;
-      if (j < n) {
+      if (j < n && chk(in_range(at, 1, (size_t)c.B * n), 84)) {
         up[k] = parent[at];
         tok[k] = draft[at];
         tgt[k] = target[at];
@@ -224,7 +227,7 @@ __global__ void __launch_bounds__(kAccThreads)
     if (h == 0) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        if (tid + 32 * k < n) {
+        if (tid + 32 * k < n && chk(in_range((size_t)b * n + tid + 32 * k, 1, (size_t)c.B * n), 84)) {
           path[(size_t)b * n + tid + 32 * k] = mine[k];
           emitted[(size_t)b * n + tid + 32 * k] = out[k];
         }
@@ -247,6 +250,8 @@ __global__ void __launch_bounds__(kAccThreads)
   for (int u = 0; u < U; ++u) {
     const int i = tid / kVec + u * (kAccThreads / kVec);
     if (i < keep && s_path[i] != i) {
+      if (!chk(i < QS_MAX_TREE && s_path[i] >= 0 && s_path[i] < n && in_range(row0, kRing, (size_t)c.B * c.H * kRing), 85))
+        continue;
       const int src = (first + s_path[i]) & (kRing - 1);
       xk[u] = bk[src * kVec + col];
       xv[u] = bv[src * kVec + col];
@@ -359,3 +364,10 @@ qs_status qs_tree_accept(const qs_cache *c, const int32_t *parent, const int32_t
 }
 
 }  // extern "C"
+
+#if QS_CHECKED
+// Checked build only: this file's failure count and first failing tag.
+extern "C" int qs_checked_failures_buffer_tree(unsigned long long *out2, int reset) {
+  return read_check_failures(out2, reset);
+}
+#endif
