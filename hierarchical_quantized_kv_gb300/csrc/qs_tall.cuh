@@ -16,7 +16,7 @@
 // Design (GB300).
 //  * One CTA per SM takes an equal range of (sequence, KV head, unit)s, as the split
 //    kernel does, and writes a partial (O, m, l) for each segment it touches; a second
-//    kernel joins them.
+//    kernel joins them, by the differences of their m, which are scores.
 //  * Roles (23 warps): one starts the bulk copies of planes and scales into a ring; one
 //    makes scales and zeros ready; eight make the operand tiles of the keys (128 rows of
 //    128 fp16, the 128-byte swizzle of K-major operands), four those of the values, in a
@@ -42,11 +42,13 @@
 //    eight channels the keys' nibbles come out as 0 4 1 5 2 6 3 7; the queries are
 //    stored in that order too.
 //
-// Measured: 240 rows over 32k tokens of 8 KV heads 66 us (17 by the two products'
-// operations, 26 with the third); there the making of a unit's tiles and its products wait for
+// Measured (replays on the same inputs): 240 rows over 32k tokens of 8 KV heads 66 us (17 by
+// the two products' operations, 26 with the third); there the making of a unit's tiles and its products wait for
 // one another, in the room that shared memory has. 26 rows over 8 x 32 heads, ragged to 64k
-// tokens, 0.95 ms (0.37 by bytes): shared memory's bandwidth, of which the scores' operands
-// take 128 KB a unit, and the chain of scores, softmax and weights.
+// tokens, 0.96 ms (0.37 by bytes): shared memory's bandwidth, of which the scores' operands
+// take 128 KB a unit, and the chain of scores, softmax and weights.  A draft takes the same
+// way, with both key tiles: 25 rows over 32k tokens of 32 heads 116 us (21 by bytes), 32
+// rows of 8 heads 41 (5).
 #pragma once
 
 #include "qs_split.cuh"

@@ -628,11 +628,12 @@ typedef enum { QS_FP16 = 0, QS_BF16 = 1, QS_FP32 = 2 } qs_dtype;
  * token).  Weights are formed to about 2^-36 of themselves and added as 64-bit
  * integers of 2^-44, so a result does not depend on an order of summation; a token
  * that weighs less than about 2^-45 may be kept, but adds nothing to a sum and is
- * never drawn.  A temperature of 0 (of less than 2^-60, or NaN) takes the largest logit, the lowest index among
- * equal ones.  Logits of -inf or NaN are never kept; where one is +inf, those with
- * +inf weigh 1 and all others 0.  A row without any token to keep gives token -1 and
- * zero probs.  One launch.  Errors: QS_ERR_ARG (null pointers, bad type, rows or V
- * < 1, a row_stride below V, probs on the logits in another way), QS_ERR_UNSUPPORTED (V > QS_MAX_VOCAB), QS_ERR_ALIGN.
+ * never drawn.  A temperature of 0 (of less than 2^-60, or NaN) takes the largest
+ * logit, the lowest index among equal ones.  Logits of -inf or NaN are never kept;
+ * where one is +inf, those with +inf weigh 1 and all others 0.  A row without any
+ * token to keep gives token -1 and zero probs.  One launch.  Errors: QS_ERR_ARG (null
+ * pointers, bad type, rows or V < 1, a row_stride below V, probs on the logits in
+ * another way), QS_ERR_UNSUPPORTED (V > QS_MAX_VOCAB), QS_ERR_ALIGN.
  * Source: "QuantSpec Guide", "The Self-Speculative Verification Loop" (tokens are
  * drawn from draft and target distributions, which qs_spec_accept takes); the
  * filters are those in common use. */
